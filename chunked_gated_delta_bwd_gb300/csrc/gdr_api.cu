@@ -8,20 +8,26 @@
 
 #include "../../include/gdr.h"
 #include "gdr_common.cuh"
+#include "gdr_host.h"
 #include "gdr_internal.h"
 
 namespace gdr {
 
 static thread_local char g_err[512] = "";
 
-static gdr_status fail(gdr_status s, const char* fmt, const char* what = "") {
+gdr_status fail(gdr_status s, const char* fmt, const char* what) {
     snprintf(g_err, sizeof(g_err), fmt, what);
     return s;
 }
 
-static gdr_status cuda_fail(cudaError_t e, const char* where) {
+gdr_status cuda_fail(cudaError_t e, const char* where) {
     snprintf(g_err, sizeof(g_err), "%s: %s", where, cudaGetErrorString(e));
     return GDR_ERR_CUDA;
+}
+
+gdr_status ok() {
+    g_err[0] = 0;
+    return GDR_OK;
 }
 
 // chunk_off[s] = sum_{i<s} ceil(len_i / 64); validates cu_seqlens on the device.
@@ -244,18 +250,6 @@ static Layout layout(const gdr_shape* sh) {
     return L;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
-#define NEED(ptr)                                                                    \
-    do {                                                                             \
-        if (!(ptr)) return fail(GDR_ERR_INVALID, "required pointer %s is NULL", #ptr); \
-        if (!aligned16(ptr)) return fail(GDR_ERR_INVALID, "pointer %s is not 16-byte aligned", #ptr); \
-    } while (0)
-#define OPT(ptr)                                                                     \
-    do {                                                                             \
-        if ((ptr) && !aligned16(ptr)) return fail(GDR_ERR_INVALID, "pointer %s is not 16-byte aligned", #ptr); \
-    } while (0)
-
 static void base_params(Params& p, const gdr_shape* sh, const Layout& L, void* ws, int kda) {
     memset(&p, 0, sizeof(p));
     p.N = sh->num_seqs;
@@ -291,31 +285,7 @@ static void base_params(Params& p, const gdr_shape* sh, const Layout& L, void* w
     p.segS = reinterpret_cast<float*>(w + L.segS);
 }
 
-// ---------------------------------------------------------------------------
-// optional per-kernel event timing (gdr_profile_begin / gdr_profile_end)
-// ---------------------------------------------------------------------------
-struct Prof {
-    bool on = false;
-    int max_launches = 0, n = 0;
-    cudaEvent_t* ev = nullptr;  // 2 per timed section
-    int* kind = nullptr;
-    int* kernels = nullptr;     // kernels launched in each timed section
-};
-static Prof g_prof;
-
-// Launches `f` (which launches `kernels` kernels) between two recorded events when
-// profiling is on.
-template <class F>
-static cudaError_t timed(int kind, cudaStream_t s, F&& f, int kernels = 1) {
-    if (!g_prof.on || g_prof.n >= g_prof.max_launches) return f();
-    const int i = g_prof.n++;
-    g_prof.kind[i] = kind;
-    g_prof.kernels[i] = kernels;
-    cudaEventRecord(g_prof.ev[2 * i], s);
-    cudaError_t e = f();
-    cudaEventRecord(g_prof.ev[2 * i + 1], s);
-    return e;
-}
+Prof g_prof;
 
 // status reset + chunk table (+ prep)
 static gdr_status common_front(const Params& p, cudaStream_t s) {

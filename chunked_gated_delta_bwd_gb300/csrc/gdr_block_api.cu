@@ -1,0 +1,276 @@
+// C ABI of the operators around the delta rule in a recurrent block (declared in
+// include/gdr.h): argument checks and launches.
+#include <limits.h>
+#include <string.h>
+
+#include "gdr_block.h"
+#include "gdr_common.cuh"
+#include "gdr_host.h"
+
+namespace gdr {
+
+// a pointer to rows read two elements at a time: aligned to a pair
+#define NEED_ROWS(ptr, f32)                                                                       \
+    do {                                                                                          \
+        if (!(ptr)) return fail(GDR_ERR_INVALID, "required pointer %s is NULL", #ptr);            \
+        if (!aligned_to(ptr, (f32) ? 8 : 4))                                                      \
+            return fail(GDR_ERR_INVALID, "pointer %s is not aligned to two elements", #ptr);      \
+    } while (0)
+
+// a row stride in elements: 0 means contiguous rows; resolves it
+static gdr_status row_stride(int64_t given, int64_t channels, int64_t* out) {
+    if (given == 0) given = channels;
+    if (given < channels || given % 2 != 0)
+        return fail(GDR_ERR_INVALID, "a row stride must be even and at least the number of channels%s");
+    *out = given;
+    return GDR_OK;
+}
+
+static gdr_status check_channels(int32_t channels) {
+    if (channels < 1) return fail(GDR_ERR_INVALID, "channels must be >= 1%s");
+    if (channels % 2 != 0) return fail(GDR_ERR_INVALID, "channels must be even%s");
+    return GDR_OK;
+}
+
+static gdr_status check_glr_choices(int32_t gate, int32_t act_type, int32_t gate_type) {
+    if (gate != GLR_GATE_LOG && gate != GLR_GATE_SOFTPLUS) return fail(GDR_ERR_INVALID, "unknown gate function%s");
+    if ((act_type != GDR_TYPE_BF16 && act_type != GDR_TYPE_F32) || (gate_type != GDR_TYPE_BF16 && gate_type != GDR_TYPE_F32))
+        return fail(GDR_ERR_UNSUPPORTED, "element types are bf16 and float32%s");
+    if (act_type == GDR_TYPE_F32 && gate_type == GDR_TYPE_BF16)
+        return fail(GDR_ERR_UNSUPPORTED, "float32 activations need a float32 gate%s");
+    return GDR_OK;
+}
+
+static gdr_status check_tokens(int32_t num_seqs, int64_t total_tokens, const int64_t* cu_seqlens, int64_t channels) {
+    if (num_seqs < 1 || total_tokens < 0) return fail(GDR_ERR_INVALID, "num_seqs must be >= 1, total_tokens >= 0%s");
+    if (!cu_seqlens && total_tokens % num_seqs != 0)
+        return fail(GDR_ERR_INVALID, "dense layout needs total_tokens divisible by num_seqs%s");
+    if (total_tokens > ((int64_t)1 << 36) || channels * total_tokens > ((int64_t)1 << 40))
+        return fail(GDR_ERR_INVALID, "problem too large%s");
+    return GDR_OK;
+}
+
+static gdr_status check_glr(const glr_shape* sh, GlrParams* p) {
+    if (!sh) return fail(GDR_ERR_INVALID, "shape is NULL%s");
+    gdr_status st = check_channels(sh->channels);
+    if (st == GDR_OK) st = check_tokens(sh->num_seqs, sh->total_tokens, sh->cu_seqlens, sh->channels);
+    if (st == GDR_OK) st = check_glr_choices(sh->gate, sh->act_type, sh->gate_type);
+    int64_t ldx = 0, ldg = 0;
+    if (st == GDR_OK) st = row_stride(sh->x_stride, sh->channels, &ldx);
+    if (st == GDR_OK) st = row_stride(sh->g_stride, sh->channels, &ldg);
+    if (st != GDR_OK || !p) return st;
+    memset(p, 0, sizeof(*p));
+    p->N = sh->num_seqs;
+    p->C = sh->channels;
+    p->T = sh->total_tokens;
+    p->seq_len = sh->cu_seqlens ? 0 : sh->total_tokens / sh->num_seqs;
+    p->cu_seqlens = sh->cu_seqlens;
+    p->ldx = ldx;
+    p->ldg = ldg;
+    p->gate = sh->gate;
+    p->complement = sh->complement != 0;
+    p->act_f32 = sh->act_type == GDR_TYPE_F32;
+    p->gate_f32 = sh->gate_type == GDR_TYPE_F32;
+    return GDR_OK;
+}
+
+static size_t glr_workspace(const glr_shape*) { return 256; }  // the status word
+
+// the status word cleared; every sequence empty: the states pass through
+static gdr_status glr_front(const GlrParams& p, void* ws, size_t ws_bytes, size_t need, float* to, const float* from,
+                            cudaStream_t s, bool* done) {
+    if (ws_bytes < need) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
+    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
+    *done = p.T == 0;
+    if (p.T || !to) return GDR_OK;
+    const size_t bytes = sizeof(float) * (size_t)p.N * p.C;
+    e = from ? cudaMemcpyAsync(to, from, bytes, cudaMemcpyDeviceToDevice, s) : cudaMemsetAsync(to, 0, bytes, s);
+    return e == cudaSuccess ? GDR_OK : cuda_fail(e, "states of empty sequences");
+}
+
+}  // namespace gdr
+
+using namespace gdr;
+
+extern "C" {
+
+size_t glr_workspace_bytes(const glr_shape* shape) {
+    if (check_glr(shape, nullptr) != GDR_OK) return 0;
+    return glr_workspace(shape);
+}
+
+gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const float* A_log, const float* dt_bias,
+                   const float* h0, void* h, float* ht, void* workspace, size_t workspace_bytes, void* stream) {
+    GlrParams p;
+    if (gdr_status st = check_glr(shape, &p)) return st;
+    if (p.T) {
+        NEED_ROWS(x, p.act_f32); NEED_ROWS(g, p.gate_f32); NEED(h);
+        if (p.gate == GLR_GATE_SOFTPLUS) { NEED(A_log); NEED(dt_bias); }
+    }
+    OPT(h0); OPT(ht); NEED(workspace);
+    cudaStream_t s = (cudaStream_t)stream;
+    bool done = false;
+    if (gdr_status st = glr_front(p, workspace, workspace_bytes, glr_workspace(shape), ht, h0, s, &done)) return st;
+    if (done) return ok();
+    p.status = static_cast<int*>(workspace);
+    p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0; p.h = h; p.ht = ht;
+    cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_fwd(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence launch");
+}
+
+gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const float* A_log, const float* dt_bias,
+                   const void* h, const float* h0, const void* dh, const float* dht, void* workspace,
+                   size_t workspace_bytes, void* dx, void* dg, float* dh0, float* dA_log, float* ddt_bias,
+                   void* stream) {
+    GlrParams p;
+    if (gdr_status st = check_glr(shape, &p)) return st;
+    const bool soft = p.gate == GLR_GATE_SOFTPLUS;
+    if (p.T) {
+        if (p.complement) NEED_ROWS(x, p.act_f32);
+        NEED_ROWS(g, p.gate_f32); NEED(h); NEED(dh); NEED(dx); NEED(dg);
+        if (soft) { NEED(A_log); NEED(dt_bias); }
+    }
+    NEED(dh0); OPT(h0); OPT(dht); NEED(workspace);
+    if (soft) { NEED(dA_log); NEED(ddt_bias); }
+    cudaStream_t s = (cudaStream_t)stream;
+    bool done = false;
+    if (gdr_status st = glr_front(p, workspace, workspace_bytes, glr_workspace(shape), dh0, dht, s, &done)) return st;
+    if (done) {
+        if (!soft) return ok();
+        cudaError_t e = cudaMemsetAsync(dA_log, 0, sizeof(float) * p.C, s);
+        if (e == cudaSuccess) e = cudaMemsetAsync(ddt_bias, 0, sizeof(float) * p.C, s);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync(dA_log/ddt_bias)");
+    }
+    p.status = static_cast<int*>(workspace);
+    p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h_in = h; p.h0 = h0; p.dh = dh; p.dht = dht;
+    p.dx = dx; p.dg = dg; p.dh0 = dh0; p.dA_log = dA_log; p.ddt_bias = ddt_bias;
+    cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_bwd(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence backward launch");
+}
+
+gdr_status glr_step(int32_t rows, int32_t channels, int32_t pool, int32_t gate, int32_t complement, int32_t act_type,
+                    int32_t gate_type, const void* x, int64_t x_stride, const void* g, int64_t g_stride,
+                    const float* A_log, const float* dt_bias, const int64_t* slots, float* state, void* y,
+                    void* stream) {
+    GlrStepParams p;
+    if (gdr_status st = check_channels(channels)) return st;
+    if (gdr_status st = check_glr_choices(gate, act_type, gate_type)) return st;
+    if (rows < 0 || pool < 0) return fail(GDR_ERR_INVALID, "rows and pool must be >= 0%s");
+    if (!slots && pool < rows) return fail(GDR_ERR_INVALID, "the pool holds fewer states than there are rows%s");
+    if (gdr_status st = row_stride(x_stride, channels, &p.ldx)) return st;
+    if (gdr_status st = row_stride(g_stride, channels, &p.ldg)) return st;
+    if (rows == 0) return ok();
+    NEED_ROWS(x, act_type == GDR_TYPE_F32); NEED_ROWS(g, gate_type == GDR_TYPE_F32); NEED(y);
+    if (pool) NEED(state);
+    if (gate == GLR_GATE_SOFTPLUS) { NEED(A_log); NEED(dt_bias); }
+    if (slots && !aligned_to(slots, 8)) return fail(GDR_ERR_INVALID, "pointer %s is not 8-byte aligned", "slots");
+    p.N = rows; p.C = channels; p.pool = pool;
+    p.gate = gate; p.complement = complement != 0;
+    p.act_f32 = act_type == GDR_TYPE_F32; p.gate_f32 = gate_type == GDR_TYPE_F32;
+    p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.slots = slots; p.state = state; p.y = y;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_step(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence step launch");
+}
+
+static gdr_status check_norm(int64_t rows, int32_t channels, int32_t res_type) {
+    if (rows < 0 || rows > INT_MAX) return fail(GDR_ERR_INVALID, "rows must be 0 to 2^31 - 1%s");
+    if (gdr_status st = check_channels(channels)) return st;
+    if (res_type != GDR_TYPE_BF16 && res_type != GDR_TYPE_F32)
+        return fail(GDR_ERR_UNSUPPORTED, "the residual's type is bf16 or float32%s");
+    return GDR_OK;
+}
+
+gdr_status gdr_rmsnorm_fwd(int64_t rows, int32_t channels, const void* x, int64_t x_stride, const void* residual,
+                           int32_t res_type, const float* weight, float eps, int32_t quant, void* y, float* scale,
+                           void* residual_out, float* rstd, void* stream) {
+    NormParams p;
+    memset(&p, 0, sizeof(p));
+    if (gdr_status st = check_norm(rows, channels, res_type)) return st;
+    if (quant != GDR_QUANT_NONE && quant != GDR_QUANT_ROW && quant != GDR_QUANT_BLOCK)
+        return fail(GDR_ERR_INVALID, "unknown output form%s");
+    if (!(eps >= 0.f)) return fail(GDR_ERR_INVALID, "eps must be >= 0%s");
+    if (gdr_status st = row_stride(x_stride, channels, &p.ldx)) return st;
+    if (rows == 0) return ok();
+    NEED_ROWS(x, 0); NEED(weight); NEED(y); NEED(rstd); OPT(residual);
+    if (residual) NEED(residual_out);
+    if (quant != GDR_QUANT_NONE) NEED(scale);
+    p.R = rows; p.C = channels; p.res_f32 = residual && res_type == GDR_TYPE_F32; p.quant = quant; p.eps = eps;
+    p.x = (const __nv_bfloat16*)x; p.residual = residual; p.weight = weight; p.y = y; p.scale = scale;
+    p.res_out = residual ? residual_out : nullptr; p.rstd = rstd;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = timed(GDR_KERNEL_NORM, s, [&] { return launch_rmsnorm_fwd(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rms norm launch");
+}
+
+size_t gdr_rmsnorm_workspace_bytes(int64_t rows, int32_t channels) {
+    if (check_norm(rows, channels, GDR_TYPE_BF16) != GDR_OK) return 0;
+    return 256;
+}
+
+gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const void* s_in, int32_t res_type,
+                           const float* weight, const float* rstd, const void* dres, void* workspace,
+                           size_t workspace_bytes, void* dx, float* dweight, void* stream) {
+    NormParams p;
+    memset(&p, 0, sizeof(p));
+    if (gdr_status st = check_norm(rows, channels, res_type)) return st;
+    if (rows) {
+        NEED(dy); NEED(s_in); NEED(weight); NEED(rstd); NEED(dx);
+    }
+    NEED(dweight); OPT(dres); NEED(workspace);
+    if (workspace_bytes < gdr_rmsnorm_workspace_bytes(rows, channels))
+        return fail(GDR_ERR_WORKSPACE, "workspace smaller than gdr_rmsnorm_workspace_bytes%s");
+    p.R = rows; p.C = channels; p.ldx = channels; p.res_f32 = res_type == GDR_TYPE_F32;
+    p.dy = (const __nv_bfloat16*)dy; p.s = s_in; p.weight = weight; p.rstd_in = rstd; p.dres = dres; p.dx = dx;
+    p.dweight = dweight;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = timed(GDR_KERNEL_NORM, s, [&] { return launch_rmsnorm_bwd(p, s); }, 2);
+    return e == cudaSuccess ? ok() : cuda_fail(e, "rms norm backward launch");
+}
+
+gdr_status gdr_conv1d_fwd(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t width,
+                          const int64_t* cu_seqlens, const void* x, int64_t x_stride, const float* weight,
+                          const float* bias, const void* state, int32_t silu, void* y, void* state_out,
+                          void* stream) {
+    ConvFwdParams p;
+    memset(&p, 0, sizeof(p));
+    if (gdr_status st = check_channels(channels)) return st;
+    if (width < 1 || width > 4) return fail(GDR_ERR_UNSUPPORTED, "width must be 1 to 4%s");
+    if (gdr_status st = check_tokens(num_seqs, total_tokens, cu_seqlens, channels)) return st;
+    if (gdr_status st = row_stride(x_stride, channels, &p.ldx)) return st;
+    if (total_tokens) { NEED_ROWS(x, 0); NEED(y); }
+    NEED(weight); OPT(bias); OPT(state); OPT(state_out);
+    if (state && state == state_out) return fail(GDR_ERR_INVALID, "state_out must not be the initial state's buffer%s");
+    p.N = num_seqs; p.T = total_tokens; p.seq_len = cu_seqlens ? 0 : total_tokens / num_seqs;
+    p.C = channels; p.K = width; p.silu = silu != 0; p.cu_seqlens = cu_seqlens;
+    p.x = (const __nv_bfloat16*)x; p.w = weight; p.bias = bias; p.state = (const __nv_bfloat16*)state;
+    p.state_out = (__nv_bfloat16*)state_out; p.y = (__nv_bfloat16*)y;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = timed(GDR_KERNEL_CONV, s, [&] { return launch_conv1d_fwd(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "conv1d launch");
+}
+
+gdr_status gdr_conv1d_step(int32_t rows, int32_t channels, int32_t width, int32_t pool, const void* x,
+                           int64_t x_stride, void* state, const float* weight, const float* bias,
+                           const int64_t* slots, int32_t silu, void* y, void* stream) {
+    ConvFwdParams p;
+    memset(&p, 0, sizeof(p));
+    if (gdr_status st = check_channels(channels)) return st;
+    if (width < 1 || width > 4) return fail(GDR_ERR_UNSUPPORTED, "width must be 1 to 4%s");
+    if (rows < 0 || pool < 0) return fail(GDR_ERR_INVALID, "rows and pool must be >= 0%s");
+    if (!slots && pool < rows) return fail(GDR_ERR_INVALID, "the pool holds fewer states than there are rows%s");
+    if (gdr_status st = row_stride(x_stride, channels, &p.ldx)) return st;
+    if (rows == 0) return ok();
+    NEED_ROWS(x, 0); NEED(weight); NEED(y); OPT(bias);
+    if (pool && width > 1) NEED(state);
+    if (slots && !aligned_to(slots, 8)) return fail(GDR_ERR_INVALID, "pointer %s is not 8-byte aligned", "slots");
+    p.N = rows; p.C = channels; p.K = width; p.pool = pool; p.silu = silu != 0; p.slots = slots;
+    p.x = (const __nv_bfloat16*)x; p.w = weight; p.bias = bias; p.state_out = (__nv_bfloat16*)state;
+    p.y = (__nv_bfloat16*)y;
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = timed(GDR_KERNEL_CONV, s, [&] { return launch_conv1d_step(p, s); });
+    return e == cudaSuccess ? ok() : cuda_fail(e, "conv1d step launch");
+}
+
+}  // extern "C"

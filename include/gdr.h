@@ -229,6 +229,113 @@ gdr_status gdr_conv1d_bwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
                           const int64_t* cu_seqlens, const void* x, const float* weight,
                           const float* bias, const void* dy, int32_t silu, void* dx,
                           float* dweight, float* dbias, void* stream);
+/* ---------------------------------------------------------------------------
+ * The operators around the delta rule in a recurrent block: the causal conv1d's forward and
+ * single-token step, a gated linear recurrence (channel-wise state) with its backward and
+ * step, and the RMS norm with the residual's addition and its backward.  The conventions
+ * above hold (device pointers, asynchronous on `stream`, nothing allocated, argument errors
+ * before anything is enqueued), and:
+ *  * channels C is even.
+ *  * x and g may be rows of a wider tensor (a column slice of a projection's output): the
+ *    row stride is given in elements (0 = C), even, and the pointer aligned to two elements;
+ *    every other tensor is contiguous and 16-byte aligned.
+ *  * Every result is the same, bit for bit, from one call to the next.
+ *  * Single-token steps work on a pool of states: row n of the batch has state slots[n]
+ *    (int64; slots NULL: state n).  A row whose slot is negative (padding) or not below
+ *    `pool` touches no state and its y is zero.  Two rows must not share a slot.
+ * --------------------------------------------------------------------------- */
+#define GDR_TYPE_BF16 0
+#define GDR_TYPE_F32 1
+
+/* Causal depthwise conv1d (optionally followed by SiLU): z and y as for gdr_conv1d_bwd.
+ *  * x, y: bf16 [T_total, C]; weight fp32 [C, K], 1 <= K <= 4; bias fp32 [C] or NULL (zero).
+ *  * state: bf16 [N, K - 1, C], the K - 1 inputs before each sequence's first token, oldest
+ *    first, or NULL (zero, as gdr_conv1d_bwd takes it).
+ *  * state_out: bf16 [N, K - 1, C], the last K - 1 inputs of each sequence (and of its state,
+ *    where the sequence is shorter), or NULL; not the buffer of `state`.
+ *  * Inconsistent cu_seqlens give meaningless results but no access outside the tensors. */
+gdr_status gdr_conv1d_fwd(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t width,
+                          const int64_t* cu_seqlens, const void* x, int64_t x_stride, const float* weight,
+                          const float* bias, const void* state, int32_t silu, void* y, void* state_out,
+                          void* stream);
+/* One token of `rows` sequences: x, y bf16 [rows, C]; state bf16 [pool, K - 1, C], shifted by
+ * the token in place. */
+gdr_status gdr_conv1d_step(int32_t rows, int32_t channels, int32_t width, int32_t pool, const void* x,
+                           int64_t x_stride, void* state, const float* weight, const float* bias,
+                           const int64_t* slots, int32_t silu, void* y, void* stream);
+
+/* Gated linear recurrence, per channel, the state in fp32:
+ *     h_t = a_t h_{t-1} + s_t x_t,   a_t = exp(g_t),   s_t = 1, or 1 - a_t with `complement`
+ * from h0 (or zero) at each sequence's first token.  The log gate g is given (GLR_GATE_LOG)
+ * or, as the KDA gate's softplus form with per-channel parameters (GLR_GATE_SOFTPLUS),
+ *     g = -exp(A_log[c]) softplus(g_raw + dt_bias[c]).
+ *  * x, h, dh, dx: [T_total, C] of act_type; g (or g_raw), dg: [T_total, C] of gate_type;
+ *    types: bf16 / bf16, bf16 / float32 and float32 / float32 (activations / gate).
+ *  * A_log, dt_bias, dA_log, ddt_bias: float [C] (softplus gate only; else ignored).
+ *  * h0, ht, dht, dh0: float [N, C]; h0, ht and dht may be NULL.  An empty sequence passes its
+ *    state through (ht = h0, dh0 = dht).  T_total = 0 is a valid call.
+ *  * Inconsistent cu_seqlens raise GDR_DEV_BAD_SEQLENS in the workspace's status word; the
+ *    results are then meaningless, but no access leaves the tensors. */
+#define GLR_GATE_LOG 0
+#define GLR_GATE_SOFTPLUS 1
+typedef struct {
+    int32_t num_seqs;          /* N >= 1 */
+    int64_t total_tokens;      /* T_total >= 0 */
+    int32_t channels;          /* C, even */
+    const int64_t* cu_seqlens; /* device int64 [N + 1], or NULL for dense */
+    int32_t gate;              /* GLR_GATE_* */
+    int32_t complement;        /* x scaled by 1 - a */
+    int32_t act_type;          /* GDR_TYPE_* of x, h, dh, dx */
+    int32_t gate_type;         /* GDR_TYPE_* of g, dg */
+    int64_t x_stride, g_stride; /* row strides of x and g in elements, 0 = C */
+} glr_shape;
+
+/* Bytes of the workspace of glr_fwd and glr_bwd (0 for an invalid shape). */
+size_t glr_workspace_bytes(const glr_shape* shape);
+gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const float* A_log,
+                   const float* dt_bias, const float* h0, void* h, float* ht, void* workspace,
+                   size_t workspace_bytes, void* stream);
+/* The gradients of sum <dh_t, h_t> + sum <dht, ht>; h is the forward's output.  x is read only
+ * with `complement` (NULL otherwise allowed).  dg is with respect to g (or g_raw); dA_log and
+ * ddt_bias are overwritten. */
+gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const float* A_log,
+                   const float* dt_bias, const void* h, const float* h0, const void* dh,
+                   const float* dht, void* workspace, size_t workspace_bytes, void* dx, void* dg,
+                   float* dh0, float* dA_log, float* ddt_bias, void* stream);
+/* One token of `rows` sequences: state float [pool, C], updated in place; y (act_type) [rows, C]
+ * is the new state rounded. */
+gdr_status glr_step(int32_t rows, int32_t channels, int32_t pool, int32_t gate, int32_t complement,
+                    int32_t act_type, int32_t gate_type, const void* x, int64_t x_stride,
+                    const void* g, int64_t g_stride, const float* A_log, const float* dt_bias,
+                    const int64_t* slots, float* state, void* y, void* stream);
+
+/* RMS norm with the residual's addition, per row:
+ *     s = x + residual (rounded to the residual's type; s = x without a residual)
+ *     rstd = 1 / sqrt(mean s^2 + eps),   y = s rstd weight
+ *  * x: bf16 [rows, C]; residual, residual_out (= s): [rows, C] of res_type, residual may be
+ *    NULL (then residual_out is not written) and residual_out may be its buffer;
+ *    weight fp32 [C]; rstd fp32 [rows].
+ *  * quant: GDR_QUANT_NONE: y bf16.  GDR_QUANT_ROW / GDR_QUANT_BLOCK: y in 8 bits (e4m3) and
+ *    scale fp32 [rows, 1] / [rows, ceil(C / 128)]: scale = max |y| / 448 over the row / over
+ *    each 128 channels (1 where they are all zero), y stored as e4m3(y / scale). */
+#define GDR_QUANT_NONE 0
+#define GDR_QUANT_ROW 1
+#define GDR_QUANT_BLOCK 2
+gdr_status gdr_rmsnorm_fwd(int64_t rows, int32_t channels, const void* x, int64_t x_stride,
+                           const void* residual, int32_t res_type, const float* weight, float eps,
+                           int32_t quant, void* y, float* scale, void* residual_out, float* rstd,
+                           void* stream);
+/* Its backward from dy (bf16 [rows, C], the gradient of y before any rounding to 8 bits), the
+ * stored sum s (res_type; the forward's x without a residual) and rstd:
+ *     dx = rstd (u - n mean(u n)) + dres,  n = s rstd,  u = weight dy;   dweight = sum_rows dy n
+ * dres (res_type, or NULL) is the gradient that reaches s directly; dx (res_type) is the
+ * gradient of s, hence of both x and the residual. */
+size_t gdr_rmsnorm_workspace_bytes(int64_t rows, int32_t channels);
+gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const void* s,
+                           int32_t res_type, const float* weight, const float* rstd,
+                           const void* dres, void* workspace, size_t workspace_bytes, void* dx,
+                           float* dweight, void* stream);
+
 /* Waits for `stream`, then returns in *device_status the OR of the GDR_DEV_*
  * bits raised by the last call that used `workspace` (0 = none). */
 gdr_status gdr_workspace_status(const void* workspace, void* stream, int* device_status);
@@ -258,8 +365,10 @@ const char* gdr_last_error(void);
 #define GDR_KERNEL_STATES 2      /* serial state / state-gradient recurrences */
 #define GDR_KERNEL_MAIN 3        /* chunk-parallel main backward */
 #define GDR_KERNEL_OUT 4         /* chunk-parallel forward output (gdr_fwd / kda_fwd) */
-#define GDR_KERNEL_CONV 5        /* causal conv1d backward (gdr_conv1d_bwd) */
-#define GDR_KERNEL_COUNT 6
+#define GDR_KERNEL_CONV 5        /* causal conv1d (gdr_conv1d_bwd, _fwd, _step) */
+#define GDR_KERNEL_GLR 6         /* gated linear recurrence (glr_fwd, glr_bwd, glr_step) */
+#define GDR_KERNEL_NORM 7        /* RMS norm (gdr_rmsnorm_fwd, gdr_rmsnorm_bwd) */
+#define GDR_KERNEL_COUNT 8
 gdr_status gdr_profile_begin(int max_launches);
 gdr_status gdr_profile_end(double* total_ms, int* launches);
 
