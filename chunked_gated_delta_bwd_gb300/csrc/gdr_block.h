@@ -13,11 +13,13 @@ struct GlrParams {
     int N, C;                   // sequences, channels (even)
     int64_t T;                  // tokens
     int64_t seq_len;            // dense layout: tokens per sequence (T / N)
+    double inv_len;             // 1 / seq_len
     const int64_t* cu_seqlens;  // device [N+1] or nullptr (dense)
     int64_t ldx, ldg;           // row strides of x and g in elements
     int gate, complement;       // gate function (gdr.h), x scaled by 1 - a
     int act_f32, gate_f32;      // element types: float32 instead of bf16
-    int* status;                // workspace status word
+    int* status;                // workspace: status word, ticket counter, published runs
+    float4* sums;               // workspace: per-chunk sums of the softplus gate's parameters
     const void *x, *g;          // [T][C]
     const float *A_log, *dt_bias;  // [C] (softplus gate)
     const float *h0, *dht;      // [N][C] or nullptr
@@ -26,6 +28,10 @@ struct GlrParams {
     float *ht, *dh0;            // [N][C]; ht may be nullptr
     float *dA_log, *ddt_bias;   // [C] (softplus gate)
 };
+// workspace: the status word and a ticket counter, then what the kernels publish (zero before a
+// launch), then the backward's per-chunk sums
+size_t glr_published_bytes(const GlrParams& p);
+size_t glr_sums_bytes(const GlrParams& p);
 cudaError_t launch_glr_fwd(const GlrParams& p, cudaStream_t s);
 cudaError_t launch_glr_bwd(const GlrParams& p, cudaStream_t s);
 

@@ -58,12 +58,13 @@ static gdr_status check_glr(const glr_shape* sh, GlrParams* p) {
     int64_t ldx = 0, ldg = 0;
     if (st == GDR_OK) st = row_stride(sh->x_stride, sh->channels, &ldx);
     if (st == GDR_OK) st = row_stride(sh->g_stride, sh->channels, &ldg);
-    if (st != GDR_OK || !p) return st;
+    if (st != GDR_OK) return st;
     memset(p, 0, sizeof(*p));
     p->N = sh->num_seqs;
     p->C = sh->channels;
     p->T = sh->total_tokens;
     p->seq_len = sh->cu_seqlens ? 0 : sh->total_tokens / sh->num_seqs;
+    p->inv_len = p->seq_len > 0 ? 1.0 / (double)p->seq_len : 0.0;
     p->cu_seqlens = sh->cu_seqlens;
     p->ldx = ldx;
     p->ldg = ldg;
@@ -74,14 +75,19 @@ static gdr_status check_glr(const glr_shape* sh, GlrParams* p) {
     return GDR_OK;
 }
 
-static size_t glr_workspace(const glr_shape*) { return 256; }  // the status word
+static size_t glr_workspace(const GlrParams& p) { return 256 + glr_published_bytes(p) + glr_sums_bytes(p); }
 
-// the status word cleared; every sequence empty: the states pass through
-static gdr_status glr_front(const GlrParams& p, void* ws, size_t ws_bytes, size_t need, float* to, const float* from,
-                            cudaStream_t s, bool* done) {
-    if (ws_bytes < need) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
-    cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int), s);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(status)");
+// Checks and clears the workspace (a launch of one chunk writes its status word itself); every
+// sequence empty: the states pass through.
+static gdr_status glr_front(GlrParams& p, void* ws, size_t ws_bytes, float* to, const float* from, cudaStream_t s,
+                            bool* done) {
+    if (ws_bytes < glr_workspace(p)) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
+    const size_t published = glr_published_bytes(p);
+    cudaError_t e = cudaSuccess;
+    if (published || p.T == 0) e = cudaMemsetAsync(ws, 0, 256 + published, s);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync(workspace)");
+    p.status = static_cast<int*>(ws);
+    p.sums = reinterpret_cast<float4*>(static_cast<unsigned char*>(ws) + 256 + published);
     *done = p.T == 0;
     if (p.T || !to) return GDR_OK;
     const size_t bytes = sizeof(float) * (size_t)p.N * p.C;
@@ -96,8 +102,9 @@ using namespace gdr;
 extern "C" {
 
 size_t glr_workspace_bytes(const glr_shape* shape) {
-    if (check_glr(shape, nullptr) != GDR_OK) return 0;
-    return glr_workspace(shape);
+    GlrParams p;
+    if (check_glr(shape, &p) != GDR_OK) return 0;
+    return glr_workspace(p);
 }
 
 gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const float* A_log, const float* dt_bias,
@@ -111,9 +118,8 @@ gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const f
     OPT(h0); OPT(ht); NEED(workspace);
     cudaStream_t s = (cudaStream_t)stream;
     bool done = false;
-    if (gdr_status st = glr_front(p, workspace, workspace_bytes, glr_workspace(shape), ht, h0, s, &done)) return st;
+    if (gdr_status st = glr_front(p, workspace, workspace_bytes, ht, h0, s, &done)) return st;
     if (done) return ok();
-    p.status = static_cast<int*>(workspace);
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0; p.h = h; p.ht = ht;
     cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_fwd(p, s); });
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence launch");
@@ -135,17 +141,16 @@ gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const f
     if (soft) { NEED(dA_log); NEED(ddt_bias); }
     cudaStream_t s = (cudaStream_t)stream;
     bool done = false;
-    if (gdr_status st = glr_front(p, workspace, workspace_bytes, glr_workspace(shape), dh0, dht, s, &done)) return st;
+    if (gdr_status st = glr_front(p, workspace, workspace_bytes, dh0, dht, s, &done)) return st;
     if (done) {
         if (!soft) return ok();
         cudaError_t e = cudaMemsetAsync(dA_log, 0, sizeof(float) * p.C, s);
         if (e == cudaSuccess) e = cudaMemsetAsync(ddt_bias, 0, sizeof(float) * p.C, s);
         return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync(dA_log/ddt_bias)");
     }
-    p.status = static_cast<int*>(workspace);
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h_in = h; p.h0 = h0; p.dh = dh; p.dht = dht;
     p.dx = dx; p.dg = dg; p.dh0 = dh0; p.dA_log = dA_log; p.ddt_bias = ddt_bias;
-    cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_bwd(p, s); });
+    cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_bwd(p, s); }, soft ? 2 : 1);
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence backward launch");
 }
 

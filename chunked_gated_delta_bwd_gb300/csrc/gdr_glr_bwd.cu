@@ -6,69 +6,162 @@
 //   softplus gate, z = g_raw + dt_bias: dg_raw = dg (-e^{A_log} sigmoid z),
 //   ddt_bias = sum_t dg_raw,  dA_log = sum_t dg g
 //
-// The simplest form: a thread owns two channels and walks every sequence backwards, so the
-// sums over tokens have a fixed order.
+// The scan (gdr_glr.cuh) runs against time on y_t = a_t l_t = a_t (dh_t + y_{t+1}), restarted from
+// dht at each sequence's last token; what it leaves at the first token is dh0.
 #include "gdr_glr.cuh"
 #include "gdr_internal.h"
 
 namespace gdr {
 
+// Bytes bound it: g, h, dh (and x with the complement) are read once, dx and dg written once (10
+// or 12 bytes a token and channel in bf16).  g and dh are loaded first, for the run that is
+// published; h and x only then, so that they arrive while the block waits for the state.
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(64) k_glr_bwd(const GlrParams p) {
+__global__ void __launch_bounds__(GLR_THREADS, sizeof(TG) == 4 && sizeof(TX) == 2 ? 2 : 3) k_glr_bwd(const GlrParams p) {
+    constexpr int SUB = glr_sub(sizeof(TX) == 4), CHUNK = SUB * GLR_WARPS;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
-    if (blockIdx.x == 0) glr_check_seqlens(p.cu_seqlens, p.N, p.T, threadIdx.x, 64, p.status);
-    const int c = (blockIdx.x * 64 + threadIdx.x) * 2;
-    if (c >= p.C) return;
-    GlrGate<GATE> gt[2];
-    gt[0].load(p.A_log, p.dt_bias, c);
-    gt[1].load(p.A_log, p.dt_bias, c + 1);
-    const TX* x = static_cast<const TX*>(p.x) + c;
-    const TG* g = static_cast<const TG*>(p.g) + c;
-    const TX* h = static_cast<const TX*>(p.h_in) + c;
-    const TX* dh = static_cast<const TX*>(p.dh) + c;
-    TX* dx = static_cast<TX*>(p.dx) + c;
-    TG* dg = static_cast<TG*>(p.dg) + c;
-    float sumA[2] = {0.f, 0.f}, sumB[2] = {0.f, 0.f};
-    for (int n = 0; n < p.N; ++n) {
-        int64_t b, e;
-        glr_bounds(p.cu_seqlens, p.seq_len, p.T, n, b, e);
-        const int64_t row = (int64_t)n * p.C + c;
-        float2 carry = make_float2(0.f, 0.f), h0 = make_float2(0.f, 0.f);  // carry: a_{t+1} l_{t+1}
-        if (p.dht) carry = *reinterpret_cast<const float2*>(p.dht + row);
-        if (p.h0) h0 = *reinterpret_cast<const float2*>(p.h0 + row);
-        for (int64_t t = e - 1; t >= b; --t) {
-            const float2 gv = PG::widen(*reinterpret_cast<const typename PG::raw*>(g + t * p.ldg));
-            const float2 dv = PX::widen(*reinterpret_cast<const typename PX::raw*>(dh + t * p.C));
-            const float2 hv = t > b ? PX::widen(*reinterpret_cast<const typename PX::raw*>(h + (t - 1) * p.C)) : h0;
-            float2 xv = make_float2(0.f, 0.f);
-            if (COMP) xv = PX::widen(*reinterpret_cast<const typename PX::raw*>(x + t * p.ldx));
-            float2 odx, odg;
+    using RX = typename PX::raw;
+    using RG = typename PG::raw;
+    __shared__ GlrShared sm;
+    const int chunks = glr_chunks(p.T, sizeof(TX) == 4);
+    const int tiles = (p.C + GLR_TILE - 1) / GLR_TILE;
+    const unsigned id = glr_ticket(p, sm, chunks);
+    const int k = id / (unsigned)tiles, kc = chunks - 1 - k;  // the chunk's number against and in the order of time
+    const int tile = id - k * tiles, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int c = tile * GLR_TILE + 2 * lane, i0 = w * SUB, ld = p.C / 2;
+    const bool live = c < p.C;
+    const int64_t t0 = (int64_t)kc * CHUNK, t = t0 + i0;  // the chunk's first token, this warp's
+    const int len = (int)min((int64_t)CHUNK, p.T - t0);
+    const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));  // tokens of this warp
+    const int n = live ? nt : 0;
+    RG gr[SUB];
+    RX dr[SUB], hr[SUB], xr[SUB];
+    {
+        const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
+        const RX* dh = reinterpret_cast<const RX*>(static_cast<const TX*>(p.dh) + t * p.C + c);
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                float slope, a, s;
-                const float lg = gt[j].log_gate_slope(j ? gv.y : gv.x, slope);
-                decay(lg, a, s);
-                float& cr = j ? carry.y : carry.x;
-                const float l = (j ? dv.y : dv.x) + cr;
-                cr = a * l;
-                const float d = cr * ((j ? hv.y : hv.x) - (j ? xv.y : xv.x));
-                (j ? odx.y : odx.x) = COMP ? s * l : l;
-                if (GATE == GLR_SOFTPLUS) {
-                    sumA[j] = fmaf(d, lg, sumA[j]);
-                    sumB[j] = fmaf(d, slope, sumB[j]);
-                }
-                (j ? odg.y : odg.x) = d * slope;
-            }
-            *reinterpret_cast<typename PX::raw*>(dx + t * p.C) = PX::narrow(odx);
-            *reinterpret_cast<typename PG::raw*>(dg + t * p.C) = PG::narrow(odg);
+        for (int i = 0; i < SUB; ++i) {
+            gr[i] = i < n ? __ldcs(g + i * (p.ldg / 2)) : PG::zero();
+            dr[i] = i < n ? __ldcs(dh + i * ld) : PX::zero();
         }
-        *reinterpret_cast<float2*>(p.dh0 + row) = carry;
     }
-    if (GATE == GLR_SOFTPLUS) {
-        *reinterpret_cast<float2*>(p.dA_log + c) = make_float2(sumA[0], sumA[1]);
-        *reinterpret_cast<float2*>(p.ddt_bias + c) = make_float2(sumB[0], sumB[1]);
+    GlrGate<GATE> gate;
+    if (live) gate.load(p.A_log, p.dt_bias, c);
+    if (w == 0) glr_find_sequences(p, sm, t0, len, lane);
+    if (w == GLR_WARPS - 1) glr_empty_sequences(p, p.dht, p.dh0, kc, chunks, c, live, tile == 0);
+    __syncthreads();
+    const uint32_t bits = glr_start_bits(sm, i0, nt);  // of this warp's tokens and the one after
+    const uint32_t starts = bits & ((1u << nt) - 1u), ends = bits >> 1;
+
+    auto state_of = [&](const float* from, int i) {
+        return from && live ? *reinterpret_cast<const float2*>(from + (int64_t)glr_seq_at(sm, i) * p.C + c) : splat(0.f);
+    };
+    // this warp's run
+    Run r = run_identity();
+#pragma unroll
+    for (int i = SUB - 1; i >= 0; --i) {
+        float2 a, s;
+        decay(gate.log_gate(PG::widen(gr[i])), a, s);
+        if (ends >> i & 1) {
+            r.A = splat(-0.f);
+            r.H = state_of(p.dht, i0 + i);
+        } else {
+            r.A = __fmul2_rn(r.A, a);
+        }
+        r.H = __fmul2_rn(a, __fadd2_rn(r.H, PX::widen(dr[i])));
     }
+    const int pos = GLR_WARPS - 1 - w;
+    sm.sub[pos][lane] = run_bits(r);
+    {
+        const RX* h = reinterpret_cast<const RX*>(static_cast<const TX*>(p.h_in) + (t - 1) * p.C + c);  // the state before
+        const RX* x = COMP ? reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c) : nullptr;
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            hr[i] = i < n && !(starts >> i & 1) && t + i > 0 ? __ldcs(h + i * ld) : PX::zero();
+            xr[i] = COMP && i < n ? __ldcs(x + i * (p.ldx / 2)) : PX::zero();
+        }
+    }
+    __syncthreads();
+    float2 y = glr_carry(p, sm, chunks, k, chunks - 1 - (int)((uint64_t)(sm.end1 - 1) / CHUNK), sm.starts[len >> 5] >> (len & 31) & 1, pos,
+                         lane, c / 2, live);
+
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) forget(gr[i]);
+    RX* dx = reinterpret_cast<RX*>(static_cast<TX*>(p.dx) + t * p.C + c);
+    RG* dg = reinterpret_cast<RG*>(static_cast<TG*>(p.dg) + t * p.C + c);
+    float2 sumA = splat(0.f), sumB = splat(0.f);
+#pragma unroll
+    for (int i = SUB - 1; i >= 0; --i) {
+        float2 slope, a, s;
+        const float2 lg = gate.log_gate_slope(PG::widen(gr[i]), slope);
+        decay(lg, a, s);
+        if (ends >> i & 1) y = state_of(p.dht, i0 + i);
+        const float2 l = __fadd2_rn(y, PX::widen(dr[i]));
+        y = __fmul2_rn(a, l);
+        float2 before = PX::widen(hr[i]);
+        if (starts >> i & 1) before = state_of(p.h0, i0 + i);
+        if (COMP) {
+            const float2 xv = PX::widen(xr[i]);
+            before = __fadd2_rn(before, make_float2(-xv.x, -xv.y));
+        }
+        float2 d = __fmul2_rn(y, before);
+        if (i < n) {
+            if (GATE == GLR_SOFTPLUS) sumA = __ffma2_rn(d, lg, sumA);
+            d = GATE == GLR_SOFTPLUS ? __fmul2_rn(d, slope) : d;
+            if (GATE == GLR_SOFTPLUS) sumB = __fadd2_rn(sumB, d);
+            dx[i * ld] = PX::narrow(COMP ? __fmul2_rn(s, l) : l);
+            dg[i * ld] = PG::narrow(d);
+            if (starts >> i & 1) *reinterpret_cast<float2*>(p.dh0 + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = y;
+        }
+    }
+    if (GATE == GLR_SOFTPLUS) {  // the chunk's sums, the warps' in a fixed order
+        __shared__ float4 sums[GLR_WARPS][32];
+        sums[w][lane] = make_float4(sumA.x, sumA.y, sumB.x, sumB.y);
+        __syncthreads();
+        if (w == 0 && live) {
+            float4 v = sums[0][lane];
+            for (int q = 1; q < GLR_WARPS; ++q) {
+                const float4 u = sums[q][lane];
+                v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+            }
+            p.sums[(int64_t)kc * ld + c / 2] = v;
+        }
+    }
+}
+
+// dA_log and ddt_bias: the chunks' sums, added in a fixed order.  A block takes 32 pairs of
+// channels, each of its 32 warps every 32nd chunk.
+__global__ void __launch_bounds__(1024) k_glr_sums(const float4* sums, int chunks, int C, float* dA_log, float* ddt_bias) {
+    __shared__ float4 part[32][33];
+    const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c2 = blockIdx.x * 32 + lane;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c2 < C / 2) {
+#pragma unroll 4
+        for (int k = w; k < chunks; k += 32) {
+            const float4 u = sums[(int64_t)k * (C / 2) + c2];
+            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
+        }
+    }
+    part[w][lane] = v;
+    __syncthreads();
+    v = part[lane][w];  // the pair w of the block, the warps' sums across the lanes
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        v.x += __shfl_xor_sync(~0u, v.x, o);
+        v.y += __shfl_xor_sync(~0u, v.y, o);
+        v.z += __shfl_xor_sync(~0u, v.z, o);
+        v.w += __shfl_xor_sync(~0u, v.w, o);
+    }
+    const int c = (blockIdx.x * 32 + w) * 2;
+    if (lane == 0 && c < C) {
+        *reinterpret_cast<float2*>(dA_log + c) = make_float2(v.x, v.y);
+        *reinterpret_cast<float2*>(ddt_bias + c) = make_float2(v.z, v.w);
+    }
+}
+
+size_t glr_sums_bytes(const GlrParams& p) {
+    return p.gate == GLR_SOFTPLUS ? sizeof(float4) * (size_t)(p.C / 2) * glr_chunks(p.T, p.act_f32) : 0;
 }
 
 namespace {
@@ -77,7 +170,10 @@ struct Launch {
     cudaStream_t s;
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
-        k_glr_bwd<TX, TG, GATE, COMP><<<(p.C / 2 + 63) / 64, 64, 0, s>>>(p);
+        const int chunks = glr_chunks(p.T, sizeof(TX) == 4);
+        k_glr_bwd<TX, TG, GATE, COMP><<<(unsigned)(chunks * ((p.C + GLR_TILE - 1) / GLR_TILE)), GLR_THREADS, 0, s>>>(p);
+        if (GATE == GLR_SOFTPLUS)
+            k_glr_sums<<<(p.C / 2 + 31) / 32, 1024, 0, s>>>(p.sums, chunks, p.C, p.dA_log, p.ddt_bias);
         return cudaGetLastError();
     }
 };

@@ -1,42 +1,124 @@
 // Gated linear recurrence, forward and single-token step: h_t = a_t h_{t-1} + s_t x_t per
-// channel, the state kept in fp32.
-//
-// The simplest form: a thread owns two channels and walks every sequence from its first to its
-// last token.
+// channel, the state kept in fp32 (the scan's scheme is in gdr_glr.cuh).
 #include "gdr_glr.cuh"
 #include "gdr_internal.h"
 
 namespace gdr {
 
+size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p.T, p.act_f32), p.C); }
+
+// Bytes bound it: x and g are read once and h is written once (6 bytes a token and channel in
+// bf16).  A thread keeps its tokens of x and g in registers as loaded and evaluates the gate
+// twice, before and after the state in front of the chunk is known.
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(64) k_glr_fwd(const GlrParams p) {
+__global__ void __launch_bounds__(GLR_THREADS, sizeof(TX) == 2 && sizeof(TG) == 4 ? 3 : 4) k_glr_fwd(const GlrParams p) {
+    constexpr int SUB = glr_sub(sizeof(TX) == 4), CHUNK = SUB * GLR_WARPS;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
-    if (blockIdx.x == 0) glr_check_seqlens(p.cu_seqlens, p.N, p.T, threadIdx.x, 64, p.status);
-    const int c = (blockIdx.x * 64 + threadIdx.x) * 2;
-    if (c >= p.C) return;
-    GlrGate<GATE> g0, g1;
-    g0.load(p.A_log, p.dt_bias, c);
-    g1.load(p.A_log, p.dt_bias, c + 1);
-    const TX* x = static_cast<const TX*>(p.x) + c;
-    const TG* g = static_cast<const TG*>(p.g) + c;
-    TX* h = static_cast<TX*>(p.h) + c;
-    for (int n = 0; n < p.N; ++n) {
-        int64_t b, e;
-        glr_bounds(p.cu_seqlens, p.seq_len, p.T, n, b, e);
-        float2 st = make_float2(0.f, 0.f);
-        if (p.h0) st = *reinterpret_cast<const float2*>(p.h0 + (int64_t)n * p.C + c);
-        for (int64_t t = b; t < e; ++t) {
-            const float2 xv = PX::widen(*reinterpret_cast<const typename PX::raw*>(x + t * p.ldx));
-            const float2 gv = PG::widen(*reinterpret_cast<const typename PG::raw*>(g + t * p.ldg));
-            float2 a, s;
-            decay(g0.log_gate(gv.x), a.x, s.x);
-            decay(g1.log_gate(gv.y), a.y, s.y);
-            st.x = fmaf(a.x, st.x, COMP ? s.x * xv.x : xv.x);
-            st.y = fmaf(a.y, st.y, COMP ? s.y * xv.y : xv.y);
-            *reinterpret_cast<typename PX::raw*>(h + t * p.C) = PX::narrow(st);
+    using RX = typename PX::raw;
+    using RG = typename PG::raw;
+    __shared__ GlrShared sm;
+    const int chunks = glr_chunks(p.T, sizeof(TX) == 4);
+    const int tiles = (p.C + GLR_TILE - 1) / GLR_TILE;
+    const unsigned id = glr_ticket(p, sm, chunks);
+    const int k = id / (unsigned)tiles;
+    const int tile = id - k * tiles, w = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int c = tile * GLR_TILE + 2 * lane, i0 = w * SUB;
+    const bool live = c < p.C;
+    const int64_t t0 = (int64_t)k * CHUNK, t = t0 + i0;  // the chunk's first token, this warp's
+    const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));  // tokens of this warp
+    const int n = live ? nt : 0;
+    RX xr[SUB];
+    RG gr[SUB];
+    {
+        const RX* x = reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c);
+        const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
+        if (n == SUB) {
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) {
+                gr[i] = __ldcs(g + i * (p.ldg / 2));
+                xr[i] = __ldcs(x + i * (p.ldx / 2));
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < SUB; ++i) {
+                gr[i] = i < n ? __ldcs(g + i * (p.ldg / 2)) : PG::zero();
+                xr[i] = i < n ? __ldcs(x + i * (p.ldx / 2)) : PX::zero();
+            }
         }
-        if (p.ht) *reinterpret_cast<float2*>(p.ht + (int64_t)n * p.C + c) = st;
+    }
+    GlrGate<GATE> gate;
+    if (live) gate.load(p.A_log, p.dt_bias, c);
+    if (w == 0) glr_find_sequences(p, sm, t0, (int)min((int64_t)CHUNK, p.T - t0), lane);
+    if (w == GLR_WARPS - 1) glr_empty_sequences(p, p.h0, p.ht, k, chunks, c, live, tile == 0);
+    __syncthreads();
+    const uint32_t bits = glr_start_bits(sm, i0, nt);  // of this warp's tokens and the one after
+    const uint32_t starts = bits & ((1u << nt) - 1u), ends = bits >> 1;
+
+    auto token = [&](int i, float2& a, float2& b) {
+        float2 s;
+        decay(gate.log_gate(PG::widen(gr[i])), a, s);
+        b = PX::widen(xr[i]);
+        if (COMP) b = __fmul2_rn(s, b);
+    };
+    auto first_state = [&](int i) {
+        return p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(sm, i) * p.C + c) : splat(0.f);
+    };
+    // this warp's run
+    Run r = run_identity();
+    if (starts == 0) {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            float2 a, b;
+            token(i, a, b);
+            r.A = __fmul2_rn(r.A, a);
+            r.H = __ffma2_rn(a, r.H, b);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            float2 a, b;
+            token(i, a, b);
+            if (starts >> i & 1) {
+                r.A = splat(-0.f);
+                r.H = first_state(i0 + i);
+            } else {
+                r.A = __fmul2_rn(r.A, a);
+            }
+            r.H = __ffma2_rn(a, r.H, b);
+        }
+    }
+    sm.sub[w][lane] = run_bits(r);
+    __syncthreads();
+    float2 y = glr_carry(p, sm, chunks, k, (int)((uint64_t)sm.begin0 / CHUNK), sm.starts[0] & 1, w, lane, c / 2, live);
+
+#pragma unroll
+    for (int i = 0; i < SUB; ++i) {
+        forget(gr[i]);
+        forget(xr[i]);
+    }
+    RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
+    if (bits == 0 && n == SUB) {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            float2 a, b;
+            token(i, a, b);
+            y = __ffma2_rn(a, y, b);
+            h[i * (p.C / 2)] = PX::narrow(y);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < SUB; ++i) {
+            float2 a, b;
+            token(i, a, b);
+            if (starts >> i & 1) y = first_state(i0 + i);
+            y = __ffma2_rn(a, y, b);
+            if (i < n) {
+                h[i * (p.C / 2)] = PX::narrow(y);
+                if (p.ht && (ends >> i & 1))
+                    *reinterpret_cast<float2*>(p.ht + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = y;
+            }
+        }
     }
 }
 
@@ -46,7 +128,8 @@ struct Launch {
     cudaStream_t s;
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
-        k_glr_fwd<TX, TG, GATE, COMP><<<(p.C / 2 + 63) / 64, 64, 0, s>>>(p);
+        const int chunks = glr_chunks(p.T, sizeof(TX) == 4);
+        k_glr_fwd<TX, TG, GATE, COMP><<<(unsigned)(chunks * ((p.C + GLR_TILE - 1) / GLR_TILE)), GLR_THREADS, 0, s>>>(p);
         return cudaGetLastError();
     }
 };
@@ -69,17 +152,14 @@ __global__ void __launch_bounds__(128) k_glr_step(const GlrStepParams p) {
         float2 st = make_float2(0.f, 0.f);
         if (slot >= 0 && slot < p.pool) {
             float2* home = reinterpret_cast<float2*>(p.state + slot * p.C + c);
-            GlrGate<GATE> g0, g1;
-            g0.load(p.A_log, p.dt_bias, c);
-            g1.load(p.A_log, p.dt_bias, c + 1);
+            GlrGate<GATE> gate;
+            gate.load(p.A_log, p.dt_bias, c);
             const float2 xv = PX::widen(*reinterpret_cast<const typename PX::raw*>(static_cast<const TX*>(p.x) + n * p.ldx + c));
             const float2 gv = PG::widen(*reinterpret_cast<const typename PG::raw*>(static_cast<const TG*>(p.g) + n * p.ldg + c));
             st = *home;
             float2 a, s;
-            decay(g0.log_gate(gv.x), a.x, s.x);
-            decay(g1.log_gate(gv.y), a.y, s.y);
-            st.x = fmaf(a.x, st.x, COMP ? s.x * xv.x : xv.x);
-            st.y = fmaf(a.y, st.y, COMP ? s.y * xv.y : xv.y);
+            decay(gate.log_gate(gv), a, s);
+            st = __ffma2_rn(a, st, COMP ? __fmul2_rn(s, xv) : xv);
             *home = st;
         }
         *reinterpret_cast<typename PX::raw*>(static_cast<TX*>(p.y) + n * p.C + c) = PX::narrow(st);
