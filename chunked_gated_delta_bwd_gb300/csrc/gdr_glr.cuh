@@ -28,32 +28,69 @@ template <> struct PairOf<float> {
     static __device__ __forceinline__ raw zero() { return make_float2(0.f, 0.f); }
 };
 
-// Makes the compiler forget what it derived from a loaded value, so that a later use derives it
-// again instead of keeping the result in a register.
+// Makes the compiler forget what it derived from a value, so that a later use derives it again
+// instead of keeping the result in a register.
 __device__ __forceinline__ void forget(uint32_t& v) { asm volatile("" : "+r"(v)); }
 __device__ __forceinline__ void forget(float2& v) { asm volatile("" : "+f"(v.x), "+f"(v.y)); }
 
-// a = e^g and, where asked for, s = 1 - e^g, for two channels.  A slow channel (|g| below 1/4)
-// keeps its state for hundreds of tokens, over which a relative error of a that has one sign
-// grows by the number of tokens; there both come from the Taylor series of e^g - 1 (six terms,
-// truncation |g|^7 / 7! < 1.3e-8 absolute and 5e-8 relative to g), so a is rounded once and s
-// does not cancel.  Elsewhere the memory is a few tokens and the hardware exponential's 2^-22
-// is enough.
-__device__ __forceinline__ void decay(float2 g, float2& a, float2& s) {
-    float2 m = __ffma2_rn(g, splat(1.f / 720.f), splat(1.f / 120.f));
-    m = __ffma2_rn(g, m, splat(1.f / 24.f));
-    m = __ffma2_rn(g, m, splat(1.f / 6.f));
-    m = __ffma2_rn(g, m, splat(0.5f));
-    m = __ffma2_rn(g, m, splat(1.f));
-    m = __fmul2_rn(g, m);
-    const float2 e = make_float2(__expf(g.x), __expf(g.y));
-    const bool sx = fabsf(g.x) < 0.25f, sy = fabsf(g.y) < 0.25f;
-    const float2 one = __fadd2_rn(m, splat(1.f));
-    a = make_float2(sx ? one.x : e.x, sy ? one.y : e.y);
-    s = make_float2(sx ? -m.x : 1.f - e.x, sy ? -m.y : 1.f - e.y);
+// The gate is evaluated in base 2: t = g / ln 2, a = 2^t.
+//
+// 2^t = 2^n (1 + m) with n the integer nearest t and m = 2^f - 1 = f q(f), |f| <= 1/2, q the
+// polynomial of degree 5 with the least relative error (1.1e-8; fitted by Lawson's reweighted
+// least squares).  A slow channel (t near 0) keeps its state for hundreds of tokens, over which
+// an error of a that has one sign grows with the number of tokens; n is 0 there, so a = 1 + m is
+// rounded once, and s = 1 - a = -m does not cancel.  No hardware exponential and no branch: 17
+// two-lane instructions for two channels.  Decays below 2^-126 count as 2^-126; NaN stays NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void exp2_parts(float2 t, float2& m, float2& scale) {
+    t = make_float2(max_nan(t.x, -126.f), max_nan(t.y, -126.f));
+    const float2 shifted = __fadd2_rn(t, splat(12582912.f));  // 1.5 * 2^23: n in the low bits
+    const float2 f = __fadd2_rn(t, __fadd2_rn(splat(12582912.f), make_float2(-shifted.x, -shifted.y)));
+    float2 q = __ffma2_rn(f, splat(1.5403508e-4f), splat(1.3390735e-3f));
+    q = __ffma2_rn(f, q, splat(9.6182376e-3f));
+    q = __ffma2_rn(f, q, splat(5.5503573e-2f));
+    q = __ffma2_rn(f, q, splat(2.4022649e-1f));
+    q = __ffma2_rn(f, q, splat(6.9314718e-1f));
+    m = __fmul2_rn(f, q);
+    scale = make_float2(__uint_as_float((__float_as_uint(shifted.x) << 23) + 0x3f800000u),
+                        __uint_as_float((__float_as_uint(shifted.y) << 23) + 0x3f800000u));
+}
+__device__ __forceinline__ float2 decay(float2 t) {
+    float2 m, scale;
+    exp2_parts(t, m, scale);
+    return __ffma2_rn(scale, m, scale);
+}
+__device__ __forceinline__ void decay(float2 t, float2& a, float2& s) {  // s = 1 - a
+    float2 m, scale;
+    exp2_parts(t, m, scale);
+    a = __ffma2_rn(scale, m, scale);
+    const float2 down = make_float2(-scale.x, -scale.y);
+    s = __ffma2_rn(down, m, __fadd2_rn(splat(1.f), down));
 }
 
-// the gate of two channels: its parameters and the log gate of raw values
+// softplus(z) = max(z, 0) + log(1 + y), y = e^{-|z|} in (0, 1]; log(1 + y) = y p(y) with the
+// polynomial p of degree 8 of the least relative error on [0, 1] (3e-8, fitted likewise), which
+// keeps the relative accuracy of the slow channels' small softplus.  Returns y too.
+__device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
+    y = make_float2(__expf(-fabsf(z.x)), __expf(-fabsf(z.y)));
+    float2 q = __ffma2_rn(y, splat(5.2326238e-3f), splat(-2.9504957e-2f));
+    q = __ffma2_rn(y, q, splat(7.8225493e-2f));
+    q = __ffma2_rn(y, q, splat(-1.3663207e-1f));
+    q = __ffma2_rn(y, q, splat(1.9105989e-1f));
+    q = __ffma2_rn(y, q, splat(-2.4842978e-1f));
+    q = __ffma2_rn(y, q, splat(3.3319095e-1f));
+    q = __ffma2_rn(y, q, splat(-4.9999493e-1f));
+    q = __ffma2_rn(y, q, splat(9.9999994e-1f));
+    return __ffma2_rn(y, q, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
+}
+
+// the gate of two channels: its parameters, the base-2 log gate of raw values, and what a
+// gradient of g is multiplied by to give that of the raw value
+constexpr float kLog2e = 1.4426950408889634f;
 template <int GATE>
 struct GlrGate {
     float2 nA, bias;  // -e^{A_log}, dt_bias
@@ -64,25 +101,30 @@ struct GlrGate {
             bias = *reinterpret_cast<const float2*>(dt_bias + c);
         }
     }
-    __device__ __forceinline__ float2 log_gate(float2 raw) const {
-        if constexpr (GATE == GLR_LOG) return raw;
-        const float2 z = __fadd2_rn(raw, bias);
-        return __fmul2_rn(nA, make_float2(softplus_f(z.x), softplus_f(z.y)));
-    }
-    // the log gate, and dg/d(raw) = -e^{A_log} sigmoid(z)
-    __device__ __forceinline__ float2 log_gate_slope(float2 raw, float2& slope) const {
-        if constexpr (GATE == GLR_LOG) {
-            slope = splat(1.f);
-            return raw;
+    __device__ __forceinline__ float2 log2_gate(float2 raw) const {
+        if constexpr (GATE == GLR_LOG) {  // (growth saturates at 2^127)
+            const float2 t = __fmul2_rn(raw, splat(kLog2e));
+            return make_float2(t.x > 127.f ? 127.f : t.x, t.y > 127.f ? 127.f : t.y);
+        } else {
+            float2 y;
+            return __fmul2_rn(__fmul2_rn(nA, splat(kLog2e)), softplus2(__fadd2_rn(raw, bias), y));
         }
+    }
+    // dg / d(raw) = -e^{A_log} sigmoid(z): sigmoid = 1 / (1 + y) for z >= 0, y / (1 + y) otherwise
+    __device__ __forceinline__ float2 slope(float2 raw) const {
+        if constexpr (GATE == GLR_LOG) return splat(1.f);
         const float2 z = __fadd2_rn(raw, bias);
-        float2 sp, sg;
-        softplus_sigmoid(z.x, sp.x, sg.x);
-        softplus_sigmoid(z.y, sp.y, sg.y);
-        slope = __fmul2_rn(nA, sg);
-        return __fmul2_rn(nA, sp);
+        const float2 y = make_float2(__expf(-fabsf(z.x)), __expf(-fabsf(z.y)));
+        const float2 inv = make_float2(__fdividef(1.f, 1.f + y.x), __fdividef(1.f, 1.f + y.y));
+        return __fmul2_rn(nA, __fmul2_rn(inv, make_float2(z.x >= 0.f ? 1.f : y.x, z.y >= 0.f ? 1.f : y.y)));
     }
 };
+
+// The new state of a token: a h + x, or a h + (1 - a) x with the complement, as x + a (h - x).
+template <bool COMP>
+__device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
+    return __ffma2_rn(a, COMP ? __fadd2_rn(h, make_float2(-x.x, -x.y)) : h, x);
+}
 
 // ---------------------------------------------------------------------------
 // The scan over tokens, y_t = a_t y_{t-1} + b_t with y restarted from a given state at each
@@ -274,6 +316,7 @@ __host__ __device__ inline size_t glr_runs_bytes(int chunks, int C) {  // of one
 // comes (it does: its block holds an earlier ticket) is recorded and left out.
 __device__ __forceinline__ Run glr_fold(const uint4* rows, int64_t stride, int from, int to, int* status) {
     Run r = run_identity();
+#pragma unroll 1
     for (int i = from; i < to; i += 4) {
         uint4 v[4];
         const int n = min(to - i, 4);
@@ -305,6 +348,7 @@ __device__ __forceinline__ float2 glr_carry(const GlrParams& p, GlrShared& sm, i
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
         Run own = run_identity();
         if (pos == 0) {
+#pragma unroll 1
             for (int w = 0; w < GLR_WARPS; ++w) own = run_then(own, run_from_bits(sm.sub[w][lane]));
             if (live) run_publish(runs.chunk + k * stride + c2, own);
         }
@@ -328,24 +372,31 @@ __device__ __forceinline__ float2 glr_carry(const GlrParams& p, GlrShared& sm, i
             __syncthreads();
         }
         float2 y = splat(0.f);
+#pragma unroll 1
         for (int q = 0; q < ns; ++q) y = run_apply(run_from_bits(sm.part[0][q][lane]), y);
+#pragma unroll 1
         for (int q = 0; q < ng; ++q) y = run_apply(run_from_bits(sm.part[1][q][lane]), y);
+#pragma unroll 1
         for (int q = 0; q < nc; ++q) y = run_apply(run_from_bits(sm.part[2][q][lane]), y);
         if (pos == 0 && k % GLR_GROUP == GLR_GROUP - 1 && live) {
             Run r = run_identity();
+#pragma unroll 1
             for (int q = 0; q < nc; ++q) r = run_then(r, run_from_bits(sm.part[2][q][lane]));
             r = run_then(r, own);
             run_publish(runs.group + k / GLR_GROUP * stride + c2, r);
             if (k % GLR_SUPER == GLR_SUPER - 1) {
                 Run u = run_identity();
+#pragma unroll 1
                 for (int q = 0; q < ng; ++q) u = run_then(u, run_from_bits(sm.part[1][q][lane]));
                 run_publish(runs.super + k / GLR_SUPER * stride + c2, run_then(u, r));
             }
         }
+#pragma unroll 1
         for (int w = 0; w < pos; ++w) y = run_apply(run_from_bits(sm.sub[w][lane]), y);
         return y;
     }
     float2 y = splat(0.f);
+#pragma unroll 1
     for (int w = 0; w < pos; ++w) y = run_apply(run_from_bits(sm.sub[w][lane]), y);
     return y;
 }

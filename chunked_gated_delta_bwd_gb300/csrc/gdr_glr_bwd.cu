@@ -17,7 +17,7 @@ namespace gdr {
 // or 12 bytes a token and channel in bf16).  g and dh are loaded first, for the run that is
 // published; h and x only then, so that they arrive while the block waits for the state.
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(GLR_THREADS, sizeof(TG) == 4 && sizeof(TX) == 2 ? 2 : 3) k_glr_bwd(const GlrParams p) {
+__global__ void __launch_bounds__(GLR_THREADS, 2) k_glr_bwd(const GlrParams p) {
     constexpr int SUB = glr_sub(sizeof(TX) == 4), CHUNK = SUB * GLR_WARPS;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
@@ -34,16 +34,26 @@ __global__ void __launch_bounds__(GLR_THREADS, sizeof(TG) == 4 && sizeof(TX) == 
     const int64_t t0 = (int64_t)kc * CHUNK, t = t0 + i0;  // the chunk's first token, this warp's
     const int len = (int)min((int64_t)CHUNK, p.T - t0);
     const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));  // tokens of this warp
-    const int n = live ? nt : 0;
+    const int64_t ldx = p.ldx / 2, ldg = p.ldg / 2;
+    const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
+    const RX* dh = reinterpret_cast<const RX*>(static_cast<const TX*>(p.dh) + t * p.C + c);
+    const RX* h = reinterpret_cast<const RX*>(static_cast<const TX*>(p.h_in) + (t - 1) * p.C + c);  // the state before
+    const RX* x = COMP ? reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c) : nullptr;
+    RX* dx = reinterpret_cast<RX*>(static_cast<TX*>(p.dx) + t * p.C + c);
+    RG* dg = reinterpret_cast<RG*>(static_cast<TG*>(p.dg) + t * p.C + c);
     RG gr[SUB];
     RX dr[SUB], hr[SUB], xr[SUB];
-    {
-        const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
-        const RX* dh = reinterpret_cast<const RX*>(static_cast<const TX*>(p.dh) + t * p.C + c);
+    if (nt == SUB && live) {
+#pragma unroll
+        for (int i = SUB - 1; i >= 0; --i) {
+            gr[i] = __ldg(g + i * ldg);
+            dr[i] = __ldg(dh + i * ld);
+        }
+    } else {
 #pragma unroll
         for (int i = 0; i < SUB; ++i) {
-            gr[i] = i < n ? __ldcs(g + i * (p.ldg / 2)) : PG::zero();
-            dr[i] = i < n ? __ldcs(dh + i * ld) : PX::zero();
+            gr[i] = PG::zero();
+            dr[i] = PX::zero();
         }
     }
     GlrGate<GATE> gate;
@@ -52,72 +62,98 @@ __global__ void __launch_bounds__(GLR_THREADS, sizeof(TG) == 4 && sizeof(TX) == 
     if (w == GLR_WARPS - 1) glr_empty_sequences(p, p.dht, p.dh0, kc, chunks, c, live, tile == 0);
     __syncthreads();
     const uint32_t bits = glr_start_bits(sm, i0, nt);  // of this warp's tokens and the one after
-    const uint32_t starts = bits & ((1u << nt) - 1u), ends = bits >> 1;
+    const bool whole = bits == 0 && nt == SUB;
+    float2 sumA = splat(0.f), sumB = splat(0.f);
 
+    // one token's gradients from l a (y) and the state before it
+    auto token = [&](float2 tg, typename PG::raw graw, float2 l, float2 s, float2 y, float2 before, float2 xv, RX* to_dx,
+                     RG* to_dg) {
+        float2 d = __fmul2_rn(y, COMP ? __fadd2_rn(before, make_float2(-xv.x, -xv.y)) : before);
+        if (GATE == GLR_SOFTPLUS) {
+            sumA = __ffma2_rn(d, tg, sumA);
+            d = __fmul2_rn(d, gate.slope(PG::widen(graw)));
+            sumB = __fadd2_rn(sumB, d);
+        }
+        if (live) {
+            *to_dx = PX::narrow(COMP ? __fmul2_rn(s, l) : l);
+            *to_dg = PG::narrow(d);
+        }
+    };
     auto state_of = [&](const float* from, int i) {
         return from && live ? *reinterpret_cast<const float2*>(from + (int64_t)glr_seq_at(sm, i) * p.C + c) : splat(0.f);
     };
-    // this warp's run
-    Run r = run_identity();
-#pragma unroll
-    for (int i = SUB - 1; i >= 0; --i) {
-        float2 a, s;
-        decay(gate.log_gate(PG::widen(gr[i])), a, s);
-        if (ends >> i & 1) {
-            r.A = splat(-0.f);
-            r.H = state_of(p.dht, i0 + i);
-        } else {
-            r.A = __fmul2_rn(r.A, a);
+    // the rolled walk from the state y (or, for the run, from none), with outputs or without
+    auto walk = [&](Run r, bool out) {
+#pragma unroll 1
+        for (int i = nt - 1; i >= 0; --i) {
+            const RG graw = live ? g[i * ldg] : PG::zero();
+            const float2 tg = gate.log2_gate(PG::widen(graw));
+            float2 a, s;
+            decay(tg, a, s);
+            if (bits >> (i + 1) & 1) {
+                r.A = splat(-0.f);
+                r.H = state_of(p.dht, i0 + i);
+            } else {
+                r.A = __fmul2_rn(r.A, a);
+            }
+            const float2 l = __fadd2_rn(r.H, live ? PX::widen(dh[i * ld]) : splat(0.f));
+            r.H = __fmul2_rn(a, l);
+            if (out) {
+                const bool first = bits >> i & 1;
+                const float2 before = first ? state_of(p.h0, i0 + i) : live && t + i > 0 ? PX::widen(h[i * ld]) : splat(0.f);
+                token(tg, graw, l, s, r.H, before, COMP && live ? PX::widen(x[i * ldx]) : splat(0.f), dx + i * ld, dg + i * ld);
+                if (first && live) *reinterpret_cast<float2*>(p.dh0 + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = r.H;
+            }
         }
-        r.H = __fmul2_rn(a, __fadd2_rn(r.H, PX::widen(dr[i])));
+        return r;
+    };
+    Run r = run_identity();
+    float2 tg[SUB];  // the base-2 log gates
+    if (whole) {
+#pragma unroll
+        for (int i = SUB - 1; i >= 0; --i) {
+            tg[i] = gate.log2_gate(PG::widen(gr[i]));
+            const float2 a = decay(tg[i]);
+            r.A = __fmul2_rn(r.A, a);
+            r.H = __fmul2_rn(a, __fadd2_rn(r.H, PX::widen(dr[i])));
+        }
+    } else {
+        r = walk(r, false);
     }
     const int pos = GLR_WARPS - 1 - w;
     sm.sub[pos][lane] = run_bits(r);
-    {
-        const RX* h = reinterpret_cast<const RX*>(static_cast<const TX*>(p.h_in) + (t - 1) * p.C + c);  // the state before
-        const RX* x = COMP ? reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c) : nullptr;
+    if (whole && live) {
 #pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            hr[i] = i < n && !(starts >> i & 1) && t + i > 0 ? __ldcs(h + i * ld) : PX::zero();
-            xr[i] = COMP && i < n ? __ldcs(x + i * (p.ldx / 2)) : PX::zero();
+        for (int i = SUB - 1; i >= 0; --i) {
+            hr[i] = t + i > 0 ? __ldg(h + i * ld) : PX::zero();
+            xr[i] = COMP ? __ldg(x + i * ldx) : PX::zero();
         }
     }
     __syncthreads();
-    float2 y = glr_carry(p, sm, chunks, k, chunks - 1 - (int)((uint64_t)(sm.end1 - 1) / CHUNK), sm.starts[len >> 5] >> (len & 31) & 1, pos,
-                         lane, c / 2, live);
+    float2 y = glr_carry(p, sm, chunks, k, chunks - 1 - (int)((uint64_t)(sm.end1 - 1) / CHUNK),
+                         sm.starts[len >> 5] >> (len & 31) & 1, pos, lane, c / 2, live);
 
+    if (whole) {
+        dx += (SUB - 1) * ld;
+        dg += (SUB - 1) * ld;
 #pragma unroll
-    for (int i = 0; i < SUB; ++i) forget(gr[i]);
-    RX* dx = reinterpret_cast<RX*>(static_cast<TX*>(p.dx) + t * p.C + c);
-    RG* dg = reinterpret_cast<RG*>(static_cast<TG*>(p.dg) + t * p.C + c);
-    float2 sumA = splat(0.f), sumB = splat(0.f);
-#pragma unroll
-    for (int i = SUB - 1; i >= 0; --i) {
-        float2 slope, a, s;
-        const float2 lg = gate.log_gate_slope(PG::widen(gr[i]), slope);
-        decay(lg, a, s);
-        if (ends >> i & 1) y = state_of(p.dht, i0 + i);
-        const float2 l = __fadd2_rn(y, PX::widen(dr[i]));
-        y = __fmul2_rn(a, l);
-        float2 before = PX::widen(hr[i]);
-        if (starts >> i & 1) before = state_of(p.h0, i0 + i);
-        if (COMP) {
-            const float2 xv = PX::widen(xr[i]);
-            before = __fadd2_rn(before, make_float2(-xv.x, -xv.y));
+        for (int i = SUB - 1; i >= 0; --i, dx -= ld, dg -= ld) {
+            forget(tg[i]);
+            forget(dr[i]);
+            forget(gr[i]);
+            float2 a, s;
+            decay(tg[i], a, s);
+            const float2 l = __fadd2_rn(y, PX::widen(dr[i]));
+            y = __fmul2_rn(a, l);
+            token(tg[i], gr[i], l, s, y, PX::widen(hr[i]), PX::widen(xr[i]), dx, dg);
         }
-        float2 d = __fmul2_rn(y, before);
-        if (i < n) {
-            if (GATE == GLR_SOFTPLUS) sumA = __ffma2_rn(d, lg, sumA);
-            d = GATE == GLR_SOFTPLUS ? __fmul2_rn(d, slope) : d;
-            if (GATE == GLR_SOFTPLUS) sumB = __fadd2_rn(sumB, d);
-            dx[i * ld] = PX::narrow(COMP ? __fmul2_rn(s, l) : l);
-            dg[i * ld] = PG::narrow(d);
-            if (starts >> i & 1) *reinterpret_cast<float2*>(p.dh0 + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = y;
-        }
+    } else {
+        r.H = y;
+        walk(r, true);
     }
     if (GATE == GLR_SOFTPLUS) {  // the chunk's sums, the warps' in a fixed order
         __shared__ float4 sums[GLR_WARPS][32];
-        sums[w][lane] = make_float4(sumA.x, sumA.y, sumB.x, sumB.y);
+        sums[w][lane] = make_float4(kLn2f * sumA.x, kLn2f * sumA.y, sumB.x, sumB.y);
         __syncthreads();
         if (w == 0 && live) {
             float4 v = sums[0][lane];

@@ -8,10 +8,13 @@ namespace gdr {
 size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p.T, p.act_f32), p.C); }
 
 // Bytes bound it: x and g are read once and h is written once (6 bytes a token and channel in
-// bf16).  A thread keeps its tokens of x and g in registers as loaded and evaluates the gate
-// twice, before and after the state in front of the chunk is known.
+// bf16).  A thread keeps its tokens' x as loaded and their decays in fp32 in registers from the
+// one evaluation of the gate to the second walk, after the state in front of the chunk is known.
+// A warp among whose tokens a sequence begins or ends walks them in a rolled loop that reads
+// them again: unrolled, those branches made three quarters of the code and the instruction
+// cache bound the kernel.
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(GLR_THREADS, sizeof(TX) == 2 && sizeof(TG) == 4 ? 3 : 4) k_glr_fwd(const GlrParams p) {
+__global__ void __launch_bounds__(GLR_THREADS, sizeof(TX) == 2 ? 3 : 4) k_glr_fwd(const GlrParams p) {
     constexpr int SUB = glr_sub(sizeof(TX) == 4), CHUNK = SUB * GLR_WARPS;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
@@ -23,28 +26,27 @@ __global__ void __launch_bounds__(GLR_THREADS, sizeof(TX) == 2 && sizeof(TG) == 
     const unsigned id = glr_ticket(p, sm, chunks);
     const int k = id / (unsigned)tiles;
     const int tile = id - k * tiles, w = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int c = tile * GLR_TILE + 2 * lane, i0 = w * SUB;
+    const int c = tile * GLR_TILE + 2 * lane, i0 = w * SUB, ld = p.C / 2;
     const bool live = c < p.C;
     const int64_t t0 = (int64_t)k * CHUNK, t = t0 + i0;  // the chunk's first token, this warp's
     const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));  // tokens of this warp
-    const int n = live ? nt : 0;
+    const RX* x = reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c);
+    const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
+    const int64_t ldx = p.ldx / 2, ldg = p.ldg / 2;
+    RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
     RX xr[SUB];
     RG gr[SUB];
-    {
-        const RX* x = reinterpret_cast<const RX*>(static_cast<const TX*>(p.x) + t * p.ldx + c);
-        const RG* g = reinterpret_cast<const RG*>(static_cast<const TG*>(p.g) + t * p.ldg + c);
-        if (n == SUB) {
+    if (nt == SUB && live) {
 #pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                gr[i] = __ldcs(g + i * (p.ldg / 2));
-                xr[i] = __ldcs(x + i * (p.ldx / 2));
-            }
-        } else {
+        for (int i = 0; i < SUB; ++i) {
+            gr[i] = __ldg(g + i * ldg);
+            xr[i] = __ldg(x + i * ldx);
+        }
+    } else {
 #pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                gr[i] = i < n ? __ldcs(g + i * (p.ldg / 2)) : PG::zero();
-                xr[i] = i < n ? __ldcs(x + i * (p.ldx / 2)) : PX::zero();
-            }
+        for (int i = 0; i < SUB; ++i) {
+            gr[i] = PG::zero();
+            xr[i] = PX::zero();
         }
     }
     GlrGate<GATE> gate;
@@ -53,72 +55,56 @@ __global__ void __launch_bounds__(GLR_THREADS, sizeof(TX) == 2 && sizeof(TG) == 
     if (w == GLR_WARPS - 1) glr_empty_sequences(p, p.h0, p.ht, k, chunks, c, live, tile == 0);
     __syncthreads();
     const uint32_t bits = glr_start_bits(sm, i0, nt);  // of this warp's tokens and the one after
-    const uint32_t starts = bits & ((1u << nt) - 1u), ends = bits >> 1;
+    const bool whole = bits == 0 && nt == SUB;
+    float2 a[SUB];
 
-    auto token = [&](int i, float2& a, float2& b) {
-        float2 s;
-        decay(gate.log_gate(PG::widen(gr[i])), a, s);
-        b = PX::widen(xr[i]);
-        if (COMP) b = __fmul2_rn(s, b);
+    // the rolled walk from the state y (or, for the run, from none), with outputs or without
+    auto walk = [&](Run r, bool out) {
+#pragma unroll 1
+        for (int i = 0; i < nt; ++i) {
+            const float2 d = decay(gate.log2_gate(live ? PG::widen(g[i * ldg]) : splat(0.f)));
+            const float2 xv = live ? PX::widen(x[i * ldx]) : splat(0.f);
+            if (bits >> i & 1) {
+                r.A = splat(-0.f);
+                r.H = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c)
+                                   : splat(0.f);
+            } else {
+                r.A = __fmul2_rn(r.A, d);
+            }
+            r.H = glr_update<COMP>(d, r.H, xv);
+            if (out && live) {
+                h[(int64_t)i * ld] = PX::narrow(r.H);
+                if (p.ht && (bits >> (i + 1) & 1))
+                    *reinterpret_cast<float2*>(p.ht + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = r.H;
+            }
+        }
+        return r;
     };
-    auto first_state = [&](int i) {
-        return p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(sm, i) * p.C + c) : splat(0.f);
-    };
-    // this warp's run
     Run r = run_identity();
-    if (starts == 0) {
+    if (whole) {
 #pragma unroll
         for (int i = 0; i < SUB; ++i) {
-            float2 a, b;
-            token(i, a, b);
-            r.A = __fmul2_rn(r.A, a);
-            r.H = __ffma2_rn(a, r.H, b);
+            a[i] = decay(gate.log2_gate(PG::widen(gr[i])));
+            r.A = __fmul2_rn(r.A, a[i]);
+            r.H = glr_update<COMP>(a[i], r.H, PX::widen(xr[i]));
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            float2 a, b;
-            token(i, a, b);
-            if (starts >> i & 1) {
-                r.A = splat(-0.f);
-                r.H = first_state(i0 + i);
-            } else {
-                r.A = __fmul2_rn(r.A, a);
-            }
-            r.H = __ffma2_rn(a, r.H, b);
-        }
+        r = walk(r, false);
     }
     sm.sub[w][lane] = run_bits(r);
     __syncthreads();
     float2 y = glr_carry(p, sm, chunks, k, (int)((uint64_t)sm.begin0 / CHUNK), sm.starts[0] & 1, w, lane, c / 2, live);
 
+    if (whole) {
 #pragma unroll
-    for (int i = 0; i < SUB; ++i) {
-        forget(gr[i]);
-        forget(xr[i]);
-    }
-    RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
-    if (bits == 0 && n == SUB) {
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            float2 a, b;
-            token(i, a, b);
-            y = __ffma2_rn(a, y, b);
-            h[i * (p.C / 2)] = PX::narrow(y);
+        for (int i = 0; i < SUB; ++i, h += ld) {
+            forget(xr[i]);
+            y = glr_update<COMP>(a[i], y, PX::widen(xr[i]));
+            if (live) *h = PX::narrow(y);
         }
     } else {
-#pragma unroll
-        for (int i = 0; i < SUB; ++i) {
-            float2 a, b;
-            token(i, a, b);
-            if (starts >> i & 1) y = first_state(i0 + i);
-            y = __ffma2_rn(a, y, b);
-            if (i < n) {
-                h[i * (p.C / 2)] = PX::narrow(y);
-                if (p.ht && (ends >> i & 1))
-                    *reinterpret_cast<float2*>(p.ht + (int64_t)glr_seq_at(sm, i0 + i) * p.C + c) = y;
-            }
-        }
+        r.H = y;
+        walk(r, true);
     }
 }
 
@@ -157,9 +143,7 @@ __global__ void __launch_bounds__(128) k_glr_step(const GlrStepParams p) {
             const float2 xv = PX::widen(*reinterpret_cast<const typename PX::raw*>(static_cast<const TX*>(p.x) + n * p.ldx + c));
             const float2 gv = PG::widen(*reinterpret_cast<const typename PG::raw*>(static_cast<const TG*>(p.g) + n * p.ldg + c));
             st = *home;
-            float2 a, s;
-            decay(gate.log_gate(gv), a, s);
-            st = __ffma2_rn(a, st, COMP ? __fmul2_rn(s, xv) : xv);
+            st = glr_update<COMP>(decay(gate.log2_gate(gv)), st, xv);
             *home = st;
         }
         *reinterpret_cast<typename PX::raw*>(static_cast<TX*>(p.y) + n * p.C + c) = PX::narrow(st);
