@@ -77,6 +77,12 @@ static gdr_status check_glr(const glr_shape* sh, GlrParams* p) {
 
 static size_t glr_workspace(const GlrParams& p) { return 256 + glr_published_bytes(p) + glr_sums_bytes(p); }
 
+// whether rows of C elements at this stride are whole numbers of aligned 16-byte pieces
+static int rows_wide(const GlrParams& p, const void* at, int64_t ld, int f32) {
+    const int piece = f32 ? 4 : 8;
+    return aligned16(at) && ld % piece == 0 && p.C % piece == 0;
+}
+
 // Checks and clears the workspace (a launch of one chunk writes its status word itself); every
 // sequence empty: the states pass through.
 static gdr_status glr_front(GlrParams& p, void* ws, size_t ws_bytes, float* to, const float* from, cudaStream_t s,
@@ -121,6 +127,7 @@ gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const f
     if (gdr_status st = glr_front(p, workspace, workspace_bytes, ht, h0, s, &done)) return st;
     if (done) return ok();
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0; p.h = h; p.ht = ht;
+    p.wide = rows_wide(p, x, p.ldx, p.act_f32) && rows_wide(p, g, p.ldg, p.gate_f32);
     cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_fwd(p, s); });
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence launch");
 }
@@ -150,6 +157,8 @@ gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const f
     }
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h_in = h; p.h0 = h0; p.dh = dh; p.dht = dht;
     p.dx = dx; p.dg = dg; p.dh0 = dh0; p.dA_log = dA_log; p.ddt_bias = ddt_bias;
+    p.wide = (!p.complement || rows_wide(p, x, p.ldx, p.act_f32)) && rows_wide(p, g, p.ldg, p.gate_f32) &&
+             rows_wide(p, h, p.C, p.act_f32);
     cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_bwd(p, s); }, soft ? 2 : 1);
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence backward launch");
 }
