@@ -9,6 +9,7 @@
 #include "gdr_block.h"
 #include "gdr_common.cuh"
 #include "gdr_internal.h"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 
@@ -94,12 +95,13 @@ __device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
 constexpr float kLog2e = 1.4426950408889634f;
 template <int GATE>
 struct GlrGate {
-    float2 nA, bias;  // -e^{A_log}, dt_bias
+    float2 nA, bias, inv;  // -e^{A_log}, dt_bias, e^{-A_log} (0 where the gate is shut)
     __device__ __forceinline__ void load(const float* A_log, const float* dt_bias, int c) {
         if constexpr (GATE == GLR_SOFTPLUS) {
             const float2 l = *reinterpret_cast<const float2*>(A_log + c);
             nA = make_float2(-expf(l.x), -expf(l.y));
             bias = *reinterpret_cast<const float2*>(dt_bias + c);
+            inv = make_float2(nA.x < -1e-30f ? -1.f / nA.x : 0.f, nA.y < -1e-30f ? -1.f / nA.y : 0.f);
         }
     }
     __device__ __forceinline__ float2 log2_gate(float2 raw) const {
@@ -110,13 +112,13 @@ struct GlrGate {
             return __fmul2_rn(__fmul2_rn(nA, splat(kLog2e)), softplus2(__fadd2_rn(raw, bias), y));
         }
     }
-    // dg / d(raw) = -e^{A_log} sigmoid(z): sigmoid = 1 / (1 + y) for z >= 0, y / (1 + y) otherwise
-    __device__ __forceinline__ float2 slope(float2 raw) const {
+    // dg / d(raw) = -e^{A_log} sigmoid(z) from the base-2 log gate t = -e^{A_log} softplus(z) / ln 2:
+    // sigmoid(z) = 1 - e^{-softplus(z)} = 1 - 2^{t e^{-A_log}}
+    __device__ __forceinline__ float2 slope(float2 t) const {
         if constexpr (GATE == GLR_LOG) return splat(1.f);
-        const float2 z = __fadd2_rn(raw, bias);
-        const float2 y = make_float2(__expf(-fabsf(z.x)), __expf(-fabsf(z.y)));
-        const float2 inv = make_float2(__fdividef(1.f, 1.f + y.x), __fdividef(1.f, 1.f + y.y));
-        return __fmul2_rn(nA, __fmul2_rn(inv, make_float2(z.x >= 0.f ? 1.f : y.x, z.y >= 0.f ? 1.f : y.y)));
+        float2 a, s;
+        decay(__fmul2_rn(t, inv), a, s);
+        return __fmul2_rn(nA, s);
     }
 };
 
@@ -130,8 +132,8 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 // The scan over tokens, y_t = a_t y_{t-1} + b_t with y restarted from a given state at each
 // sequence (the forward in the order of time; the backward, whose y is a_t l_t, against it).
 //
-// The tokens of all sequences are cut into chunks of 8 SUB; a tile is one chunk of 64 channels,
-// a warp takes SUB consecutive tokens of it, a lane two channels.  A run of tokens acts on the
+// The tokens of all sequences are cut into chunks of 64; a tile is one chunk of 64 channels, a
+// warp takes 64 / (compute warps) consecutive tokens of it, a lane two channels.  A run of tokens acts on the
 // state before it as y -> A y + H.  Each tile's run (A, H) is published; the state before a chunk
 // is the fold of the runs before it, back to the chunk its sequence begins in.  So that no tile
 // folds many, the last chunk of every 16 also publishes the run of all 16 and the last of every
@@ -140,23 +142,20 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 // results do not depend on the order in which blocks run.
 //
 // Blocks stay resident and take tiles by ticket, chunks in the order of the scan: a tile waits
-// only for tiles with earlier tickets, which are being worked on.  The loads of the next tile are
-// in flight while a tile is worked on; each warp loads its own tokens, so a tile has two barriers.
+// only for tiles with earlier tickets, which are being worked on.  A block's compute warps walk
+// tile j for its run, then tile j - 1 for its results, each warp on rows that it copied itself,
+// two tiles ahead; four exchange warps, one for every fourth tile, publish and gather in between
+// (GlrRing).  So neither the loads nor the way to the other blocks and back is waited for, and
+// what a tile costs besides its tokens does not fall to the warps that work on them.
 //
 // A run that contains a restart does not depend on the state before it: its A is -0 (a product
 // of decays is +0 at least), and a fold that meets it takes H as it is, so that no infinity or
 // NaN crosses from one sequence into the next.
 // ---------------------------------------------------------------------------
-constexpr int GLR_WARPS = 8, GLR_MAX_CHUNK = 128, GLR_TILE = 64;
-// tokens of a warp: 32 KB of inputs to a chunk's run at most, whatever the types
-__host__ __device__ constexpr int glr_sub(bool act_f32, bool gate_f32) { return act_f32 || gate_f32 ? 8 : 16; }
-__host__ __device__ inline int glr_chunks(int64_t T, bool act_f32, bool gate_f32) {  // (T is below 2^36)
-    const unsigned chunk = glr_sub(act_f32, gate_f32) * GLR_WARPS;
-    return (int)((uint64_t)(T + chunk - 1) / chunk);
-}
-constexpr int GLR_THREADS = 32 * GLR_WARPS;
+constexpr int GLR_CHUNK = 64, GLR_TILE = 64;
 constexpr int GLR_GROUP = 16, GLR_SUPER = 256;  // chunks in a published group / super group
 constexpr int GLR_SPIN = 1 << 20;               // polls of one published run before giving up
+__host__ __device__ inline int glr_chunks(const GlrParams& p) { return (int)((uint64_t)(p.T + GLR_CHUNK - 1) / GLR_CHUNK); }
 
 // a run of tokens for two channels
 struct Run {
@@ -207,87 +206,115 @@ __device__ __forceinline__ Run run_of(const uint4& v) {
     return Run{make_float2(__uint_as_float(~v.x), __uint_as_float(~v.y)),
                make_float2(__uint_as_float(~v.z), __uint_as_float(~v.w))};
 }
+// Where published runs lie in the workspace, after the status word and the ticket counter.
+struct GlrRuns {
+    uint4 *chunk, *group, *super;  // [..][C / 2]
+};
+__host__ __device__ inline GlrRuns glr_runs(void* ws, int chunks, int C) {
+    GlrRuns r;
+    r.chunk = reinterpret_cast<uint4*>(static_cast<unsigned char*>(ws) + 256);
+    r.group = r.chunk + (int64_t)chunks * (C / 2);
+    r.super = r.group + (int64_t)(chunks / GLR_GROUP) * (C / 2);
+    return r;
+}
+__host__ __device__ inline size_t glr_runs_bytes(int chunks, int C) {  // of one chunk's tokens: none
+    return chunks > 1 ? sizeof(uint4) * (size_t)(C / 2) * ((size_t)chunks + chunks / GLR_GROUP + chunks / GLR_SUPER) : 0;
+}
 
-// the sequences of a chunk's tokens
+// a tile's sequences and its place in the scan
 struct GlrInfo {
-    uint32_t starts[6];         // bit i: token t0 + i begins a sequence (the chunk's end and the end of all tokens count)
-    int seq_at_start[GLR_MAX_CHUNK];  // the sequence beginning at token t0 + i, where one does
+    uint32_t starts[4];         // bit i: token t0 + i begins a sequence (the chunk's end and the end of all tokens count)
+    int any;                    // whether any of them does, or restarts the scan
     int seq0;                   // the sequence of token t0
-    int64_t begin0, end1;       // where that sequence begins; where the one of the last token ends
-};
-constexpr int GLR_PARTS = 8;
-struct GlrShared {
-    uint4 sub[GLR_WARPS][32];   // the warps' runs
-    uint4 part[GLR_PARTS][32];  // folds of published runs: chunks (4), groups (2), super groups (2)
-    GlrInfo info[2];            // of this tile and the next
-    unsigned ticket;
+    int seq_at_start[GLR_CHUNK];  // the sequence beginning at token t0 + i, where one does
+    // published runs of chunks [chunk0, k), groups [group0, group1) and super groups [super0, super1)
+    // make up the state before chunk k (none of them: it begins with a restart)
+    int chunk0, group0, group1, super0, super1, none;
 };
 
-// Finds the sequences of a chunk's tokens [t0, t0 + len); all threads of one warp.  Indexes stay
-// in range for inconsistent cu_seqlens too.
-__device__ __forceinline__ void glr_find_sequences(const GlrParams& p, GlrInfo& sm, int64_t t0, int len, int lane) {
-    if (lane < 6) sm.starts[lane] = 0;
-    for (int i = lane; i < GLR_MAX_CHUNK; i += 32) sm.seq_at_start[i] = 0;
+// Works out a chunk's sequences and place; all threads of one warp.  Its tokens are
+// [t0, t0 + len), `k` is its number in the order of the scan.  Indexes stay in range for
+// inconsistent cu_seqlens too.
+template <bool BWD>
+__device__ __forceinline__ void glr_find_place(const GlrParams& p, GlrInfo& sm, int chunks, int k, int64_t t0, int len, int lane) {
+    if (lane < 4) sm.starts[lane] = 0;
     __syncwarp();
+    int64_t begin0, end1;  // where the sequence of token t0 begins; where the one of the last token ends
     const int64_t* cu = p.cu_seqlens;
+    bool some = false;
     if (!cu) {
         // t0 / seq_len, from its product with 1 / seq_len, which is off by less than one
         int64_t n0 = (int64_t)((double)t0 * p.inv_len);
         if (n0 * p.seq_len > t0) --n0;
         if ((n0 + 1) * p.seq_len <= t0) ++n0;
-        const int64_t begin = n0 * p.seq_len;
-        if (lane == 0) {
-            sm.seq0 = (int)n0;
-            sm.begin0 = begin;
+        begin0 = n0 * p.seq_len;
+        if (lane == 0) sm.seq0 = (int)n0;
+        end1 = begin0 + p.seq_len;
+        if (begin0 == t0 || end1 <= t0 + len) {
+            for (int64_t n = n0 + (begin0 < t0) + lane, b; (b = n * p.seq_len) <= t0 + len; n += 32) {
+                const int i = (int)(b - t0);
+                atomicOr(&sm.starts[i >> 5], 1u << (i & 31));
+                if (i < GLR_CHUNK) sm.seq_at_start[i] = (int)n;
+            }
+            some = true;
         }
-        for (int64_t n = n0 + (begin < t0) + lane, b; (b = n * p.seq_len) <= t0 + len; n += 32) {
-            const int i = (int)(b - t0);
-            atomicOr(&sm.starts[i >> 5], 1u << (i & 31));
-            if (i < GLR_MAX_CHUNK) sm.seq_at_start[i] = (int)n;
-        }
+        if (end1 < t0 + len)  // (a sequence of over GLR_CHUNK tokens has one such boundary here)
+            end1 += p.seq_len > GLR_CHUNK ? p.seq_len
+                                              : ((unsigned)(t0 + len - 1 - end1) / (unsigned)p.seq_len + 1) * p.seq_len;
+    } else {
+        for (int i = lane; i < GLR_CHUNK; i += 32) sm.seq_at_start[i] = 0;
         __syncwarp();
-        if (lane == 0) {  // the end of the last token's sequence
-            int64_t e = begin + p.seq_len;
-            if (e < t0 + len)  // (a sequence of over GLR_MAX_CHUNK tokens has one such boundary here)
-                e += p.seq_len > GLR_MAX_CHUNK ? p.seq_len : ((unsigned)(t0 + len - 1 - e) / (unsigned)p.seq_len + 1) * p.seq_len;
-            sm.end1 = e;
+        // the last sequence that begins at or before t0, by 32 probes at a time
+        int lo = 0, hi = p.N;
+        while (hi - lo > 1) {
+            const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+            const bool before = lane == 0 || (at < hi && cu[at] <= t0);
+            lo += (__popc(__ballot_sync(~0u, before)) - 1) * step;
+            hi = min(hi, lo + step);
         }
-        return;
+        if (lane == 0) sm.seq0 = lo;
+        begin0 = min(max(cu[lo], (int64_t)0), t0);
+        end1 = p.T;
+        // the boundaries inside the chunk and at its end, 32 at a time
+        for (int n0 = lo; n0 <= p.N; n0 += 32) {
+            const int n = n0 + lane;
+            const int64_t b = n <= p.N ? cu[n] : p.T;
+            const int64_t i = b - t0;
+            if (n <= p.N && i >= 0 && i <= len) {
+                // of the sequences that begin here the last one is not empty.  (A boundary of inconsistent
+                // cu_seqlens gets some sequence's number all the same: no index leaves the states.)
+                atomicOr(&sm.starts[i >> 5], 1u << (i & 31));
+                if (i < GLR_CHUNK) atomicMax(&sm.seq_at_start[i], min(n, p.N - 1));
+                some = true;
+            }
+            // the end of the last token's sequence: the first boundary at or past the chunk's end
+            const unsigned past = __ballot_sync(~0u, n <= p.N && b >= t0 + len);
+            if (past) {
+                end1 = min(__shfl_sync(~0u, b, __ffs(past) - 1), p.T);
+                break;
+            }
+        }
+        if (t0 + len == p.T) {
+            if (lane == 0) atomicOr(&sm.starts[len >> 5], 1u << (len & 31));
+            some = true;
+        }
     }
-    // the last sequence that begins at or before t0, by 32 probes at a time
-    int lo = 0, hi = p.N;
-    while (hi - lo > 1) {
-        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-        const bool before = lane == 0 || (at < hi && cu[at] <= t0);
-        lo += (__popc(__ballot_sync(~0u, before)) - 1) * step;
-        hi = min(hi, lo + step);
-    }
-    if (lane == 0) {
-        sm.seq0 = lo;
-        const int64_t b = cu[lo];
-        sm.begin0 = b < 0 ? 0 : (b > t0 ? t0 : b);
-        sm.end1 = p.T;
-    }
+    some = __any_sync(~0u, some);
     __syncwarp();
-    // the boundaries inside the chunk and at its end, 32 at a time
-    for (int n0 = lo; n0 <= p.N; n0 += 32) {
-        const int n = n0 + lane;
-        const int64_t b = n <= p.N ? cu[n] : p.T;
-        const int64_t i = b - t0;
-        if (n <= p.N && i >= 0 && i <= len) {
-            // of the sequences that begin here the last one is not empty.  (A boundary of inconsistent
-            // cu_seqlens gets some sequence's number all the same: no index leaves the states.)
-            atomicOr(&sm.starts[i >> 5], 1u << (i & 31));
-            if (i < GLR_MAX_CHUNK) atomicMax(&sm.seq_at_start[i], min(n, p.N - 1));
-        }
-        // the end of the last token's sequence: the first boundary at or past the chunk's end
-        const unsigned past = __ballot_sync(~0u, n <= p.N && b >= t0 + len);
-        if (past) {
-            if (lane == __ffs(past) - 1) sm.end1 = b > p.T ? p.T : b;
-            break;
-        }
+    if (lane == 0) {
+        // the chunk in which the sequence running into this one begins; whether this one begins with a restart
+        const int lo = BWD ? chunks - 1 - (int)((uint64_t)(end1 - 1) / GLR_CHUNK) : (int)((uint64_t)begin0 / GLR_CHUNK);
+        const bool fresh = BWD ? sm.starts[len >> 5] >> (len & 31) & 1 : sm.starts[0] & 1;
+        const int g0 = k / GLR_GROUP * GLR_GROUP, s0 = k / GLR_SUPER * GLR_SUPER;
+        const bool none = fresh || k == 0;
+        sm.any = some;
+        sm.chunk0 = max(lo, g0);
+        sm.group0 = max(lo, s0) / GLR_GROUP;
+        sm.group1 = k / GLR_GROUP;
+        sm.super0 = lo / GLR_SUPER;
+        sm.super1 = k / GLR_SUPER;
+        sm.none = none;
     }
-    if (lane == 0 && t0 + len == p.T) atomicOr(&sm.starts[len >> 5], 1u << (len & 31));
     __syncwarp();
 }
 // start bits of tokens i0 .. i0 + n of the chunk (n <= 16)
@@ -305,36 +332,21 @@ __device__ __forceinline__ int glr_seq_at(const GlrInfo& sm, int i) {
     }
 }
 
-// Where published runs lie in the workspace, after the status word and the ticket counter.
-struct GlrRuns {
-    uint4 *chunk, *group, *super;  // [..][C / 2]
-};
-__host__ __device__ inline GlrRuns glr_runs(void* ws, int chunks, int C) {
-    GlrRuns r;
-    r.chunk = reinterpret_cast<uint4*>(static_cast<unsigned char*>(ws) + 256);
-    r.group = r.chunk + (int64_t)chunks * (C / 2);
-    r.super = r.group + (int64_t)(chunks / GLR_GROUP) * (C / 2);
-    return r;
-}
-__host__ __device__ inline size_t glr_runs_bytes(int chunks, int C) {  // of one chunk's tokens: none
-    return chunks > 1 ? sizeof(uint4) * (size_t)(C / 2) * ((size_t)chunks + chunks / GLR_GROUP + chunks / GLR_SUPER) : 0;
-}
-
 // Folds published runs [from, to) of `rows` for this lane's channels in order; only the first one
 // of all may contain a restart.  A run that never comes (it does: its block holds an earlier
 // ticket) is recorded and left out.
 __device__ __forceinline__ Run glr_fold(const uint4* rows, int64_t stride, int from, int to, int* status) {
     Run r = run_identity();
 #pragma unroll 1
-    for (int i = from; i < to; i += 4) {
-        uint4 v[4];
+    for (int i = from; i < to; i += 8) {
+        uint4 v[8];
         const uint4* at = rows + i * stride;
-        const int n = min(to - i, 4);
+        const int n = min(to - i, 8);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int j = 0; j < 8; ++j)
             if (j < n) v[j] = run_poll(at + j * stride);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < 8; ++j) {
             if (j < n) {
 #pragma unroll 1
                 for (int spin = 0; !run_there(v[j]) && spin < GLR_SPIN; ++spin) v[j] = run_poll(at + j * stride);
@@ -344,144 +356,6 @@ __device__ __forceinline__ Run glr_fold(const uint4* rows, int64_t stride, int f
         }
     }
     return r;
-}
-
-// A tile's place in the scan: which published runs make up the state before it.
-struct GlrPlace {
-    int k;                   // the chunk's number in the order of the scan
-    int chunk0, group0, group1, super0, super1;  // chunks [chunk0, k), groups [group0, group1), super groups
-    int nc, ng, ns;          // parts of each level: 4 runs, 8 runs, half of the runs
-    // `lo`: the chunk the sequence running into this one begins in; `fresh`: the chunk begins with a restart
-    __device__ __forceinline__ GlrPlace(int k_, int lo, bool fresh) : k(k_) {
-        const int g0 = k / GLR_GROUP * GLR_GROUP, s0 = k / GLR_SUPER * GLR_SUPER;
-        chunk0 = max(lo, g0);
-        group0 = max(lo, s0) / GLR_GROUP;
-        group1 = k / GLR_GROUP;
-        super0 = lo / GLR_SUPER;
-        super1 = k / GLR_SUPER;
-        const bool none = fresh || k == 0;
-        nc = none ? 0 : (k - chunk0 + 3) / 4;
-        ng = none ? 0 : (group1 - group0 + 7) / 8;
-        ns = none ? 0 : super1 - super0 > 1 ? 2 : super1 - super0;
-    }
-};
-
-// Between a tile's barriers.  Warp 0 publishes the tile's run and returns it; warps 1 to 4 fold
-// published runs of chunks, 5 and 6 of groups and super groups (warp 7 is left to look ahead).
-// `c2`: this lane's pair of channels (valid if `live`).
-__device__ __forceinline__ Run glr_exchange(const GlrParams& p, GlrShared& sm, const GlrPlace& at, const GlrRuns& runs, int w,
-                                            int lane, int c2, bool live) {
-    const int64_t stride = p.C / 2;
-    Run own = run_identity();
-    if (w == 0) {
-#pragma unroll
-        for (int i = 0; i < GLR_WARPS; ++i) own = run_then(own, run_from_bits(sm.sub[i][lane]));
-        if (live) run_publish(runs.chunk + at.k * stride + c2, own);
-    } else if (w <= 4) {
-        if (w <= at.nc && live) {
-            const int from = at.chunk0 + 4 * (w - 1);
-            sm.part[w - 1][lane] = run_bits(glr_fold(runs.chunk + c2, stride, from, min(at.k, from + 4), p.status));
-        }
-    } else if (w <= 6 && live) {
-        const int q = w - 5;
-        if (q < at.ng) {
-            const int from = at.group0 + 8 * q;
-            sm.part[4 + q][lane] = run_bits(glr_fold(runs.group + c2, stride, from, min(at.group1, from + 8), p.status));
-        }
-        if (q < at.ns) {
-            const int half = at.ns == 1 ? 1 : (at.super1 - at.super0) / 2, from = at.super0 + q * half;
-            sm.part[6 + q][lane] =
-                run_bits(glr_fold(runs.super + c2, stride, from, q == at.ns - 1 ? at.super1 : from + half, p.status));
-        }
-    }
-    return own;
-}
-
-// After the second barrier: the state before the chunk.
-__device__ __forceinline__ float2 glr_state_before(const GlrShared& sm, const GlrPlace& at, int lane) {
-    Run y = run_identity();
-#pragma unroll 1
-    for (int q = 0; q < at.ns; ++q) y = run_then_plain(y, run_from_bits(sm.part[6 + q][lane]));
-#pragma unroll 1
-    for (int q = 0; q < at.ng; ++q) y = run_then_plain(y, run_from_bits(sm.part[4 + q][lane]));
-#pragma unroll 1
-    for (int q = 0; q < at.nc; ++q) y = run_then_plain(y, run_from_bits(sm.part[q][lane]));
-    return y.H;
-}
-
-// Warp 0 of the last chunk of a group (super group) publishes its run.
-__device__ __forceinline__ void glr_publish_groups(const GlrParams& p, const GlrShared& sm, const GlrPlace& at,
-                                                   const GlrRuns& runs, const Run& own, int lane, int c2, bool live) {
-    if (at.k % GLR_GROUP != GLR_GROUP - 1 || !live) return;
-    const int64_t stride = p.C / 2;
-    Run r = run_identity();
-#pragma unroll 1
-    for (int q = 0; q < at.nc; ++q) r = run_then_plain(r, run_from_bits(sm.part[q][lane]));
-    r = run_then(r, own);
-    run_publish(runs.group + at.k / GLR_GROUP * stride + c2, r);
-    if (at.k % GLR_SUPER != GLR_SUPER - 1) return;
-    Run u = run_identity();
-#pragma unroll 1
-    for (int q = 0; q < at.ng; ++q) u = run_then_plain(u, run_from_bits(sm.part[4 + q][lane]));
-    run_publish(runs.super + at.k / GLR_SUPER * stride + c2, run_then(u, r));
-}
-
-// The run of the warps before this one in the order of the scan (`pos` of them), and the state
-// it leaves behind a given one.  `restarts`: the chunk may contain restarts.
-__device__ __forceinline__ Run glr_before_warp(const GlrShared& sm, int pos, int lane, bool restarts) {
-    Run r = run_identity();
-    if (restarts) {
-#pragma unroll 1
-        for (int i = 0; i < pos; ++i) r = run_then(r, run_from_bits(sm.sub[i][lane]));
-    } else {
-#pragma unroll 1
-        for (int i = 0; i < pos; ++i) r = run_then_plain(r, run_from_bits(sm.sub[i][lane]));
-    }
-    return r;
-}
-__device__ __forceinline__ float2 glr_after(const Run& r, float2 y) {
-    return run_then(Run{splat(0.f), y}, r).H;
-}
-
-// The next tile.  Tickets count in the workspace when there is something to wait for.
-__device__ __forceinline__ unsigned glr_next(const GlrParams& p, int chunks, unsigned id) {
-    return chunks == 1 ? id + gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
-}
-
-// Asynchronous copies of a warp's rows [0, nt) of 64 channels into shared memory, zeros past them
-// and past the `cols` channels there are; rows before `skip` are zeros too.  16 bytes a copy
-// where every row of the call's tensors allows it (`wide`), else one pair of channels.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void* dst, const void* src, bool there) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_u32(dst)), "l"(src), "r"(there ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(smem_u32(dst)), "l"(src), "n"(BYTES), "r"(there ? BYTES : 0) : "memory");
-}
-template <int SUB, class T>
-__device__ __forceinline__ void glr_copy_rows(T* dst, const T* src, int64_t ld, int skip, int nt, int cols, bool wide, int lane,
-                                              const T* somewhere) {
-    if (wide) {
-        constexpr int E = 16 / sizeof(T), S = GLR_TILE / E;  // elements a copy, copies a row
-#pragma unroll
-        for (int j = 0; j < SUB * S / 32; ++j) {
-            const int at = j * 32 + lane, row = at / S, e = at % S * E;
-            const bool there = row >= skip && row < nt && e < cols;
-            copy_async<16>(dst + row * GLR_TILE + e, there ? src + row * ld + e : somewhere, there);
-        }
-    } else {
-#pragma unroll 4
-        for (int row = 0; row < SUB; ++row) {
-            const bool there = row >= skip && row < nt && 2 * lane < cols;
-            copy_async<2 * sizeof(T)>(dst + row * GLR_TILE + 2 * lane, there ? src + row * ld + 2 * lane : somewhere, there);
-        }
-    }
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the N most recent groups of this thread, then of its warp
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
-    __syncwarp();
 }
 
 // Empty sequences pass their state through; the first tile's blocks also check cu_seqlens against
@@ -512,10 +386,174 @@ __device__ __forceinline__ void glr_empty_sequences(const GlrParams& p, const fl
     }
 }
 
+// The ring through which a block's warps hand tiles to each other; tile j of the block uses slot
+// j % 4, or j % 2 of what is only needed from its first walk to its second (which comes after the
+// first one of tile j + 1).  CW compute warps, 4 exchange warps.
+//   tick:  the tile's chunk and channels are known (compute warp 0 takes the tickets, in order)
+//   place: its sequences and place are known (exchange warp)
+//   runs:  the warps' runs are there (compute warps)
+//   state: the states before each warp's tokens are there (exchange warp)
+//   free:  the results are written; the slot may be used for tile j + 4 (compute warps)
+template <int CW>
+struct GlrRing {
+    uint4 sub[2][CW][32];       // the warps' runs, in the order of the scan; then the states before them
+    GlrInfo info[4];
+    int2 tick[4];               // the tile's chunk in the order of the scan (-1: no more) and first channel
+    uint64_t bar[5][4];
+};
+enum { GLR_TICK = 0, GLR_PLACE = 1, GLR_RUNS = 2, GLR_STATE = 3, GLR_FREE = 4 };
+
+template <int CW>
+__device__ __forceinline__ void glr_ring_init(GlrRing<CW>& ring) {
+    if (threadIdx.x < 20) {
+        const int kind = threadIdx.x / 4;
+        tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]), kind == GLR_RUNS || kind == GLR_FREE ? CW : 1);
+    }
+    __syncthreads();
+}
+// Waits for tile j's barrier.  (Every barrier is reached: what its warp waits for elsewhere is bounded.)
+template <int CW>
+__device__ __forceinline__ void glr_wait(const GlrParams& p, GlrRing<CW>& ring, int kind, int j) {
+    if (!tc::mbar_wait(smem_u32(&ring.bar[kind][j & 3]), (j >> 2) & 1, 1 << 18)) atomicOr(p.status, ST_MMA_TIMEOUT);
+}
+// What this warp has written for tile j is there.
+template <int CW>
+__device__ __forceinline__ void glr_signal(GlrRing<CW>& ring, int kind, int j) {
+    __syncwarp();
+    if (threadIdx.x % 32 == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(&ring.bar[kind][j & 3])) : "memory");
+}
+
+// A block's tickets, in the order of its tiles: they count in the workspace when there is something
+// to wait for.
+__device__ __forceinline__ unsigned glr_ticket(const GlrParams& p, int chunks, int j) {
+    return chunks == 1 ? blockIdx.x + j * gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
+}
+template <int CW>
+__device__ __forceinline__ void glr_set_tick(GlrRing<CW>& ring, int j, unsigned id, unsigned tiles, unsigned all) {
+    const unsigned k = id / tiles;
+    ring.tick[j & 3] = make_int2(id < all ? (int)k : -1, (int)((id - k * tiles) * GLR_TILE));
+}
+
+// One exchange warp's work on tile j: its place; its run, published; the states before its warps.
+// `done` is called with the chunk and first channel of tile j - 4 once that is finished.  Returns
+// false when there are no more tiles.
+template <bool BWD, int CW, class F>
+__device__ __forceinline__ bool glr_exchange(const GlrParams& p, GlrRing<CW>& ring, const GlrRuns& runs, int chunks, int j, int lane,
+                                             int2& tick, const F& done) {
+    const int slot = j & 3, half = j & 1;
+    if (j >= 4) {
+        glr_wait(p, ring, GLR_FREE, j - 4);
+        done(tick, j - 4);
+    }
+    glr_wait(p, ring, GLR_TICK, j);
+    tick = ring.tick[slot];
+    const int k = tick.x;
+    GlrInfo& at = ring.info[slot];
+    if (k < 0) {
+        glr_signal(ring, GLR_PLACE, j);
+        return false;
+    }
+    const int kc = BWD ? chunks - 1 - k : k, c = tick.y + 2 * lane;
+    const bool live = c < p.C;
+    const int64_t t0 = (int64_t)kc * GLR_CHUNK, stride = p.C / 2;
+    glr_find_place<BWD>(p, at, chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
+    glr_signal(ring, GLR_PLACE, j);
+    glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, live, tick.y == 0);
+    glr_wait(p, ring, GLR_RUNS, j);
+    float2 y = splat(0.f);
+    if (chunks > 1) {
+        Run own = run_from_bits(ring.sub[half][0][lane]);
+#pragma unroll
+        for (int i = 1; i < CW; ++i) own = run_then(own, run_from_bits(ring.sub[half][i][lane]));
+        if (live) {
+            const int c2 = c / 2;
+            run_publish(runs.chunk + k * stride + c2, own);
+            Run all = run_identity(), level = all, groups = all;
+            // super groups, groups, chunks (one call site: three would be three copies of the fold's code)
+#pragma unroll 1
+            for (int q = 0; q < 3; ++q) {
+                const uint4* rows = q == 0 ? runs.super : q == 1 ? runs.group : runs.chunk;
+                const int from = q == 0 ? at.super0 : q == 1 ? at.group0 : at.chunk0, to = q == 0 ? at.super1 : q == 1 ? at.group1 : k;
+                level = run_identity();
+                if (!at.none && to > from) level = glr_fold(rows + c2, stride, from, to, p.status);
+                if (q == 1) groups = level;
+                all = run_then_plain(all, level);
+            }
+            y = all.H;
+            if (k % GLR_GROUP == GLR_GROUP - 1) {
+                level = run_then(level, own);  // the last chunk of a group: its run (of a super group likewise)
+                run_publish(runs.group + k / GLR_GROUP * stride + c2, level);
+                if (k % GLR_SUPER == GLR_SUPER - 1)
+                    run_publish(runs.super + k / GLR_SUPER * stride + c2, run_then(groups, level));
+            }
+        }
+    }
+    Run r{splat(0.f), y};
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+        const Run of_warp = run_from_bits(ring.sub[half][i][lane]);
+        *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = r.H;
+        r = run_then(r, of_warp);
+    }
+    glr_signal(ring, GLR_STATE, j);
+    return true;
+}
+
+// Asynchronous copies of a warp's rows [0, SUB) of 64 channels into shared memory: zeros from row
+// nt on, before row `skip` and past the `cols` channels there are.  16 bytes a copy where every
+// row of the call's tensors allows it (`wide`), else one pair of channels.  PITCH: bytes from row
+// to row in shared memory.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(BYTES), "r"(there ? BYTES : 0)
+                     : "memory");
+}
+template <int SUB, int PITCH, class T>
+__device__ __forceinline__ void glr_copy_rows(void* to, const T* src, int64_t ld, int skip, int nt, int cols, bool wide, int lane,
+                                              const T* somewhere) {
+    const uint32_t dst = smem_u32(to);
+    constexpr int E = 16 / sizeof(T), S = GLR_TILE / E, R = 32 / S;  // elements a copy, copies a row, rows a pass
+    if (wide) {
+        const int row0 = lane / S, e = lane % S * E;
+        const uint32_t mine = dst + row0 * PITCH + lane % S * 16;
+        const T* at = src + row0 * ld + e;
+        if (nt == SUB && skip == 0 && cols >= GLR_TILE) {
+#pragma unroll
+            for (int j = 0; j < SUB / R; ++j, at += R * ld)
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(mine + j * R * PITCH), "l"(at) : "memory");
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < SUB / R; ++j, at += R * ld) {
+                const int row = j * R + row0;
+                const bool there = row >= skip && row < nt && e < cols;
+                copy_async<16>(mine + j * R * PITCH, there ? at : somewhere, there);
+            }
+        }
+    } else {
+#pragma unroll 4
+        for (int row = 0; row < SUB; ++row) {
+            const bool there = row >= skip && row < nt && 2 * lane < cols;
+            copy_async<2 * sizeof(T)>(dst + row * PITCH + 2 * lane * sizeof(T), there ? src + row * ld + 2 * lane : somewhere,
+                                      there);
+        }
+    }
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {  // all but the N most recent groups of this thread, then of its warp
+    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+    __syncwarp();
+}
+
 // Launches a scan kernel on as many blocks as are resident at once (or tiles, if fewer).
 // `ready`: the devices whose shared-memory limit of this kernel is raised.
 template <class K>
-cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, size_t smem, int per_sm, const GlrParams& p, cudaStream_t s) {
+cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, int threads, size_t smem, int per_sm, const GlrParams& p,
+                       cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -525,9 +563,8 @@ cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, size_t smem, int 
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
-    const int64_t all = (int64_t)glr_chunks(p.T, p.act_f32, p.gate_f32) * ((p.C + GLR_TILE - 1) / GLR_TILE);
-    const int64_t resident = (int64_t)per_sm * num_sms();
-    kernel<<<(unsigned)(all < resident ? all : resident), GLR_THREADS, smem, s>>>(p);
+    const int64_t all = (int64_t)glr_chunks(p) * ((p.C + GLR_TILE - 1) / GLR_TILE), resident = (int64_t)per_sm * num_sms();
+    kernel<<<(unsigned)(all < resident ? all : resident), threads, smem, s>>>(p);
     return cudaGetLastError();
 }
 

@@ -5,136 +5,167 @@
 
 namespace gdr {
 
-size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p.T, p.act_f32, p.gate_f32), p.C); }
+size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p), p.C); }
 
 // Bytes bound it: x and g are read once and h is written once (6 bytes a token and channel in
-// bf16).  A thread keeps its tokens' decays in fp32 in registers from the one evaluation of the
-// gate to the second walk, after the state in front of the chunk is known.  A warp among whose
-// tokens a sequence begins or ends walks them in a rolled loop: unrolled, those branches made
-// three quarters of the code and the instruction cache bound the kernel.
-template <class TX, class TG>
+// bf16).  The gate is evaluated once: the first walk leaves the decays in fp32 where g was, for
+// the second one, after the state in front of the chunk is known.  Both walk four tokens at a
+// time in a rolled loop (unrolled over a warp's tokens the code did not fit the instruction
+// cache, which then bound the kernel); a warp among whose tokens a sequence begins or ends walks
+// them one by one.
+constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS;
+template <class TX>
 struct GlrFwdTile {
-    static constexpr int SUB = glr_sub(sizeof(TX) == 4, sizeof(TG) == 4);
-    TX x[2][GLR_WARPS][SUB][GLR_TILE];
-    TG g[2][GLR_WARPS][SUB][GLR_TILE];
-    GlrShared sm;
+    float2 a[3][FWD_WARPS][FWD_SUB][32];    // g as copied (a row in the first bytes of its 256), then the decays
+    TX x[3][FWD_WARPS][FWD_SUB][GLR_TILE];
+    GlrRing<FWD_WARPS> ring;
 };
 
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(GLR_THREADS, 3) k_glr_fwd(const GlrParams p) {
-    constexpr int SUB = GlrFwdTile<TX, TG>::SUB, CHUNK = SUB * GLR_WARPS;
+__global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrParams p) {
+    constexpr int SUB = FWD_SUB;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
     using RX = typename PX::raw;
     using RG = typename PG::raw;
     extern __shared__ __align__(16) unsigned char smem[];
-    GlrFwdTile<TX, TG>& tl = *reinterpret_cast<GlrFwdTile<TX, TG>*>(smem);
-    GlrShared& sm = tl.sm;
-    const int chunks = glr_chunks(p.T, sizeof(TX) == 4, sizeof(TG) == 4);
+    GlrFwdTile<TX>& tl = *reinterpret_cast<GlrFwdTile<TX>*>(smem);
+    GlrRing<FWD_WARPS>& ring = tl.ring;
+    const int chunks = glr_chunks(p);
     const unsigned tiles = (p.C + GLR_TILE - 1) / GLR_TILE, all = tiles * chunks;
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, i0 = w * SUB, ld = p.C / 2;
-    const GlrRuns runs = glr_runs(p.status, chunks, p.C);
+    glr_ring_init(ring);
+    if (w >= FWD_WARPS) {
+        const GlrRuns runs = glr_runs(p.status, chunks, p.C);
+        int2 tick;
+        for (int j = w - FWD_WARPS; glr_exchange<false>(p, ring, runs, chunks, j, lane, tick, [](int2, int) {}); j += 4) {}
+        return;
+    }
 
-    auto copy = [&](unsigned id, int b) {  // this warp's tokens of a tile
-        if (id < all) {
-            const int k = id / tiles, c0 = (id - k * tiles) * GLR_TILE;
-            const int64_t t = (int64_t)k * CHUNK + i0;
-            const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));
+    auto copy = [&](int j) {  // this warp's tokens of tile j
+        glr_wait(p, ring, GLR_TICK, j);
+        const int2 tick = ring.tick[j & 3];
+        if (tick.x >= 0) {
+            const int64_t t = (int64_t)tick.x * GLR_CHUNK + i0;
+            const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t)), cols = p.C - tick.y;
             const TX* x = static_cast<const TX*>(p.x);
             const TG* g = static_cast<const TG*>(p.g);
-            glr_copy_rows<SUB>(&tl.g[b][w][0][0], g + t * p.ldg + c0, p.ldg, 0, nt, p.C - c0, p.wide, lane, g);
-            glr_copy_rows<SUB>(&tl.x[b][w][0][0], x + t * p.ldx + c0, p.ldx, 0, nt, p.C - c0, p.wide, lane, x);
+            glr_copy_rows<SUB, 256>(&tl.a[j % 3][w][0][0], g + t * p.ldg + tick.y, p.ldg, 0, nt, cols, p.wide, lane, g);
+            glr_copy_rows<SUB, GLR_TILE * sizeof(TX)>(&tl.x[j % 3][w][0][0], x + t * p.ldx + tick.y, p.ldx, 0, nt, cols, p.wide, lane, x);
         }
         copies_commit();
     };
-    auto look = [&](unsigned id, int b) {  // the sequences of a tile's tokens; one warp
-        if (id >= all) return;
-        const int k = id / tiles, c = (id - k * tiles) * GLR_TILE + 2 * lane;
-        glr_find_sequences(p, sm.info[b], (int64_t)k * CHUNK, (int)min((int64_t)CHUNK, p.T - (int64_t)k * CHUNK), lane);
-        glr_empty_sequences(p, p.h0, p.ht, k, chunks, c, c < p.C, id == k * tiles);
-    };
-
-    if (threadIdx.x == 0) sm.ticket = chunks == 1 ? blockIdx.x : glr_next(p, chunks, 0);
-    __syncthreads();
-    unsigned id = sm.ticket;
-    copy(id, 0);
-    if (w == GLR_WARPS - 1) look(id, 0);
-    __syncthreads();
-    if (threadIdx.x == 0) sm.ticket = glr_next(p, chunks, id);
-    __syncthreads();
-    for (int b = 0; id < all; b ^= 1) {
-        const unsigned next = sm.ticket;
-        copy(next, b ^ 1);
-        const int k = id / tiles, tile = id - k * tiles, c = tile * GLR_TILE + 2 * lane;
-        const bool live = c < p.C;
-        const int64_t t = (int64_t)k * CHUNK + i0;  // this warp's first token
-        const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));
-        const GlrInfo& info = sm.info[b];
-        const uint32_t bits = glr_start_bits(info, i0, nt);  // of this warp's tokens and the one after
-        const bool whole = bits == 0 && nt == SUB;
-        const GlrPlace at(k, (int)((uint64_t)info.begin0 / CHUNK), info.starts[0] & 1);
-        GlrGate<GATE> gate;
-        gate.load(p.A_log, p.dt_bias, live ? c : 0);
-        RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
-        auto xv = [&](int i) { return PX::widen(*reinterpret_cast<const RX*>(&tl.x[b][w][i][2 * lane])); };
-        auto tv = [&](int i) { return gate.log2_gate(PG::widen(*reinterpret_cast<const RG*>(&tl.g[b][w][i][2 * lane]))); };
-        // the rolled walk from the state r.H, with outputs or (for the run) without
-        auto walk = [&](Run r, bool out) {
+    const bool takes = w == 0 && lane == 0;  // the tickets
+    for (int j = 0; j < 3; ++j) {
+        if (w == 0) {
+            if (takes) glr_set_tick(ring, j, glr_ticket(p, chunks, j), tiles, all);
+            glr_signal(ring, GLR_TICK, j);
+        }
+        if (j < 2) copy(j);
+    }
+    int2 before = make_int2(-1, 0);  // tile j - 1
+    for (int j = 0;; ++j) {
+        glr_wait(p, ring, GLR_PLACE, j);
+        const int2 tick = ring.tick[j & 3];
+        unsigned id = 0;
+        if (tick.x >= 0) {
+            if (takes) id = glr_ticket(p, chunks, j + 3);
+            const GlrInfo& info = ring.info[j & 3];
+            const int c = tick.y + 2 * lane;
+            const bool live = c < p.C;
+            GlrGate<GATE> gate;
+            gate.load(p.A_log, p.dt_bias, live ? c : 0);
+            copies_wait<1>();
+            const TX* xs = &tl.x[j % 3][w][0][2 * lane];
+            float2* as = &tl.a[j % 3][w][0][lane];
+            const TG* gs = reinterpret_cast<const TG*>(&tl.a[j % 3][w][0][0]) + 2 * lane;
+            constexpr int GP = 256 / sizeof(TG);
+            Run r = run_identity();
+            if (!info.any) {
 #pragma unroll 1
-            for (int i = 0; i < nt; ++i) {
-                const float2 d = decay(tv(i));
-                if (bits >> i & 1) {
-                    r.A = splat(-0.f);
-                    r.H = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(info, i0 + i) * p.C + c)
-                                       : splat(0.f);
-                } else {
-                    r.A = __fmul2_rn(r.A, d);
-                }
-                r.H = glr_update<COMP>(d, r.H, xv(i));
-                if (out && live) {
-                    h[(int64_t)i * ld] = PX::narrow(r.H);
-                    if (p.ht && (bits >> (i + 1) & 1))
-                        *reinterpret_cast<float2*>(p.ht + (int64_t)glr_seq_at(info, i0 + i) * p.C + c) = r.H;
-                }
-            }
-            return r;
-        };
-        copies_wait<1>();
-        Run r = run_identity();
-        float2 a[SUB];
-        if (whole) {
+                for (int i = 0; i < SUB; i += 4) {
+                    RG graw[4];
+                    float2 xv[4];
 #pragma unroll
-            for (int i = 0; i < SUB; ++i) {
-                a[i] = decay(tv(i));
-                r.A = __fmul2_rn(r.A, a[i]);
-                r.H = glr_update<COMP>(a[i], r.H, xv(i));
-            }
-        } else {
-            r = walk(r, false);
-        }
-        sm.sub[w][lane] = run_bits(r);
-        __syncthreads();
-        const bool restarts = info.starts[0] | info.starts[1] | info.starts[2] | info.starts[3];
-        Run before = glr_before_warp(sm, w, lane, restarts), own;
-        if (chunks > 1) own = glr_exchange(p, sm, at, runs, w, lane, c / 2, live);
-        if (w == GLR_WARPS - 1) {
-            if (lane == 0) sm.ticket = glr_next(p, chunks, next);
-            look(next, b ^ 1);
-        }
-        __syncthreads();
-        float2 y = glr_after(before, glr_state_before(sm, at, lane));
-        if (w == 0 && chunks > 1) glr_publish_groups(p, sm, at, runs, own, lane, c / 2, live);
-        if (whole) {
+                    for (int q = 0; q < 4; ++q) {
+                        graw[q] = *reinterpret_cast<const RG*>(gs + (i + q) * GP);
+                        xv[q] = PX::widen(*reinterpret_cast<const RX*>(xs + (i + q) * GLR_TILE));
+                    }
+                    __syncwarp();  // every lane has its g of these rows
 #pragma unroll
-            for (int i = 0; i < SUB; ++i, h += ld) {
-                y = glr_update<COMP>(a[i], y, xv(i));
-                if (live) *h = PX::narrow(y);
+                    for (int q = 0; q < 4; ++q) {
+                        const float2 a = decay(gate.log2_gate(PG::widen(graw[q])));
+                        as[(i + q) * 32] = a;
+                        r.A = __fmul2_rn(r.A, a);
+                        r.H = glr_update<COMP>(a, r.H, xv[q]);
+                    }
+                }
+            } else {
+                const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)tick.x * GLR_CHUNK + i0)));
+                const uint32_t bits = glr_start_bits(info, i0, nt);
+#pragma unroll 1
+                for (int i = 0; i < nt; ++i) {
+                    const RG graw = *reinterpret_cast<const RG*>(gs + i * GP);
+                    __syncwarp();
+                    const float2 a = decay(gate.log2_gate(PG::widen(graw)));
+                    as[i * 32] = a;
+                    if (bits >> i & 1) {
+                        r.A = splat(-0.f);
+                        r.H = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(info, i0 + i) * p.C + c)
+                                           : splat(0.f);
+                    } else {
+                        r.A = __fmul2_rn(r.A, a);
+                    }
+                    r.H = glr_update<COMP>(a, r.H, PX::widen(*reinterpret_cast<const RX*>(xs + i * GLR_TILE)));
+                }
             }
-        } else {
-            walk(Run{splat(1.f), y}, true);
+            ring.sub[j & 1][w][lane] = run_bits(r);
+            glr_signal(ring, GLR_RUNS, j);
         }
-        __syncwarp();  // the warp's rows are free for the copies of the tile after next
-        id = next;
+        if (before.x >= 0) {
+            glr_wait(p, ring, GLR_STATE, j - 1);
+            const GlrInfo& info = ring.info[(j - 1) & 3];
+            const int c = before.y + 2 * lane;
+            const bool live = c < p.C;
+            const int64_t t = (int64_t)before.x * GLR_CHUNK + i0;
+            RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
+            const TX* xs = &tl.x[(j - 1) % 3][w][0][2 * lane];
+            const float2* as = &tl.a[(j - 1) % 3][w][0][lane];
+            float2 y = *reinterpret_cast<const float2*>(&ring.sub[(j - 1) & 1][w][lane]);
+            if (!info.any) {
+#pragma unroll 1
+                for (int i = 0; i < SUB; i += 4) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q, h += ld) {
+                        y = glr_update<COMP>(as[(i + q) * 32], y, PX::widen(*reinterpret_cast<const RX*>(xs + (i + q) * GLR_TILE)));
+                        if (live) *h = PX::narrow(y);
+                    }
+                }
+            } else {
+                const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));
+                const uint32_t bits = glr_start_bits(info, i0, nt);
+#pragma unroll 1
+                for (int i = 0; i < nt; ++i, h += ld) {
+                    if (bits >> i & 1)
+                        y = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(info, i0 + i) * p.C + c)
+                                         : splat(0.f);
+                    y = glr_update<COMP>(as[i * 32], y, PX::widen(*reinterpret_cast<const RX*>(xs + i * GLR_TILE)));
+                    if (live) {
+                        *h = PX::narrow(y);
+                        if (p.ht && (bits >> (i + 1) & 1))
+                            *reinterpret_cast<float2*>(p.ht + (int64_t)glr_seq_at(info, i0 + i) * p.C + c) = y;
+                    }
+                }
+            }
+            glr_signal(ring, GLR_FREE, j - 1);
+        }
+        if (w == 0) {
+            if (takes) glr_set_tick(ring, j + 3, tick.x < 0 ? all : id, tiles, all);
+            glr_signal(ring, GLR_TICK, j + 3);
+        }
+        if (tick.x < 0) break;
+        copy(j + 2);
+        before = tick;
     }
     copies_wait<0>();
 }
@@ -146,7 +177,7 @@ struct Launch {
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
         static std::atomic<uint64_t> ready{0};
-        return glr_launch(k_glr_fwd<TX, TG, GATE, COMP>, ready, sizeof(GlrFwdTile<TX, TG>), 3, p, s);
+        return glr_launch(k_glr_fwd<TX, TG, GATE, COMP>, ready, 32 * (FWD_WARPS + 4), sizeof(GlrFwdTile<TX>), 2, p, s);
     }
 };
 }  // namespace
