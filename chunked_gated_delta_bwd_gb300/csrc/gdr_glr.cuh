@@ -184,27 +184,25 @@ __device__ __forceinline__ Run run_from_bits(const uint4& v) {
                make_float2(__uint_as_float(v.z), __uint_as_float(v.w))};
 }
 
-// Published runs are polled word by word: the workspace starts at zero and every word is stored
-// inverted, so a word is there once it is not zero.  (All bits set, whose inverse is zero, is a
-// NaN that no arithmetic gives; a NaN is stored as the usual one.)
-__device__ __forceinline__ uint32_t run_word(float v) { return ~(v != v ? 0x7fffffffu : __float_as_uint(v)); }
+// A published run is two 64-bit words, A and H, each stored and loaded at once.  The workspace
+// starts at zero and the first half of either word is stored inverted, so a word is there once
+// that half is not zero.  (All bits set, whose inverse is zero, is a NaN that no arithmetic
+// gives; a NaN is stored as the usual one.)
+__device__ __forceinline__ uint32_t run_mark(float v) { return ~(v != v ? 0x7fffffffu : __float_as_uint(v)); }
 __device__ __forceinline__ void run_publish(uint4* at, const Run& r) {
-    asm volatile("st.relaxed.gpu.global.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"l"(at), "r"(run_word(r.A.x)),
-                 "r"(run_word(r.A.y)), "r"(run_word(r.H.x)), "r"(run_word(r.H.y))
-                 : "memory");
+    const uint64_t a = run_mark(r.A.x) | ((uint64_t)__float_as_uint(r.A.y) << 32);
+    const uint64_t h = run_mark(r.H.x) | ((uint64_t)__float_as_uint(r.H.y) << 32);
+    asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};\n" ::"l"(at), "l"(a), "l"(h) : "memory");
 }
 __device__ __forceinline__ uint4 run_poll(const uint4* at) {
-    uint4 v;
-    asm volatile("ld.relaxed.gpu.global.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(at)
-                 : "memory");
-    return v;
+    uint64_t a, h;
+    asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];\n" : "=l"(a), "=l"(h) : "l"(at) : "memory");
+    return make_uint4((uint32_t)a, (uint32_t)(a >> 32), (uint32_t)h, (uint32_t)(h >> 32));
 }
-__device__ __forceinline__ bool run_there(const uint4& v) { return v.x && v.y && v.z && v.w; }
+__device__ __forceinline__ bool run_there(const uint4& v) { return v.x != 0 && v.z != 0; }
 __device__ __forceinline__ Run run_of(const uint4& v) {
-    return Run{make_float2(__uint_as_float(~v.x), __uint_as_float(~v.y)),
-               make_float2(__uint_as_float(~v.z), __uint_as_float(~v.w))};
+    return Run{make_float2(__uint_as_float(~v.x), __uint_as_float(v.y)),
+               make_float2(__uint_as_float(~v.z), __uint_as_float(v.w))};
 }
 // Where published runs lie in the workspace, after the status word and the ticket counter.
 struct GlrRuns {
@@ -227,9 +225,9 @@ struct GlrInfo {
     int any;                    // whether any of them does, or restarts the scan
     int seq0;                   // the sequence of token t0
     int seq_at_start[GLR_CHUNK];  // the sequence beginning at token t0 + i, where one does
-    // published runs of chunks [chunk0, k), groups [group0, group1) and super groups [super0, super1)
+    // published runs of chunks [chunk0, k), groups [group0, k / 16) and super groups [super0, k / 256)
     // make up the state before chunk k (none of them: it begins with a restart)
-    int chunk0, group0, group1, super0, super1, none;
+    int chunk0, group0, super0, none;
 };
 
 // Works out a chunk's sequences and place; all threads of one warp.  Its tokens are
@@ -310,9 +308,7 @@ __device__ __forceinline__ void glr_find_place(const GlrParams& p, GlrInfo& sm, 
         sm.any = some;
         sm.chunk0 = max(lo, g0);
         sm.group0 = max(lo, s0) / GLR_GROUP;
-        sm.group1 = k / GLR_GROUP;
         sm.super0 = lo / GLR_SUPER;
-        sm.super1 = k / GLR_SUPER;
         sm.none = none;
     }
     __syncwarp();
@@ -332,26 +328,32 @@ __device__ __forceinline__ int glr_seq_at(const GlrInfo& sm, int i) {
     }
 }
 
-// Folds published runs [from, to) of `rows` for this lane's channels in order; only the first one
-// of all may contain a restart.  A run that never comes (it does: its block holds an earlier
-// ticket) is recorded and left out.
+// The run of published runs [from, to) of `rows`, for this lane's channels.  Only the first run of
+// all may contain a restart.  A run that never comes (it does: its block holds an earlier ticket)
+// is recorded.
 __device__ __forceinline__ Run glr_fold(const uint4* rows, int64_t stride, int from, int to, int* status) {
     Run r = run_identity();
+    const uint4* at = rows + from * stride;
 #pragma unroll 1
-    for (int i = from; i < to; i += 8) {
+    for (int n = to - from; n > 0; n -= 8) {
         uint4 v[8];
-        const uint4* at = rows + i * stride;
-        const int n = min(to - i, 8);
+        const uint4* here = at;
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            if (j < n) v[j] = run_poll(at + j * stride);
+        for (int j = 0; j < 8; ++j, at += stride)
+            if (j < n) v[j] = run_poll(at);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (j < n) {
+                if (!run_there(v[j])) {
+                    int spin = 0;
+                    int64_t apart = stride;
+                    asm volatile("" : "+l"(apart));  // (else eight addresses are kept for a path hardly taken)
 #pragma unroll 1
-                for (int spin = 0; !run_there(v[j]) && spin < GLR_SPIN; ++spin) v[j] = run_poll(at + j * stride);
-                if (run_there(v[j])) r = i + j == from ? run_of(v[j]) : run_then_plain(r, run_of(v[j]));
-                else atomicOr(status, ST_MMA_TIMEOUT);
+                    do v[j] = run_poll(here + j * apart);
+                    while (!run_there(v[j]) && ++spin < GLR_SPIN);
+                    if (!run_there(v[j])) atomicOr(status, ST_MMA_TIMEOUT);
+                }
+                r = run_then_plain(r, run_of(v[j]));
             }
         }
     }
@@ -398,7 +400,7 @@ template <int CW>
 struct GlrRing {
     uint4 sub[2][CW][32];       // the warps' runs, in the order of the scan; then the states before them
     GlrInfo info[4];
-    int2 tick[4];               // the tile's chunk in the order of the scan (-1: no more) and first channel
+    int4 tick[4];               // the tile's chunk in the order of the scan (-1: no more), first channel, whether it is whole
     uint64_t bar[5][4];
 };
 enum { GLR_TICK = 0, GLR_PLACE = 1, GLR_RUNS = 2, GLR_STATE = 3, GLR_FREE = 4 };
@@ -429,10 +431,13 @@ __device__ __forceinline__ void glr_signal(GlrRing<CW>& ring, int kind, int j) {
 __device__ __forceinline__ unsigned glr_ticket(const GlrParams& p, int chunks, int j) {
     return chunks == 1 ? blockIdx.x + j * gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
 }
-template <int CW>
-__device__ __forceinline__ void glr_set_tick(GlrRing<CW>& ring, int j, unsigned id, unsigned tiles, unsigned all) {
-    const unsigned k = id / tiles;
-    ring.tick[j & 3] = make_int2(id < all ? (int)k : -1, (int)((id - k * tiles) * GLR_TILE));
+template <bool BWD, int CW>
+__device__ __forceinline__ void glr_set_tick(const GlrParams& p, GlrRing<CW>& ring, int chunks, int j, unsigned id, unsigned tiles,
+                                             unsigned all) {
+    const unsigned k = id / tiles, c0 = (id - k * tiles) * GLR_TILE;
+    const unsigned kc = BWD ? chunks - 1 - k : k;
+    ring.tick[j & 3] = make_int4(id < all ? (int)k : -1, (int)c0,
+                                 ((int64_t)kc + 1) * GLR_CHUNK <= p.T && (int)c0 + GLR_TILE <= p.C && !(BWD && kc == 0), 0);
 }
 
 // One exchange warp's work on tile j: its place; its run, published; the states before its warps.
@@ -440,7 +445,7 @@ __device__ __forceinline__ void glr_set_tick(GlrRing<CW>& ring, int j, unsigned 
 // false when there are no more tiles.
 template <bool BWD, int CW, class F>
 __device__ __forceinline__ bool glr_exchange(const GlrParams& p, GlrRing<CW>& ring, const GlrRuns& runs, int chunks, int j, int lane,
-                                             int2& tick, const F& done) {
+                                             int4& tick, const F& done) {
     const int slot = j & 3, half = j & 1;
     if (j >= 4) {
         glr_wait(p, ring, GLR_FREE, j - 4);
@@ -461,40 +466,38 @@ __device__ __forceinline__ bool glr_exchange(const GlrParams& p, GlrRing<CW>& ri
     glr_signal(ring, GLR_PLACE, j);
     glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, live, tick.y == 0);
     glr_wait(p, ring, GLR_RUNS, j);
-    float2 y = splat(0.f);
-    if (chunks > 1) {
+    const bool any = at.any;
+    Run y = run_identity();
+    if (chunks > 1 && live) {
+        const int c2 = c / 2;
         Run own = run_from_bits(ring.sub[half][0][lane]);
 #pragma unroll
-        for (int i = 1; i < CW; ++i) own = run_then(own, run_from_bits(ring.sub[half][i][lane]));
-        if (live) {
-            const int c2 = c / 2;
-            run_publish(runs.chunk + k * stride + c2, own);
-            Run all = run_identity(), level = all, groups = all;
-            // super groups, groups, chunks (one call site: three would be three copies of the fold's code)
+        for (int i = 1; i < CW; ++i) {
+            const Run next = run_from_bits(ring.sub[half][i][lane]);
+            own = any ? run_then(own, next) : run_then_plain(own, next);
+        }
+        run_publish(runs.chunk + k * stride + c2, own);
+        // the runs of chunks, groups and super groups before it (in one loop: each copy of the fold's
+        // code costs registers); the last chunk of a group, of a super group, publishes that one's run
 #pragma unroll 1
-            for (int q = 0; q < 3; ++q) {
-                const uint4* rows = q == 0 ? runs.super : q == 1 ? runs.group : runs.chunk;
-                const int from = q == 0 ? at.super0 : q == 1 ? at.group0 : at.chunk0, to = q == 0 ? at.super1 : q == 1 ? at.group1 : k;
-                level = run_identity();
-                if (!at.none && to > from) level = glr_fold(rows + c2, stride, from, to, p.status);
-                if (q == 1) groups = level;
-                all = run_then_plain(all, level);
-            }
-            y = all.H;
-            if (k % GLR_GROUP == GLR_GROUP - 1) {
-                level = run_then(level, own);  // the last chunk of a group: its run (of a super group likewise)
-                run_publish(runs.group + k / GLR_GROUP * stride + c2, level);
-                if (k % GLR_SUPER == GLR_SUPER - 1)
-                    run_publish(runs.super + k / GLR_SUPER * stride + c2, run_then(groups, level));
+        for (int q = 0; q < 3; ++q) {
+            const uint4* rows = q == 0 ? runs.chunk : q == 1 ? runs.group : runs.super;
+            const int from = q == 0 ? at.chunk0 : q == 1 ? at.group0 : at.super0;
+            const int to = q == 0 ? k : q == 1 ? k / GLR_GROUP : k / GLR_SUPER;
+            Run level = run_identity();
+            if (!at.none && from < to) level = glr_fold(rows + c2, stride, from, to, p.status);
+            y = run_then_plain(level, y);
+            if (q < 2 && (k + 1) % (q == 0 ? GLR_GROUP : GLR_SUPER) == 0) {
+                own = run_then(level, own);
+                run_publish((q == 0 ? runs.group : runs.super) + (q == 0 ? k / GLR_GROUP : k / GLR_SUPER) * stride + c2, own);
             }
         }
     }
-    Run r{splat(0.f), y};
 #pragma unroll
     for (int i = 0; i < CW; ++i) {
-        const Run of_warp = run_from_bits(ring.sub[half][i][lane]);
-        *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = r.H;
-        r = run_then(r, of_warp);
+        const Run next = run_from_bits(ring.sub[half][i][lane]);
+        *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = y.H;
+        y = any ? run_then(y, next) : run_then_plain(y, next);
     }
     glr_signal(ring, GLR_STATE, j);
     return true;
@@ -513,35 +516,46 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool t
                      : "memory");
 }
 template <int SUB, int PITCH, class T>
-__device__ __forceinline__ void glr_copy_rows(void* to, const T* src, int64_t ld, int skip, int nt, int cols, bool wide, int lane,
-                                              const T* somewhere) {
-    const uint32_t dst = smem_u32(to);
-    constexpr int E = 16 / sizeof(T), S = GLR_TILE / E, R = 32 / S;  // elements a copy, copies a row, rows a pass
-    if (wide) {
-        const int row0 = lane / S, e = lane % S * E;
-        const uint32_t mine = dst + row0 * PITCH + lane % S * 16;
-        const T* at = src + row0 * ld + e;
-        if (nt == SUB && skip == 0 && cols >= GLR_TILE) {
+struct GlrRows {
+    static constexpr int E = 16 / sizeof(T), S = GLR_TILE / E, R = 32 / S;  // elements a copy, copies a row, rows a pass
+    const T *base, *safe;  // this warp's first token of chunk 0; an address for copies of nothing
+    int64_t ld;
+    int64_t mine;    // this lane's place in a pass of 16-byte copies
+    __device__ __forceinline__ GlrRows(const void* base_, int64_t ld_, int i0, int lane) : ld(ld_) {
+        safe = static_cast<const T*>(base_);
+        base = safe + i0 * ld;
+        mine = lane / S * ld + lane % S * E;
+    }
+    // tokens of chunk kc; `whole`: all of the tile's rows and channels are there
+    __device__ __forceinline__ void copy(void* to, int64_t kc, int c0, bool whole, bool wide, int skip, int64_t T0, int cols,
+                                         int lane) const {
+        const uint32_t dst = smem_u32(to);
+        const T* src = base + kc * GLR_CHUNK * ld + c0;
+        if (whole && wide) {
+            const T* at = src + mine;
+            const uint32_t here = dst + lane / S * PITCH + lane % S * 16;
 #pragma unroll
             for (int j = 0; j < SUB / R; ++j, at += R * ld)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(mine + j * R * PITCH), "l"(at) : "memory");
-        } else {
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(here + j * R * PITCH), "l"(at) : "memory");
+            return;
+        }
+        const int nt = (int)min((int64_t)SUB, max((int64_t)0, T0));  // this warp's tokens
+        if (wide) {
 #pragma unroll 1
-            for (int j = 0; j < SUB / R; ++j, at += R * ld) {
-                const int row = j * R + row0;
+            for (int j = 0; j < SUB / R; ++j) {
+                const int row = j * R + lane / S, e = lane % S * E;
                 const bool there = row >= skip && row < nt && e < cols;
-                copy_async<16>(mine + j * R * PITCH, there ? at : somewhere, there);
+                copy_async<16>(dst + row * PITCH + lane % S * 16, there ? src + row * ld + e : safe, there);
+            }
+        } else {
+#pragma unroll 4
+            for (int row = 0; row < SUB; ++row) {
+                const bool there = row >= skip && row < nt && 2 * lane < cols;
+                copy_async<2 * sizeof(T)>(dst + row * PITCH + 2 * lane * sizeof(T), there ? src + row * ld + 2 * lane : safe, there);
             }
         }
-    } else {
-#pragma unroll 4
-        for (int row = 0; row < SUB; ++row) {
-            const bool there = row >= skip && row < nt && 2 * lane < cols;
-            copy_async<2 * sizeof(T)>(dst + row * PITCH + 2 * lane * sizeof(T), there ? src + row * ld + 2 * lane : somewhere,
-                                      there);
-        }
     }
-}
+};
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void copies_wait() {  // all but the N most recent groups of this thread, then of its warp

@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     if (w >= BWD_WARPS) {
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
         // tile j's sums are added before place j + 4 is signalled, and written again only after that
-        auto add_sums = [&](int2 tick, int j) {
+        auto add_sums = [&](int4 tick, int j) {
             const int c = tick.y + 2 * lane;
             if (GATE != GLR_SOFTPLUS || c >= p.C) return;
             float4 v = tl.sums[j % 3][0][lane];
@@ -57,51 +57,49 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             }
             p.sums[(int64_t)tick.x * ld + c / 2] = v;
         };
-        int2 tick;
+        int4 tick;
         for (int j = w - BWD_WARPS; glr_exchange<true>(p, ring, runs, chunks, j, lane, tick, add_sums); j += 4) {}
         return;
     }
     const int pos = BWD_WARPS - 1 - w;  // this warp's place in the order of the scan
 
+    constexpr int XP = GLR_TILE * sizeof(TX);
+    const GlrRows<SUB, 256, TG> g_rows(p.g, p.ldg, i0, lane);
+    const GlrRows<SUB, XP, TX> dh_rows(p.dh, p.C, i0, lane), h_rows(p.h_in, p.C, i0 - 1, lane), x_rows(p.x, p.ldx, i0, lane);
+    const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's g and dh of tile j
         glr_wait(p, ring, GLR_TICK, j);
-        const int2 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 3];
         if (tick.x >= 0) {
-            const int64_t t = (int64_t)(chunks - 1 - tick.x) * GLR_CHUNK + i0;
-            const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t)), cols = p.C - tick.y;
-            const TX* dh = static_cast<const TX*>(p.dh);
-            const TG* g = static_cast<const TG*>(p.g);
-            glr_copy_rows<SUB, 256>(&tl.t[j % 3][w][0][0], g + t * p.ldg + tick.y, p.ldg, 0, nt, cols, p.wide, lane, g);
-            glr_copy_rows<SUB, GLR_TILE * sizeof(TX)>(&tl.dh[j % 3][w][0][0], dh + t * p.C + tick.y, p.C, 0, nt, cols, p.wide, lane, dh);
+            const int kc = chunks - 1 - tick.x;
+            const int64_t left = p.T - ((int64_t)kc * GLR_CHUNK + i0);
+            g_rows.copy(&tl.t[j % 3][w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
+            dh_rows.copy(&tl.dh[j % 3][w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
         }
         copies_commit();
     };
-    auto copy_h = [&](int2 tick) {  // its h and x
+    auto copy_h = [&](int4 tick) {  // its h, of the token before each, and x
         if (tick.x >= 0) {
-            const int64_t t = (int64_t)(chunks - 1 - tick.x) * GLR_CHUNK + i0;
-            const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t)), cols = p.C - tick.y;
-            const TX* h = static_cast<const TX*>(p.h_in);
-            glr_copy_rows<SUB, GLR_TILE * sizeof(TX)>(&tl.h[w][0][0], h + (t - 1) * p.C + tick.y, p.C, t == 0, nt, cols, p.wide, lane, h);
-            if (COMP) {
-                const TX* x = static_cast<const TX*>(p.x);
-                glr_copy_rows<SUB, GLR_TILE * sizeof(TX)>(&tl.x[w][0][0], x + t * p.ldx + tick.y, p.ldx, 0, nt, cols, p.wide, lane, x);
-            }
+            const int kc = chunks - 1 - tick.x;
+            const int64_t left = p.T - ((int64_t)kc * GLR_CHUNK + i0);
+            h_rows.copy(&tl.h[w][0][0], kc, tick.y, tick.z, wide, kc == 0 && w == 0, left, p.C - tick.y, lane);
+            if (COMP) x_rows.copy(&tl.x[w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
         }
         copies_commit();
     };
     const bool takes = w == 0 && lane == 0;  // the tickets
     for (int j = 0; j < 3; ++j) {
         if (w == 0) {
-            if (takes) glr_set_tick(ring, j, glr_ticket(p, chunks, j), tiles, all);
+            if (takes) glr_set_tick<true>(p, ring, chunks, j, glr_ticket(p, chunks, j), tiles, all);
             glr_signal(ring, GLR_TICK, j);
         }
         if (j < 2) copy(j);
         if (j == 0) copies_commit();  // (an h of no tile, so that every tile waits for the same number of groups)
     }
-    int2 before = make_int2(-1, 0);  // tile j - 1
+    int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
         glr_wait(p, ring, GLR_PLACE, j);
-        const int2 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 3];
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             glr_signal(ring, GLR_FREE, j - 1);
         }
         if (w == 0) {
-            if (takes) glr_set_tick(ring, j + 3, tick.x < 0 ? all : id, tiles, all);
+            if (takes) glr_set_tick<true>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
             glr_signal(ring, GLR_TICK, j + 3);
         }
         if (tick.x < 0) break;

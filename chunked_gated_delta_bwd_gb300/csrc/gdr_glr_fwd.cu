@@ -37,36 +37,36 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     glr_ring_init(ring);
     if (w >= FWD_WARPS) {
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
-        int2 tick;
-        for (int j = w - FWD_WARPS; glr_exchange<false>(p, ring, runs, chunks, j, lane, tick, [](int2, int) {}); j += 4) {}
+        int4 tick;
+        for (int j = w - FWD_WARPS; glr_exchange<false>(p, ring, runs, chunks, j, lane, tick, [](int4, int) {}); j += 4) {}
         return;
     }
 
+    const GlrRows<SUB, 256, TG> g_rows(p.g, p.ldg, i0, lane);
+    const GlrRows<SUB, GLR_TILE * sizeof(TX), TX> x_rows(p.x, p.ldx, i0, lane);
+    const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's tokens of tile j
         glr_wait(p, ring, GLR_TICK, j);
-        const int2 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 3];
         if (tick.x >= 0) {
-            const int64_t t = (int64_t)tick.x * GLR_CHUNK + i0;
-            const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t)), cols = p.C - tick.y;
-            const TX* x = static_cast<const TX*>(p.x);
-            const TG* g = static_cast<const TG*>(p.g);
-            glr_copy_rows<SUB, 256>(&tl.a[j % 3][w][0][0], g + t * p.ldg + tick.y, p.ldg, 0, nt, cols, p.wide, lane, g);
-            glr_copy_rows<SUB, GLR_TILE * sizeof(TX)>(&tl.x[j % 3][w][0][0], x + t * p.ldx + tick.y, p.ldx, 0, nt, cols, p.wide, lane, x);
+            const int64_t left = p.T - ((int64_t)tick.x * GLR_CHUNK + i0);
+            g_rows.copy(&tl.a[j % 3][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
+            x_rows.copy(&tl.x[j % 3][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
         }
         copies_commit();
     };
     const bool takes = w == 0 && lane == 0;  // the tickets
     for (int j = 0; j < 3; ++j) {
         if (w == 0) {
-            if (takes) glr_set_tick(ring, j, glr_ticket(p, chunks, j), tiles, all);
+            if (takes) glr_set_tick<false>(p, ring, chunks, j, glr_ticket(p, chunks, j), tiles, all);
             glr_signal(ring, GLR_TICK, j);
         }
         if (j < 2) copy(j);
     }
-    int2 before = make_int2(-1, 0);  // tile j - 1
+    int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
         glr_wait(p, ring, GLR_PLACE, j);
-        const int2 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 3];
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
             glr_signal(ring, GLR_FREE, j - 1);
         }
         if (w == 0) {
-            if (takes) glr_set_tick(ring, j + 3, tick.x < 0 ? all : id, tiles, all);
+            if (takes) glr_set_tick<false>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
             glr_signal(ring, GLR_TICK, j + 3);
         }
         if (tick.x < 0) break;
