@@ -74,11 +74,18 @@ __device__ __forceinline__ void decay(float2 t, float2& a, float2& s) {  // s = 
     s = __ffma2_rn(__fmul2_rn(scale, m), splat(-1.f), __ffma2_rn(scale, splat(-1.f), splat(1.f)));
 }
 
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_ftz(float x) {  // (a result below 2^-126 is zero)
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // softplus(z) = max(z, 0) + log(1 + y), y = e^{-|z|} in (0, 1]; log(1 + y) = y p(y) with the
 // polynomial p of degree 8 of the least relative error on [0, 1] (3e-8, fitted likewise), which
 // keeps the relative accuracy of the slow channels' small softplus.  Returns y too.
 __device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
-    y = make_float2(__expf(-fabsf(z.x)), __expf(-fabsf(z.y)));
+    y = make_float2(exp2_ftz(-kLog2e * fabsf(z.x)), exp2_ftz(-kLog2e * fabsf(z.y)));
     float2 q = __ffma2_rn(y, splat(5.2326238e-3f), splat(-2.9504957e-2f));
     q = __ffma2_rn(y, q, splat(7.8225493e-2f));
     q = __ffma2_rn(y, q, splat(-1.3663207e-1f));
@@ -92,7 +99,6 @@ __device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
 
 // the gate of two channels: its parameters, the base-2 log gate of raw values, and what a
 // gradient of g is multiplied by to give that of the raw value
-constexpr float kLog2e = 1.4426950408889634f;
 template <int GATE>
 struct GlrGate {
     float2 nA, bias, inv;  // -e^{A_log}, dt_bias, e^{-A_log} (0 where the gate is shut)
@@ -143,8 +149,8 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 //
 // Blocks stay resident and take tiles by ticket, chunks in the order of the scan: a tile waits
 // only for tiles with earlier tickets, which are being worked on.  A block's compute warps walk
-// tile j for its run, then tile j - 1 for its results, each warp on rows that it copied itself,
-// two tiles ahead; four exchange warps, one for every fourth tile, publish and gather in between
+// tile j for its run, then tile j - LATE for its results, each warp on rows that it copied
+// itself, two tiles ahead; four exchange warps, one for every fourth tile, publish and gather in between
 // (GlrRing).  So neither the loads nor the way to the other blocks and back is waited for, and
 // what a tile costs besides its tokens does not fall to the warps that work on them.
 //
@@ -389,38 +395,49 @@ __device__ __forceinline__ void glr_empty_sequences(const GlrParams& p, const fl
 }
 
 // The ring through which a block's warps hand tiles to each other; tile j of the block uses slot
-// j % 4, or j % 2 of what is only needed from its first walk to its second (which comes after the
-// first one of tile j + 1).  CW compute warps, 4 exchange warps.
+// j % 4, or j % (LATE + 1) of what is only needed from its first walk to its second, which comes
+// after the first one of tile j + LATE.  CW compute warps, 4 exchange warps.
 //   tick:  the tile's chunk and channels are known (compute warp 0 takes the tickets, in order)
 //   place: its sequences and place are known (exchange warp)
-//   runs:  the warps' runs are there (compute warps)
 //   state: the states before each warp's tokens are there (exchange warp)
 //   free:  the results are written; the slot may be used for tile j + 4 (compute warps)
-template <int CW>
+// and, as a named barrier (an exchange warp waits for it most of its time, which costs no
+// instructions there),
+//   runs:  the warps' runs are there (compute warps)
+template <int CW_, int LATE_>
 struct GlrRing {
-    uint4 sub[2][CW][32];       // the warps' runs, in the order of the scan; then the states before them
+    static constexpr int CW = CW_, LATE = LATE_;
+    uint4 sub[LATE + 1][CW][32];  // the warps' runs, in the order of the scan; then the states before them
     GlrInfo info[4];
-    int4 tick[4];               // the tile's chunk in the order of the scan (-1: no more), first channel, whether it is whole
-    uint64_t bar[5][4];
+    int4 tick[8];               // (j % 8) the tile's chunk in the order of the scan (-1: no more), first channel, whether it is whole
+    uint64_t bar[4][4];
 };
-enum { GLR_TICK = 0, GLR_PLACE = 1, GLR_RUNS = 2, GLR_STATE = 3, GLR_FREE = 4 };
+enum { GLR_TICK = 0, GLR_PLACE = 1, GLR_STATE = 2, GLR_FREE = 3 };
+template <class Ring>
+__device__ __forceinline__ void glr_runs_there(int j) {
+    tc::named_arrive(1 + (j & 3), 32 * (Ring::CW + 1));
+}
+template <class Ring>
+__device__ __forceinline__ void glr_runs_wait(int j) {
+    tc::named_sync(1 + (j & 3), 32 * (Ring::CW + 1));
+}
 
-template <int CW>
-__device__ __forceinline__ void glr_ring_init(GlrRing<CW>& ring) {
-    if (threadIdx.x < 20) {
+template <class Ring>
+__device__ __forceinline__ void glr_ring_init(Ring& ring) {
+    if (threadIdx.x < 16) {
         const int kind = threadIdx.x / 4;
-        tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]), kind == GLR_RUNS || kind == GLR_FREE ? CW : 1);
+        tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]), kind == GLR_FREE ? Ring::CW : 1);
     }
     __syncthreads();
 }
 // Waits for tile j's barrier.  (Every barrier is reached: what its warp waits for elsewhere is bounded.)
-template <int CW>
-__device__ __forceinline__ void glr_wait(const GlrParams& p, GlrRing<CW>& ring, int kind, int j) {
+template <class Ring>
+__device__ __forceinline__ void glr_wait(const GlrParams& p, Ring& ring, int kind, int j) {
     if (!tc::mbar_wait(smem_u32(&ring.bar[kind][j & 3]), (j >> 2) & 1, 1 << 18)) atomicOr(p.status, ST_MMA_TIMEOUT);
 }
 // What this warp has written for tile j is there.
-template <int CW>
-__device__ __forceinline__ void glr_signal(GlrRing<CW>& ring, int kind, int j) {
+template <class Ring>
+__device__ __forceinline__ void glr_signal(Ring& ring, int kind, int j) {
     __syncwarp();
     if (threadIdx.x % 32 == 0)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(&ring.bar[kind][j & 3])) : "memory");
@@ -431,28 +448,29 @@ __device__ __forceinline__ void glr_signal(GlrRing<CW>& ring, int kind, int j) {
 __device__ __forceinline__ unsigned glr_ticket(const GlrParams& p, int chunks, int j) {
     return chunks == 1 ? blockIdx.x + j * gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
 }
-template <bool BWD, int CW>
-__device__ __forceinline__ void glr_set_tick(const GlrParams& p, GlrRing<CW>& ring, int chunks, int j, unsigned id, unsigned tiles,
+template <bool BWD, class Ring>
+__device__ __forceinline__ void glr_set_tick(const GlrParams& p, Ring& ring, int chunks, int j, unsigned id, unsigned tiles,
                                              unsigned all) {
     const unsigned k = id / tiles, c0 = (id - k * tiles) * GLR_TILE;
     const unsigned kc = BWD ? chunks - 1 - k : k;
-    ring.tick[j & 3] = make_int4(id < all ? (int)k : -1, (int)c0,
+    ring.tick[j & 7] = make_int4(id < all ? (int)k : -1, (int)c0,
                                  ((int64_t)kc + 1) * GLR_CHUNK <= p.T && (int)c0 + GLR_TILE <= p.C && !(BWD && kc == 0), 0);
 }
 
 // One exchange warp's work on tile j: its place; its run, published; the states before its warps.
 // `done` is called with the chunk and first channel of tile j - 4 once that is finished.  Returns
 // false when there are no more tiles.
-template <bool BWD, int CW, class F>
-__device__ __forceinline__ bool glr_exchange(const GlrParams& p, GlrRing<CW>& ring, const GlrRuns& runs, int chunks, int j, int lane,
+template <bool BWD, class Ring, class F>
+__device__ __forceinline__ bool glr_exchange(const GlrParams& p, Ring& ring, const GlrRuns& runs, int chunks, int j, int lane,
                                              int4& tick, const F& done) {
-    const int slot = j & 3, half = j & 1;
+    constexpr int CW = Ring::CW;
+    const int slot = j & 3, half = j % (Ring::LATE + 1);
     if (j >= 4) {
         glr_wait(p, ring, GLR_FREE, j - 4);
         done(tick, j - 4);
     }
     glr_wait(p, ring, GLR_TICK, j);
-    tick = ring.tick[slot];
+    tick = ring.tick[j & 7];
     const int k = tick.x;
     GlrInfo& at = ring.info[slot];
     if (k < 0) {
@@ -465,7 +483,7 @@ __device__ __forceinline__ bool glr_exchange(const GlrParams& p, GlrRing<CW>& ri
     glr_find_place<BWD>(p, at, chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
     glr_signal(ring, GLR_PLACE, j);
     glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, live, tick.y == 0);
-    glr_wait(p, ring, GLR_RUNS, j);
+    glr_runs_wait<Ring>(j);
     const bool any = at.any;
     Run y = run_identity();
     if (chunks > 1 && live) {

@@ -25,7 +25,7 @@ struct GlrBwdTile {
     TX h[BWD_WARPS][BWD_SUB][GLR_TILE];     // of the token before
     TX x[COMP ? BWD_WARPS : 1][COMP ? BWD_SUB : 1][GLR_TILE];
     float4 sums[SUMS ? 3 : 1][BWD_WARPS][32];  // of each warp's tokens, for the softplus gate's parameters
-    GlrRing<BWD_WARPS> ring;
+    GlrRing<BWD_WARPS, 1> ring;
 };
 
 template <class TX, class TG, int GATE, bool COMP>
@@ -38,7 +38,8 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     using RG = typename PG::raw;
     extern __shared__ __align__(16) unsigned char smem[];
     Tile& tl = *reinterpret_cast<Tile*>(smem);
-    GlrRing<BWD_WARPS>& ring = tl.ring;
+    using Ring = decltype(Tile::ring);
+    Ring& ring = tl.ring;
     const int chunks = glr_chunks(p);
     const unsigned tiles = (p.C + GLR_TILE - 1) / GLR_TILE, all = tiles * chunks;
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, i0 = w * SUB, ld = p.C / 2;
@@ -69,7 +70,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's g and dh of tile j
         glr_wait(p, ring, GLR_TICK, j);
-        const int4 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 7];
         if (tick.x >= 0) {
             const int kc = chunks - 1 - tick.x;
             const int64_t left = p.T - ((int64_t)kc * GLR_CHUNK + i0);
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
         glr_wait(p, ring, GLR_PLACE, j);
-        const int4 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 7];
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
                 }
             }
             ring.sub[j & 1][pos][lane] = run_bits(r);
-            glr_signal(ring, GLR_RUNS, j);
+            glr_runs_there<Ring>(j);
         }
         if (before.x >= 0) {
             const int kc = chunks - 1 - before.x, c = before.y + 2 * lane;

@@ -16,9 +16,10 @@ size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunk
 constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS;
 template <class TX>
 struct GlrFwdTile {
-    float2 a[3][FWD_WARPS][FWD_SUB][32];    // g as copied (a row in the first bytes of its 256), then the decays
-    TX x[3][FWD_WARPS][FWD_SUB][GLR_TILE];
-    GlrRing<FWD_WARPS> ring;
+    static constexpr int LATE = 2, SLOTS = LATE + 2;
+    float2 a[SLOTS][FWD_WARPS][FWD_SUB][32];    // g as copied (a row in the first bytes of its 256), then the decays
+    TX x[SLOTS][FWD_WARPS][FWD_SUB][GLR_TILE];
+    GlrRing<FWD_WARPS, LATE> ring;
 };
 
 template <class TX, class TG, int GATE, bool COMP>
@@ -29,8 +30,11 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     using RX = typename PX::raw;
     using RG = typename PG::raw;
     extern __shared__ __align__(16) unsigned char smem[];
-    GlrFwdTile<TX>& tl = *reinterpret_cast<GlrFwdTile<TX>*>(smem);
-    GlrRing<FWD_WARPS>& ring = tl.ring;
+    using Tile = GlrFwdTile<TX>;
+    using Ring = decltype(Tile::ring);
+    constexpr int LATE = Tile::LATE, SLOTS = Tile::SLOTS;
+    Tile& tl = *reinterpret_cast<Tile*>(smem);
+    Ring& ring = tl.ring;
     const int chunks = glr_chunks(p);
     const unsigned tiles = (p.C + GLR_TILE - 1) / GLR_TILE, all = tiles * chunks;
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, i0 = w * SUB, ld = p.C / 2;
@@ -47,11 +51,11 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's tokens of tile j
         glr_wait(p, ring, GLR_TICK, j);
-        const int4 tick = ring.tick[j & 3];
+        const int4 tick = ring.tick[j & 7];
         if (tick.x >= 0) {
             const int64_t left = p.T - ((int64_t)tick.x * GLR_CHUNK + i0);
-            g_rows.copy(&tl.a[j % 3][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
-            x_rows.copy(&tl.x[j % 3][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
+            g_rows.copy(&tl.a[j % SLOTS][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
+            x_rows.copy(&tl.x[j % SLOTS][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
         }
         copies_commit();
     };
@@ -63,10 +67,16 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
         }
         if (j < 2) copy(j);
     }
-    int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
+    int4 before[LATE];  // tiles j - LATE .. j - 1
+#pragma unroll
+    for (int i = 0; i < LATE; ++i) before[i] = make_int4(-1, 0, 0, 0);
+    int4 tick = make_int4(0, 0, 0, 0);
     for (int j = 0;; ++j) {
-        glr_wait(p, ring, GLR_PLACE, j);
-        const int4 tick = ring.tick[j & 3];
+        const bool more = tick.x >= 0;  // (past the last tile only second walks are left)
+        if (more) {
+            glr_wait(p, ring, GLR_PLACE, j);
+            tick = ring.tick[j & 7];
+        }
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
@@ -76,9 +86,9 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
             GlrGate<GATE> gate;
             gate.load(p.A_log, p.dt_bias, live ? c : 0);
             copies_wait<1>();
-            const TX* xs = &tl.x[j % 3][w][0][2 * lane];
-            float2* as = &tl.a[j % 3][w][0][lane];
-            const TG* gs = reinterpret_cast<const TG*>(&tl.a[j % 3][w][0][0]) + 2 * lane;
+            const TX* xs = &tl.x[j % SLOTS][w][0][2 * lane];
+            float2* as = &tl.a[j % SLOTS][w][0][lane];
+            const TG* gs = reinterpret_cast<const TG*>(&tl.a[j % SLOTS][w][0][0]) + 2 * lane;
             constexpr int GP = 256 / sizeof(TG);
             Run r = run_identity();
             if (!info.any) {
@@ -119,19 +129,19 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
                     r.H = glr_update<COMP>(a, r.H, PX::widen(*reinterpret_cast<const RX*>(xs + i * GLR_TILE)));
                 }
             }
-            ring.sub[j & 1][w][lane] = run_bits(r);
-            glr_signal(ring, GLR_RUNS, j);
+            ring.sub[j % (LATE + 1)][w][lane] = run_bits(r);
+            glr_runs_there<Ring>(j);
         }
-        if (before.x >= 0) {
-            glr_wait(p, ring, GLR_STATE, j - 1);
-            const GlrInfo& info = ring.info[(j - 1) & 3];
-            const int c = before.y + 2 * lane;
+        if (before[0].x >= 0) {
+            glr_wait(p, ring, GLR_STATE, j - LATE);
+            const GlrInfo& info = ring.info[(j - LATE) & 3];
+            const int c = before[0].y + 2 * lane;
             const bool live = c < p.C;
-            const int64_t t = (int64_t)before.x * GLR_CHUNK + i0;
+            const int64_t t = (int64_t)before[0].x * GLR_CHUNK + i0;
             RX* h = reinterpret_cast<RX*>(static_cast<TX*>(p.h) + t * p.C + c);
-            const TX* xs = &tl.x[(j - 1) % 3][w][0][2 * lane];
-            const float2* as = &tl.a[(j - 1) % 3][w][0][lane];
-            float2 y = *reinterpret_cast<const float2*>(&ring.sub[(j - 1) & 1][w][lane]);
+            const TX* xs = &tl.x[(j - LATE) % SLOTS][w][0][2 * lane];
+            const float2* as = &tl.a[(j - LATE) % SLOTS][w][0][lane];
+            float2 y = *reinterpret_cast<const float2*>(&ring.sub[(j - LATE) % (LATE + 1)][w][lane]);
             if (!info.any) {
 #pragma unroll 1
                 for (int i = 0; i < SUB; i += 4) {
@@ -157,15 +167,22 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
                     }
                 }
             }
-            glr_signal(ring, GLR_FREE, j - 1);
+            glr_signal(ring, GLR_FREE, j - LATE);
         }
-        if (w == 0) {
-            if (takes) glr_set_tick<false>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
-            glr_signal(ring, GLR_TICK, j + 3);
+        if (more) {
+            if (w == 0) {
+                if (takes) glr_set_tick<false>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
+                glr_signal(ring, GLR_TICK, j + 3);
+            }
+            if (tick.x >= 0) copy(j + 2);
         }
-        if (tick.x < 0) break;
-        copy(j + 2);
-        before = tick;
+#pragma unroll
+        for (int i = 0; i + 1 < LATE; ++i) before[i] = before[i + 1];
+        before[LATE - 1] = tick;
+        bool left = tick.x >= 0;
+#pragma unroll
+        for (int i = 0; i < LATE; ++i) left |= before[i].x >= 0;
+        if (!left) break;
     }
     copies_wait<0>();
 }
