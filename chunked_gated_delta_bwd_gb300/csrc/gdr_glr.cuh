@@ -102,12 +102,17 @@ __device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
 template <int GATE>
 struct GlrGate {
     float2 nA, bias, inv;  // -e^{A_log}, dt_bias, e^{-A_log} (0 where the gate is shut)
+    __device__ __forceinline__ void set(float4 v) {
+        if constexpr (GATE == GLR_SOFTPLUS) {
+            nA = make_float2(v.x, v.y);
+            bias = make_float2(v.z, v.w);
+            inv = make_float2(v.x < -1e-30f ? __fdividef(-1.f, v.x) : 0.f, v.y < -1e-30f ? __fdividef(-1.f, v.y) : 0.f);
+        }
+    }
     __device__ __forceinline__ void load(const float* A_log, const float* dt_bias, int c) {
         if constexpr (GATE == GLR_SOFTPLUS) {
-            const float2 l = *reinterpret_cast<const float2*>(A_log + c);
-            nA = make_float2(-expf(l.x), -expf(l.y));
-            bias = *reinterpret_cast<const float2*>(dt_bias + c);
-            inv = make_float2(nA.x < -1e-30f ? -1.f / nA.x : 0.f, nA.y < -1e-30f ? -1.f / nA.y : 0.f);
+            const float2 l = *reinterpret_cast<const float2*>(A_log + c), b = *reinterpret_cast<const float2*>(dt_bias + c);
+            set(make_float4(-expf(l.x), -expf(l.y), b.x, b.y));
         }
     }
     __device__ __forceinline__ float2 log2_gate(float2 raw) const {
@@ -408,7 +413,8 @@ template <int CW_, int LATE_>
 struct GlrRing {
     static constexpr int CW = CW_, LATE = LATE_;
     uint4 sub[LATE + 1][CW][32];  // the warps' runs, in the order of the scan; then the states before them
-    GlrInfo info[4];
+    GlrInfo info[8];            // (j % 8)
+    float4 gate[4][32];         // the gate's parameters (softplus), as GlrGate wants them
     int4 tick[8];               // (j % 8) the tile's chunk in the order of the scan (-1: no more), first channel, whether it is whole
     uint64_t bar[4][4];
 };
@@ -430,10 +436,23 @@ __device__ __forceinline__ void glr_ring_init(Ring& ring) {
     }
     __syncthreads();
 }
-// Waits for tile j's barrier.  (Every barrier is reached: what its warp waits for elsewhere is bounded.)
-template <class Ring>
+// Waits for tile j's barrier.  (Every barrier is reached: what its warp waits for elsewhere is
+// bounded.)  NAP: nanoseconds of sleep between polls, for waits that are long and not urgent: the
+// exchange warps' polls took a quarter of the kernel's instructions.
+template <int NAP, class Ring>
 __device__ __forceinline__ void glr_wait(const GlrParams& p, Ring& ring, int kind, int j) {
-    if (!tc::mbar_wait(smem_u32(&ring.bar[kind][j & 3]), (j >> 2) & 1, 1 << 18)) atomicOr(p.status, ST_MMA_TIMEOUT);
+    const uint32_t bar = smem_u32(&ring.bar[kind][j & 3]), parity = (j >> 2) & 1;
+    if (NAP == 0) {
+        if (!tc::mbar_wait(bar, parity, 1 << 22)) atomicOr(p.status, ST_MMA_TIMEOUT);
+    } else {
+        bool there = false;
+#pragma unroll 1
+        for (int it = 0; it < 1 << 20 && !there; ++it) {
+            there = tc::mbar_wait(bar, parity, 1);
+            if (!there) __nanosleep(NAP);
+        }
+        if (!there) atomicOr(p.status, ST_MMA_TIMEOUT);
+    }
 }
 // What this warp has written for tile j is there.
 template <class Ring>
@@ -457,36 +476,39 @@ __device__ __forceinline__ void glr_set_tick(const GlrParams& p, Ring& ring, int
                                  ((int64_t)kc + 1) * GLR_CHUNK <= p.T && (int)c0 + GLR_TILE <= p.C && !(BWD && kc == 0), 0);
 }
 
-// One exchange warp's work on tile j: its place; its run, published; the states before its warps.
-// `done` is called with the chunk and first channel of tile j - 4 once that is finished.  Returns
-// false when there are no more tiles.
-template <bool BWD, class Ring, class F>
-__device__ __forceinline__ bool glr_exchange(const GlrParams& p, Ring& ring, const GlrRuns& runs, int chunks, int j, int lane,
-                                             int4& tick, const F& done) {
-    constexpr int CW = Ring::CW;
-    const int slot = j & 3, half = j % (Ring::LATE + 1);
-    if (j >= 4) {
-        glr_wait(p, ring, GLR_FREE, j - 4);
-        done(tick, j - 4);
+// An exchange warp's work ahead on tile j: its sequences and place, the gate's parameters.  Returns
+// the tile's chunk and first channel (chunk -1: no more tiles).
+template <bool BWD, class Ring>
+__device__ __forceinline__ int4 glr_look(const GlrParams& p, Ring& ring, int chunks, int j, int lane) {
+    glr_wait<50>(p, ring, GLR_TICK, j);
+    const int4 tick = ring.tick[j & 7];
+    const int k = tick.x, kc = BWD ? chunks - 1 - k : k, c = tick.y + 2 * lane;
+    if (k >= 0) {
+        if (p.gate == GLR_SOFTPLUS) {
+            const int at = c < p.C ? c : 0;
+            const float2 l = *reinterpret_cast<const float2*>(p.A_log + at), b = *reinterpret_cast<const float2*>(p.dt_bias + at);
+            ring.gate[j & 3][lane] = make_float4(-expf(l.x), -expf(l.y), b.x, b.y);
+        }
+        const int64_t t0 = (int64_t)kc * GLR_CHUNK;
+        glr_find_place<BWD>(p, ring.info[j & 7], chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
     }
-    glr_wait(p, ring, GLR_TICK, j);
-    tick = ring.tick[j & 7];
-    const int k = tick.x;
-    GlrInfo& at = ring.info[slot];
-    if (k < 0) {
-        glr_signal(ring, GLR_PLACE, j);
-        return false;
-    }
-    const int kc = BWD ? chunks - 1 - k : k, c = tick.y + 2 * lane;
-    const bool live = c < p.C;
-    const int64_t t0 = (int64_t)kc * GLR_CHUNK, stride = p.C / 2;
-    glr_find_place<BWD>(p, at, chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
     glr_signal(ring, GLR_PLACE, j);
-    glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, live, tick.y == 0);
+    if (k >= 0) glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, c < p.C, tick.y == 0);
+    return tick;
+}
+
+// An exchange warp's work on tile j: its run, published; the states before its warps.
+template <bool BWD, class Ring>
+__device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, const GlrRuns& runs, int chunks, int j, int4 tick,
+                                             int lane) {
+    constexpr int CW = Ring::CW;
+    const int half = j % (Ring::LATE + 1), k = tick.x, c = tick.y + 2 * lane;
+    const int64_t stride = p.C / 2;
+    const GlrInfo& at = ring.info[j & 7];
     glr_runs_wait<Ring>(j);
     const bool any = at.any;
     Run y = run_identity();
-    if (chunks > 1 && live) {
+    if (chunks > 1 && c < p.C) {
         const int c2 = c / 2;
         Run own = run_from_bits(ring.sub[half][0][lane]);
 #pragma unroll
@@ -518,7 +540,6 @@ __device__ __forceinline__ bool glr_exchange(const GlrParams& p, Ring& ring, con
         y = any ? run_then(y, next) : run_then_plain(y, next);
     }
     glr_signal(ring, GLR_STATE, j);
-    return true;
 }
 
 // Asynchronous copies of a warp's rows [0, SUB) of 64 channels into shared memory: zeros from row

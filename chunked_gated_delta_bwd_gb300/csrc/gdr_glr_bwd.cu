@@ -58,8 +58,13 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             }
             p.sums[(int64_t)tick.x * ld + c / 2] = v;
         };
-        int4 tick;
-        for (int j = w - BWD_WARPS; glr_exchange<true>(p, ring, runs, chunks, j, lane, tick, add_sums); j += 4) {}
+        int4 tick = glr_look<true>(p, ring, chunks, w - BWD_WARPS, lane);
+        for (int j = w - BWD_WARPS; tick.x >= 0; j += 4) {
+            glr_exchange<true>(p, ring, runs, chunks, j, tick, lane);
+            glr_wait<50>(p, ring, GLR_FREE, j);
+            add_sums(tick, j);
+            tick = glr_look<true>(p, ring, chunks, j + 4, lane);
+        }
         return;
     }
     const int pos = BWD_WARPS - 1 - w;  // this warp's place in the order of the scan
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     const GlrRows<SUB, XP, TX> dh_rows(p.dh, p.C, i0, lane), h_rows(p.h_in, p.C, i0 - 1, lane), x_rows(p.x, p.ldx, i0, lane);
     const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's g and dh of tile j
-        glr_wait(p, ring, GLR_TICK, j);
+        glr_wait<0>(p, ring, GLR_TICK, j);
         const int4 tick = ring.tick[j & 7];
         if (tick.x >= 0) {
             const int kc = chunks - 1 - tick.x;
@@ -99,16 +104,16 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
     }
     int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
-        glr_wait(p, ring, GLR_PLACE, j);
+        glr_wait<0>(p, ring, GLR_PLACE, j);
         const int4 tick = ring.tick[j & 7];
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
-            const GlrInfo& info = ring.info[j & 3];
+            const GlrInfo& info = ring.info[j & 7];
             const int c = tick.y + 2 * lane;
             const bool live = c < p.C;
             GlrGate<GATE> gate;
-            gate.load(p.A_log, p.dt_bias, live ? c : 0);
+            gate.set(ring.gate[j & 3][lane]);
             copies_wait<2>();
             const TX* ds = &tl.dh[j % 3][w][0][2 * lane];
             float2* ts = &tl.t[j % 3][w][0][lane];
@@ -163,10 +168,10 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             const bool live = c < p.C;
             const int64_t t0 = (int64_t)kc * GLR_CHUNK + i0;
             GlrGate<GATE> gate;
-            gate.load(p.A_log, p.dt_bias, live ? c : 0);
+            gate.set(ring.gate[(j - 1) & 3][lane]);
             copies_wait<1>();
-            glr_wait(p, ring, GLR_STATE, j - 1);
-            const GlrInfo& info = ring.info[(j - 1) & 3];
+            glr_wait<0>(p, ring, GLR_STATE, j - 1);
+            const GlrInfo& info = ring.info[(j - 1) & 7];
             const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - t0)) : SUB;
             const TX* ds = &tl.dh[(j - 1) % 3][w][0][2 * lane];
             const TX* hs = &tl.h[w][0][2 * lane];

@@ -41,8 +41,14 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     glr_ring_init(ring);
     if (w >= FWD_WARPS) {
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
-        int4 tick;
-        for (int j = w - FWD_WARPS; glr_exchange<false>(p, ring, runs, chunks, j, lane, tick, [](int4, int) {}); j += 4) {}
+        // a tile's place is found as soon as the exchange four tiles before it is done: the slot it takes
+        // was tile j - 8's
+        int4 tick = glr_look<false>(p, ring, chunks, w - FWD_WARPS, lane);
+        for (int j = w - FWD_WARPS; tick.x >= 0; j += 4) {
+            if (j >= 4) glr_wait<50>(p, ring, GLR_FREE, j - 4);
+            glr_exchange<false>(p, ring, runs, chunks, j, tick, lane);
+            tick = glr_look<false>(p, ring, chunks, j + 4, lane);
+        }
         return;
     }
 
@@ -50,7 +56,7 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     const GlrRows<SUB, GLR_TILE * sizeof(TX), TX> x_rows(p.x, p.ldx, i0, lane);
     const bool wide = p.wide;
     auto copy = [&](int j) {  // this warp's tokens of tile j
-        glr_wait(p, ring, GLR_TICK, j);
+        glr_wait<0>(p, ring, GLR_TICK, j);
         const int4 tick = ring.tick[j & 7];
         if (tick.x >= 0) {
             const int64_t left = p.T - ((int64_t)tick.x * GLR_CHUNK + i0);
@@ -74,17 +80,17 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     for (int j = 0;; ++j) {
         const bool more = tick.x >= 0;  // (past the last tile only second walks are left)
         if (more) {
-            glr_wait(p, ring, GLR_PLACE, j);
+            glr_wait<0>(p, ring, GLR_PLACE, j);
             tick = ring.tick[j & 7];
         }
         unsigned id = 0;
         if (tick.x >= 0) {
             if (takes) id = glr_ticket(p, chunks, j + 3);
-            const GlrInfo& info = ring.info[j & 3];
+            const GlrInfo& info = ring.info[j & 7];
             const int c = tick.y + 2 * lane;
             const bool live = c < p.C;
             GlrGate<GATE> gate;
-            gate.load(p.A_log, p.dt_bias, live ? c : 0);
+            gate.set(ring.gate[j & 3][lane]);
             copies_wait<1>();
             const TX* xs = &tl.x[j % SLOTS][w][0][2 * lane];
             float2* as = &tl.a[j % SLOTS][w][0][lane];
@@ -133,8 +139,8 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
             glr_runs_there<Ring>(j);
         }
         if (before[0].x >= 0) {
-            glr_wait(p, ring, GLR_STATE, j - LATE);
-            const GlrInfo& info = ring.info[(j - LATE) & 3];
+            glr_wait<0>(p, ring, GLR_STATE, j - LATE);
+            const GlrInfo& info = ring.info[(j - LATE) & 7];
             const int c = before[0].y + 2 * lane;
             const bool live = c < p.C;
             const int64_t t = (int64_t)before[0].x * GLR_CHUNK + i0;
