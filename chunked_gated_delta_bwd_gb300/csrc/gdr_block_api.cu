@@ -80,7 +80,7 @@ static size_t glr_workspace(const GlrParams& p) { return 256 + glr_published_byt
 // whether rows of C elements at this stride are whole numbers of aligned 16-byte pieces
 static int rows_wide(const GlrParams& p, const void* at, int64_t ld, int f32) {
     const int piece = f32 ? 4 : 8;
-    return aligned16(at) && ld % piece == 0 && p.C % piece == 0;
+    return aligned16(at) && ld % piece == 0 && p.C % piece == 0 && p.T < ((int64_t)1 << 31);
 }
 
 // Checks and clears the workspace (a launch of one chunk writes its status word itself); every

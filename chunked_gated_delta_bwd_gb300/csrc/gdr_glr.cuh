@@ -10,6 +10,7 @@
 #include "gdr_common.cuh"
 #include "gdr_internal.h"
 #include "gdr_tc.cuh"
+#include "gdr_tma.h"
 
 namespace gdr {
 
@@ -154,10 +155,11 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 //
 // Blocks stay resident and take tiles by ticket, chunks in the order of the scan: a tile waits
 // only for tiles with earlier tickets, which are being worked on.  A block's compute warps walk
-// tile j for its run, then tile j - LATE for its results, each warp on rows that it copied
-// itself, two tiles ahead; four exchange warps, one for every fourth tile, publish and gather in between
+// tile j for its run, then tile j - LATE for its results.  One warp takes the tickets and copies
+// tiles ahead, three exchange warps, one for every third tile, publish and gather in between
 // (GlrRing).  So neither the loads nor the way to the other blocks and back is waited for, and
-// what a tile costs besides its tokens does not fall to the warps that work on them.
+// what a tile costs besides its tokens (half of the instructions, when each warp copied its own
+// rows) does not fall to the warps that work on them.
 //
 // A run that contains a restart does not depend on the state before it: its A is -0 (a product
 // of decays is +0 at least), and a fold that meets it takes H as it is, so that no infinity or
@@ -401,24 +403,32 @@ __device__ __forceinline__ void glr_empty_sequences(const GlrParams& p, const fl
 
 // The ring through which a block's warps hand tiles to each other; tile j of the block uses slot
 // j % 4, or j % (LATE + 1) of what is only needed from its first walk to its second, which comes
-// after the first one of tile j + LATE.  CW compute warps, 4 exchange warps.
-//   tick:  the tile's chunk and channels are known (compute warp 0 takes the tickets, in order)
-//   place: its sequences and place are known (exchange warp)
+// after the first one of tile j + LATE.  CW compute warps, GLR_X exchange warps, one copying warp.
+//   tick:  the tile's chunk and channels are known (copying warp)
+//   full:  its rows (copying warp), its sequences, place and gate (exchange warp) are there
+//   late:  rows that only the second walk needs are there (copying warp)
 //   state: the states before each warp's tokens are there (exchange warp)
-//   free:  the results are written; the slot may be used for tile j + 4 (compute warps)
+//   free:  the results are written; the tile's rows may be overwritten (compute warps)
 // and, as a named barrier (an exchange warp waits for it most of its time, which costs no
 // instructions there),
 //   runs:  the warps' runs are there (compute warps)
+constexpr int GLR_X = 3;
 template <int CW_, int LATE_>
 struct GlrRing {
-    static constexpr int CW = CW_, LATE = LATE_;
+    static constexpr int CW = CW_, LATE = LATE_, THREADS = 32 * (CW + GLR_X + 1);
     uint4 sub[LATE + 1][CW][32];  // the warps' runs, in the order of the scan; then the states before them
     GlrInfo info[8];            // (j % 8)
     float4 gate[4][32];         // the gate's parameters (softplus), as GlrGate wants them
-    int4 tick[8];               // (j % 8) the tile's chunk in the order of the scan (-1: no more), first channel, whether it is whole
-    uint64_t bar[4][4];
+    int4 tick[8];               // (j % 8) the tile's chunk in the order of the scan (-1: no more), first channel
+    uint64_t bar[6][4];         // (the ticks take two rows: the copying warp is up to eight tiles ahead of who reads them)
 };
-enum { GLR_TICK = 0, GLR_PLACE = 1, GLR_STATE = 2, GLR_FREE = 3 };
+enum { GLR_TICK = 0, GLR_FULL = 2, GLR_LATE = 3, GLR_STATE = 4, GLR_FREE = 5 };
+// tile j's barrier and its phase
+template <class Ring>
+__device__ __forceinline__ uint32_t glr_bar(Ring& ring, int kind, int j) {
+    return smem_u32(&ring.bar[kind][kind == GLR_TICK ? j & 7 : j & 3]);
+}
+__device__ __forceinline__ uint32_t glr_phase(int kind, int j) { return (kind == GLR_TICK ? j >> 3 : j >> 2) & 1; }
 template <class Ring>
 __device__ __forceinline__ void glr_runs_there(int j) {
     tc::named_arrive(1 + (j & 3), 32 * (Ring::CW + 1));
@@ -428,11 +438,14 @@ __device__ __forceinline__ void glr_runs_wait(int j) {
     tc::named_sync(1 + (j & 3), 32 * (Ring::CW + 1));
 }
 
+// (rows copied in 16-byte pieces arrive as a count of bytes that one lane announces, others as
+// every lane's own copies)
 template <class Ring>
-__device__ __forceinline__ void glr_ring_init(Ring& ring) {
-    if (threadIdx.x < 16) {
-        const int kind = threadIdx.x / 4;
-        tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]), kind == GLR_FREE ? Ring::CW : 1);
+__device__ __forceinline__ void glr_ring_init(Ring& ring, bool wide) {
+    if (threadIdx.x < 24) {
+        const int kind = threadIdx.x / 4, rows = wide ? 1 : 32;
+        tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]),
+                      kind == GLR_FREE ? Ring::CW : kind == GLR_FULL ? rows + 1 : kind == GLR_LATE ? rows : 1);
     }
     __syncthreads();
 }
@@ -441,7 +454,7 @@ __device__ __forceinline__ void glr_ring_init(Ring& ring) {
 // exchange warps' polls took a quarter of the kernel's instructions.
 template <int NAP, class Ring>
 __device__ __forceinline__ void glr_wait(const GlrParams& p, Ring& ring, int kind, int j) {
-    const uint32_t bar = smem_u32(&ring.bar[kind][j & 3]), parity = (j >> 2) & 1;
+    const uint32_t bar = glr_bar(ring, kind, j), parity = glr_phase(kind, j);
     if (NAP == 0) {
         if (!tc::mbar_wait(bar, parity, 1 << 22)) atomicOr(p.status, ST_MMA_TIMEOUT);
     } else {
@@ -459,7 +472,7 @@ template <class Ring>
 __device__ __forceinline__ void glr_signal(Ring& ring, int kind, int j) {
     __syncwarp();
     if (threadIdx.x % 32 == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_u32(&ring.bar[kind][j & 3])) : "memory");
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(glr_bar(ring, kind, j)) : "memory");
 }
 
 // A block's tickets, in the order of its tiles: they count in the workspace when there is something
@@ -467,15 +480,6 @@ __device__ __forceinline__ void glr_signal(Ring& ring, int kind, int j) {
 __device__ __forceinline__ unsigned glr_ticket(const GlrParams& p, int chunks, int j) {
     return chunks == 1 ? blockIdx.x + j * gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
 }
-template <bool BWD, class Ring>
-__device__ __forceinline__ void glr_set_tick(const GlrParams& p, Ring& ring, int chunks, int j, unsigned id, unsigned tiles,
-                                             unsigned all) {
-    const unsigned k = id / tiles, c0 = (id - k * tiles) * GLR_TILE;
-    const unsigned kc = BWD ? chunks - 1 - k : k;
-    ring.tick[j & 7] = make_int4(id < all ? (int)k : -1, (int)c0,
-                                 ((int64_t)kc + 1) * GLR_CHUNK <= p.T && (int)c0 + GLR_TILE <= p.C && !(BWD && kc == 0), 0);
-}
-
 // An exchange warp's work ahead on tile j: its sequences and place, the gate's parameters.  Returns
 // the tile's chunk and first channel (chunk -1: no more tiles).
 template <bool BWD, class Ring>
@@ -492,7 +496,7 @@ __device__ __forceinline__ int4 glr_look(const GlrParams& p, Ring& ring, int chu
         const int64_t t0 = (int64_t)kc * GLR_CHUNK;
         glr_find_place<BWD>(p, ring.info[j & 7], chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
     }
-    glr_signal(ring, GLR_PLACE, j);
+    glr_signal(ring, GLR_FULL, j);
     if (k >= 0) glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, c < p.C, tick.y == 0);
     return tick;
 }
@@ -542,71 +546,58 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
     glr_signal(ring, GLR_STATE, j);
 }
 
-// Asynchronous copies of a warp's rows [0, SUB) of 64 channels into shared memory: zeros from row
-// nt on, before row `skip` and past the `cols` channels there are.  16 bytes a copy where every
-// row of the call's tensors allows it (`wide`), else one pair of channels.  PITCH: bytes from row
-// to row in shared memory.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;\n" ::"r"(dst), "l"(src), "n"(BYTES), "r"(there ? BYTES : 0)
-                     : "memory");
-}
-template <int SUB, int PITCH, class T>
-struct GlrRows {
-    static constexpr int E = 16 / sizeof(T), S = GLR_TILE / E, R = 32 / S;  // elements a copy, copies a row, rows a pass
-    const T *base, *safe;  // this warp's first token of chunk 0; an address for copies of nothing
-    int64_t ld;
-    int64_t mine;    // this lane's place in a pass of 16-byte copies
-    __device__ __forceinline__ GlrRows(const void* base_, int64_t ld_, int i0, int lane) : ld(ld_) {
-        safe = static_cast<const T*>(base_);
-        base = safe + i0 * ld;
-        mine = lane / S * ld + lane % S * E;
-    }
-    // tokens of chunk kc; `whole`: all of the tile's rows and channels are there
-    __device__ __forceinline__ void copy(void* to, int64_t kc, int c0, bool whole, bool wide, int skip, int64_t T0, int cols,
-                                         int lane) const {
-        const uint32_t dst = smem_u32(to);
-        const T* src = base + kc * GLR_CHUNK * ld + c0;
-        if (whole && wide) {
-            const T* at = src + mine;
-            const uint32_t here = dst + lane / S * PITCH + lane % S * 16;
-#pragma unroll
-            for (int j = 0; j < SUB / R; ++j, at += R * ld)
-                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(here + j * R * PITCH), "l"(at) : "memory");
-            return;
-        }
-        const int nt = (int)min((int64_t)SUB, max((int64_t)0, T0));  // this warp's tokens
-        if (wide) {
-#pragma unroll 1
-            for (int j = 0; j < SUB / R; ++j) {
-                const int row = j * R + lane / S, e = lane % S * E;
-                const bool there = row >= skip && row < nt && e < cols;
-                copy_async<16>(dst + row * PITCH + lane % S * 16, there ? src + row * ld + e : safe, there);
-            }
-        } else {
-#pragma unroll 4
-            for (int row = 0; row < SUB; ++row) {
-                const bool there = row >= skip && row < nt && 2 * lane < cols;
-                copy_async<2 * sizeof(T)>(dst + row * PITCH + 2 * lane * sizeof(T), there ? src + row * ld + 2 * lane : safe, there);
-            }
-        }
-    }
+// The copying warp's copies of a tile's rows of one tensor into shared memory.  Where every row of
+// the call's tensors is a whole number of aligned 16-byte pieces (`wide`) they go by the tensor's
+// map, in boxes of 64 rows, or of 8 where the rows of different warps are to lie 8 x 256 bytes
+// apart; they report to the barrier by their bytes.  (A copy of each row by itself kept the copy
+// engine busy for longer than the rows took to arrive.)  Else a lane copies a pair of channels of
+// each row there is, and reports when all of its copies are done.
+// Rows of g lie in their warp's 8 x 256 bytes, which the first walk fills with fp32 values row by
+// row: float32 rows in place, bf16 rows in the half that the walk fills last.
+template <class TG>
+__host__ __device__ constexpr int glr_raw_offset(bool bwd) { return sizeof(TG) == 2 && !bwd ? 1024 : 0; }
+struct GlrMaps {
+    CUtensorMap g, x, dh, h;
 };
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;\n" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {  // all but the N most recent groups of this thread, then of its warp
-    asm volatile("cp.async.wait_group %0;\n" ::"n"(N) : "memory");
+// rows t0 .. t0 + 63 (the first `first` of them left out), channels from c0 on.  PITCH: bytes from
+// row to row in shared memory, EVERY: from 8 rows to the next 8.
+template <int PITCH, int EVERY, class T>
+__device__ __forceinline__ void glr_copy_rows(void* to, const CUtensorMap* map, const T* base, int64_t ld, int64_t t0, int first,
+                                              int rows, int c0, int cols, bool wide, uint32_t bar, int lane) {
+    const uint32_t dst = smem_u32(to);
+    if (wide) {
+        if (EVERY == 8 * PITCH) {
+            if (lane == 0) tc::tma_load_2d(dst, map, c0, (int)t0, bar);
+        } else if (lane < 8) {
+            tc::tma_load_2d(dst + lane * EVERY, map, c0, (int)t0 + 8 * lane, bar);
+        }
+    } else if (2 * lane < cols) {
+        const T* src = base + t0 * ld + c0 + 2 * lane;
+#pragma unroll 4
+        for (int i = first; i < rows; ++i)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(dst + i / 8 * EVERY + i % 8 * PITCH +
+                                                                           2 * lane * (int)sizeof(T)),
+                         "l"(src + i * ld), "n"(2 * sizeof(T))
+                         : "memory");
+    }
+}
+// Announces the bytes of tile j's rows (wide), before the copies; after them, the lane's arrival (not wide).
+template <class Ring>
+__device__ __forceinline__ uint32_t glr_announce(Ring& ring, int kind, int j, bool wide, uint32_t bytes, int lane) {
+    const uint32_t bar = glr_bar(ring, kind, j);
+    if (wide && lane == 0) tc::mbar_expect_tx(bar, bytes);
     __syncwarp();
+    return bar;
+}
+__device__ __forceinline__ void glr_report(uint32_t bar, bool wide) {
+    if (!wide) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
 // Launches a scan kernel on as many blocks as are resident at once (or tiles, if fewer).
 // `ready`: the devices whose shared-memory limit of this kernel is raised.
 template <class K>
 cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, int threads, size_t smem, int per_sm, const GlrParams& p,
-                       cudaStream_t s) {
+                       const GlrMaps& maps, cudaStream_t s) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -617,7 +608,7 @@ cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, int threads, size
         ready.fetch_or(bit, std::memory_order_relaxed);
     }
     const int64_t all = (int64_t)glr_chunks(p) * ((p.C + GLR_TILE - 1) / GLR_TILE), resident = (int64_t)per_sm * num_sms();
-    kernel<<<(unsigned)(all < resident ? all : resident), threads, smem, s>>>(p);
+    kernel<<<(unsigned)(all < resident ? all : resident), threads, smem, s>>>(p, maps);
     return cudaGetLastError();
 }
 

@@ -20,7 +20,7 @@ namespace gdr {
 constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS;
 template <class TX, bool COMP, bool SUMS>
 struct GlrBwdTile {
-    float2 t[3][BWD_WARPS][BWD_SUB][32];    // g as copied (a row in the first bytes of its 256), then the log gates
+    float2 t[3][BWD_WARPS][BWD_SUB][32];    // g as copied (glr_raw_offset), then the log gates
     TX dh[3][BWD_WARPS][BWD_SUB][GLR_TILE];
     TX h[BWD_WARPS][BWD_SUB][GLR_TILE];     // of the token before
     TX x[COMP ? BWD_WARPS : 1][COMP ? BWD_SUB : 1][GLR_TILE];
@@ -29,24 +29,62 @@ struct GlrBwdTile {
 };
 
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrParams p) {
+__global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
     using Tile = GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>;
     constexpr int SUB = BWD_SUB;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
     using RX = typename PX::raw;
     using RG = typename PG::raw;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int RAW = glr_raw_offset<TG>(true);
+    extern __shared__ __align__(128) unsigned char smem[];
     Tile& tl = *reinterpret_cast<Tile*>(smem);
     using Ring = decltype(Tile::ring);
     Ring& ring = tl.ring;
     const int chunks = glr_chunks(p);
     const unsigned tiles = (p.C + GLR_TILE - 1) / GLR_TILE, all = tiles * chunks;
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, i0 = w * SUB, ld = p.C / 2;
-    glr_ring_init(ring);
+    const bool wide = p.wide;
+    glr_ring_init(ring, wide);
+    if (w == BWD_WARPS + GLR_X) {  // tickets and copies: g and dh of tile j, then h and x of tile j - 2
+        constexpr int XP = GLR_TILE * sizeof(TX);
+        unsigned id = lane == 0 ? glr_ticket(p, chunks, 0) : 0;
+        int k1 = -1, c1 = 0, k2 = -1, c2 = 0;  // tiles j - 1, j - 2
+        for (int j = 0, over = 0; over < GLR_X; ++j) {
+            id = __shfl_sync(~0u, id, 0);
+            const unsigned next = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
+            const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
+            if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
+            glr_signal(ring, GLR_TICK, j);
+            if (j >= 3 && (k >= 0 || k2 >= 0)) glr_wait<20>(p, ring, GLR_FREE, j - 3);
+            if (k >= 0) {
+                const int64_t t0 = (int64_t)(chunks - 1 - k) * GLR_CHUNK;
+                const int rows = (int)min((int64_t)GLR_CHUNK, p.T - t0), cols = min(GLR_TILE, p.C - c0);
+                const uint32_t bar = glr_announce(ring, GLR_FULL, j, wide, GLR_CHUNK * GLR_TILE * (sizeof(TX) + sizeof(TG)), lane);
+                glr_copy_rows<GLR_TILE * sizeof(TG), 2048>(reinterpret_cast<char*>(&tl.t[j % 3]) + RAW, &maps.g,
+                                                           static_cast<const TG*>(p.g), p.ldg, t0, 0, rows, c0, cols, wide, bar, lane);
+                glr_copy_rows<XP, 8 * XP>(&tl.dh[j % 3], &maps.dh, static_cast<const TX*>(p.dh), p.C, t0, 0, rows, c0, cols, wide, bar, lane);
+                glr_report(bar, wide);
+            } else {
+                if (over++ == 0) glr_report(glr_announce(ring, GLR_FULL, j, wide, 0, lane), wide);
+            }
+            if (k2 >= 0) {
+                const int64_t t0 = (int64_t)(chunks - 1 - k2) * GLR_CHUNK;
+                const int rows = (int)min((int64_t)GLR_CHUNK, p.T - t0), cols = min(GLR_TILE, p.C - c2);
+                const uint32_t bar = glr_announce(ring, GLR_LATE, j - 2, wide, GLR_CHUNK * XP * (COMP ? 2 : 1), lane);
+                glr_copy_rows<XP, 8 * XP>(&tl.h, &maps.h, static_cast<const TX*>(p.h_in), p.C, t0 - 1, t0 == 0, rows, c2, cols, wide, bar, lane);
+                if (COMP)
+                    glr_copy_rows<XP, 8 * XP>(&tl.x, &maps.x, static_cast<const TX*>(p.x), p.ldx, t0, 0, rows, c2, cols, wide, bar, lane);
+                glr_report(bar, wide);
+            }
+            k2 = k1; c2 = c1; k1 = k; c1 = c0;
+            id = next;
+        }
+        return;
+    }
     if (w >= BWD_WARPS) {
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
-        // tile j's sums are added before place j + 4 is signalled, and written again only after that
+        // tile j's sums are added before tile j + 3 is looked at, and written again only after that
         auto add_sums = [&](int4 tick, int j) {
             const int c = tick.y + 2 * lane;
             if (GATE != GLR_SOFTPLUS || c >= p.C) return;
@@ -59,66 +97,30 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             p.sums[(int64_t)tick.x * ld + c / 2] = v;
         };
         int4 tick = glr_look<true>(p, ring, chunks, w - BWD_WARPS, lane);
-        for (int j = w - BWD_WARPS; tick.x >= 0; j += 4) {
+        for (int j = w - BWD_WARPS; tick.x >= 0; j += GLR_X) {
             glr_exchange<true>(p, ring, runs, chunks, j, tick, lane);
             glr_wait<50>(p, ring, GLR_FREE, j);
             add_sums(tick, j);
-            tick = glr_look<true>(p, ring, chunks, j + 4, lane);
+            tick = glr_look<true>(p, ring, chunks, j + GLR_X, lane);
         }
         return;
     }
     const int pos = BWD_WARPS - 1 - w;  // this warp's place in the order of the scan
 
-    constexpr int XP = GLR_TILE * sizeof(TX);
-    const GlrRows<SUB, 256, TG> g_rows(p.g, p.ldg, i0, lane);
-    const GlrRows<SUB, XP, TX> dh_rows(p.dh, p.C, i0, lane), h_rows(p.h_in, p.C, i0 - 1, lane), x_rows(p.x, p.ldx, i0, lane);
-    const bool wide = p.wide;
-    auto copy = [&](int j) {  // this warp's g and dh of tile j
-        glr_wait<0>(p, ring, GLR_TICK, j);
-        const int4 tick = ring.tick[j & 7];
-        if (tick.x >= 0) {
-            const int kc = chunks - 1 - tick.x;
-            const int64_t left = p.T - ((int64_t)kc * GLR_CHUNK + i0);
-            g_rows.copy(&tl.t[j % 3][w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
-            dh_rows.copy(&tl.dh[j % 3][w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
-        }
-        copies_commit();
-    };
-    auto copy_h = [&](int4 tick) {  // its h, of the token before each, and x
-        if (tick.x >= 0) {
-            const int kc = chunks - 1 - tick.x;
-            const int64_t left = p.T - ((int64_t)kc * GLR_CHUNK + i0);
-            h_rows.copy(&tl.h[w][0][0], kc, tick.y, tick.z, wide, kc == 0 && w == 0, left, p.C - tick.y, lane);
-            if (COMP) x_rows.copy(&tl.x[w][0][0], kc, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
-        }
-        copies_commit();
-    };
-    const bool takes = w == 0 && lane == 0;  // the tickets
-    for (int j = 0; j < 3; ++j) {
-        if (w == 0) {
-            if (takes) glr_set_tick<true>(p, ring, chunks, j, glr_ticket(p, chunks, j), tiles, all);
-            glr_signal(ring, GLR_TICK, j);
-        }
-        if (j < 2) copy(j);
-        if (j == 0) copies_commit();  // (an h of no tile, so that every tile waits for the same number of groups)
-    }
     int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
-        glr_wait<0>(p, ring, GLR_PLACE, j);
+        glr_wait<0>(p, ring, GLR_FULL, j);
         const int4 tick = ring.tick[j & 7];
-        unsigned id = 0;
         if (tick.x >= 0) {
-            if (takes) id = glr_ticket(p, chunks, j + 3);
             const GlrInfo& info = ring.info[j & 7];
             const int c = tick.y + 2 * lane;
             const bool live = c < p.C;
             GlrGate<GATE> gate;
             gate.set(ring.gate[j & 3][lane]);
-            copies_wait<2>();
             const TX* ds = &tl.dh[j % 3][w][0][2 * lane];
             float2* ts = &tl.t[j % 3][w][0][lane];
-            const TG* gs = reinterpret_cast<const TG*>(&tl.t[j % 3][w][0][0]) + 2 * lane;
-            constexpr int GP = 256 / sizeof(TG);
+            const TG* gs = reinterpret_cast<const TG*>(reinterpret_cast<char*>(&tl.t[j % 3][w]) + RAW) + 2 * lane;
+            constexpr int GP = GLR_TILE;
             Run r = run_identity();
             if (!info.any) {
 #pragma unroll 1
@@ -169,7 +171,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             const int64_t t0 = (int64_t)kc * GLR_CHUNK + i0;
             GlrGate<GATE> gate;
             gate.set(ring.gate[(j - 1) & 3][lane]);
-            copies_wait<1>();
+            glr_wait<0>(p, ring, GLR_LATE, j - 1);
             glr_wait<0>(p, ring, GLR_STATE, j - 1);
             const GlrInfo& info = ring.info[(j - 1) & 7];
             const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - t0)) : SUB;
@@ -222,18 +224,12 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + 4), 2) k_glr_bwd(const GlrPa
             }
             if (GATE == GLR_SOFTPLUS)
                 tl.sums[(j - 1) % 3][w][lane] = make_float4(kLn2f * sumA.x, kLn2f * sumA.y, sumB.x, sumB.y);
+            tc::fence_async_smem();  // (the next copy into these rows comes after the reads and writes above)
             glr_signal(ring, GLR_FREE, j - 1);
         }
-        if (w == 0) {
-            if (takes) glr_set_tick<true>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
-            glr_signal(ring, GLR_TICK, j + 3);
-        }
         if (tick.x < 0) break;
-        copy_h(tick);
-        copy(j + 2);
         before = tick;
     }
-    copies_wait<0>();
 }
 
 // dA_log and ddt_bias: the chunks' sums, added in a fixed order.  A block takes 32 pairs of
@@ -277,8 +273,14 @@ struct Launch {
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
         static std::atomic<uint64_t> ready{0};
-        cudaError_t e = glr_launch(k_glr_bwd<TX, TG, GATE, COMP>, ready, 32 * (BWD_WARPS + 4), sizeof(GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>), 2,
-                                   p, s);
+        GlrMaps maps;
+        if (p.wide && !(encode_plain_map(&maps.g, p.g, p.gate_f32, p.T, p.C, p.ldg, p.gate_f32 ? 64 : 8) &&
+                        encode_plain_map(&maps.dh, p.dh, p.act_f32, p.T, p.C, p.C, 64) &&
+                        encode_plain_map(&maps.h, p.h_in, p.act_f32, p.T, p.C, p.C, 64) &&
+                        (!COMP || encode_plain_map(&maps.x, p.x, p.act_f32, p.T, p.C, p.ldx, 64))))
+            return cudaErrorInvalidValue;
+        cudaError_t e = glr_launch(k_glr_bwd<TX, TG, GATE, COMP>, ready, 32 * (BWD_WARPS + GLR_X + 1), sizeof(GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>), 2,
+                                   p, maps, s);
         if (e != cudaSuccess || GATE != GLR_SOFTPLUS) return e;
         k_glr_sums<<<(p.C / 2 + 31) / 32, 1024, 0, s>>>(p.sums, glr_chunks(p), p.C, p.dA_log,
                                                         p.ddt_bias);

@@ -17,19 +17,20 @@ constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS;
 template <class TX>
 struct GlrFwdTile {
     static constexpr int LATE = 2, SLOTS = LATE + 2;
-    float2 a[SLOTS][FWD_WARPS][FWD_SUB][32];    // g as copied (a row in the first bytes of its 256), then the decays
+    float2 a[SLOTS][FWD_WARPS][FWD_SUB][32];    // g as copied (glr_raw_offset), then the decays
     TX x[SLOTS][FWD_WARPS][FWD_SUB][GLR_TILE];
     GlrRing<FWD_WARPS, LATE> ring;
 };
 
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrParams p) {
+__global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
     constexpr int SUB = FWD_SUB;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
     using RX = typename PX::raw;
     using RG = typename PG::raw;
-    extern __shared__ __align__(16) unsigned char smem[];
+    constexpr int RAW = glr_raw_offset<TG>(false);
+    extern __shared__ __align__(128) unsigned char smem[];
     using Tile = GlrFwdTile<TX>;
     using Ring = decltype(Tile::ring);
     constexpr int LATE = Tile::LATE, SLOTS = Tile::SLOTS;
@@ -38,40 +39,41 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     const int chunks = glr_chunks(p);
     const unsigned tiles = (p.C + GLR_TILE - 1) / GLR_TILE, all = tiles * chunks;
     const int w = threadIdx.x / 32, lane = threadIdx.x % 32, i0 = w * SUB, ld = p.C / 2;
-    glr_ring_init(ring);
-    if (w >= FWD_WARPS) {
-        const GlrRuns runs = glr_runs(p.status, chunks, p.C);
-        // a tile's place is found as soon as the exchange four tiles before it is done: the slot it takes
-        // was tile j - 8's
-        int4 tick = glr_look<false>(p, ring, chunks, w - FWD_WARPS, lane);
-        for (int j = w - FWD_WARPS; tick.x >= 0; j += 4) {
-            if (j >= 4) glr_wait<50>(p, ring, GLR_FREE, j - 4);
-            glr_exchange<false>(p, ring, runs, chunks, j, tick, lane);
-            tick = glr_look<false>(p, ring, chunks, j + 4, lane);
+    const bool wide = p.wide;
+    glr_ring_init(ring, wide);
+    if (w == FWD_WARPS + GLR_X) {  // tickets and copies
+        unsigned id = lane == 0 ? glr_ticket(p, chunks, 0) : 0;
+        for (int j = 0, over = 0; over < GLR_X; ++j) {
+            id = __shfl_sync(~0u, id, 0);
+            const unsigned next = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
+            const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
+            if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
+            glr_signal(ring, GLR_TICK, j);
+            if (k >= 0) {
+                if (j >= SLOTS) glr_wait<20>(p, ring, GLR_FREE, j - SLOTS);
+                const int64_t t0 = (int64_t)k * GLR_CHUNK;
+                const int rows = (int)min((int64_t)GLR_CHUNK, p.T - t0), cols = min(GLR_TILE, p.C - c0);
+                const uint32_t bar = glr_announce(ring, GLR_FULL, j, wide, GLR_CHUNK * GLR_TILE * (sizeof(TX) + sizeof(TG)), lane);
+                glr_copy_rows<GLR_TILE * sizeof(TG), 2048>(reinterpret_cast<char*>(&tl.a[j % SLOTS]) + RAW, &maps.g,
+                                                           static_cast<const TG*>(p.g), p.ldg, t0, 0, rows, c0, cols, wide, bar, lane);
+                glr_copy_rows<GLR_TILE * sizeof(TX), 8 * GLR_TILE * sizeof(TX)>(
+                    &tl.x[j % SLOTS], &maps.x, static_cast<const TX*>(p.x), p.ldx, t0, 0, rows, c0, cols, wide, bar, lane);
+                glr_report(bar, wide);
+            } else {
+                if (over++ == 0) glr_report(glr_announce(ring, GLR_FULL, j, wide, 0, lane), wide);
+            }
+            id = next;
         }
         return;
     }
-
-    const GlrRows<SUB, 256, TG> g_rows(p.g, p.ldg, i0, lane);
-    const GlrRows<SUB, GLR_TILE * sizeof(TX), TX> x_rows(p.x, p.ldx, i0, lane);
-    const bool wide = p.wide;
-    auto copy = [&](int j) {  // this warp's tokens of tile j
-        glr_wait<0>(p, ring, GLR_TICK, j);
-        const int4 tick = ring.tick[j & 7];
-        if (tick.x >= 0) {
-            const int64_t left = p.T - ((int64_t)tick.x * GLR_CHUNK + i0);
-            g_rows.copy(&tl.a[j % SLOTS][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
-            x_rows.copy(&tl.x[j % SLOTS][w][0][0], tick.x, tick.y, tick.z, wide, 0, left, p.C - tick.y, lane);
+    if (w >= FWD_WARPS) {
+        const GlrRuns runs = glr_runs(p.status, chunks, p.C);
+        int4 tick = glr_look<false>(p, ring, chunks, w - FWD_WARPS, lane);
+        for (int j = w - FWD_WARPS; tick.x >= 0; j += GLR_X) {
+            glr_exchange<false>(p, ring, runs, chunks, j, tick, lane);
+            tick = glr_look<false>(p, ring, chunks, j + GLR_X, lane);
         }
-        copies_commit();
-    };
-    const bool takes = w == 0 && lane == 0;  // the tickets
-    for (int j = 0; j < 3; ++j) {
-        if (w == 0) {
-            if (takes) glr_set_tick<false>(p, ring, chunks, j, glr_ticket(p, chunks, j), tiles, all);
-            glr_signal(ring, GLR_TICK, j);
-        }
-        if (j < 2) copy(j);
+        return;
     }
     int4 before[LATE];  // tiles j - LATE .. j - 1
 #pragma unroll
@@ -80,22 +82,19 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
     for (int j = 0;; ++j) {
         const bool more = tick.x >= 0;  // (past the last tile only second walks are left)
         if (more) {
-            glr_wait<0>(p, ring, GLR_PLACE, j);
+            glr_wait<0>(p, ring, GLR_FULL, j);
             tick = ring.tick[j & 7];
         }
-        unsigned id = 0;
         if (tick.x >= 0) {
-            if (takes) id = glr_ticket(p, chunks, j + 3);
             const GlrInfo& info = ring.info[j & 7];
             const int c = tick.y + 2 * lane;
             const bool live = c < p.C;
             GlrGate<GATE> gate;
             gate.set(ring.gate[j & 3][lane]);
-            copies_wait<1>();
             const TX* xs = &tl.x[j % SLOTS][w][0][2 * lane];
             float2* as = &tl.a[j % SLOTS][w][0][lane];
-            const TG* gs = reinterpret_cast<const TG*>(&tl.a[j % SLOTS][w][0][0]) + 2 * lane;
-            constexpr int GP = 256 / sizeof(TG);
+            const TG* gs = reinterpret_cast<const TG*>(reinterpret_cast<char*>(&tl.a[j % SLOTS][w]) + RAW) + 2 * lane;
+            constexpr int GP = GLR_TILE;
             Run r = run_identity();
             if (!info.any) {
 #pragma unroll 1
@@ -173,14 +172,8 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
                     }
                 }
             }
+            tc::fence_async_smem();  // (the next copy into these rows comes after the reads and writes above)
             glr_signal(ring, GLR_FREE, j - LATE);
-        }
-        if (more) {
-            if (w == 0) {
-                if (takes) glr_set_tick<false>(p, ring, chunks, j + 3, tick.x < 0 ? all : id, tiles, all);
-                glr_signal(ring, GLR_TICK, j + 3);
-            }
-            if (tick.x >= 0) copy(j + 2);
         }
 #pragma unroll
         for (int i = 0; i + 1 < LATE; ++i) before[i] = before[i + 1];
@@ -190,7 +183,6 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + 4), 2) k_glr_fwd(const GlrPa
         for (int i = 0; i < LATE; ++i) left |= before[i].x >= 0;
         if (!left) break;
     }
-    copies_wait<0>();
 }
 
 namespace {
@@ -200,7 +192,11 @@ struct Launch {
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
         static std::atomic<uint64_t> ready{0};
-        return glr_launch(k_glr_fwd<TX, TG, GATE, COMP>, ready, 32 * (FWD_WARPS + 4), sizeof(GlrFwdTile<TX>), 2, p, s);
+        GlrMaps maps;
+        if (p.wide && !(encode_plain_map(&maps.g, p.g, p.gate_f32, p.T, p.C, p.ldg, p.gate_f32 ? 64 : 8) &&
+                        encode_plain_map(&maps.x, p.x, p.act_f32, p.T, p.C, p.ldx, 64)))
+            return cudaErrorInvalidValue;
+        return glr_launch(k_glr_fwd<TX, TG, GATE, COMP>, ready, 32 * (FWD_WARPS + GLR_X + 1), sizeof(GlrFwdTile<TX>), 2, p, maps, s);
     }
 };
 }  // namespace

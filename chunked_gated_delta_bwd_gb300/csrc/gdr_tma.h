@@ -74,4 +74,18 @@ inline bool encode_tokens_map(CUtensorMap* m, const void* base, uint64_t T, uint
     return encode_bf16_map(m, base, 3, dims, strides, box);
 }
 
+// [rows][cols] bf16 or float32 rows of stride ld elements, boxes of box_rows x 64 columns, not
+// swizzled (a box lies row after row in shared memory); what is outside the tensor reads as zero
+inline bool encode_plain_map(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t cols, uint64_t ld,
+                             uint32_t box_rows) {
+    memset(m, 0, sizeof(*m));
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {ld * (f32 ? 4 : 2)};
+    const cuuint32_t box[2] = {64, box_rows}, elem[2] = {1, 1};
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims,
+              strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace gdr
