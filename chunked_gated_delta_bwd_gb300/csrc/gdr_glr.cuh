@@ -148,10 +148,11 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 // warp takes 64 / (compute warps) consecutive tokens of it, a lane two channels.  A run of tokens acts on the
 // state before it as y -> A y + H.  Each tile's run (A, H) is published; the state before a chunk
 // is the fold of the runs before it, back to the chunk its sequence begins in.  So that no tile
-// folds many, the last chunk of every 16 also publishes the run of all 16 and the last of every
-// 256 the run of those: a chunk reads at most 15 + 15 published runs and one for each 256 chunks
-// before.  Which runs are folded, and in which order, depends on the position alone, so the
-// results do not depend on the order in which blocks run.
+// folds many, the last chunk of every 8 also publishes the run of all 8, and the last of every 64
+// the state after it: a chunk reads at most 7 + 7 published runs and a state, in two rounds of
+// loads.  (The states make a chain, one step for 4096 tokens.)  Which runs are folded, and in which
+// order, depends on the position alone, so the results do not depend on the order in which blocks
+// run.
 //
 // Blocks stay resident and take tiles by ticket, chunks in the order of the scan: a tile waits
 // only for tiles with earlier tickets, which are being worked on.  A block's compute warps walk
@@ -166,7 +167,7 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 // NaN crosses from one sequence into the next.
 // ---------------------------------------------------------------------------
 constexpr int GLR_CHUNK = 64, GLR_TILE = 64;
-constexpr int GLR_GROUP = 16, GLR_SUPER = 256;  // chunks in a published group / super group
+constexpr int GLR_GROUP = 8, GLR_SUPER = 64;  // chunks in a published group; from one published state to the next
 constexpr int GLR_SPIN = 1 << 20;               // polls of one published run before giving up
 __host__ __device__ inline int glr_chunks(const GlrParams& p) { return (int)((uint64_t)(p.T + GLR_CHUNK - 1) / GLR_CHUNK); }
 
@@ -219,13 +220,13 @@ __device__ __forceinline__ Run run_of(const uint4& v) {
 }
 // Where published runs lie in the workspace, after the status word and the ticket counter.
 struct GlrRuns {
-    uint4 *chunk, *group, *super;  // [..][C / 2]
+    uint4 *chunk, *group, *state;  // [..][C / 2]
 };
 __host__ __device__ inline GlrRuns glr_runs(void* ws, int chunks, int C) {
     GlrRuns r;
     r.chunk = reinterpret_cast<uint4*>(static_cast<unsigned char*>(ws) + 256);
     r.group = r.chunk + (int64_t)chunks * (C / 2);
-    r.super = r.group + (int64_t)(chunks / GLR_GROUP) * (C / 2);
+    r.state = r.group + (int64_t)(chunks / GLR_GROUP) * (C / 2);
     return r;
 }
 __host__ __device__ inline size_t glr_runs_bytes(int chunks, int C) {  // of one chunk's tokens: none
@@ -238,9 +239,9 @@ struct GlrInfo {
     int any;                    // whether any of them does, or restarts the scan
     int seq0;                   // the sequence of token t0
     int seq_at_start[GLR_CHUNK];  // the sequence beginning at token t0 + i, where one does
-    // published runs of chunks [chunk0, k), groups [group0, k / 16) and super groups [super0, k / 256)
-    // make up the state before chunk k (none of them: it begins with a restart)
-    int chunk0, group0, super0, none;
+    // the state before chunk k: the published state after chunk 64 [k / 64] - 1 (if `state`), then the
+    // runs of groups [group0, group0 + groups) and of chunks [chunk0, chunk0 + chunks)
+    int state, group0, groups, chunk0, chunks;
 };
 
 // Works out a chunk's sequences and place; all threads of one warp.  Its tokens are
@@ -321,8 +322,9 @@ __device__ __forceinline__ void glr_find_place(const GlrParams& p, GlrInfo& sm, 
         sm.any = some;
         sm.chunk0 = max(lo, g0);
         sm.group0 = max(lo, s0) / GLR_GROUP;
-        sm.super0 = lo / GLR_SUPER;
-        sm.none = none;
+        sm.chunks = none ? 0 : k - sm.chunk0;
+        sm.groups = none ? 0 : k / GLR_GROUP - sm.group0;
+        sm.state = !none && lo < s0;
     }
     __syncwarp();
 }
@@ -341,36 +343,42 @@ __device__ __forceinline__ int glr_seq_at(const GlrInfo& sm, int i) {
     }
 }
 
-// The run of published runs [from, to) of `rows`, for this lane's channels.  Only the first run of
-// all may contain a restart.  A run that never comes (it does: its block holds an earlier ticket)
-// is recorded.
-__device__ __forceinline__ Run glr_fold(const uint4* rows, int64_t stride, int from, int to, int* status) {
-    Run r = run_identity();
-    const uint4* at = rows + from * stride;
-#pragma unroll 1
-    for (int n = to - from; n > 0; n -= 8) {
-        uint4 v[8];
-        const uint4* here = at;
+// Up to eight published runs for this lane's channels, all loads in flight at once: one at `first`
+// (if `has`), then n <= 7 rows.  Their fold in order; only the first run of all may contain a
+// restart (or be a state: A = -0).  Waiting: for each as long as it takes (one that never comes,
+// whose block holds an earlier ticket, is recorded).  Not waiting: false if one is missing.
+__device__ __forceinline__ bool glr_fold(Run& r, const uint4* first, bool has, const uint4* rows, int64_t stride, int n, bool wait,
+                                         int* status) {
+    uint4 v[8];
+    bool there = true;
+    const uint4* at = rows;
 #pragma unroll
-        for (int j = 0; j < 8; ++j, at += stride)
-            if (j < n) v[j] = run_poll(at);
+    for (int j = 0; j < 8; ++j) {
+        v[j] = make_uint4(~__float_as_uint(1.f), __float_as_uint(1.f), ~0u, 0);  // the identity
+        if (j == 0 ? has : j <= n) v[j] = run_poll(j == 0 ? first : at);
+        if (j > 0) at += stride;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) there &= run_there(v[j]);
+    if (!there) {
+        if (!wait) return false;
+        at = rows;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            if (j < n) {
-                if (!run_there(v[j])) {
-                    int spin = 0;
-                    int64_t apart = stride;
-                    asm volatile("" : "+l"(apart));  // (else eight addresses are kept for a path hardly taken)
+            if (!run_there(v[j])) {
+                int spin = 0;
 #pragma unroll 1
-                    do v[j] = run_poll(here + j * apart);
-                    while (!run_there(v[j]) && ++spin < GLR_SPIN);
-                    if (!run_there(v[j])) atomicOr(status, ST_MMA_TIMEOUT);
-                }
-                r = run_then_plain(r, run_of(v[j]));
+                do v[j] = run_poll(j == 0 ? first : at);
+                while (!run_there(v[j]) && ++spin < GLR_SPIN);
+                if (!run_there(v[j])) atomicOr(status, ST_MMA_TIMEOUT);
             }
+            if (j > 0) at += stride;
         }
     }
-    return r;
+    r = run_of(v[0]);
+#pragma unroll
+    for (int j = 1; j < 8; ++j) r = run_then_plain(r, run_of(v[j]));
+    return true;
 }
 
 // Empty sequences pass their state through; the first tile's blocks also check cu_seqlens against
@@ -507,35 +515,46 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
                                              int lane) {
     constexpr int CW = Ring::CW;
     const int half = j % (Ring::LATE + 1), k = tick.x, c = tick.y + 2 * lane;
-    const int64_t stride = p.C / 2;
     const GlrInfo& at = ring.info[j & 7];
-    glr_runs_wait<Ring>(j);
     const bool any = at.any;
     Run y = run_identity();
-    if (chunks > 1 && c < p.C) {
-        const int c2 = c / 2;
-        Run own = run_from_bits(ring.sub[half][0][lane]);
-#pragma unroll
-        for (int i = 1; i < CW; ++i) {
-            const Run next = run_from_bits(ring.sub[half][i][lane]);
-            own = any ? run_then(own, next) : run_then_plain(own, next);
-        }
-        run_publish(runs.chunk + k * stride + c2, own);
-        // the runs of chunks, groups and super groups before it (in one loop: each copy of the fold's
-        // code costs registers); the last chunk of a group, of a super group, publishes that one's run
+    if (chunks > 1) {
+        const int64_t stride = p.C / 2;
+        const int c2 = (c < p.C ? c : 0) / 2;  // (a lane without channels folds channel 0's)
+        Run own = y, older = y, near = y;
+        bool folded = false;
+        // step 0: the state and the groups' runs, if they are all there; step 1: the block's own run is
+        // published, and what was not there waited for; step 2: the chunks' runs
 #pragma unroll 1
-        for (int q = 0; q < 3; ++q) {
-            const uint4* rows = q == 0 ? runs.chunk : q == 1 ? runs.group : runs.super;
-            const int from = q == 0 ? at.chunk0 : q == 1 ? at.group0 : at.super0;
-            const int to = q == 0 ? k : q == 1 ? k / GLR_GROUP : k / GLR_SUPER;
-            Run level = run_identity();
-            if (!at.none && from < to) level = glr_fold(rows + c2, stride, from, to, p.status);
-            y = run_then_plain(level, y);
-            if (q < 2 && (k + 1) % (q == 0 ? GLR_GROUP : GLR_SUPER) == 0) {
-                own = run_then(level, own);
-                run_publish((q == 0 ? runs.group : runs.super) + (q == 0 ? k / GLR_GROUP : k / GLR_SUPER) * stride + c2, own);
+        for (int step = 0; step < 3; ++step) {
+            if (step == 1) {
+                glr_runs_wait<Ring>(j);
+                own = run_from_bits(ring.sub[half][0][lane]);
+#pragma unroll
+                for (int i = 1; i < CW; ++i) {
+                    const Run next = run_from_bits(ring.sub[half][i][lane]);
+                    own = any ? run_then(own, next) : run_then_plain(own, next);
+                }
+                if (c < p.C) run_publish(runs.chunk + k * stride + c2, own);
+                if (folded) continue;
             }
+            const bool last = step == 2;
+            const int64_t from = last ? at.chunk0 : at.group0;
+            const int n = last ? at.chunks : at.groups;
+            Run r;
+            const bool done = glr_fold(r, runs.state + (k / GLR_SUPER - 1) * stride + c2, !last && at.state,
+                                       (last ? runs.chunk : runs.group) + from * stride + c2, stride, n, step > 0, p.status);
+            if (last) near = r;
+            else if (folded = __all_sync(~0u, done)) older = r;
         }
+        y = run_then_plain(older, near);
+        if ((k + 1) % GLR_GROUP == 0 && c < p.C) {
+            run_publish(runs.group + k / GLR_GROUP * stride + c2, run_then(near, own));
+            if ((k + 1) % GLR_SUPER == 0)
+                run_publish(runs.state + k / GLR_SUPER * stride + c2, Run{splat(-0.f), run_then(Run{splat(-0.f), y.H}, own).H});
+        }
+    } else {
+        glr_runs_wait<Ring>(j);
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) {

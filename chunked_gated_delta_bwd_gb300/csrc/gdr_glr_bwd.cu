@@ -65,6 +65,10 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                                                            static_cast<const TG*>(p.g), p.ldg, t0, 0, rows, c0, cols, wide, bar, lane);
                 glr_copy_rows<XP, 8 * XP>(&tl.dh[j % 3], &maps.dh, static_cast<const TX*>(p.dh), p.C, t0, 0, rows, c0, cols, wide, bar, lane);
                 glr_report(bar, wide);
+                if (wide && lane == 0) {  // h and x have one buffer: on their way to L2 until it is free
+                    tc::tma_prefetch_2d(&maps.h, c0, (int)t0 - 1);
+                    if (COMP) tc::tma_prefetch_2d(&maps.x, c0, (int)t0);
+                }
             } else {
                 if (over++ == 0) glr_report(glr_announce(ring, GLR_FULL, j, wide, 0, lane), wide);
             }
