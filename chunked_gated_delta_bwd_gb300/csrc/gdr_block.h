@@ -68,7 +68,10 @@ struct NormParams {
     const float* rstd_in;        // [R]
     void* dx;                    // [R][C], of the residual stream's type
     float* dweight;              // [C]
+    float* partial;              // workspace: sums of dweight, a row for each group of threads
 };
+int rmsnorm_bwd_blocks(int64_t R, int C);
+size_t rmsnorm_partial_bytes(int64_t R, int C);
 cudaError_t launch_rmsnorm_fwd(const NormParams& p, cudaStream_t s);
 cudaError_t launch_rmsnorm_bwd(const NormParams& p, cudaStream_t s);
 

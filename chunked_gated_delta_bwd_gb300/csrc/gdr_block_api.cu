@@ -220,7 +220,7 @@ gdr_status gdr_rmsnorm_fwd(int64_t rows, int32_t channels, const void* x, int64_
 
 size_t gdr_rmsnorm_workspace_bytes(int64_t rows, int32_t channels) {
     if (check_norm(rows, channels, GDR_TYPE_BF16) != GDR_OK) return 0;
-    return 256;
+    return 256 + rmsnorm_partial_bytes(rows, channels);
 }
 
 gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const void* s_in, int32_t res_type,
@@ -238,6 +238,7 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
     p.R = rows; p.C = channels; p.ldx = channels; p.res_f32 = res_type == GDR_TYPE_F32;
     p.dy = (const __nv_bfloat16*)dy; p.s = s_in; p.weight = weight; p.rstd_in = rstd; p.dres = dres; p.dx = dx;
     p.dweight = dweight;
+    p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + 256);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = timed(GDR_KERNEL_NORM, s, [&] { return launch_rmsnorm_bwd(p, s); }, 2);
     return e == cudaSuccess ? ok() : cuda_fail(e, "rms norm backward launch");

@@ -52,7 +52,6 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
         int k1 = -1, c1 = 0, k2 = -1, c2 = 0;  // tiles j - 1, j - 2
         for (int j = 0, over = 0; over < GLR_X; ++j) {
             id = __shfl_sync(~0u, id, 0);
-            const unsigned next = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
             const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
             if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
             glr_signal(ring, GLR_TICK, j);
@@ -82,7 +81,8 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                 glr_report(bar, wide);
             }
             k2 = k1; c2 = c1; k1 = k; c1 = c0;
-            id = next;
+            // (taken as late as that, so that tiles with near tickets are worked on at the same time)
+            id = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
         }
         return;
     }

@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
         unsigned id = lane == 0 ? glr_ticket(p, chunks, 0) : 0;
         for (int j = 0, over = 0; over < GLR_X; ++j) {
             id = __shfl_sync(~0u, id, 0);
-            const unsigned next = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
             const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
             if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
             glr_signal(ring, GLR_TICK, j);
@@ -62,7 +61,8 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
             } else {
                 if (over++ == 0) glr_report(glr_announce(ring, GLR_FULL, j, wide, 0, lane), wide);
             }
-            id = next;
+            // (taken as late as that, so that tiles with near tickets are worked on at the same time)
+            id = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
         }
         return;
     }
