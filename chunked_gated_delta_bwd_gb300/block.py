@@ -30,6 +30,11 @@ class GlrShape(ctypes.Structure):
 _LIB = None
 
 
+def _like(t):
+    """An uninitialised contiguous tensor of t's shape and type."""
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
 def _lib():
     global _LIB
     if _LIB is None:
@@ -161,7 +166,7 @@ def glr_fwd(x, g, h0=None, A_log=None, dt_bias=None, cu_seqlens=None, num_seqs=N
     P, sh = _glr_shape(x, g, cu_seqlens, num_seqs, gate, complement)
     _opt(h0, torch.float32, (P.N, P.C), "h0")
     ws = _glr_workspace(sh, workspace, x)
-    h = torch.empty(P.shape, dtype=x.dtype, device=x.device)
+    h = _like(x)
     ht = torch.empty((P.N, P.C), dtype=torch.float32, device=x.device) if want_ht else None
     rc = _lib().glr_fwd(sh, x.data_ptr(), g.data_ptr(), _ptr(A_log), _ptr(dt_bias), _ptr(h0), h.data_ptr(), _ptr(ht),
                         ws.data_ptr(), ws.numel(), _stream(x))
@@ -181,8 +186,7 @@ def glr_bwd(x, g, h, dh, h0=None, dht=None, A_log=None, dt_bias=None, cu_seqlens
     _opt(h0, torch.float32, (P.N, P.C), "h0")
     _opt(dht, torch.float32, (P.N, P.C), "dht")
     ws = _glr_workspace(sh, workspace, x)
-    out = {"dx": torch.empty(P.shape, dtype=x.dtype, device=x.device),
-           "dg": torch.empty(P.shape, dtype=g.dtype, device=x.device),
+    out = {"dx": _like(x), "dg": _like(g),
            "dh0": torch.empty((P.N, P.C), dtype=torch.float32, device=x.device)}
     if gate:
         out["dA_log"] = torch.empty(P.C, dtype=torch.float32, device=x.device)
@@ -218,7 +222,7 @@ def glr_step(x, g, state, slots=None, A_log=None, dt_bias=None, gate="log", comp
     ldg = _rows(g, _ACT, shape, "g")
     _glr_types(x, g)
     pool = _pool(state, torch.float32, (C,), slots, rows, "state")
-    y = torch.empty(shape, dtype=x.dtype, device=x.device) if out is None else _need(out, x.dtype, shape, "out")
+    y = _like(x) if out is None else _need(out, x.dtype, shape, "out")
     rc = _lib().glr_step(rows, C, pool, gate, bool(complement), _TYPES[x.dtype], _TYPES[g.dtype], x.data_ptr(), ldx,
                          g.data_ptr(), ldg, _ptr(A_log), _ptr(dt_bias), _ptr(slots), state.data_ptr(), y.data_ptr(),
                          _stream(x))
@@ -243,15 +247,18 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-6, quant=None):
     rows = x.shape[0]
     ldx = _rows(x, (torch.bfloat16,), (rows, C), "x")
     _need(weight, torch.float32, (C,), "weight")
-    out = {"y": torch.empty(shape, dtype=torch.float8_e4m3fn if quant else torch.bfloat16, device=x.device),
-           "rstd": torch.empty(shape[:-1], dtype=torch.float32, device=x.device)}
+    if quant:
+        y = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+    else:
+        y = _like(x) if x.shape == shape else torch.empty(shape, dtype=torch.bfloat16, device=x.device)
+    out = {"y": y, "rstd": torch.empty(shape[:-1], dtype=torch.float32, device=x.device)}
     res_type = 0
     if residual is not None:
         if residual.dtype not in _TYPES:
             _bad(residual, "bfloat16 / float32", shape, "residual")
         _need(residual, residual.dtype, shape, "residual")
         res_type = _TYPES[residual.dtype]
-        out["residual"] = torch.empty(shape, dtype=residual.dtype, device=x.device)
+        out["residual"] = torch.empty_like(residual)
     if quant:
         out["scale"] = torch.empty((rows, 1 if quant == "token" else (C + 127) // 128), dtype=torch.float32,
                                    device=x.device)
@@ -282,7 +289,7 @@ def rmsnorm_bwd(dy, s, weight, rstd, dres=None, workspace=None):
         workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=s.device)
     elif workspace.dtype is not torch.uint8 or workspace.numel() < need:
         raise ValueError("workspace must be a uint8 tensor of at least %d bytes" % need)
-    out = {"dx": torch.empty(shape, dtype=s.dtype, device=s.device),
+    out = {"dx": torch.empty_like(s),
            "dweight": torch.empty(C, dtype=torch.float32, device=s.device)}
     rc = _lib().gdr_rmsnorm_bwd(rows, C, dy.data_ptr(), s.data_ptr(), _TYPES[s.dtype], weight.data_ptr(),
                                 rstd.data_ptr(), _ptr(dres), workspace.data_ptr(), workspace.numel(),
@@ -307,7 +314,7 @@ def conv1d_fwd(x, weight, bias=None, state=None, cu_seqlens=None, num_seqs=None,
     ldx = _rows(x, (torch.bfloat16,), P.shape, "x")
     K = _conv_weights(weight, bias, P.C)
     _opt(state, torch.bfloat16, (P.N, K - 1, P.C), "state")
-    y = torch.empty(P.shape, dtype=torch.bfloat16, device=x.device)
+    y = _like(x)
     new = torch.empty((P.N, K - 1, P.C), dtype=torch.bfloat16, device=x.device) if want_state else None
     rc = _lib().gdr_conv1d_fwd(P.N, P.T, P.C, K, _ptr(P.cu), x.data_ptr(), ldx, weight.data_ptr(), _ptr(bias),
                                _ptr(state), bool(silu), y.data_ptr(), _ptr(new), _stream(x))
@@ -325,7 +332,7 @@ def conv1d_step(x, state, weight, bias=None, slots=None, silu=True, out=None):
     ldx = _rows(x, (torch.bfloat16,), shape, "x")
     K = _conv_weights(weight, bias, C)
     pool = _pool(state, torch.bfloat16, (K - 1, C), slots, rows, "state")
-    y = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if out is None else \
+    y = _like(x) if out is None else \
         _need(out, torch.bfloat16, shape, "out")
     rc = _lib().gdr_conv1d_step(rows, C, K, pool, x.data_ptr(), ldx, state.data_ptr(), weight.data_ptr(), _ptr(bias),
                                 _ptr(slots), bool(silu), y.data_ptr(), _stream(x))
