@@ -150,7 +150,8 @@ __device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
 // is the fold of the runs before it, back to the chunk its sequence begins in.  So that no tile
 // folds many, the last chunk of every 8 also publishes the run of all 8, and the last of every 64
 // the state after it: a chunk reads at most 7 + 7 published runs and a state, in two rounds of
-// loads.  (The states make a chain, one step for 4096 tokens.)  Which runs are folded, and in which
+// loads.  (The states make a chain, one step for 4096 tokens: some 2 us of 7 us that 2048 channels
+// of them take to pass; 65536 tokens of 64 channels take 32 us.)  Which runs are folded, and in which
 // order, depends on the position alone, so the results do not depend on the order in which blocks
 // run.
 //
@@ -345,10 +346,9 @@ __device__ __forceinline__ int glr_seq_at(const GlrInfo& sm, int i) {
 
 // Up to eight published runs for this lane's channels, all loads in flight at once: one at `first`
 // (if `has`), then n <= 7 rows.  Their fold in order; only the first run of all may contain a
-// restart (or be a state: A = -0).  Waiting: for each as long as it takes (one that never comes,
-// whose block holds an earlier ticket, is recorded).  Not waiting: false if one is missing.
-__device__ __forceinline__ bool glr_fold(Run& r, const uint4* first, bool has, const uint4* rows, int64_t stride, int n, bool wait,
-                                         int* status) {
+// restart (or be a state: A = -0).  Waits for each as long as it takes; one that never comes, whose
+// block holds an earlier ticket, is recorded.
+__device__ __forceinline__ Run glr_fold(const uint4* first, bool has, const uint4* rows, int64_t stride, int n, int* status) {
     uint4 v[8];
     bool there = true;
     const uint4* at = rows;
@@ -361,7 +361,6 @@ __device__ __forceinline__ bool glr_fold(Run& r, const uint4* first, bool has, c
 #pragma unroll
     for (int j = 0; j < 8; ++j) there &= run_there(v[j]);
     if (!there) {
-        if (!wait) return false;
         at = rows;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -375,10 +374,10 @@ __device__ __forceinline__ bool glr_fold(Run& r, const uint4* first, bool has, c
             if (j > 0) at += stride;
         }
     }
-    r = run_of(v[0]);
+    Run r = run_of(v[0]);
 #pragma unroll
     for (int j = 1; j < 8; ++j) r = run_then_plain(r, run_of(v[j]));
-    return true;
+    return r;
 }
 
 // Empty sequences pass their state through; the first tile's blocks also check cu_seqlens against
@@ -518,43 +517,37 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
     const GlrInfo& at = ring.info[j & 7];
     const bool any = at.any;
     Run y = run_identity();
+    glr_runs_wait<Ring>(j);
     if (chunks > 1) {
         const int64_t stride = p.C / 2;
         const int c2 = (c < p.C ? c : 0) / 2;  // (a lane without channels folds channel 0's)
-        Run own = y, older = y, near = y;
-        bool folded = false;
-        // step 0: the state and the groups' runs, if they are all there; step 1: the block's own run is
-        // published, and what was not there waited for; step 2: the chunks' runs
-#pragma unroll 1
-        for (int step = 0; step < 3; ++step) {
-            if (step == 1) {
-                glr_runs_wait<Ring>(j);
-                own = run_from_bits(ring.sub[half][0][lane]);
+        Run own = run_from_bits(ring.sub[half][0][lane]);
 #pragma unroll
-                for (int i = 1; i < CW; ++i) {
-                    const Run next = run_from_bits(ring.sub[half][i][lane]);
-                    own = any ? run_then(own, next) : run_then_plain(own, next);
-                }
-                if (c < p.C) run_publish(runs.chunk + k * stride + c2, own);
-                if (folded) continue;
+        for (int i = 1; i < CW; ++i) {
+            const Run next = run_from_bits(ring.sub[half][i][lane]);
+            own = any ? run_then(own, next) : run_then_plain(own, next);
+        }
+        if (c < p.C) run_publish(runs.chunk + k * stride + c2, own);
+        // The chunks' runs, of which the last chunk of a group makes the group's; then the state and the
+        // groups' runs.  (Nothing is published later than what it is made of allows, for others wait for
+        // it: groups published only after the state before them made one chain of everything, four times
+        // slower on few channels.  One loop: each copy of the fold's code costs registers.)
+        Run near = y;
+#pragma unroll 1
+        for (int older = 0; older < 2; ++older) {
+            const Run r = glr_fold(runs.state + (int64_t)(k / GLR_SUPER - 1) * stride + c2, older && at.state,
+                                   (older ? runs.group + at.group0 * stride : runs.chunk + at.chunk0 * stride) + c2, stride,
+                                   older ? at.groups : at.chunks, p.status);
+            if (older) {
+                y = run_then_plain(r, near);
+            } else {
+                near = r;
+                if ((k + 1) % GLR_GROUP == 0 && c < p.C)
+                    run_publish(runs.group + k / GLR_GROUP * stride + c2, run_then(near, own));
             }
-            const bool last = step == 2;
-            const int64_t from = last ? at.chunk0 : at.group0;
-            const int n = last ? at.chunks : at.groups;
-            Run r;
-            const bool done = glr_fold(r, runs.state + (k / GLR_SUPER - 1) * stride + c2, !last && at.state,
-                                       (last ? runs.chunk : runs.group) + from * stride + c2, stride, n, step > 0, p.status);
-            if (last) near = r;
-            else if (folded = __all_sync(~0u, done)) older = r;
         }
-        y = run_then_plain(older, near);
-        if ((k + 1) % GLR_GROUP == 0 && c < p.C) {
-            run_publish(runs.group + k / GLR_GROUP * stride + c2, run_then(near, own));
-            if ((k + 1) % GLR_SUPER == 0)
-                run_publish(runs.state + k / GLR_SUPER * stride + c2, Run{splat(-0.f), run_then(Run{splat(-0.f), y.H}, own).H});
-        }
-    } else {
-        glr_runs_wait<Ring>(j);
+        if ((k + 1) % GLR_SUPER == 0 && c < p.C)
+            run_publish(runs.state + k / GLR_SUPER * stride + c2, Run{splat(-0.f), run_then(Run{splat(-0.f), y.H}, own).H});
     }
 #pragma unroll
     for (int i = 0; i < CW; ++i) {

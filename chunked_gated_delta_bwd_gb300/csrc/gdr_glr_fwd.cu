@@ -13,7 +13,7 @@ size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunk
 // time in a rolled loop (unrolled over a warp's tokens the code did not fit the instruction
 // cache, which then bound the kernel); a warp among whose tokens a sequence begins or ends walks
 // them one by one.
-constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS;
+constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS, AT_ONCE = 8;
 template <class TX>
 struct GlrFwdTile {
     static constexpr int LATE = 2, SLOTS = LATE + 2;
@@ -98,17 +98,17 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
             Run r = run_identity();
             if (!info.any) {
 #pragma unroll 1
-                for (int i = 0; i < SUB; i += 4) {
-                    RG graw[4];
-                    float2 xv[4];
+                for (int i = 0; i < SUB; i += AT_ONCE) {
+                    RG graw[AT_ONCE];
+                    float2 xv[AT_ONCE];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < AT_ONCE; ++q) {
                         graw[q] = *reinterpret_cast<const RG*>(gs + (i + q) * GP);
                         xv[q] = PX::widen(*reinterpret_cast<const RX*>(xs + (i + q) * GLR_TILE));
                     }
                     __syncwarp();  // every lane has its g of these rows
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < AT_ONCE; ++q) {
                         const float2 a = decay(gate.log2_gate(PG::widen(graw[q])));
                         as[(i + q) * 32] = a;
                         r.A = __fmul2_rn(r.A, a);

@@ -295,9 +295,9 @@ __global__ void __launch_bounds__(512) k_rmsnorm_fwd_long(const NormParams p) {
 }
 
 // dx of a row held in registers, and dweight's sum over the rows of this group of threads, which
-// walks the rows with the grid's stride: one partial row of sums for each group.
+// walks the rows with the grid's stride: one partial row of sums for each block.
 template <int G, int P, class TR, bool DRES>
-__global__ void __launch_bounds__(G > 128 ? G : 128) k_rmsnorm_bwd(const NormParams p, int wide) {
+__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1024 / (G > 128 ? G : 128) : 1) k_rmsnorm_bwd(const NormParams p, int wide) {
     constexpr int THREADS = G > 128 ? G : 128, ROWS = THREADS / G;
     __shared__ float red[THREADS / 32];
     const int t = threadIdx.x % G, C = p.C;
@@ -371,7 +371,17 @@ __global__ void __launch_bounds__(G > 128 ? G : 128) k_rmsnorm_bwd(const NormPar
             }
         }
     }
-    float* part = p.partial + ((int64_t)blockIdx.x * ROWS + threadIdx.x / G) * C;
+    if (ROWS > 1) {  // the groups' sums of a block, in a fixed order
+        __shared__ Eight sums[ROWS > 1 ? THREADS : 1];
+        sums[ROWS > 1 ? threadIdx.x : 0] = dw[0];
+        __syncthreads();
+        if (threadIdx.x >= G) return;
+#pragma unroll
+        for (int r = 1; r < ROWS; ++r)
+#pragma unroll
+            for (int q = 0; q < 8; ++q) dw[0].v[q] += sums[ROWS > 1 ? r * G + t : 0].v[q];
+    }
+    float* part = p.partial + (int64_t)blockIdx.x * C;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
         const int c = (t + i * G) * 8;
@@ -442,7 +452,7 @@ Split split_of(int C) {
     const int pieces = (C + 7) / 8;
     for (int g = 8; g <= 512; g *= 2)
         if (pieces <= g) return {g, 1};
-    return pieces <= 1024 ? Split{512, 2} : pieces <= 2048 ? Split{512, 4} : Split{0, 0};
+    return pieces <= 1024 ? Split{512, 2} : pieces <= 1536 ? Split{512, 3} : pieces <= 2048 ? Split{512, 4} : Split{0, 0};
 }
 
 int grid_of(int64_t rows, int group, int per_sm) {
@@ -468,7 +478,7 @@ cudaError_t fwd(const NormParams& p, cudaStream_t s) {
         k_rmsnorm_fwd<G, P, TR, RES, QUANT><<<grid, threads, 0, s>>>(p, wide);      \
         break
         ROWS_OF(8, 1); ROWS_OF(16, 1); ROWS_OF(32, 1); ROWS_OF(64, 1); ROWS_OF(128, 1); ROWS_OF(256, 1); ROWS_OF(512, 1);
-        ROWS_OF(512, 2); ROWS_OF(512, 4);
+        ROWS_OF(512, 2); ROWS_OF(512, 3); ROWS_OF(512, 4);
 #undef ROWS_OF
     }
     return cudaGetLastError();
@@ -482,7 +492,6 @@ template <class TR, bool DRES>
 cudaError_t bwd(const NormParams& p, cudaStream_t s) {
     const Split sp = split_of(p.C);
     const int wide = p.C % 8 == 0, grid = rmsnorm_bwd_blocks(p.R, p.C);
-    const int rows = sp.group == 0 ? grid : grid * (sp.group >= 128 ? 1 : 128 / sp.group);
     if (sp.group == 0) {
         k_rmsnorm_bwd_long<TR><<<grid, 512, 0, s>>>(p);
     } else {
@@ -493,13 +502,13 @@ cudaError_t bwd(const NormParams& p, cudaStream_t s) {
         k_rmsnorm_bwd<G, P, TR, DRES><<<grid, threads, 0, s>>>(p, wide);            \
         break
             ROWS_OF(8, 1); ROWS_OF(16, 1); ROWS_OF(32, 1); ROWS_OF(64, 1); ROWS_OF(128, 1); ROWS_OF(256, 1); ROWS_OF(512, 1);
-            ROWS_OF(512, 2); ROWS_OF(512, 4);
+            ROWS_OF(512, 2); ROWS_OF(512, 3); ROWS_OF(512, 4);
 #undef ROWS_OF
         }
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_rmsnorm_dw<<<(p.C + 31) / 32, 1024, 0, s>>>(p.partial, rows, p.C, p.dweight);
+    k_rmsnorm_dw<<<(p.C + 31) / 32, 1024, 0, s>>>(p.partial, grid, p.C, p.dweight);
     return cudaGetLastError();
 }
 
@@ -511,11 +520,7 @@ int rmsnorm_bwd_blocks(int64_t R, int C) {
     if (sp.group == 0) return grid_of(R, 512, 1);
     return grid_of(R, sp.group, 1024 / (sp.group > 128 ? sp.group : 128));
 }
-size_t rmsnorm_partial_bytes(int64_t R, int C) {
-    const Split sp = split_of(C);
-    const int64_t rows = (int64_t)rmsnorm_bwd_blocks(R, C) * (sp.group == 0 || sp.group >= 128 ? 1 : 128 / sp.group);
-    return sizeof(float) * (size_t)rows * C;
-}
+size_t rmsnorm_partial_bytes(int64_t R, int C) { return sizeof(float) * (size_t)rmsnorm_bwd_blocks(R, C) * C; }
 
 cudaError_t launch_rmsnorm_fwd(const NormParams& p, cudaStream_t s) {
     if (!p.residual) return fwd_q<__nv_bfloat16, false>(p, s);
