@@ -50,8 +50,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ void exp2_parts(float2 t, float2& m, float2& scale) {
-    t = make_float2(max_nan(t.x, -126.f), max_nan(t.y, -126.f));
+__device__ __forceinline__ float2 clamp_exponent(float2 t) { return make_float2(max_nan(t.x, -126.f), max_nan(t.y, -126.f)); }
+__device__ __forceinline__ void exp2_parts(float2 t, float2& m, float2& scale) {  // (t clamped)
     const float2 shifted = __fadd2_rn(t, splat(12582912.f));  // 1.5 * 2^23: n in the low bits
     const float2 f = __ffma2_rn(__fadd2_rn(shifted, splat(-12582912.f)), splat(-1.f), t);
     float2 q = __ffma2_rn(f, splat(1.5403508e-4f), splat(1.3390735e-3f));
@@ -118,10 +118,10 @@ struct GlrGate {
     }
     __device__ __forceinline__ float2 log2_gate(float2 raw) const {
         if constexpr (GATE == GLR_LOG) {
-            return __fmul2_rn(raw, splat(kLog2e));
+            return clamp_exponent(__fmul2_rn(raw, splat(kLog2e)));
         } else {
             float2 y;
-            return __fmul2_rn(__fmul2_rn(nA, splat(kLog2e)), softplus2(__fadd2_rn(raw, bias), y));
+            return clamp_exponent(__fmul2_rn(__fmul2_rn(nA, splat(kLog2e)), softplus2(__fadd2_rn(raw, bias), y)));
         }
     }
     // dg / d(raw) = -e^{A_log} sigmoid(z) from the base-2 log gate t = -e^{A_log} softplus(z) / ln 2:
@@ -129,7 +129,7 @@ struct GlrGate {
     __device__ __forceinline__ float2 slope(float2 t) const {
         if constexpr (GATE == GLR_LOG) return splat(1.f);
         float2 a, s;
-        decay(__fmul2_rn(t, inv), a, s);
+        decay(clamp_exponent(__fmul2_rn(t, inv)), a, s);
         return __fmul2_rn(nA, s);
     }
 };

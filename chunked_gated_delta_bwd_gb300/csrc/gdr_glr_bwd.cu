@@ -13,11 +13,15 @@
 
 namespace gdr {
 
-// Bytes bound it: g, h, dh (and x with the complement) are read once, dx and dg written once (10
-// or 12 bytes a token and channel in bf16).  The first walk leaves the base-2 log gates in fp32
-// where g was; the second derives the decays, and the softplus gate's slope, from them.  g and dh
-// are copied two tiles ahead, h and x, which only the second walk needs, one.
-constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS;
+// Bytes bound it with a given log gate (g, h, dh, and x with the complement, are read once, dx and
+// dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 68 us, 74%
+// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 232 us, 52%).
+// The first walk leaves the base-2 log gates in fp32 where g was; the second derives the decays, and
+// the softplus gate's slope, from them.  g and dh are copied ahead, h and x, which only the second
+// walk needs, when their one buffer is free.
+// tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (8: 266 us
+// for 32768 x 2048 with the softplus gate, 4: 247, 2: 232, 1: 239)
+constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS, AT_ONCE = 2;
 template <class TX, bool COMP, bool SUMS>
 struct GlrBwdTile {
     float2 t[3][BWD_WARPS][BWD_SUB][32];    // g as copied (glr_raw_offset), then the log gates
@@ -128,17 +132,17 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
             Run r = run_identity();
             if (!info.any) {
 #pragma unroll 1
-                for (int i = SUB - 4; i >= 0; i -= 4) {
-                    RG graw[4];
-                    float2 dv[4];
+                for (int i = SUB - AT_ONCE; i >= 0; i -= AT_ONCE) {
+                    RG graw[AT_ONCE];
+                    float2 dv[AT_ONCE];
 #pragma unroll
-                    for (int q = 3; q >= 0; --q) {
+                    for (int q = AT_ONCE - 1; q >= 0; --q) {
                         graw[q] = *reinterpret_cast<const RG*>(gs + (i + q) * GP);
                         dv[q] = PX::widen(*reinterpret_cast<const RX*>(ds + (i + q) * GLR_TILE));
                     }
                     __syncwarp();  // every lane has its g of these rows
 #pragma unroll
-                    for (int q = 3; q >= 0; --q) {
+                    for (int q = AT_ONCE - 1; q >= 0; --q) {
                         const float2 t = gate.log2_gate(PG::widen(graw[q]));
                         const float2 a = decay(t);
                         ts[(i + q) * 32] = t;
@@ -209,9 +213,9 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
             };
             if (!info.any) {
 #pragma unroll 1
-                for (int i = SUB - 4; i >= 0; i -= 4) {
+                for (int i = SUB - AT_ONCE; i >= 0; i -= AT_ONCE) {
 #pragma unroll
-                    for (int q = 3; q >= 0; --q) token(i + q, PX::widen(*reinterpret_cast<const RX*>(hs + (i + q) * GLR_TILE)));
+                    for (int q = AT_ONCE - 1; q >= 0; --q) token(i + q, PX::widen(*reinterpret_cast<const RX*>(hs + (i + q) * GLR_TILE)));
                 }
             } else {
                 const uint32_t bits = glr_start_bits(info, i0, nt);
