@@ -246,6 +246,7 @@ __global__ void __launch_bounds__(1024) k_glr_sums(const float4* sums, int chunk
     __shared__ float4 part[32][33];
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c2 = blockIdx.x * 32 + lane;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    cudaGridDependencySynchronize();  // (launched ahead of the end of the kernel before it)
     if (c2 < C / 2) {
 #pragma unroll 4
         for (int k = w; k < chunks; k += 32) {
@@ -290,9 +291,8 @@ struct Launch {
         cudaError_t e = glr_launch(k_glr_bwd<TX, TG, GATE, COMP>, ready, 32 * (BWD_WARPS + GLR_X + 1), sizeof(GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>), 2,
                                    p, maps, s);
         if (e != cudaSuccess || GATE != GLR_SOFTPLUS) return e;
-        k_glr_sums<<<(p.C / 2 + 31) / 32, 1024, 0, s>>>(p.sums, glr_chunks(p), p.C, p.dA_log,
-                                                        p.ddt_bias);
-        return cudaGetLastError();
+        return launch_after((p.C / 2 + 31) / 32, 1024, s, k_glr_sums, (const float4*)p.sums, glr_chunks(p), (int)p.C, p.dA_log,
+                            p.ddt_bias);
     }
 };
 }  // namespace

@@ -114,7 +114,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 // G threads a row, P pieces a thread (G * P * 8 >= C); blocks of `threads` hold threads / G rows and
 // walk the rows with the grid's stride.  TR: the residual stream's type.
 template <int G, int P, class TR, bool RES, int QUANT>
-__global__ void __launch_bounds__(G > 128 ? G : 128) k_rmsnorm_fwd(const NormParams p, int wide) {
+__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1536 / (G > 128 ? G : 128) : 1) k_rmsnorm_fwd(const NormParams p, int wide) {
     constexpr int THREADS = G > 128 ? G : 128, ROWS = THREADS / G;
     __shared__ float red[THREADS / 32];
     const int t = threadIdx.x % G, C = p.C;
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(512) k_rmsnorm_fwd_long(const NormParams p) {
 // dx of a row held in registers, and dweight's sum over the rows of this group of threads, which
 // walks the rows with the grid's stride: one partial row of sums for each block.
 template <int G, int P, class TR, bool DRES>
-__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1024 / (G > 128 ? G : 128) : 1) k_rmsnorm_bwd(const NormParams p, int wide) {
+__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? (768 + G - 1) / (G > 128 ? G : 128) : 1) k_rmsnorm_bwd(const NormParams p, int wide) {
     constexpr int THREADS = G > 128 ? G : 128, ROWS = THREADS / G;
     __shared__ float red[THREADS / 32];
     const int t = threadIdx.x % G, C = p.C;
@@ -429,6 +429,7 @@ __global__ void __launch_bounds__(1024) k_rmsnorm_dw(const float* partial, int r
     __shared__ float part[32][33];
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float v = 0.f;
+    cudaGridDependencySynchronize();  // (launched ahead of the end of the kernel before it)
     if (c < C) {
 #pragma unroll 8
         for (int i = w; i < rows; i += 32) v += partial[(int64_t)i * C + c];
@@ -471,7 +472,7 @@ cudaError_t fwd(const NormParams& p, cudaStream_t s) {
         k_rmsnorm_fwd_long<TR><<<grid_of(p.R, 512, 4), 512, 0, s>>>(p);
         return cudaGetLastError();
     }
-    const int threads = sp.group > 128 ? sp.group : 128, grid = grid_of(p.R, sp.group, 1024 / threads);
+    const int threads = sp.group > 128 ? sp.group : 128, grid = grid_of(p.R, sp.group, 1536 / threads);
     switch (sp.group * 8 + sp.pieces) {
 #define ROWS_OF(G, P)                                                               \
     case G * 8 + P:                                                                 \
@@ -508,17 +509,17 @@ cudaError_t bwd(const NormParams& p, cudaStream_t s) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    k_rmsnorm_dw<<<(p.C + 31) / 32, 1024, 0, s>>>(p.partial, grid, p.C, p.dweight);
-    return cudaGetLastError();
+    return launch_after((p.C + 31) / 32, 1024, s, k_rmsnorm_dw, (const float*)p.partial, grid, (int)p.C, p.dweight);
 }
 
 }  // namespace
 
-// Blocks of the backward: what is resident, so that each walks many rows and the partial rows stay few.
+// Blocks of the backward: what is resident without spilling registers (768 threads), so that each
+// walks many rows and the partial rows stay few.
 int rmsnorm_bwd_blocks(int64_t R, int C) {
     const Split sp = split_of(C);
     if (sp.group == 0) return grid_of(R, 512, 1);
-    return grid_of(R, sp.group, 1024 / (sp.group > 128 ? sp.group : 128));
+    return grid_of(R, sp.group, sp.group == 512 ? (sp.pieces == 1 ? 2 : 1) : 768 / (sp.group > 128 ? sp.group : 128));
 }
 size_t rmsnorm_partial_bytes(int64_t R, int C) { return sizeof(float) * (size_t)rmsnorm_bwd_blocks(R, C) * C; }
 
