@@ -114,7 +114,7 @@ __device__ __forceinline__ float row_reduce(float v, float* red) {
 // G threads a row, P pieces a thread (G * P * 8 >= C); blocks of `threads` hold threads / G rows and
 // walk the rows with the grid's stride.  TR: the residual stream's type.
 template <int G, int P, class TR, bool RES, int QUANT>
-__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1536 / (G > 128 ? G : 128) : 1) k_rmsnorm_fwd(const NormParams p, int wide) {
+__global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? G : 128) : 1) k_rmsnorm_fwd(const NormParams p, int wide) {
     constexpr int THREADS = G > 128 ? G : 128, ROWS = THREADS / G;
     __shared__ float red[THREADS / 32];
     const int t = threadIdx.x % G, C = p.C;
@@ -472,7 +472,7 @@ cudaError_t fwd(const NormParams& p, cudaStream_t s) {
         k_rmsnorm_fwd_long<TR><<<grid_of(p.R, 512, 4), 512, 0, s>>>(p);
         return cudaGetLastError();
     }
-    const int threads = sp.group > 128 ? sp.group : 128, grid = grid_of(p.R, sp.group, 1536 / threads);
+    const int threads = sp.group > 128 ? sp.group : 128, grid = grid_of(p.R, sp.group, sp.pieces == 1 ? 1280 / threads : 1);
     switch (sp.group * 8 + sp.pieces) {
 #define ROWS_OF(G, P)                                                               \
     case G * 8 + P:                                                                 \
