@@ -83,18 +83,17 @@ __device__ __forceinline__ float exp2_ftz(float x) {  // (a result below 2^-126 
 }
 
 // softplus(z) = max(z, 0) + log(1 + y), y = e^{-|z|} in (0, 1]; log(1 + y) = y p(y) with the
-// polynomial p of degree 8 of the least relative error on [0, 1] (3e-8, fitted likewise), which
+// polynomial p of degree 7 of the least relative error on [0, 1] (2e-7, fitted likewise), which
 // keeps the relative accuracy of the slow channels' small softplus.  Returns y too.
 __device__ __forceinline__ float2 softplus2(float2 z, float2& y) {
     y = make_float2(exp2_ftz(-kLog2e * fabsf(z.x)), exp2_ftz(-kLog2e * fabsf(z.y)));
-    float2 q = __ffma2_rn(y, splat(5.2326238e-3f), splat(-2.9504957e-2f));
-    q = __ffma2_rn(y, q, splat(7.8225493e-2f));
-    q = __ffma2_rn(y, q, splat(-1.3663207e-1f));
-    q = __ffma2_rn(y, q, splat(1.9105989e-1f));
-    q = __ffma2_rn(y, q, splat(-2.4842978e-1f));
-    q = __ffma2_rn(y, q, splat(3.3319095e-1f));
-    q = __ffma2_rn(y, q, splat(-4.9999493e-1f));
-    q = __ffma2_rn(y, q, splat(9.9999994e-1f));
+    float2 q = __ffma2_rn(y, splat(-8.5390965e-3f), splat(4.4089239e-2f));
+    q = __ffma2_rn(y, q, splat(-1.0768117e-1f));
+    q = __ffma2_rn(y, q, splat(1.7745204e-1f));
+    q = __ffma2_rn(y, q, splat(-2.4495450e-1f));
+    q = __ffma2_rn(y, q, splat(3.3275476e-1f));
+    q = __ffma2_rn(y, q, splat(-4.9997404e-1f));
+    q = __ffma2_rn(y, q, splat(9.9999982e-1f));
     return __ffma2_rn(y, q, make_float2(fmaxf(z.x, 0.f), fmaxf(z.y, 0.f)));
 }
 
