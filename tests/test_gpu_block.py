@@ -145,6 +145,59 @@ def test_glr_wide_channels():
     _check_glr(_glr_inputs([257, 100], 2050, 62, gate="softplus"), "softplus", True)
 
 
+# Sequences far past one block's reach, where states travel through runs of chunks and of groups of
+# chunks and through the stored states: log gates between 1 / 650 and 2 / 650, whose memory of at most
+# 650 tokens is the one that the tolerances are derived for and carries a state over many chunks
+# (C = 72: whole 16-byte pieces of a row; 66: not; 520: more tiles than are resident).
+LONG = [([9000], 72, 0), ([9000], 66, 2), ([4096, 4096, 64], 72, 1), ([10, 8300, 0, 5, 63, 4097, 1], 66, 0),
+        ([30, 4161, 1, 700, 0, 4099], 72, 2), ([9000], 520, 0), ([1] * 70 + [5000] + [9] * 130 + [2600], 520, 1)]
+
+
+def _long_inputs(lens, C, types, gate):
+    act, gt = TYPES[types]
+    d = _glr_inputs(lens, C, 500 + C + len(lens), act, gt, gate)
+    if gate == "log":
+        gen = torch.Generator().manual_seed(C)
+        d["g"] = (-(1.0 + 1.0 / 64 + 0.9 * torch.rand(sum(lens), C, generator=gen)) / 650.0).to(gt).cuda()
+    return d
+
+
+@pytest.mark.parametrize("gate", ["log", "softplus"])
+@pytest.mark.parametrize("comp", [False, True])
+@pytest.mark.parametrize("lens,C,types", LONG)
+def test_glr_long_sequences(gate, comp, lens, C, types):
+    _check_glr(_long_inputs(lens, C, types, gate), gate, comp)
+
+
+@pytest.mark.parametrize("C", [512, 514])
+def test_glr_calls_on_two_streams_at_once(C):
+    """Two streams, each its own workspace (the second one's blocks wait for room behind the first's)."""
+    ds = [_long_inputs([6000, 200, 3000], C, 0, gate) for gate in ("log", "softplus")]
+
+    def run(d, gate):
+        how = dict(gate=gate, cu_seqlens=d["cu_dev"], h0=d["h0"], **d["par"])
+        f = gdr.glr_fwd(d["x"], d["g"], **how)
+        b = gdr.glr_bwd(d["x"], d["g"], f["h"], d["dh"], dht=d["dht"], **how)
+        return [f["h"], f["ht"]] + [b[k] for k in sorted(b) if b[k] is not None]
+
+    for d in ds:
+        d["cu_dev"], d["par"] = d["cu"].cuda(), _params(d)
+    want = [run(d, gate) for d, gate in zip(ds, ("log", "softplus"))]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [[], []]
+    for _ in range(6):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(ds[i], ("log", "softplus")[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for outs in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
+
+
 def test_glr_gates_of_zero_and_infinity():
     # log gate 0 (nothing forgotten), -inf (everything forgotten) and large positive is not used;
     # the state stays finite and follows the definition exactly enough
