@@ -280,8 +280,6 @@ __device__ __forceinline__ void glr_find_place(const GlrParams& p, GlrInfo& sm, 
             end1 += p.seq_len > GLR_CHUNK ? p.seq_len
                                               : ((unsigned)(t0 + len - 1 - end1) / (unsigned)p.seq_len + 1) * p.seq_len;
     } else {
-        for (int i = lane; i < GLR_CHUNK; i += 32) sm.seq_at_start[i] = 0;
-        __syncwarp();
         // the last sequence that begins at or before t0, by 32 probes at a time
         int lo = 0, hi = p.N;
         while (hi - lo > 1) {
@@ -292,9 +290,15 @@ __device__ __forceinline__ void glr_find_place(const GlrParams& p, GlrInfo& sm, 
         }
         if (lane == 0) sm.seq0 = lo;
         begin0 = min(max(cu[lo], (int64_t)0), t0);
-        end1 = p.T;
+        end1 = cu[lo + 1];
+        const bool inside = begin0 < t0 && end1 > t0 + len && t0 + len < p.T;  // of one sequence
+        end1 = inside ? min(end1, p.T) : p.T;
+        if (!inside) {
+            for (int i = lane; i < GLR_CHUNK; i += 32) sm.seq_at_start[i] = 0;
+            __syncwarp();
+        }
         // the boundaries inside the chunk and at its end, 32 at a time
-        for (int n0 = lo; n0 <= p.N; n0 += 32) {
+        for (int n0 = inside ? p.N + 1 : lo; n0 <= p.N; n0 += 32) {
             const int n = n0 + lane;
             const int64_t b = n <= p.N ? cu[n] : p.T;
             const int64_t i = b - t0;
@@ -527,10 +531,12 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
         const int64_t stride = p.C / 2;
         const int c2 = (c < p.C ? c : 0) / 2;  // (a lane without channels folds channel 0's)
         Run own = run_from_bits(ring.sub[half][0][lane]);
+        if (!any) {
 #pragma unroll
-        for (int i = 1; i < CW; ++i) {
-            const Run next = run_from_bits(ring.sub[half][i][lane]);
-            own = any ? run_then(own, next) : run_then_plain(own, next);
+            for (int i = 1; i < CW; ++i) own = run_then_plain(own, run_from_bits(ring.sub[half][i][lane]));
+        } else {
+#pragma unroll 1
+            for (int i = 1; i < CW; ++i) own = run_then(own, run_from_bits(ring.sub[half][i][lane]));
         }
         if (c < p.C) run_publish(runs.chunk + k * stride + c2, own);
         // The chunks' runs, of which the last chunk of a group makes the group's; then the state and the
@@ -554,11 +560,20 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
         if ((k + 1) % GLR_SUPER == 0 && c < p.C)
             run_publish(runs.state + k / GLR_SUPER * stride + c2, Run{splat(-0.f), run_then(Run{splat(-0.f), y.H}, own).H});
     }
+    if (!any) {
 #pragma unroll
-    for (int i = 0; i < CW; ++i) {
-        const Run next = run_from_bits(ring.sub[half][i][lane]);
-        *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = y.H;
-        y = any ? run_then(y, next) : run_then_plain(y, next);
+        for (int i = 0; i < CW; ++i) {
+            const Run next = run_from_bits(ring.sub[half][i][lane]);
+            *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = y.H;
+            y.H = __ffma2_rn(next.A, y.H, next.H);
+        }
+    } else {
+#pragma unroll 1
+        for (int i = 0; i < CW; ++i) {
+            const Run next = run_from_bits(ring.sub[half][i][lane]);
+            *reinterpret_cast<float2*>(&ring.sub[half][i][lane]) = y.H;
+            y = run_then(y, next);
+        }
     }
     glr_signal(ring, GLR_STATE, j);
 }
