@@ -8,12 +8,13 @@ namespace gdr {
 size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p), p.C); }
 
 // Bytes bound it with a given log gate (x and g are read once, h is written once: 6 bytes a token
-// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 107 us, 75% of the measured copy
-// rate), the arithmetic with the softplus gate (some 45 instructions a token and channel;
-// 30011 x 4096: 228 us, 48%).  The gate is evaluated once: the first walk leaves the decays in fp32
+// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 105 us, 76% of the measured copy
+// rate), the arithmetic with the softplus gate (some 40 instructions a token and channel, all warps'
+// counted; 30011 x 4096: 211 us, 52%) and, in both, the states' way from block to block.  The gate is evaluated once: the first walk leaves the decays in fp32
 // where g was, for the second one, after the state in front of the chunk is known.  Both walk in
 // rolled loops (unrolled over restarts too, the code did not fit the instruction cache, which then
 // bound the kernel); a warp of a chunk in which a sequence begins or ends walks token by token.
+// (tokens of an unrolled step: 30011 x 4096 took 215 us with 8, 219 with 4 or 2)
 constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS, AT_ONCE = 8;
 template <class TX>
 struct GlrFwdTile {
@@ -208,26 +209,51 @@ cudaError_t launch_glr_fwd(const GlrParams& p, cudaStream_t s) {
 
 // One token for each row: y = h = a h + s x on the row's state, in place.  A row whose slot is
 // negative (padding of the batch) or past the pool reads and writes no state; its y is zero.
-template <class TX, class TG, int GATE, bool COMP>
+//
+// Bytes bound it, and at the sizes of a decoding batch the two memory latencies of a slot and its
+// state: a thread takes V channels, four (8 bytes of bf16, 16 of the state) where rows are whole
+// numbers of aligned pieces, else two, and asks for everything else while the slot is on its way.
+// 509 x 4096 with slots and the softplus gate, from cold caches: 7.0 us (8.3 with two channels and the slot first).
+template <class R, int P>
+struct __align__(sizeof(R) * P) Pairs {
+    R v[P];
+};
+template <class TX, class TG, int GATE, bool COMP, int V>
 __global__ void __launch_bounds__(128) k_glr_step(const GlrStepParams p) {
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
-    const int c = (blockIdx.x * 128 + threadIdx.x) * 2;
+    constexpr int P = V / 2;
+    using XS = Pairs<typename PX::raw, P>;
+    using GS = Pairs<typename PG::raw, P>;
+    using States = Pairs<float2, P>;
+    const int c = (blockIdx.x * 128 + threadIdx.x) * V;
     if (c >= p.C) return;
     for (int64_t n = blockIdx.y; n < p.N; n += gridDim.y) {
         const int64_t slot = p.slots ? p.slots[n] : n;
-        float2 st = make_float2(0.f, 0.f);
-        if (slot >= 0 && slot < p.pool) {
-            float2* home = reinterpret_cast<float2*>(p.state + slot * p.C + c);
+        const XS x = *reinterpret_cast<const XS*>(static_cast<const TX*>(p.x) + n * p.ldx + c);
+        const GS g = *reinterpret_cast<const GS*>(static_cast<const TG*>(p.g) + n * p.ldg + c);
+        float2 t[P];
+#pragma unroll
+        for (int i = 0; i < P; ++i) {
             GlrGate<GATE> gate;
-            gate.load(p.A_log, p.dt_bias, c);
-            const float2 xv = PX::widen(*reinterpret_cast<const typename PX::raw*>(static_cast<const TX*>(p.x) + n * p.ldx + c));
-            const float2 gv = PG::widen(*reinterpret_cast<const typename PG::raw*>(static_cast<const TG*>(p.g) + n * p.ldg + c));
-            st = *home;
-            st = glr_update<COMP>(decay(gate.log2_gate(gv)), st, xv);
-            *home = st;
+            gate.load(p.A_log, p.dt_bias, c + 2 * i);
+            t[i] = gate.log2_gate(PG::widen(g.v[i]));
         }
-        *reinterpret_cast<typename PX::raw*>(static_cast<TX*>(p.y) + n * p.C + c) = PX::narrow(st);
+        XS y;
+        if (slot >= 0 && slot < p.pool) {
+            States* home = reinterpret_cast<States*>(p.state + slot * p.C + c);
+            States st = *home;
+#pragma unroll
+            for (int i = 0; i < P; ++i) {
+                st.v[i] = glr_update<COMP>(decay(t[i]), st.v[i], PX::widen(x.v[i]));
+                y.v[i] = PX::narrow(st.v[i]);
+            }
+            *home = st;
+        } else {
+#pragma unroll
+            for (int i = 0; i < P; ++i) y.v[i] = PX::zero();
+        }
+        *reinterpret_cast<XS*>(static_cast<TX*>(p.y) + n * p.C + c) = y;
     }
 }
 
@@ -237,8 +263,11 @@ struct StepLaunch {
     cudaStream_t s;
     template <class TX, class TG, int GATE, bool COMP>
     cudaError_t run() const {
-        const dim3 grid((p.C / 2 + 127) / 128, p.N < 65535 ? p.N : 65535);
-        k_glr_step<TX, TG, GATE, COMP><<<grid, 128, 0, s>>>(p);
+        const unsigned rows = p.N < 65535 ? p.N : 65535;
+        const bool wide = p.C % 4 == 0 && p.ldx % 4 == 0 && p.ldg % 4 == 0 &&
+                          ((reinterpret_cast<uintptr_t>(p.x) % (4 * sizeof(TX))) | (reinterpret_cast<uintptr_t>(p.g) % (4 * sizeof(TG)))) == 0;
+        if (wide) k_glr_step<TX, TG, GATE, COMP, 4><<<dim3((p.C / 4 + 127) / 128, rows), 128, 0, s>>>(p);
+        else k_glr_step<TX, TG, GATE, COMP, 2><<<dim3((p.C / 2 + 127) / 128, rows), 128, 0, s>>>(p);
         return cudaGetLastError();
     }
 };
