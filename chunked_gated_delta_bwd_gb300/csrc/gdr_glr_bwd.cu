@@ -14,13 +14,13 @@
 namespace gdr {
 
 // Bytes bound it with a given log gate (g, h, dh, and x with the complement, are read once, dx and
-// dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 68 us, 74%
-// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 232 us, 52%).
+// dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 69 us, 73%
+// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 218 us, 55%).
 // The first walk leaves the base-2 log gates in fp32 where g was; the second derives the decays, and
 // the softplus gate's slope, from them.  g and dh are copied ahead, h and x, which only the second
 // walk needs, when their one buffer is free.
-// tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (8: 266 us
-// for 32768 x 2048 with the softplus gate, 4: 247, 2: 232, 1: 239)
+// tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (4: 226 us
+// for 32768 x 2048 with the softplus gate, 2: 218, 1: 229)
 constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS, AT_ONCE = 2;
 template <class TX, bool COMP, bool SUMS>
 struct GlrBwdTile {

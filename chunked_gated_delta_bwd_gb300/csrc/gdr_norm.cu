@@ -12,7 +12,8 @@
 // Bytes bound both.  A group of threads holds a row in registers, eight channels (16 bytes of
 // bf16) a thread at a time, from its loads to its stores, so that every tensor passes once; the
 // next row's loads are in flight meanwhile (without that the 8-bit forward of 32768 x 2048 took
-// 175 us instead of 86).  The group is the smallest with one piece a thread: a row of up to
+// 175 us instead of 81, which is 87% of the measured copy rate; the backward of 8191 x 2048 with a
+// float32 stream takes 44 us, 79%).  The group is the smallest with one piece a thread: a row of up to
 // 256 channels needs no barrier but the warp's shuffles.
 #include <cuda_fp8.h>
 
