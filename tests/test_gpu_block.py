@@ -570,3 +570,31 @@ def test_conv_step_on_a_pool(K, rows, C):
         want[s] = torch.tensor(new[0]).to(BF16)
         assert _close(f64(y[i]), yi[0], BF16)
     assert torch.equal(state, want) and not y[~on.cuda()].any()
+
+
+# Steps of four channels a thread (rows of whole aligned pieces) and of two (all others).
+@pytest.mark.parametrize("shift", [0, 2, 4])
+@pytest.mark.parametrize("C", [4, 516, 518])
+def test_steps_on_column_slices(shift, C):
+    """x and g as slices at an offset of `shift` columns of wider rows, against the contiguous step's answer."""
+    gen = torch.Generator().manual_seed(300 + C)
+    rows, wide = 9, C + 12
+    both = torch.randn(rows, 2 * wide, generator=gen).to(BF16).cuda()
+    x, g = both[:, shift:shift + C], both[:, wide + shift:wide + shift + C]
+    pool = torch.randn(rows, C, generator=gen).cuda()
+    A_log, dt_bias = torch.rand(C, generator=gen).cuda() - 1.0, torch.randn(C, generator=gen).cuda()
+    how = dict(gate="softplus", complement=True, A_log=A_log, dt_bias=dt_bias)
+    state, again = pool.clone(), pool.clone()
+    y = gdr.glr_step(x, g, state, **how)
+    assert torch.equal(y, gdr.glr_step(x.contiguous(), g.contiguous(), again, **how)) and torch.equal(state, again)
+    for i in range(rows):
+        want, _ = ref.glr_fwd(f64(x[i:i + 1]), f64(g[i:i + 1]), [0, 1], f64(pool[i:i + 1]), complement=True,
+                              A_log=f64(A_log), dt_bias=f64(dt_bias))
+        assert rel_l2(f64(state[i]), want[0]) <= 5e-6  # one token: the gate's 3e-6 and roundings
+    w, b = torch.randn(C, 4, generator=gen).cuda(), torch.randn(C, generator=gen).cuda()
+    taps = torch.randn(rows, 3, C, generator=gen).to(BF16).cuda()
+    state = taps.clone()
+    y = gdr.conv1d_step(x, state, w, b)
+    want, new = ref.conv1d_fwd(f64(x), f64(w), f64(b), list(range(rows + 1)), True, f64(taps))
+    assert _close(f64(y), want, BF16)
+    assert torch.equal(state, torch.tensor(new).to(BF16).cuda())
