@@ -37,10 +37,6 @@ template <> struct PairOf<float> {
     static __device__ __forceinline__ raw zero() { return make_float2(0.f, 0.f); }
 };
 
-// Makes the compiler forget what it derived from a value, so that a later use derives it again
-// instead of keeping the result in a register.
-__device__ __forceinline__ void forget(float2& v) { asm volatile("" : "+f"(v.x), "+f"(v.y)); }
-
 // The gate is evaluated in base 2: t = g / ln 2, a = 2^t.
 //
 // 2^t = 2^n (1 + m) with n the integer nearest t and m = 2^f - 1 = f q(f), |f| <= 1/2, q the
