@@ -15,10 +15,13 @@ namespace gdr {
 
 // Bytes bound it with a given log gate (g, h, dh, and x with the complement, are read once, dx and
 // dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 69 us, 73%
-// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 218 us, 55%).
+// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 219 us, 55%).
 // The first walk leaves the base-2 log gates in fp32 where g was; the second derives the decays, and
 // the softplus gate's slope, from them.  g and dh are copied ahead, h and x, which only the second
 // walk needs, when their one buffer is free.
+// Warps without a sequence's beginning or end among their tokens walk in the short loops also where
+// the chunk has one (512 sequences of 32768 tokens, 2048 channels, softplus: 271 us; 286 when all of
+// the chunk's warps walked token by token).
 // tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (4: 226 us
 // for 32768 x 2048 with the softplus gate, 2: 218, 1: 229)
 constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS, AT_ONCE = 2;
@@ -130,7 +133,10 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
             const TG* gs = reinterpret_cast<const TG*>(reinterpret_cast<char*>(&tl.t[j % 3][w]) + RAW) + 2 * lane;
             constexpr int GP = GLR_TILE;
             Run r = run_identity();
-            if (!info.any) {
+            const int nt =
+                info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)(chunks - 1 - tick.x) * GLR_CHUNK + i0))) : SUB;
+            const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
+            if (bits == 0 && nt == SUB) {
 #pragma unroll 1
                 for (int i = SUB - AT_ONCE; i >= 0; i -= AT_ONCE) {
                     RG graw[AT_ONCE];
@@ -151,8 +157,6 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                     }
                 }
             } else {
-                const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)(chunks - 1 - tick.x) * GLR_CHUNK + i0)));
-                const uint32_t bits = glr_start_bits(info, i0, nt);
 #pragma unroll 1
                 for (int i = nt - 1; i >= 0; --i) {
                     const RG graw = *reinterpret_cast<const RG*>(gs + i * GP);
@@ -211,14 +215,14 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                 dx -= ld;
                 dg -= ld;
             };
-            if (!info.any) {
+            const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
+            if (bits == 0 && nt == SUB) {
 #pragma unroll 1
                 for (int i = SUB - AT_ONCE; i >= 0; i -= AT_ONCE) {
 #pragma unroll
                     for (int q = AT_ONCE - 1; q >= 0; --q) token(i + q, PX::widen(*reinterpret_cast<const RX*>(hs + (i + q) * GLR_TILE)));
                 }
             } else {
-                const uint32_t bits = glr_start_bits(info, i0, nt);
 #pragma unroll 1
                 for (int i = nt - 1; i >= 0; --i) {
                     const int64_t row = (int64_t)glr_seq_at(info, i0 + i) * p.C + c;

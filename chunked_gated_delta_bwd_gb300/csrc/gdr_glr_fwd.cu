@@ -8,12 +8,15 @@ namespace gdr {
 size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p), p.C); }
 
 // Bytes bound it with a given log gate (x and g are read once, h is written once: 6 bytes a token
-// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 105 us, 76% of the measured copy
+// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 106 us, 75% of the measured copy
 // rate), the arithmetic with the softplus gate (some 40 instructions a token and channel, all warps'
-// counted; 30011 x 4096: 211 us, 52%) and, in both, the states' way from block to block.  The gate is evaluated once: the first walk leaves the decays in fp32
-// where g was, for the second one, after the state in front of the chunk is known.  Both walk in
-// rolled loops (unrolled over restarts too, the code did not fit the instruction cache, which then
-// bound the kernel); a warp of a chunk in which a sequence begins or ends walks token by token.
+// counted; 30011 x 4096: 211 us, 52%) and, in both, the states' way from block to block.  The gate is
+// evaluated once: the first walk leaves the decays in fp32 where g was, for the second one, after the
+// state in front of the chunk is known.  Both walk in rolled loops (unrolled over restarts too, the
+// code did not fit the instruction cache, which then bound the kernel); a warp in whose tokens a
+// sequence begins or ends folds its run again, token by token, from the decays it has just left
+// (32768 tokens in 512 sequences, 2048 channels, softplus: 151 us; 167 with the gates evaluated token
+// by token in every warp of such a chunk; 119 for one sequence).
 // (tokens of an unrolled step: 30011 x 4096 took 215 us with 8, 219 with 4 or 2)
 constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS, AT_ONCE = 8;
 template <class TX>
@@ -98,34 +101,31 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
             const TG* gs = reinterpret_cast<const TG*>(reinterpret_cast<char*>(&tl.a[j % SLOTS][w]) + RAW) + 2 * lane;
             constexpr int GP = GLR_TILE;
             Run r = run_identity();
-            if (!info.any) {
+            const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)tick.x * GLR_CHUNK + i0))) : SUB;
+            const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
 #pragma unroll 1
-                for (int i = 0; i < SUB; i += AT_ONCE) {
-                    RG graw[AT_ONCE];
-                    float2 xv[AT_ONCE];
+            for (int i = 0; i < SUB; i += AT_ONCE) {
+                RG graw[AT_ONCE];
+                float2 xv[AT_ONCE];
 #pragma unroll
-                    for (int q = 0; q < AT_ONCE; ++q) {
-                        graw[q] = *reinterpret_cast<const RG*>(gs + (i + q) * GP);
-                        xv[q] = PX::widen(*reinterpret_cast<const RX*>(xs + (i + q) * GLR_TILE));
-                    }
-                    __syncwarp();  // every lane has its g of these rows
-#pragma unroll
-                    for (int q = 0; q < AT_ONCE; ++q) {
-                        const float2 a = decay(gate.log2_gate(PG::widen(graw[q])));
-                        as[(i + q) * 32] = a;
-                        r.A = __fmul2_rn(r.A, a);
-                        r.H = glr_update<COMP>(a, r.H, xv[q]);
-                    }
+                for (int q = 0; q < AT_ONCE; ++q) {
+                    graw[q] = *reinterpret_cast<const RG*>(gs + (i + q) * GP);
+                    xv[q] = PX::widen(*reinterpret_cast<const RX*>(xs + (i + q) * GLR_TILE));
                 }
-            } else {
-                const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)tick.x * GLR_CHUNK + i0)));
-                const uint32_t bits = glr_start_bits(info, i0, nt);
+                __syncwarp();  // every lane has its g of these rows
+#pragma unroll
+                for (int q = 0; q < AT_ONCE; ++q) {
+                    const float2 a = decay(gate.log2_gate(PG::widen(graw[q])));
+                    as[(i + q) * 32] = a;
+                    r.A = __fmul2_rn(r.A, a);
+                    r.H = glr_update<COMP>(a, r.H, xv[q]);
+                }
+            }
+            if (bits != 0 || nt < SUB) {  // again with the restarts
+                r = run_identity();
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i) {
-                    const RG graw = *reinterpret_cast<const RG*>(gs + i * GP);
-                    __syncwarp();
-                    const float2 a = decay(gate.log2_gate(PG::widen(graw)));
-                    as[i * 32] = a;
+                    const float2 a = as[i * 32];
                     if (bits >> i & 1) {
                         r.A = splat(-0.f);
                         r.H = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(info, i0 + i) * p.C + c)
@@ -149,7 +149,9 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
             const TX* xs = &tl.x[(j - LATE) % SLOTS][w][0][2 * lane];
             const float2* as = &tl.a[(j - LATE) % SLOTS][w][0][lane];
             float2 y = *reinterpret_cast<const float2*>(&ring.sub[(j - LATE) % (LATE + 1)][w][lane]);
-            if (!info.any) {
+            const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - t)) : SUB;
+            const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
+            if (bits == 0 && nt == SUB) {
 #pragma unroll 1
                 for (int i = 0; i < SUB; i += 4) {
 #pragma unroll
@@ -159,8 +161,6 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                     }
                 }
             } else {
-                const int nt = (int)min((int64_t)SUB, max((int64_t)0, p.T - t));
-                const uint32_t bits = glr_start_bits(info, i0, nt);
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i, h += ld) {
                     if (bits >> i & 1)
