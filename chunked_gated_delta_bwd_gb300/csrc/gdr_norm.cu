@@ -12,7 +12,7 @@
 // Bytes bound both.  A group of threads holds a row in registers, eight channels (16 bytes of
 // bf16) a thread at a time, from its loads to its stores, so that every tensor passes once; the
 // next row's loads are in flight meanwhile (without that the 8-bit forward of 32768 x 2048 took
-// 175 us instead of 81, which is 87% of the measured copy rate; the backward of 8191 x 2048 with a
+// 175 us; now 85, 83% of the measured copy rate; the backward of 8191 x 2048 with a
 // float32 stream takes 44 us, 79%).  The group is the smallest with one piece a thread: a row of up to
 // 256 channels needs no barrier but the warp's shuffles.
 #include <cuda_fp8.h>
@@ -29,6 +29,13 @@ namespace {
 struct Eight {
     float v[8];
 };
+__device__ __forceinline__ float2 two(const Eight& e, int q) { return make_float2(e.v[2 * q], e.v[2 * q + 1]); }
+__device__ __forceinline__ void set_two(Eight& e, int q, float2 f) {
+    e.v[2 * q] = f.x;
+    e.v[2 * q + 1] = f.y;
+}
+// two bf16, by a shift and a mask (the conversion function takes three instructions)
+__device__ __forceinline__ float2 widen_pair(uint32_t r) { return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u)); }
 template <class T> struct RawOf;
 template <> struct RawOf<__nv_bfloat16> {
     uint4 u;
@@ -37,7 +44,7 @@ template <> struct RawOf<__nv_bfloat16> {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack_bf16(w[i]);
+            const float2 f = widen_pair(w[i]);
             e.v[2 * i] = f.x;
             e.v[2 * i + 1] = f.y;
         }
@@ -87,6 +94,28 @@ __device__ __forceinline__ void st8n(T* p, const Eight& e, int n, bool wide) {
 }
 __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
     return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+// The scale of values up to m: m / 448, 1 where all are zero.  Where m / 448 rounds to zero it is the
+// smallest float32, so that zeros stay zero.
+__device__ __forceinline__ float scale_of(float m) { return m > 0.f ? fmaxf(m / 448.f, 1.4e-45f) : 1.f; }
+// The codes of y / scale.  A product with 1 / scale (two steps of the last place off at most) is within
+// 3 2^-23 of the quotient, so that products to either side by 2^-21 have the quotient's code unless a tie
+// lies between them: then (some 10^-5 of the values), or where 1 / scale is far from the normal numbers,
+// the division itself decides.  (Dividing every value of 32768 x 2048 takes 98 us, this 85, the product
+// alone, which takes the other code next to a tie and is infinite for scales below 2^-128, 81.)
+__device__ __forceinline__ void codes_of(const Eight& y, float scale, uint32_t (&h)[4]) {
+    const float inv = __fdividef(1.f, scale), under = inv * (1.f - 0x1p-21f), over = inv * (1.f + 0x1p-21f);
+    uint32_t differ = scale > 0x1p-120f && scale < 0x1p120f ? 0 : 1;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float2 a = __fmul2_rn(two(y, q), make_float2(under, under)), b = __fmul2_rn(two(y, q), make_float2(over, over));
+        h[q] = e4m3x2(a.x, a.y);
+        differ |= h[q] ^ e4m3x2(b.x, b.y);
+    }
+    if (differ) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) h[q] = e4m3x2(y.v[2 * q] / scale, y.v[2 * q + 1] / scale);
+    }
 }
 
 // A row of C channels is walked in pieces of 8 by G threads: thread t has pieces t, t + G, ...
@@ -150,7 +179,7 @@ __global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? 
         const int64_t row = row0 + threadIdx.x / G;
         const bool live = row < p.R;
         Eight s[P];
-        float ss = 0.f;
+        float2 ss = make_float2(0.f, 0.f);
         if (live) {
 #pragma unroll
             for (int i = 0; i < P; ++i) {
@@ -160,13 +189,13 @@ __global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? 
                     if (RES) {
                         const Eight r = rr[i].widen();
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) {
-                            const float v = s[i].v[q] + r.v[q];
-                            s[i].v[q] = sizeof(TR) == 4 ? v : __bfloat162float(__float2bfloat16_rn(v));
+                        for (int q = 0; q < 4; ++q) {
+                            const float2 v = __fadd2_rn(two(s[i], q), two(r, q));
+                            set_two(s[i], q, sizeof(TR) == 4 ? v : widen_pair(pack_bf16(v.x, v.y)));
                         }
                     }
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) ss = fmaf(s[i].v[q], s[i].v[q], ss);
+                    for (int q = 0; q < 4; ++q) ss = __ffma2_rn(two(s[i], q), two(s[i], q), ss);
                 }
             }
         }
@@ -178,7 +207,7 @@ __global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? 
                 if (c < C) st8n(static_cast<TR*>(p.res_out) + row * C + c, s[i], C - c, wide);
             }
         }
-        const float rstd = rsqrtf(fmaf(row_reduce<G, false>(ss, red), invC, p.eps));
+        const float rstd = rsqrtf(fmaf(row_reduce<G, false>(ss.x + ss.y, red), invC, p.eps));
         if (live && t == 0) p.rstd[row] = rstd;
         float most[QUANT == 2 ? P : 1];
         most[0] = 0.f;
@@ -188,9 +217,10 @@ __global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? 
             float m = 0.f;
             if (live && c < C) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    s[i].v[q] = s[i].v[q] * rstd * w[i].v[q];
-                    if (QUANT) m = fmaxf(m, fabsf(s[i].v[q]));
+                for (int q = 0; q < 4; ++q) {
+                    const float2 y = __fmul2_rn(__fmul2_rn(two(s[i], q), make_float2(rstd, rstd)), two(w[i], q));
+                    set_two(s[i], q, y);
+                    if (QUANT) m = fmaxf(m, fmaxf(fabsf(y.x), fabsf(y.y)));
                 }
             }
             if (QUANT == 1) most[0] = fmaxf(most[0], m);
@@ -210,12 +240,10 @@ __global__ void __launch_bounds__(G > 128 ? G : 128, P == 1 ? 1280 / (G > 128 ? 
             if (QUANT == 0) {
                 st8n(static_cast<__nv_bfloat16*>(p.y) + row * C + c, s[i], C - c, wide);
             } else {
-                const float m = most[QUANT == 2 ? i : 0], scale = m > 0.f ? m * (1.f / 448.f) : 1.f,
-                            inv = m > 0.f ? __fdividef(448.f, m) : 1.f;
+                const float scale = scale_of(most[QUANT == 2 ? i : 0]);
                 if (QUANT == 2 ? c % 128 == 0 : c == 0) p.scale[row * nb + (QUANT == 2 ? c / 128 : 0)] = scale;
                 uint32_t h[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) h[q] = e4m3x2(s[i].v[2 * q] * inv, s[i].v[2 * q + 1] * inv);
+                codes_of(s[i], scale, h);
                 unsigned char* y = static_cast<unsigned char*>(p.y) + row * C + c;
                 if (wide) {
                     *reinterpret_cast<uint2*>(y) = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
@@ -286,10 +314,10 @@ __global__ void __launch_bounds__(512) k_rmsnorm_fwd_long(const NormParams p) {
                 __syncthreads();
                 m = fmaxf(red[threadIdx.x / 64 * 2], red[threadIdx.x / 64 * 2 + 1]);
             }
-            const float scale = m > 0.f ? m / 448.f : 1.f, inv = 1.f / scale;
+            const float scale = scale_of(m);
             if (c < C) {
                 if (p.quant == 2 ? threadIdx.x % 64 == 0 : c == 0) p.scale[row * nb + (p.quant == 2 ? c / 128 : 0)] = scale;
-                *reinterpret_cast<uint16_t*>(static_cast<unsigned char*>(p.y) + row * C + c) = (uint16_t)e4m3x2(y.x * inv, y.y * inv);
+                *reinterpret_cast<uint16_t*>(static_cast<unsigned char*>(p.y) + row * C + c) = (uint16_t)e4m3x2(y.x / scale, y.y / scale);
             }
         }
     }

@@ -322,7 +322,8 @@ gdr_status glr_step(int32_t rows, int32_t channels, int32_t pool, int32_t gate, 
  *    weight fp32 [C]; rstd fp32 [rows].
  *  * quant: GDR_QUANT_NONE: y bf16.  GDR_QUANT_ROW / GDR_QUANT_BLOCK: y in 8 bits (e4m3) and
  *    scale fp32 [rows, 1] / [rows, ceil(C / 128)]: scale = max |y| / 448 over the row / over
- *    each 128 channels (1 where they are all zero), y stored as e4m3(y / scale). */
+ *    each 128 channels (1 where they are all zero; the smallest float32 where the quotient
+ *    rounds to zero), y stored as e4m3(y / scale). */
 #define GDR_QUANT_NONE 0
 #define GDR_QUANT_ROW 1
 #define GDR_QUANT_BLOCK 2

@@ -446,6 +446,54 @@ def test_rmsnorm_rows_of_zero_and_huge():
             assert torch.isfinite(out["scale"][[0, 2, 5]]).all()
 
 
+@pytest.mark.parametrize("C", [64, 256, 1000, 12290, 40000])
+@pytest.mark.parametrize("quant", ["token", "block"])
+def test_rmsnorm_codes_of_tiny_values(C, quant):
+    """Rows around the smallest floats, zeros among them: max |y| / 448 is subnormal or rounds to zero,
+    and 448 / max |y| overflows.  Zeros are code 0, no code is NaN, and codes times scale are y to
+    e4m3's half step and the subnormal scale's (2^-150 of up to 448 each)."""
+    tiny = torch.tensor([1e-37, 1e-38, 1e-39, 1e-40, 0.0], dtype=F32)
+    gen = torch.Generator().manual_seed(C)
+    x = (torch.rand(5, C, generator=gen) + 0.5) * torch.sign(torch.randn(5, C, generator=gen)) * tiny[:, None]
+    x[:, ::3] = 0
+    x[:, 0] = tiny
+    w = 1.0 + 0.2 * torch.randn(C, generator=gen)
+    w[C // 2:] *= 1e-6  # blocks whose values are a millionth of the others': scales below the floats
+    x, w = x.to(BF16).cuda(), w.cuda()
+    out = gdr.rmsnorm_fwd(x, w, quant=quant)
+    code, scale = f64(out["y"].float()), f64(out["scale"])
+    assert np.isfinite(code).all() and np.isfinite(scale).all() and (scale > 0).all()
+    y, _ = ref.rmsnorm(f64(x), f64(w), 1e-6)
+    assert (code[y == 0] == 0).all()
+    block = C if quant == "token" else 128
+    scale = np.repeat(scale, block, axis=1)[:, :C]
+    assert np.all(np.abs(code * scale - y) <= 2.0 ** -4 * np.abs(y) + 2.0 ** -10 * scale + 1e-4 * np.abs(y) + 450 * 2.0 ** -150)
+
+
+@pytest.mark.parametrize("R,C", [(40, 64), (9, 2048), (5, 8192), (3, 20000)])
+@pytest.mark.parametrize("quant", ["token", "block"])
+def test_rmsnorm_codes_are_of_the_quotient(R, C, quant):
+    """The scale is max |y| / 448 and the code e4m3(y / scale), both to the last bit, for the float32 y
+    = s rstd w of the returned rstd: also where the quotient lies next to the middle of two codes."""
+    gen = torch.Generator().manual_seed(R)
+    x = torch.sign(torch.randn(R, C, generator=gen))
+    codes = torch.arange(1, 126, dtype=torch.uint8).view(torch.float8_e4m3fn).float()
+    middle = (codes[1:] + codes[:-1]) / 2
+    w = middle[torch.randint(0, 124, (C,), generator=gen)] * (447.0 + torch.rand(1, generator=gen)) / 448.0
+    w[::64] = 447.7
+    w = w * (1 + torch.randint(-2, 3, (C,), generator=gen) * 2.0 ** -23)
+    x, w = x.to(BF16).cuda(), w.cuda()
+    out = gdr.rmsnorm_fwd(x, w, quant=quant)
+    y = (x.float() * out["rstd"][:, None] * w).cpu()
+    block = C if quant == "token" else 128
+    nb = -(-C // block)
+    most = torch.nn.functional.pad(y.abs(), (0, nb * block - C)).view(R, nb, block).amax(2)
+    scale = most / 448.0
+    assert torch.equal(out["scale"].cpu(), scale)
+    want = (y / scale.repeat_interleave(block, dim=1)[:, :C]).to(torch.float8_e4m3fn)
+    assert torch.equal(out["y"].cpu().view(torch.uint8), want.view(torch.uint8))
+
+
 def test_rmsnorm_layouts():
     # [B, T, H, D] per head, column slices of a wider tensor, no rows
     x, w, _ = _norm_inputs(24, 64, None, 8)
