@@ -137,6 +137,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                 info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)(chunks - 1 - tick.x) * GLR_CHUNK + i0))) : SUB;
             const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
             if (bits == 0 && nt == SUB) {
+                float2 sum = splat(0.f);
 #pragma unroll 1
                 for (int i = SUB - AT_ONCE; i >= 0; i -= AT_ONCE) {
                     RG graw[AT_ONCE];
@@ -152,10 +153,11 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                         const float2 t = gate.log2_gate(PG::widen(graw[q]));
                         const float2 a = decay(t);
                         ts[(i + q) * 32] = t;
-                        r.A = __fmul2_rn(r.A, a);
+                        sum = __fadd2_rn(sum, t);
                         r.H = __fmul2_rn(a, __fadd2_rn(r.H, dv[q]));
                     }
                 }
+                r.A = run_decay<GATE>(sum);
             } else {
 #pragma unroll 1
                 for (int i = nt - 1; i >= 0; --i) {

@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
             const TG* gs = reinterpret_cast<const TG*>(reinterpret_cast<char*>(&tl.a[j % SLOTS][w]) + RAW) + 2 * lane;
             constexpr int GP = GLR_TILE;
             Run r = run_identity();
+            float2 sum = splat(0.f);
             const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - ((int64_t)tick.x * GLR_CHUNK + i0))) : SUB;
             const uint32_t bits = info.any ? glr_start_bits(info, i0, nt) : 0;
 #pragma unroll 1
@@ -115,12 +116,13 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                 __syncwarp();  // every lane has its g of these rows
 #pragma unroll
                 for (int q = 0; q < AT_ONCE; ++q) {
-                    const float2 a = decay(gate.log2_gate(PG::widen(graw[q])));
+                    const float2 t = gate.log2_gate(PG::widen(graw[q])), a = decay(t);
                     as[(i + q) * 32] = a;
-                    r.A = __fmul2_rn(r.A, a);
+                    sum = __fadd2_rn(sum, t);
                     r.H = glr_update<COMP>(a, r.H, xv[q]);
                 }
             }
+            r.A = run_decay<GATE>(sum);
             if (bits != 0 || nt < SUB) {  // again with the restarts
                 r = run_identity();
 #pragma unroll 1

@@ -198,6 +198,39 @@ def test_glr_calls_on_two_streams_at_once(C):
             assert all(torch.equal(a, b) for a, b in zip(outs, want[i]))
 
 
+# Slow channels, each by itself, over 5000 tokens.  The state is rounded twice a token, at random:
+# sqrt(5000) 2^-24 = 4.2e-6 of it; 1 - a is off by a few 2^-24 of itself (the softplus gate's polynomial:
+# 2e-7), which the state follows, 6e-7.  1e-5.
+def _slow(gate, C):
+    gen = torch.Generator().manual_seed(400 + C)
+    n = lambda *s: torch.randn(*s, generator=gen)  # noqa: E731
+    slow = torch.tensor([1e-2, 1e-3, 1e-4, 1e-5])[torch.arange(C) % 4]
+    x, h0 = n(5000, C), n(1, C)
+    if gate == "log":
+        return x, h0, -slow * torch.exp(0.3 * n(5000, C)), {}
+    # (softplus(z) is near e^z here)
+    g = 0.3 * n(5000, C)
+    return x, h0, g, {"A_log": torch.rand(C, generator=gen) - 0.5, "dt_bias": torch.log(slow)}
+
+
+def _off(got, want):
+    return np.sqrt(((f64(got) - want) ** 2).sum(0) / (want ** 2).sum(0))
+
+
+@pytest.mark.parametrize("gate", ["log", "softplus"])
+@pytest.mark.parametrize("C", [64, 66])
+def test_glr_decay_of_slow_channels(gate, C):
+    """The decay of h0 over many tokens, forward and (of dht) backward."""
+    _, h0, g, par = _slow(gate, C)
+    zero, par_gpu = torch.zeros_like(g), {k: v.cuda() for k, v in par.items()}
+    out = gdr.glr_fwd(zero.cuda(), g.cuda(), h0=h0.cuda(), gate=gate, **par_gpu)
+    want, _ = ref.glr_fwd(f64(zero), f64(g), [0, 5000], f64(h0), **{k: f64(v) for k, v in par.items()})
+    assert _off(out["h"], want).max() <= 1e-5
+    back = gdr.glr_bwd(zero.cuda(), g.cuda(), out["h"], zero.cuda(), dht=h0.cuda(), gate=gate, **par_gpu)
+    want = ref.glr_bwd(f64(zero), f64(g), want, f64(zero), [0, 5000], None, f64(h0), **{k: f64(v) for k, v in par.items()})
+    assert _off(back["dx"], want["dx"]).max() <= 1e-5
+
+
 def test_glr_gates_of_zero_and_infinity():
     # log gate 0 (nothing forgotten), -inf (everything forgotten) and large positive is not used;
     # the state stays finite and follows the definition exactly enough
