@@ -43,7 +43,7 @@ template <> struct PairOf<float> {
 // polynomial of degree 5 with the least relative error (1.1e-8; fitted by Lawson's reweighted
 // least squares).  A slow channel (t near 0) keeps its state for hundreds of tokens, over which
 // an error of a that has one sign grows with the number of tokens; n is 0 there, so a = 1 + m is
-// rounded once, and s = 1 - a = -m does not cancel.  No hardware exponential and no branch: 15
+// rounded once, and s = 1 - a = -m does not cancel (glr_update).  No hardware exponential and no branch: 15
 // instructions for two channels.  Decays below 2^-126 count as 2^-126; NaN stays NaN.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
@@ -145,10 +145,37 @@ struct GlrGate {
     }
 };
 
-// The new state of a token: a h + x, or a h + (1 - a) x with the complement, as x + a (h - x).
+// The new state of a token, a h + x, or with the complement a h + (1 - a) x, from the number that the
+// forward keeps of a token.  1 - a of a slow channel is not to be had from a (rounded, a is off by up to
+// 3e-8 whatever 1 - a is: at 1e-4 the states came out 3e-4 off), nor the a of a fast one from 1 - a.  So
+// with the complement what is kept is a - 1 (its sign bit set, also for zero) where the integer part of
+// -t is 0, and a (at least +0) elsewhere: h + (a - 1) (h - x), or x + a (h - x).  A token with a = 1 leaves
+// the state as it is, whatever x.
+__device__ __forceinline__ bool keeps_rest(float v) { return __float_as_int(v) < 0; }  // v is a - 1
 template <bool COMP>
-__device__ __forceinline__ float2 glr_update(float2 a, float2 h, float2 x) {
-    return __ffma2_rn(a, COMP ? __ffma2_rn(x, splat(-1.f), h) : h, x);
+__device__ __forceinline__ float2 decay_of_kept(float2 v) {
+    return COMP ? make_float2(keeps_rest(v.x) ? 1.f + v.x : v.x, keeps_rest(v.y) ? 1.f + v.y : v.y) : v;
+}
+template <bool COMP>
+__device__ __forceinline__ float2 glr_update(float2 v, float2 h, float2 x) {
+    if (!COMP) return __ffma2_rn(v, h, x);
+    const float2 from = make_float2(keeps_rest(v.x) ? h.x : x.x, keeps_rest(v.y) ? h.y : x.y);
+    return __ffma2_rn(v, __ffma2_rn(x, splat(-1.f), h), from);
+}
+// the same from the base-2 log gate t; returns what is kept.  (The softplus gate's t is -0 at most.)
+template <int GATE, bool COMP>
+__device__ __forceinline__ float2 glr_update_by_gate(float2 t, float2& h, float2 x) {
+    float2 m, scale;
+    exp2_parts(t, m, scale);
+    float2 v = __ffma2_rn(scale, m, scale), from = x;
+    if (!COMP) {
+        h = __ffma2_rn(v, h, x);
+        return v;
+    }
+    if (t.x >= -0.5f && (GATE == GLR_SOFTPLUS || t.x <= 0.f)) v.x = -fabsf(m.x), from.x = h.x;
+    if (t.y >= -0.5f && (GATE == GLR_SOFTPLUS || t.y <= 0.f)) v.y = -fabsf(m.y), from.y = h.y;
+    h = __ffma2_rn(v, __ffma2_rn(x, splat(-1.f), h), from);
+    return v;
 }
 
 // ---------------------------------------------------------------------------

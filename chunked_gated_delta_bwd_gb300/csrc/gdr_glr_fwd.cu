@@ -22,7 +22,7 @@ constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS, AT_ONCE = 8;
 template <class TX>
 struct GlrFwdTile {
     static constexpr int LATE = 2, SLOTS = LATE + 2;
-    float2 a[SLOTS][FWD_WARPS][FWD_SUB][32];    // g as copied (glr_raw_offset), then the decays
+    float2 a[SLOTS][FWD_WARPS][FWD_SUB][32];    // g as copied (glr_raw_offset), then what is kept of the decays
     TX x[SLOTS][FWD_WARPS][FWD_SUB][GLR_TILE];
     GlrRing<FWD_WARPS, LATE> ring;
 };
@@ -116,10 +116,9 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                 __syncwarp();  // every lane has its g of these rows
 #pragma unroll
                 for (int q = 0; q < AT_ONCE; ++q) {
-                    const float2 t = gate.log2_gate(PG::widen(graw[q])), a = decay(t);
-                    as[(i + q) * 32] = a;
+                    const float2 t = gate.log2_gate(PG::widen(graw[q]));
+                    as[(i + q) * 32] = glr_update_by_gate<GATE, COMP>(t, r.H, xv[q]);
                     sum = __fadd2_rn(sum, t);
-                    r.H = glr_update<COMP>(a, r.H, xv[q]);
                 }
             }
             r.A = run_decay<GATE>(sum);
@@ -127,15 +126,15 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                 r = run_identity();
 #pragma unroll 1
                 for (int i = 0; i < nt; ++i) {
-                    const float2 a = as[i * 32];
+                    const float2 v = as[i * 32];
                     if (bits >> i & 1) {
                         r.A = splat(-0.f);
                         r.H = p.h0 && live ? *reinterpret_cast<const float2*>(p.h0 + (int64_t)glr_seq_at(info, i0 + i) * p.C + c)
                                            : splat(0.f);
                     } else {
-                        r.A = __fmul2_rn(r.A, a);
+                        r.A = __fmul2_rn(r.A, decay_of_kept<COMP>(v));
                     }
-                    r.H = glr_update<COMP>(a, r.H, PX::widen(*reinterpret_cast<const RX*>(xs + i * GLR_TILE)));
+                    r.H = glr_update<COMP>(v, r.H, PX::widen(*reinterpret_cast<const RX*>(xs + i * GLR_TILE)));
                 }
             }
             ring.sub[j % (LATE + 1)][w][lane] = run_bits(r);
@@ -247,7 +246,9 @@ __global__ void __launch_bounds__(128) k_glr_step(const GlrStepParams p) {
             States st = *home;
 #pragma unroll
             for (int i = 0; i < P; ++i) {
-                st.v[i] = glr_update<COMP>(decay(t[i]), st.v[i], PX::widen(x.v[i]));
+                float2 a, s, xv = PX::widen(x.v[i]);
+                decay(t[i], a, s);
+                st.v[i] = __ffma2_rn(a, st.v[i], COMP ? __fmul2_rn(s, xv) : xv);
                 y.v[i] = PX::narrow(st.v[i]);
             }
             *home = st;

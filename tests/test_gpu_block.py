@@ -231,6 +231,38 @@ def test_glr_decay_of_slow_channels(gate, C):
     assert _off(back["dx"], want["dx"]).max() <= 1e-5
 
 
+@pytest.mark.parametrize("gate", ["log", "softplus"])
+@pytest.mark.parametrize("C", [64, 66])
+def test_glr_complement_of_slow_channels(gate, C):
+    """The input scale 1 - a to its own precision."""
+    x, h0, g, par = _slow(gate, C)
+    par_gpu, par = {k: v.cuda() for k, v in par.items()}, {k: f64(v) for k, v in par.items()}
+    out = gdr.glr_fwd(x.cuda(), g.cuda(), h0=h0.cuda(), gate=gate, complement=True, **par_gpu)
+    want, _ = ref.glr_fwd(f64(x), f64(g), [0, 5000], f64(h0), complement=True, **par)
+    assert _off(out["h"], want).max() <= 1e-5
+    # one token on a state of zero: y = (1 - a) x (the gate and three roundings)
+    y = gdr.glr_step(x[:1].cuda(), g[:1].cuda(), torch.zeros(1, C, device="cuda"), gate=gate, complement=True, **par_gpu)
+    want, _ = ref.glr_fwd(f64(x[:1]), f64(g[:1]), [0, 1], complement=True, **par)
+    assert np.all(np.abs(f64(y) - want) <= 1e-6 * np.abs(want))
+
+
+@pytest.mark.parametrize("types", range(3))
+def test_glr_complement_keeps_the_state_at_decay_one(types):
+    """A log gate of zero (either sign) passes the state on to the last bit, however large x is."""
+    act, gt = TYPES[types]
+    gen = torch.Generator().manual_seed(17)
+    h0 = torch.randn(2, 72, generator=gen).to(act).float().cuda()
+    x = (1e6 * torch.randn(300, 72, generator=gen)).to(act).cuda()
+    g = torch.zeros(300, 72, dtype=gt, device="cuda")
+    g[::2] = -0.0
+    out = gdr.glr_fwd(x, g, h0=h0, cu_seqlens=_cu([130, 170]).cuda(), complement=True)
+    assert torch.equal(out["ht"], h0)
+    assert torch.equal(out["h"].float(), torch.cat([h0[:1].expand(130, 72), h0[1:].expand(170, 72)]))
+    state = h0.clone()
+    gdr.glr_step(x[:2], g[:2], state, complement=True)
+    assert torch.equal(state, h0)
+
+
 def test_glr_gates_of_zero_and_infinity():
     # log gate 0 (nothing forgotten), -inf (everything forgotten) and large positive is not used;
     # the state stays finite and follows the definition exactly enough
