@@ -53,6 +53,7 @@ def _lib():
                 ("gdr_conv1d_step", st, [i32] * 4 + [vp, i64] + [vp] * 4 + [i32, vp, vp])):
             f = getattr(L, name)
             f.restype, f.argtypes = res, args
+        L.glr_test_stall_next_call.restype, L.glr_test_stall_next_call.argtypes = None, [ctypes.c_int]
         _LIB = L
     return _LIB
 
@@ -339,3 +340,9 @@ def conv1d_step(x, state, weight, bias=None, slots=None, silu=True, out=None):
     if rc:
         _check(rc, "gdr_conv1d_step")
     return y
+
+
+def test_stall_next_glr(block: int):
+    """Test hook: block ``block`` of the next glr_fwd / glr_bwd gives up at its second tile, as after a
+    wait that ran out (GDR_DEV_TIMEOUT)."""
+    _lib().glr_test_stall_next_call(int(block))

@@ -34,6 +34,7 @@ struct GlrParams {
     int64_t ldx, ldg;           // row strides of x and g in elements
     int gate, complement;       // gate function (gdr.h), x scaled by 1 - a
     int act_f32, gate_f32;      // element types: float32 instead of bf16
+    int test_stall;             // test hook: block index + 1 held at its second tile (0: none)
     int wide;                   // every row of every tensor read is a whole number of aligned 16-byte pieces
     int* status;                // workspace: status word, ticket counter, published runs
     float4* sums;               // workspace: per-chunk sums of the softplus gate's parameters

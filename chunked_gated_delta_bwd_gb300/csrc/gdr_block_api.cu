@@ -1,6 +1,7 @@
 // C ABI of the operators around the delta rule in a recurrent block (declared in
 // include/gdr.h): argument checks and launches.
 #include <limits.h>
+#include <atomic>
 #include <string.h>
 
 #include "gdr_block.h"
@@ -75,6 +76,8 @@ static gdr_status check_glr(const glr_shape* sh, GlrParams* p) {
     return GDR_OK;
 }
 
+static std::atomic<int> g_glr_stall{0};  // glr_test_stall_next_call: block index + 1, or 0
+
 static size_t glr_workspace(const GlrParams& p) { return 256 + glr_published_bytes(p) + glr_sums_bytes(p); }
 
 // whether rows of C elements at this stride are whole numbers of aligned 16-byte pieces
@@ -128,6 +131,7 @@ gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const f
     if (done) return ok();
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0; p.h = h; p.ht = ht;
     p.wide = rows_wide(p, x, p.ldx, p.act_f32) && rows_wide(p, g, p.ldg, p.gate_f32);
+    p.test_stall = g_glr_stall.exchange(0);
     cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_fwd(p, s); });
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence launch");
 }
@@ -159,9 +163,12 @@ gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const f
     p.dx = dx; p.dg = dg; p.dh0 = dh0; p.dA_log = dA_log; p.ddt_bias = ddt_bias;
     p.wide = (!p.complement || rows_wide(p, x, p.ldx, p.act_f32)) && rows_wide(p, g, p.ldg, p.gate_f32) &&
              rows_wide(p, h, p.C, p.act_f32);
+    p.test_stall = g_glr_stall.exchange(0);
     cudaError_t e = timed(GDR_KERNEL_GLR, s, [&] { return launch_glr_bwd(p, s); }, soft ? 2 : 1);
     return e == cudaSuccess ? ok() : cuda_fail(e, "gated linear recurrence backward launch");
 }
+
+void glr_test_stall_next_call(int block) { g_glr_stall.store(block >= 0 ? block + 1 : 0); }
 
 gdr_status glr_step(int32_t rows, int32_t channels, int32_t pool, int32_t gate, int32_t complement, int32_t act_type,
                     int32_t gate_type, const void* x, int64_t x_stride, const void* g, int64_t g_stride,

@@ -207,7 +207,10 @@ __device__ __forceinline__ float2 glr_update_by_gate(float2 t, float2& h, float2
 // ---------------------------------------------------------------------------
 constexpr int GLR_CHUNK = 64, GLR_TILE = 64;
 constexpr int GLR_GROUP = 8, GLR_SUPER = 64;  // chunks in a published group; from one published state to the next
-constexpr int GLR_SPIN = 1 << 20;               // polls of one published run before giving up
+// After how many polls waits are given up: for another block's run (a poll takes 0.7 us: 50 ms, once a
+// block), of a compute warp for its block's others, and of those (the hardware holds a poll of a barrier for
+// some 4 us: 0.5 s and 4 s; each longer than what it waits for may take).
+constexpr int GLR_SPIN = 1 << 16, GLR_SPIN_COMPUTE = 1 << 17, GLR_SPIN_LONG = 1 << 20;
 __host__ __device__ inline int glr_chunks(const GlrParams& p) { return (int)((uint64_t)(p.T + GLR_CHUNK - 1) / GLR_CHUNK); }
 
 // a run of tokens for two channels
@@ -386,11 +389,18 @@ __device__ __forceinline__ int glr_seq_at(const GlrInfo& sm, int i) {
     }
 }
 
+// A wait has run out: the block's warps wait no more.
+__device__ __forceinline__ void glr_give_up(volatile int* over, int* status) {
+    *over = 1;
+    atomicOr(status, ST_MMA_TIMEOUT);
+}
+
 // Up to eight published runs for this lane's channels, all loads in flight at once: one at `first`
 // (if `has`), then n <= 7 rows.  Their fold in order; only the first run of all may contain a
-// restart (or be a state: A = -0).  Waits for each as long as it takes; one that never comes, whose
-// block holds an earlier ticket, is recorded.
-__device__ __forceinline__ Run glr_fold(const uint4* first, bool has, const uint4* rows, int64_t stride, int n, int* status) {
+// restart (or be a state: A = -0).  Waits for each; one that does not come, whose block holds an earlier
+// ticket, is recorded, and what is there is taken (`over` set: without waiting any more).
+__device__ __forceinline__ Run glr_fold(const uint4* first, bool has, const uint4* rows, int64_t stride, int n, volatile int* over,
+                                        int* status) {
     uint4 v[8];
     bool there = true;
     const uint4* at = rows;
@@ -403,6 +413,7 @@ __device__ __forceinline__ Run glr_fold(const uint4* first, bool has, const uint
 #pragma unroll
     for (int j = 0; j < 8; ++j) there &= run_there(v[j]);
     if (!there) {
+        int limit = *over ? 1 : GLR_SPIN;
         at = rows;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -410,8 +421,11 @@ __device__ __forceinline__ Run glr_fold(const uint4* first, bool has, const uint
                 int spin = 0;
 #pragma unroll 1
                 do v[j] = run_poll(j == 0 ? first : at);
-                while (!run_there(v[j]) && ++spin < GLR_SPIN);
-                if (!run_there(v[j])) atomicOr(status, ST_MMA_TIMEOUT);
+                while (!run_there(v[j]) && ++spin < limit);
+                if (!run_there(v[j])) {
+                    glr_give_up(over, status);
+                    limit = 1;
+                }
             }
             if (j > 0) at += stride;
         }
@@ -458,9 +472,10 @@ __device__ __forceinline__ void glr_empty_sequences(const GlrParams& p, const fl
 //   late:  rows that only the second walk needs are there (copying warp)
 //   state: the states before each warp's tokens are there (exchange warp)
 //   free:  the results are written; the tile's rows may be overwritten (compute warps)
-// and, as a named barrier (an exchange warp waits for it most of its time, which costs no
-// instructions there),
 //   runs:  the warps' runs are there (compute warps)
+// Every wait is bounded.  The warp whose wait for another warp runs out records it in the status word and in
+// `over`, which the exchange warps and the copying one look at while they wait for long, and leaves, storing
+// nothing more; so do the others when theirs run out, the copying warp when its copies have landed.
 constexpr int GLR_X = 3;
 template <int CW_, int LATE_>
 struct GlrRing {
@@ -469,52 +484,66 @@ struct GlrRing {
     GlrInfo info[8];            // (j % 8)
     float4 gate[4][32];         // the gate's parameters (softplus), as GlrGate wants them
     int4 tick[8];               // (j % 8) the tile's chunk in the order of the scan (-1: no more), first channel
-    uint64_t bar[6][4];         // (the ticks take two rows: the copying warp is up to eight tiles ahead of who reads them)
+    uint64_t bar[7][4];         // (the ticks take two rows: the copying warp is up to eight tiles ahead of who reads them)
+    uint64_t never;             // (nothing arrives here: for the test of a wait that runs out)
+    int over;                   // a wait has run out
+    int looked[GLR_X], left;    // the last tile that each exchange warp has looked at; how many of them have left
 };
-enum { GLR_TICK = 0, GLR_FULL = 2, GLR_LATE = 3, GLR_STATE = 4, GLR_FREE = 5 };
+enum { GLR_TICK = 0, GLR_FULL = 2, GLR_LATE = 3, GLR_STATE = 4, GLR_FREE = 5, GLR_RUNS = 6 };
 // tile j's barrier and its phase
 template <class Ring>
 __device__ __forceinline__ uint32_t glr_bar(Ring& ring, int kind, int j) {
     return smem_u32(&ring.bar[kind][kind == GLR_TICK ? j & 7 : j & 3]);
 }
 __device__ __forceinline__ uint32_t glr_phase(int kind, int j) { return (kind == GLR_TICK ? j >> 3 : j >> 2) & 1; }
-template <class Ring>
-__device__ __forceinline__ void glr_runs_there(int j) {
-    tc::named_arrive(1 + (j & 3), 32 * (Ring::CW + 1));
-}
-template <class Ring>
-__device__ __forceinline__ void glr_runs_wait(int j) {
-    tc::named_sync(1 + (j & 3), 32 * (Ring::CW + 1));
-}
 
 // (rows copied in 16-byte pieces arrive as a count of bytes that one lane announces, others as
 // every lane's own copies)
 template <class Ring>
 __device__ __forceinline__ void glr_ring_init(Ring& ring, bool wide) {
-    if (threadIdx.x < 24) {
+    if (threadIdx.x < 28) {
         const int kind = threadIdx.x / 4, rows = wide ? 1 : 32;
         tc::mbar_init(smem_u32(&ring.bar[kind][threadIdx.x % 4]),
-                      kind == GLR_FREE ? Ring::CW : kind == GLR_FULL ? rows + 1 : kind == GLR_LATE ? rows : 1);
+                      kind == GLR_FREE ? Ring::CW : kind == GLR_RUNS ? 32 * Ring::CW : kind == GLR_FULL ? rows + 1 : kind == GLR_LATE ? rows : 1);
+    } else if (threadIdx.x == 28) {
+        tc::mbar_init(smem_u32(&ring.never), 1);
+        for (int i = 0; i < 8; ++i) ring.tick[i] = make_int4(-1, 0, 0, 0);
+        for (int i = 0; i < GLR_X; ++i) ring.looked[i] = -1;
+        ring.over = ring.left = 0;
     }
     __syncthreads();
 }
-// Waits for tile j's barrier.  (Every barrier is reached: what its warp waits for elsewhere is
-// bounded.)  NAP: nanoseconds of sleep between polls, for waits that are long and not urgent: the
-// exchange warps' polls took a quarter of the kernel's instructions.
-template <int NAP, class Ring>
+// The compute warps' wait for tile j's barrier; the thread leaves if it runs out.  (Threads of its warp that
+// still saw the phase complete go on, rightly, to their next wait.  What else is done between the polls, or
+// called after many, makes every wait end later: with a look at the clock and the flag 30011 x 4096 took
+// 275 us instead of 241.)
+template <class Ring>
 __device__ __forceinline__ void glr_wait(const GlrParams& p, Ring& ring, int kind, int j) {
-    const uint32_t bar = glr_bar(ring, kind, j), parity = glr_phase(kind, j);
-    if (NAP == 0) {
-        if (!tc::mbar_wait(bar, parity, 1 << 22)) atomicOr(p.status, ST_MMA_TIMEOUT);
-    } else {
-        bool there = false;
-#pragma unroll 1
-        for (int it = 0; it < 1 << 20 && !there; ++it) {
-            there = tc::mbar_wait(bar, parity, 1);
-            if (!there) __nanosleep(NAP);
-        }
-        if (!there) atomicOr(p.status, ST_MMA_TIMEOUT);
+    if (!tc::mbar_wait(glr_bar(ring, kind, j), glr_phase(kind, j), GLR_SPIN_COMPUTE)) {
+        glr_give_up(&ring.over, p.status);
+        asm volatile("exit;");
     }
+}
+// The other warps', who talk across their lanes: false for the whole warp if it or another wait of the block
+// has run out.  Their waits are long and not urgent: NAP nanoseconds of sleep between polls (which took a
+// quarter of the kernel's instructions).
+static __device__ __noinline__ bool glr_wait_on(uint32_t bar, uint32_t parity, volatile int* over, int* status) {
+    for (int it = 0; it < GLR_SPIN_LONG / 16 && !*over; ++it)
+        if (tc::mbar_wait(bar, parity, 16)) return true;
+    glr_give_up(over, status);
+    return false;
+}
+template <int NAP, class Ring>
+__device__ __forceinline__ bool glr_wait_long(const GlrParams& p, Ring& ring, int kind, int j) {
+    const uint32_t bar = glr_bar(ring, kind, j), parity = glr_phase(kind, j);
+    bool there = false;
+#pragma unroll 1
+    for (int it = 0; it < 1 << 14 && !there; ++it) {
+        there = tc::mbar_wait(bar, parity, 1);
+        if (!there) __nanosleep(NAP);
+    }
+    if (!there) there = glr_wait_on(bar, parity, &ring.over, p.status);
+    return __all_sync(~0u, there);
 }
 // What this warp has written for tile j is there.
 template <class Ring>
@@ -523,17 +552,49 @@ __device__ __forceinline__ void glr_signal(Ring& ring, int kind, int j) {
     if (threadIdx.x % 32 == 0)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(glr_bar(ring, kind, j)) : "memory");
 }
-
+// The same for this thread, without waiting for the others of its warp (backward 32768 x 2048: 230 us, 232
+// with one arrival a warp).
+template <class Ring>
+__device__ __forceinline__ void glr_arrive(Ring& ring, int kind, int j) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(glr_bar(ring, kind, j)) : "memory");
+}
+// The copying warp's end: its copies for tiles [from, to) have landed.  They report to the barrier that the
+// tile's exchange warp reports to as well; if that has left before it did, this warp does in its place.
+template <class Ring>
+__device__ __forceinline__ void glr_landed(const GlrParams& p, Ring& ring, int from, int to) {
+    for (int j = max(from, 0); j < to; ++j) {
+        if (glr_wait_long<20>(p, ring, GLR_FULL, j)) continue;
+        for (int it = 0; *const_cast<volatile int*>(&ring.left) < GLR_X && it < 1 << 24; ++it) __nanosleep(100);
+        __syncwarp();
+        if (threadIdx.x % 32 == 0 && *const_cast<volatile int*>(&ring.looked[j % GLR_X]) < j)
+            asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(glr_bar(ring, GLR_FULL, j)) : "memory");
+        tc::mbar_wait(glr_bar(ring, GLR_FULL, j), glr_phase(GLR_FULL, j), GLR_SPIN_COMPUTE);
+    }
+}
+// An exchange warp leaves.
+template <class Ring>
+__device__ __forceinline__ void glr_leave(Ring& ring) {
+    __syncwarp();
+    __threadfence_block();
+    if (threadIdx.x % 32 == 0) atomicAdd(&ring.left, 1);
+}
+// (test hook) A wait of block test_stall - 1 for what never comes.
+template <class Ring>
+__device__ __forceinline__ bool glr_stalled(const GlrParams& p, Ring& ring, int j) {
+    if (p.test_stall != (int)blockIdx.x + 1 || j != 1) return false;
+    if (!tc::mbar_wait(smem_u32(&ring.never), 0, 1 << 12)) glr_give_up(&ring.over, p.status);
+    return true;
+}
 // A block's tickets, in the order of its tiles: they count in the workspace when there is something
 // to wait for.
 __device__ __forceinline__ unsigned glr_ticket(const GlrParams& p, int chunks, int j) {
     return chunks == 1 ? blockIdx.x + j * gridDim.x : atomicAdd(reinterpret_cast<unsigned*>(p.status) + 1, 1u);
 }
 // An exchange warp's work ahead on tile j: its sequences and place, the gate's parameters.  Returns
-// the tile's chunk and first channel (chunk -1: no more tiles).
+// the tile's chunk and first channel (chunk -1: no more tiles, or a wait has run out).
 template <bool BWD, class Ring>
 __device__ __forceinline__ int4 glr_look(const GlrParams& p, Ring& ring, int chunks, int j, int lane) {
-    glr_wait<50>(p, ring, GLR_TICK, j);
+    if (!glr_wait_long<50>(p, ring, GLR_TICK, j)) return make_int4(-1, 0, 0, 0);
     const int4 tick = ring.tick[j & 7];
     const int k = tick.x, kc = BWD ? chunks - 1 - k : k, c = tick.y + 2 * lane;
     if (k >= 0) {
@@ -546,20 +607,22 @@ __device__ __forceinline__ int4 glr_look(const GlrParams& p, Ring& ring, int chu
         glr_find_place<BWD>(p, ring.info[j & 7], chunks, k, t0, (int)min((int64_t)GLR_CHUNK, p.T - t0), lane);
     }
     glr_signal(ring, GLR_FULL, j);
+    if (lane == 0) *const_cast<volatile int*>(&ring.looked[j % GLR_X]) = j;
     if (k >= 0) glr_empty_sequences(p, BWD ? p.dht : p.h0, BWD ? p.dh0 : p.ht, kc, chunks, c, c < p.C, tick.y == 0);
     return tick;
 }
 
-// An exchange warp's work on tile j: its run, published; the states before its warps.
+// An exchange warp's work on tile j: its run, published; the states before its warps.  False if its wait
+// has run out.
 template <bool BWD, class Ring>
-__device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, const GlrRuns& runs, int chunks, int j, int4 tick,
+__device__ __forceinline__ bool glr_exchange(const GlrParams& p, Ring& ring, const GlrRuns& runs, int chunks, int j, int4 tick,
                                              int lane) {
     constexpr int CW = Ring::CW;
     const int half = j % (Ring::LATE + 1), k = tick.x, c = tick.y + 2 * lane;
     const GlrInfo& at = ring.info[j & 7];
     const bool any = at.any;
     Run y = run_identity();
-    glr_runs_wait<Ring>(j);
+    if (!glr_wait_long<50>(p, ring, GLR_RUNS, j)) return false;
     if (chunks > 1) {
         const int64_t stride = p.C / 2;
         const int c2 = (c < p.C ? c : 0) / 2;  // (a lane without channels folds channel 0's)
@@ -589,7 +652,7 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
         for (int older = 0; older < 2; ++older) {
             const Run r = glr_fold(runs.state + (int64_t)(k / GLR_SUPER - 1) * stride + c2, older && at.state,
                                    (older ? runs.group + at.group0 * stride : runs.chunk + at.chunk0 * stride) + c2, stride,
-                                   older ? at.groups : at.chunks, p.status);
+                                   older ? at.groups : at.chunks, &ring.over, p.status);
             if (older) {
                 y = run_then_plain(r, near);
             } else {
@@ -617,6 +680,7 @@ __device__ __forceinline__ void glr_exchange(const GlrParams& p, Ring& ring, con
         }
     }
     glr_signal(ring, GLR_STATE, j);
+    return true;
 }
 
 // The copying warp's copies of a tile's rows of one tensor into shared memory.  Where every row of

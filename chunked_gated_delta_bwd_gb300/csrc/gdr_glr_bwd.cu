@@ -57,12 +57,14 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
         constexpr int XP = GLR_TILE * sizeof(TX);
         unsigned id = lane == 0 ? glr_ticket(p, chunks, 0) : 0;
         int k1 = -1, c1 = 0, k2 = -1, c2 = 0;  // tiles j - 1, j - 2
+        int copied = 0, late = 0;
         for (int j = 0, over = 0; over < GLR_X; ++j) {
             id = __shfl_sync(~0u, id, 0);
             const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
             if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
             glr_signal(ring, GLR_TICK, j);
-            if (j >= 3 && (k >= 0 || k2 >= 0)) glr_wait<20>(p, ring, GLR_FREE, j - 3);
+            if (j >= 3 && (k >= 0 || k2 >= 0) && !glr_wait_long<20>(p, ring, GLR_FREE, j - 3)) break;
+            if (glr_stalled(p, ring, j)) break;
             if (k >= 0) {
                 const int64_t t0 = (int64_t)(chunks - 1 - k) * GLR_CHUNK;
                 const int rows = (int)min((int64_t)GLR_CHUNK, p.T - t0), cols = min(GLR_TILE, p.C - c0);
@@ -71,6 +73,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                                                            static_cast<const TG*>(p.g), p.ldg, t0, 0, rows, c0, cols, wide, bar, lane);
                 glr_copy_rows<XP, 8 * XP>(&tl.dh[j % 3], &maps.dh, static_cast<const TX*>(p.dh), p.C, t0, 0, rows, c0, cols, wide, bar, lane);
                 glr_report(bar, wide);
+                copied = j + 1;
                 if (wide && lane == 0) {  // h and x have one buffer: on their way to L2 until it is free
                     tc::tma_prefetch_2d(&maps.h, c0, (int)t0 - 1);
                     if (COMP) tc::tma_prefetch_2d(&maps.x, c0, (int)t0);
@@ -86,11 +89,14 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                 if (COMP)
                     glr_copy_rows<XP, 8 * XP>(&tl.x, &maps.x, static_cast<const TX*>(p.x), p.ldx, t0, 0, rows, c2, cols, wide, bar, lane);
                 glr_report(bar, wide);
+                late = j - 1;
             }
             k2 = k1; c2 = c1; k1 = k; c1 = c0;
             // (taken as late as that, so that tiles with near tickets are worked on at the same time)
             id = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
         }
+        glr_landed(p, ring, copied - 3, copied);
+        for (int j = max(late - 2, 0); j < late; ++j) tc::mbar_wait(glr_bar(ring, GLR_LATE, j), glr_phase(GLR_LATE, j), GLR_SPIN_COMPUTE);
         return;
     }
     if (w >= BWD_WARPS) {
@@ -109,18 +115,18 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
         };
         int4 tick = glr_look<true>(p, ring, chunks, w - BWD_WARPS, lane);
         for (int j = w - BWD_WARPS; tick.x >= 0; j += GLR_X) {
-            glr_exchange<true>(p, ring, runs, chunks, j, tick, lane);
-            glr_wait<50>(p, ring, GLR_FREE, j);
+            if (!glr_exchange<true>(p, ring, runs, chunks, j, tick, lane) || !glr_wait_long<50>(p, ring, GLR_FREE, j)) break;
             add_sums(tick, j);
             tick = glr_look<true>(p, ring, chunks, j + GLR_X, lane);
         }
+        glr_leave(ring);
         return;
     }
     const int pos = BWD_WARPS - 1 - w;  // this warp's place in the order of the scan
 
     int4 before = make_int4(-1, 0, 0, 0);  // tile j - 1
     for (int j = 0;; ++j) {
-        glr_wait<0>(p, ring, GLR_FULL, j);
+        glr_wait(p, ring, GLR_FULL, j);
         const int4 tick = ring.tick[j & 7];
         if (tick.x >= 0) {
             const GlrInfo& info = ring.info[j & 7];
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
                 }
             }
             ring.sub[j & 1][pos][lane] = run_bits(r);
-            glr_runs_there<Ring>(j);
+            glr_arrive(ring, GLR_RUNS, j);
         }
         if (before.x >= 0) {
             const int kc = chunks - 1 - before.x, c = before.y + 2 * lane;
@@ -185,8 +191,8 @@ __global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(con
             const int64_t t0 = (int64_t)kc * GLR_CHUNK + i0;
             GlrGate<GATE> gate;
             gate.set(ring.gate[(j - 1) & 3][lane]);
-            glr_wait<0>(p, ring, GLR_LATE, j - 1);
-            glr_wait<0>(p, ring, GLR_STATE, j - 1);
+            glr_wait(p, ring, GLR_LATE, j - 1);
+            glr_wait(p, ring, GLR_STATE, j - 1);
             const GlrInfo& info = ring.info[(j - 1) & 7];
             const int nt = info.any ? (int)min((int64_t)SUB, max((int64_t)0, p.T - t0)) : SUB;
             const TX* ds = &tl.dh[(j - 1) % 3][w][0][2 * lane];

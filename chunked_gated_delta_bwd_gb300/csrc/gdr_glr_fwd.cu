@@ -48,13 +48,15 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
     glr_ring_init(ring, wide);
     if (w == FWD_WARPS + GLR_X) {  // tickets and copies
         unsigned id = lane == 0 ? glr_ticket(p, chunks, 0) : 0;
-        for (int j = 0, over = 0; over < GLR_X; ++j) {
+        int copied = 0, over = 0;
+        for (int j = 0; over < GLR_X; ++j) {
             id = __shfl_sync(~0u, id, 0);
             const int k = id < all ? (int)(id / tiles) : -1, c0 = (int)(id - id / tiles * tiles) * GLR_TILE;
             if (lane == 0) ring.tick[j & 7] = make_int4(k, c0, 0, 0);
             glr_signal(ring, GLR_TICK, j);
+            if ((k >= 0 || over == 0) && j >= SLOTS && !glr_wait_long<20>(p, ring, GLR_FREE, j - SLOTS)) break;
+            if (glr_stalled(p, ring, j)) break;
             if (k >= 0) {
-                if (j >= SLOTS) glr_wait<20>(p, ring, GLR_FREE, j - SLOTS);
                 const int64_t t0 = (int64_t)k * GLR_CHUNK;
                 const int rows = (int)min((int64_t)GLR_CHUNK, p.T - t0), cols = min(GLR_TILE, p.C - c0);
                 const uint32_t bar = glr_announce(ring, GLR_FULL, j, wide, GLR_CHUNK * GLR_TILE * (sizeof(TX) + sizeof(TG)), lane);
@@ -63,21 +65,24 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                 glr_copy_rows<GLR_TILE * sizeof(TX), 8 * GLR_TILE * sizeof(TX)>(
                     &tl.x[j % SLOTS], &maps.x, static_cast<const TX*>(p.x), p.ldx, t0, 0, rows, c0, cols, wide, bar, lane);
                 glr_report(bar, wide);
+                copied = j + 1;
             } else {
                 if (over++ == 0) glr_report(glr_announce(ring, GLR_FULL, j, wide, 0, lane), wide);
             }
             // (taken as late as that, so that tiles with near tickets are worked on at the same time)
             id = lane == 0 && id < all ? glr_ticket(p, chunks, j + 1) : id;
         }
+        glr_landed(p, ring, copied - SLOTS + (over > 0), copied);  // (the end's mark has the next tile's barrier)
         return;
     }
     if (w >= FWD_WARPS) {
         const GlrRuns runs = glr_runs(p.status, chunks, p.C);
         int4 tick = glr_look<false>(p, ring, chunks, w - FWD_WARPS, lane);
         for (int j = w - FWD_WARPS; tick.x >= 0; j += GLR_X) {
-            glr_exchange<false>(p, ring, runs, chunks, j, tick, lane);
+            if (!glr_exchange<false>(p, ring, runs, chunks, j, tick, lane)) break;
             tick = glr_look<false>(p, ring, chunks, j + GLR_X, lane);
         }
+        glr_leave(ring);
         return;
     }
     int4 before[LATE];  // tiles j - LATE .. j - 1
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
     for (int j = 0;; ++j) {
         const bool more = tick.x >= 0;  // (past the last tile only second walks are left)
         if (more) {
-            glr_wait<0>(p, ring, GLR_FULL, j);
+            glr_wait(p, ring, GLR_FULL, j);
             tick = ring.tick[j & 7];
         }
         if (tick.x >= 0) {
@@ -138,10 +143,10 @@ __global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(con
                 }
             }
             ring.sub[j % (LATE + 1)][w][lane] = run_bits(r);
-            glr_runs_there<Ring>(j);
+            glr_arrive(ring, GLR_RUNS, j);
         }
         if (before[0].x >= 0) {
-            glr_wait<0>(p, ring, GLR_STATE, j - LATE);
+            glr_wait(p, ring, GLR_STATE, j - LATE);
             const GlrInfo& info = ring.info[(j - LATE) & 7];
             const int c = before[0].y + 2 * lane;
             const bool live = c < p.C;

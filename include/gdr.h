@@ -279,7 +279,8 @@ gdr_status gdr_conv1d_step(int32_t rows, int32_t channels, int32_t width, int32_
  *    leaves fp32 gives infinities or NaN even where the state itself would not.
  *  * Inconsistent cu_seqlens raise GDR_DEV_BAD_SEQLENS in the workspace's status word; the
  *    results are then meaningless, but no access leaves the tensors.  GDR_DEV_TIMEOUT there means
- *    that a bounded wait between blocks ran out (results meaningless too).
+ *    that a bounded wait ran out: results are missing or meaningless, again without such an access.
+ *    To read the word, give a workspace of your own.
  *  * The workspace need not be initialised; calls that may overlap need one each. */
 #define GLR_GATE_LOG 0
 #define GLR_GATE_SOFTPLUS 1
@@ -355,6 +356,12 @@ gdr_status gdr_workspace_status(const void* workspace, void* stream, int* device
  * wait of the kernels takes when the tensor cores do not answer, without a GPU fault.
  * cta < 0 clears a pending request.  Not thread-safe with concurrent gdr_bwd calls. */
 void gdr_test_stall_next_call(int cta);
+
+/* The same for the next glr_fwd or glr_bwd call on any thread: block `block` of its kernel gives up at
+ * its second tile, as after a bounded wait inside a block that ran out (GDR_DEV_TIMEOUT): its warps store
+ * nothing more and leave when its copies have landed; the waits of other blocks for what it would have
+ * published run out too, and they end without.  block < 0 clears a pending request. */
+void glr_test_stall_next_call(int block);
 
 /* Message of the last error returned on the calling thread ("" if none). */
 const char* gdr_last_error(void);

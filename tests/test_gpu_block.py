@@ -374,6 +374,32 @@ def test_glr_inconsistent_cu_seqlens_reported():
     assert gdr.workspace_status(ws) == 0
 
 
+@pytest.mark.parametrize("C", [1024, 1026])  # copies by tensor maps, by pairs of channels
+@pytest.mark.parametrize("types", [0, 2])
+@pytest.mark.parametrize("block", [0, 100])
+def test_glr_wait_that_runs_out_is_reported(C, types, block):
+    """A block that gives up stops those that wait for it; the status word says so, and the next call on
+    the same workspace is right."""
+    from chunked_gated_delta_bwd_gb300.block import test_stall_next_glr as stall_next
+    act, gt = TYPES[types]
+    d = _glr_inputs([3000, 64 * 80 - 3000], C, 71, act, gt, "softplus")
+    how = dict(gate="softplus", cu_seqlens=d["cu"].cuda(), h0=d["h0"], **_params(d))
+    ws = torch.empty(gdr.glr_workspace_bytes(d["x"], d["g"], cu_seqlens=how["cu_seqlens"], gate="softplus"), dtype=torch.uint8,
+                     device="cuda")
+    fwd = lambda: gdr.glr_fwd(d["x"], d["g"], workspace=ws, **how)  # noqa: E731
+    want = fwd()
+    bwd = lambda: gdr.glr_bwd(d["x"], d["g"], want["h"], d["dh"], dht=d["dht"], workspace=ws, **how)  # noqa: E731
+    for call in (fwd, bwd):
+        first = call()
+        assert gdr.workspace_status(ws) == 0
+        stall_next(block)
+        call()
+        assert gdr.workspace_status(ws) == 4  # GDR_DEV_TIMEOUT
+        again = call()
+        assert gdr.workspace_status(ws) == 0
+        assert all(torch.equal(again[k], first[k]) for k in first)
+
+
 def test_glr_no_tokens():
     x = torch.empty(0, 8, dtype=BF16, device="cuda")
     h0 = torch.randn(3, 8, device="cuda")
