@@ -336,7 +336,8 @@ gdr_status gdr_rmsnorm_fwd(int64_t rows, int32_t channels, const void* x, int64_
  * stored sum s (res_type; the forward's x without a residual) and rstd:
  *     dx = rstd (u - n mean(u n)) + dres,  n = s rstd,  u = weight dy;   dweight = sum_rows dy n
  * dres (res_type, or NULL) is the gradient that reaches s directly; dx (res_type) is the
- * gradient of s, hence of both x and the residual. */
+ * gradient of s, hence of both x and the residual.  rows = 0 is a valid call: dweight is zero, and
+ * everything but dweight and the workspace may be NULL. */
 size_t gdr_rmsnorm_workspace_bytes(int64_t rows, int32_t channels);
 gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const void* s,
                            int32_t res_type, const float* weight, const float* rstd,

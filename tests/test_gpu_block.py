@@ -619,6 +619,16 @@ def test_rmsnorm_backward(R, C, res):
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dweight"], out["dweight"])
 
 
+def test_rmsnorm_backward_of_no_rows():
+    """Nothing but dweight and the workspace is needed, and nothing else is read."""
+    from chunked_gated_delta_bwd_gb300 import block
+    dw = torch.full((24,), 7.0, device="cuda")
+    ws = torch.empty(block._lib().gdr_rmsnorm_workspace_bytes(0, 24), dtype=torch.uint8, device="cuda")
+    rc = block._lib().gdr_rmsnorm_bwd(0, 24, None, None, 0, None, None, None, ws.data_ptr(), ws.numel(), None, dw.data_ptr(),
+                                      torch.cuda.current_stream().cuda_stream)
+    assert rc == 0 and not dw.any()
+
+
 def test_rmsnorm_offsets_past_32_bits():
     R, C = (1 << 20) + 3, 2050
     gen = torch.Generator("cuda").manual_seed(6)
