@@ -85,6 +85,7 @@ struct NormParams {
     const float* rstd_in;        // [R]
     void* dx;                    // [R][C], of the residual stream's type
     float* dweight;              // [C]
+    int* status;                 // workspace: status word
     float* partial;              // workspace: sums of dweight, a row for each group of threads
 };
 int rmsnorm_bwd_blocks(int64_t R, int C);

@@ -245,11 +245,13 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
     cudaStream_t s = (cudaStream_t)stream;
     if (rows == 0) {  // (the weight may be NULL, as everything of the rows)
         cudaError_t e = cudaMemsetAsync(dweight, 0, sizeof(float) * channels, s);
-        return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync(dweight)");
+        if (e == cudaSuccess) e = cudaMemsetAsync(workspace, 0, 256, s);
+        return e == cudaSuccess ? ok() : cuda_fail(e, "cudaMemsetAsync(dweight/workspace)");
     }
     p.R = rows; p.C = channels; p.ldx = channels; p.res_f32 = res_type == GDR_TYPE_F32;
     p.dy = (const __nv_bfloat16*)dy; p.s = s_in; p.weight = weight; p.rstd_in = rstd; p.dres = dres; p.dx = dx;
     p.dweight = dweight;
+    p.status = static_cast<int*>(workspace);
     p.partial = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + 256);
     cudaError_t e = timed(GDR_KERNEL_NORM, s, [&] { return launch_rmsnorm_bwd(p, s); }, 2);
     return e == cudaSuccess ? ok() : cuda_fail(e, "rms norm backward launch");

@@ -453,12 +453,13 @@ __global__ void __launch_bounds__(512) k_rmsnorm_bwd_long(const NormParams p) {
 }
 
 // dweight: the partial rows added in a fixed order.  A block takes 32 channels, each of its 32 warps
-// every 32nd row.
-__global__ void __launch_bounds__(1024) k_rmsnorm_dw(const float* partial, int rows, int C, float* dw) {
+// every 32nd row.  (The workspace's status word: there is nothing to report.)
+__global__ void __launch_bounds__(1024) k_rmsnorm_dw(const float* partial, int rows, int C, float* dw, int* status) {
     __shared__ float part[32][33];
     const int lane = threadIdx.x % 32, w = threadIdx.x / 32, c = blockIdx.x * 32 + lane;
     float v = 0.f;
     cudaGridDependencySynchronize();  // (launched ahead of the end of the kernel before it)
+    if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
     if (c < C) {
 #pragma unroll 8
         for (int i = w; i < rows; i += 32) v += partial[(int64_t)i * C + c];
@@ -538,7 +539,7 @@ cudaError_t bwd(const NormParams& p, cudaStream_t s) {
     }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_after((p.C + 31) / 32, 1024, s, k_rmsnorm_dw, (const float*)p.partial, grid, (int)p.C, p.dweight);
+    return launch_after((p.C + 31) / 32, 1024, s, k_rmsnorm_dw, (const float*)p.partial, grid, (int)p.C, p.dweight, p.status);
 }
 
 }  // namespace

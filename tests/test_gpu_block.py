@@ -629,6 +629,16 @@ def test_rmsnorm_backward_of_no_rows():
     assert rc == 0 and not dw.any()
 
 
+@pytest.mark.parametrize("R,C", [(0, 64), (5, 64), (3, 40000)])
+def test_rmsnorm_backward_leaves_a_clear_status_word(R, C):
+    """gdr_workspace_status tells of the last call that used the workspace, not of an earlier one."""
+    from chunked_gated_delta_bwd_gb300 import block
+    dy, w, s = _norm_inputs(R, C, BF16, 12)
+    ws = torch.full((block._lib().gdr_rmsnorm_workspace_bytes(R, C),), 255, dtype=torch.uint8, device="cuda")
+    gdr.rmsnorm_bwd(dy, s, w, torch.ones(R, device="cuda"), workspace=ws)
+    assert gdr.workspace_status(ws) == 0
+
+
 def test_rmsnorm_offsets_past_32_bits():
     R, C = (1 << 20) + 3, 2050
     gen = torch.Generator("cuda").manual_seed(6)
