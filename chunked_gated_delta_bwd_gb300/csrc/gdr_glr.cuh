@@ -742,11 +742,17 @@ __device__ __forceinline__ void glr_report(uint32_t bar, bool wide) {
     if (!wide) asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
 }
 
+// Blocks of a scan kernel that an SM's 228 KB of shared memory hold (1 KB of it goes with each block): two with bf16
+// tiles, one with float32's.
+__host__ __device__ constexpr int glr_per_sm(size_t smem) { return 2 * (smem + 1024) <= 228 * 1024 ? 2 : 1; }
+
 // Launches a scan kernel on as many blocks as are resident at once (or tiles, if fewer).
 // `ready`: the devices whose shared-memory limit of this kernel is raised.
-template <class K>
-cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, int threads, size_t smem, int per_sm, const GlrParams& p,
-                       const GlrMaps& maps, cudaStream_t s) {
+template <class Tile, class K>
+cudaError_t glr_launch(K kernel, std::atomic<uint64_t>& ready, const GlrParams& p, const GlrMaps& maps, cudaStream_t s) {
+    constexpr size_t smem = sizeof(Tile);
+    constexpr int per_sm = glr_per_sm(smem), threads = decltype(Tile::ring)::THREADS;
+    static_assert(per_sm * (smem + 1024) <= 228 * 1024, "a resident block's tiles");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;

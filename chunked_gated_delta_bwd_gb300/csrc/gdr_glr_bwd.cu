@@ -36,7 +36,8 @@ struct GlrBwdTile {
 };
 
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), 2) k_glr_bwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
+__global__ void __launch_bounds__(32 * (BWD_WARPS + GLR_X + 1), glr_per_sm(sizeof(GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>)))
+    k_glr_bwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
     using Tile = GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>;
     constexpr int SUB = BWD_SUB;
     using PX = PairOf<TX>;
@@ -300,8 +301,9 @@ struct Launch {
                         encode_plain_map(&maps.h, p.h_in, p.act_f32, p.T, p.C, p.C, 64) &&
                         (!COMP || encode_plain_map(&maps.x, p.x, p.act_f32, p.T, p.C, p.ldx, 64))))
             return cudaErrorInvalidValue;
-        cudaError_t e = glr_launch(k_glr_bwd<TX, TG, GATE, COMP>, ready, 32 * (BWD_WARPS + GLR_X + 1), sizeof(GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>), 2,
-                                   p, maps, s);
+        using Tile = GlrBwdTile<TX, COMP, GATE == GLR_SOFTPLUS>;
+        static_assert(sizeof(TX) == 4 || glr_per_sm(sizeof(Tile)) == 2, "bf16 tiles: two blocks an SM");
+        cudaError_t e = glr_launch<Tile>(k_glr_bwd<TX, TG, GATE, COMP>, ready, p, maps, s);
         if (e != cudaSuccess || GATE != GLR_SOFTPLUS) return e;
         return launch_after((p.C / 2 + 31) / 32, 1024, s, k_glr_sums, (const float4*)p.sums, glr_chunks(p), (int)p.C, p.dA_log,
                             p.ddt_bias);

@@ -28,7 +28,7 @@ struct GlrFwdTile {
 };
 
 template <class TX, class TG, int GATE, bool COMP>
-__global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), 2) k_glr_fwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
+__global__ void __launch_bounds__(32 * (FWD_WARPS + GLR_X + 1), glr_per_sm(sizeof(GlrFwdTile<TX>))) k_glr_fwd(const GlrParams p, const __grid_constant__ GlrMaps maps) {
     constexpr int SUB = FWD_SUB;
     using PX = PairOf<TX>;
     using PG = PairOf<TG>;
@@ -204,7 +204,8 @@ struct Launch {
         if (p.wide && !(encode_plain_map(&maps.g, p.g, p.gate_f32, p.T, p.C, p.ldg, p.gate_f32 ? 64 : 8) &&
                         encode_plain_map(&maps.x, p.x, p.act_f32, p.T, p.C, p.ldx, 64)))
             return cudaErrorInvalidValue;
-        return glr_launch(k_glr_fwd<TX, TG, GATE, COMP>, ready, 32 * (FWD_WARPS + GLR_X + 1), sizeof(GlrFwdTile<TX>), 2, p, maps, s);
+        static_assert(sizeof(TX) == 4 || glr_per_sm(sizeof(GlrFwdTile<TX>)) == 2, "bf16 tiles: two blocks an SM");
+        return glr_launch<GlrFwdTile<TX>>(k_glr_fwd<TX, TG, GATE, COMP>, ready, p, maps, s);
     }
 };
 }  // namespace
