@@ -27,6 +27,12 @@ static gdr_status row_stride(int64_t given, int64_t channels, int64_t* out) {
     return GDR_OK;
 }
 
+// whether two buffers (or NULL) share memory
+static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+    const uintptr_t u = reinterpret_cast<uintptr_t>(a), v = reinterpret_cast<uintptr_t>(b);
+    return a && b && u < v + b_bytes && v < u + a_bytes;
+}
+
 static gdr_status check_channels(int32_t channels) {
     if (channels < 1) return fail(GDR_ERR_INVALID, "channels must be >= 1%s");
     if (channels % 2 != 0) return fail(GDR_ERR_INVALID, "channels must be even%s");
@@ -86,11 +92,9 @@ static int rows_wide(const GlrParams& p, const void* at, int64_t ld, int f32) {
     return aligned16(at) && ld % piece == 0 && p.C % piece == 0 && p.T < ((int64_t)1 << 31);
 }
 
-// Checks and clears the workspace (a launch of one chunk writes its status word itself); every
+// Clears the workspace (a launch of one chunk writes its status word itself); every
 // sequence empty: the states pass through.
-static gdr_status glr_front(GlrParams& p, void* ws, size_t ws_bytes, float* to, const float* from, cudaStream_t s,
-                            bool* done) {
-    if (ws_bytes < glr_workspace(p)) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
+static gdr_status glr_front(GlrParams& p, void* ws, float* to, const float* from, cudaStream_t s, bool* done) {
     const size_t published = glr_published_bytes(p);
     cudaError_t e = cudaSuccess;
     if (published || p.T == 0) e = cudaMemsetAsync(ws, 0, 256 + published, s);
@@ -125,9 +129,13 @@ gdr_status glr_fwd(const glr_shape* shape, const void* x, const void* g, const f
         if (p.gate == GLR_GATE_SOFTPLUS) { NEED(A_log); NEED(dt_bias); }
     }
     OPT(h0); OPT(ht); NEED(workspace);
+    if (workspace_bytes < glr_workspace(p)) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
+    // (h0 is read again when another block may have written ht)
+    const size_t states = sizeof(float) * (size_t)p.N * p.C;
+    if (p.T && overlap(h0, states, ht, states)) return fail(GDR_ERR_INVALID, "ht must not share memory with h0%s");
     cudaStream_t s = (cudaStream_t)stream;
     bool done = false;
-    if (gdr_status st = glr_front(p, workspace, workspace_bytes, ht, h0, s, &done)) return st;
+    if (gdr_status st = glr_front(p, workspace, ht, h0, s, &done)) return st;
     if (done) return ok();
     p.x = x; p.g = g; p.A_log = A_log; p.dt_bias = dt_bias; p.h0 = h0; p.h = h; p.ht = ht;
     p.wide = rows_wide(p, x, p.ldx, p.act_f32) && rows_wide(p, g, p.ldg, p.gate_f32);
@@ -150,9 +158,18 @@ gdr_status glr_bwd(const glr_shape* shape, const void* x, const void* g, const f
     }
     NEED(dh0); OPT(h0); OPT(dht); NEED(workspace);
     if (soft) { NEED(dA_log); NEED(ddt_bias); }
+    if (workspace_bytes < glr_workspace(p)) return fail(GDR_ERR_WORKSPACE, "workspace smaller than glr_workspace_bytes%s");
+    // (the states are read again when another block may have written dh0, and h of the token before a tile
+    // when another block may have written that token's gradients)
+    const size_t states = sizeof(float) * (size_t)p.N * p.C, tokens = (size_t)p.T * p.C;
+    if (p.T && (overlap(dht, states, dh0, states) || overlap(h0, states, dh0, states)))
+        return fail(GDR_ERR_INVALID, "dh0 must not share memory with dht or h0%s");
+    if (overlap(h, tokens * (p.act_f32 ? 4 : 2), dx, tokens * (p.act_f32 ? 4 : 2)) ||
+        overlap(h, tokens * (p.act_f32 ? 4 : 2), dg, tokens * (p.gate_f32 ? 4 : 2)))
+        return fail(GDR_ERR_INVALID, "dx and dg must not share memory with h%s");
     cudaStream_t s = (cudaStream_t)stream;
     bool done = false;
-    if (gdr_status st = glr_front(p, workspace, workspace_bytes, dh0, dht, s, &done)) return st;
+    if (gdr_status st = glr_front(p, workspace, dh0, dht, s, &done)) return st;
     if (done) {
         if (!soft) return ok();
         cudaError_t e = cudaMemsetAsync(dA_log, 0, sizeof(float) * p.C, s);
@@ -269,7 +286,8 @@ gdr_status gdr_conv1d_fwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
     if (gdr_status st = row_stride(x_stride, channels, &p.ldx)) return st;
     if (total_tokens) { NEED_ROWS(x, 0); NEED(y); }
     NEED(weight); OPT(bias); OPT(state); OPT(state_out);
-    if (state && state == state_out) return fail(GDR_ERR_INVALID, "state_out must not be the initial state's buffer%s");
+    const size_t states = 2 * (size_t)num_seqs * (width - 1) * channels;
+    if (overlap(state, states, state_out, states)) return fail(GDR_ERR_INVALID, "state_out must not share memory with the initial state%s");
     p.N = num_seqs; p.T = total_tokens; p.seq_len = cu_seqlens ? 0 : total_tokens / num_seqs;
     p.C = channels; p.K = width; p.silu = silu != 0; p.cu_seqlens = cu_seqlens;
     p.x = (const __nv_bfloat16*)x; p.w = weight; p.bias = bias; p.state = (const __nv_bfloat16*)state;

@@ -239,6 +239,9 @@ gdr_status gdr_conv1d_bwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
  *  * x and g may be rows of a wider tensor (a column slice of a projection's output): the
  *    row stride is given in elements (0 = C), even, and the pointer aligned to two elements;
  *    every other tensor is contiguous and 16-byte aligned.
+ *  * An output shares no memory with an input or another output, except where that is said to be
+ *    allowed.  Refused are the cases in which one block would read what another has written: glr_fwd's
+ *    ht in h0, glr_bwd's dh0 in dht or h0 and dx or dg in h, gdr_conv1d_fwd's state_out in state.
  *  * Every result is the same, bit for bit, from one call to the next.
  *  * Single-token steps work on a pool of states: row n of the batch has state slots[n]
  *    (int64; slots NULL: state n).  A row whose slot is negative (padding) or not below
@@ -252,7 +255,7 @@ gdr_status gdr_conv1d_bwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
  *  * state: bf16 [N, K - 1, C], the K - 1 inputs before each sequence's first token, oldest
  *    first, or NULL (zero, as gdr_conv1d_bwd takes it).
  *  * state_out: bf16 [N, K - 1, C], the last K - 1 inputs of each sequence (and of its state,
- *    where the sequence is shorter), or NULL; not the buffer of `state`.
+ *    where the sequence is shorter), or NULL.
  *  * Inconsistent cu_seqlens give meaningless results but no access outside the tensors. */
 gdr_status gdr_conv1d_fwd(int32_t num_seqs, int64_t total_tokens, int32_t channels, int32_t width,
                           const int64_t* cu_seqlens, const void* x, int64_t x_stride, const float* weight,

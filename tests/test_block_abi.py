@@ -58,6 +58,26 @@ def test_glr_pointers_refused(L):
     assert L.glr_bwd(*args[:10], need - 1, *args[11:]) == WORKSPACE
 
 
+def test_states_that_share_memory_refused(L):
+    """Buffers of two sequences' states (2 x 8 float32) and of 256 x 8 bf16 tokens, at distinct addresses but
+    for the pair in question."""
+    sh = _shape()
+    need = L.glr_workspace_bytes(sh)
+    at = lambda i: A + i * (1 << 20)  # noqa: E731
+    for ht in (at(2), at(2) + 32, at(2) - 48):
+        assert L.glr_fwd(sh, at(0), at(1), None, None, at(2), at(3), ht, at(4), need, None) == INVALID, ht
+        assert b"share" in L.gdr_last_error()
+    call = lambda dx, dg, dh0: L.glr_bwd(sh, at(0), at(1), None, None, at(2), at(3), at(4), at(5), at(6), need,  # noqa: E731
+                                         dx, dg, dh0, None, None, None)
+    for bad in ((at(7), at(8), at(3)), (at(7), at(8), at(5)), (at(7), at(8), at(5) + 16), (at(2), at(8), at(9)),
+                (at(7), at(2), at(9)), (at(2) + 4080, at(8), at(9)), (at(7), at(2) - 16, at(9))):
+        assert call(*bad) == INVALID, bad
+        assert b"share" in L.gdr_last_error()
+    for new in (at(3), at(3) + 80, at(3) - 80):  # states: 2 x 3 x 8 bf16
+        assert L.gdr_conv1d_fwd(2, 256, 8, 4, None, at(0), 0, at(1), None, at(3), 1, at(2), new, None) == INVALID
+        assert b"share" in L.gdr_last_error()
+
+
 def test_steps_refused(L):
     ok = [3, 8, 5, 1, 0, 0, 0, A, 0, A, 0, A, A, A, A, A, None]
     for i, v, code in ((0, -1, INVALID), (1, 5, INVALID), (2, -1, INVALID), (3, 7, INVALID), (5, 3, UNSUPPORTED),
