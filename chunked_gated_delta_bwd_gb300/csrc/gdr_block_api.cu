@@ -23,6 +23,7 @@ static gdr_status row_stride(int64_t given, int64_t channels, int64_t* out) {
     if (given == 0) given = channels;
     if (given < channels || given % 2 != 0)
         return fail(GDR_ERR_INVALID, "a row stride must be even and at least the number of channels%s");
+    if (given > ((int64_t)1 << 38)) return fail(GDR_ERR_INVALID, "row stride too large%s");
     *out = given;
     return GDR_OK;
 }
@@ -36,6 +37,8 @@ static bool overlap(const void* a, size_t a_bytes, const void* b, size_t b_bytes
 static gdr_status check_channels(int32_t channels) {
     if (channels < 1) return fail(GDR_ERR_INVALID, "channels must be >= 1%s");
     if (channels % 2 != 0) return fail(GDR_ERR_INVALID, "channels must be even%s");
+    // (the kernels count channels, and the conv1d's weights of them, in 32 bits)
+    if (channels > GDR_MAX_CHANNELS) return fail(GDR_ERR_INVALID, "channels must be at most 2^28%s");
     return GDR_OK;
 }
 
@@ -52,7 +55,8 @@ static gdr_status check_tokens(int32_t num_seqs, int64_t total_tokens, const int
     if (num_seqs < 1 || total_tokens < 0) return fail(GDR_ERR_INVALID, "num_seqs must be >= 1, total_tokens >= 0%s");
     if (!cu_seqlens && total_tokens % num_seqs != 0)
         return fail(GDR_ERR_INVALID, "dense layout needs total_tokens divisible by num_seqs%s");
-    if (total_tokens > ((int64_t)1 << 36) || channels * total_tokens > ((int64_t)1 << 40))
+    const int64_t most = (int64_t)1 << 40;  // elements (the product of the sizes may leave 64 bits)
+    if (total_tokens > ((int64_t)1 << 36) || total_tokens > most / channels || num_seqs > most / channels)
         return fail(GDR_ERR_INVALID, "problem too large%s");
     return GDR_OK;
 }

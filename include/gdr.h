@@ -235,7 +235,8 @@ gdr_status gdr_conv1d_bwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
  * step, and the RMS norm with the residual's addition and its backward.  The conventions
  * above hold (device pointers, asynchronous on `stream`, nothing allocated, argument errors
  * before anything is enqueued), and:
- *  * channels C is even.
+ *  * channels C is even, at most GDR_MAX_CHANNELS.  Sequences have at most 2^36 tokens in all, 2^40
+ *    elements, and as many elements of states.
  *  * x and g may be rows of a wider tensor (a column slice of a projection's output): the
  *    row stride is given in elements (0 = C), even, and the pointer aligned to two elements;
  *    every other tensor is contiguous and 16-byte aligned.
@@ -247,6 +248,7 @@ gdr_status gdr_conv1d_bwd(int32_t num_seqs, int64_t total_tokens, int32_t channe
  *    (int64; slots NULL: state n).  A row whose slot is negative (padding) or not below
  *    `pool` touches no state and its y is zero.  Two rows must not share a slot.
  * --------------------------------------------------------------------------- */
+#define GDR_MAX_CHANNELS (1 << 28)
 #define GDR_TYPE_BF16 0
 #define GDR_TYPE_F32 1
 

@@ -58,6 +58,29 @@ def test_glr_pointers_refused(L):
     assert L.glr_bwd(*args[:10], need - 1, *args[11:]) == WORKSPACE
 
 
+@pytest.mark.parametrize("tokens,channels,seqs", [
+    (1 << 36, 1 << 30, 1), (1 << 36, 1 << 28, 1), (1 << 20, (1 << 20) + 2, 1), (1 << 36, 32, 1), (1 << 37, 2, 1),
+    (2, (1 << 28) + 2, 1), (0, 1 << 28, 1 << 30)])
+def test_sizes_past_the_limits_refused(L, tokens, channels, seqs):
+    """Also where the product of the sizes leaves 64 bits."""
+    sh = _shape(total_tokens=tokens, channels=channels, num_seqs=seqs)
+    assert L.glr_workspace_bytes(sh) == 0
+    assert L.glr_fwd(sh, A, A, None, None, None, A, None, A, (1 << 63) - 1, None) == INVALID
+    assert L.glr_bwd(sh, A, A, None, None, A, None, A, None, A, (1 << 63) - 1, A, A, A, None, None, None) == INVALID
+    assert L.gdr_conv1d_fwd(seqs, tokens, channels, 4, None, A, 0, A, None, None, 1, A, None, None) == INVALID
+
+
+def test_channels_and_strides_past_the_limits_refused(L):
+    C = (1 << 28) + 2
+    assert L.glr_step(3, C, 3, 0, 0, 0, 0, A, 0, A, 0, None, None, None, A, A, None) == INVALID
+    assert L.gdr_conv1d_step(3, C, 4, 3, A, 0, A, A, None, None, 1, A, None) == INVALID
+    assert L.gdr_rmsnorm_fwd(3, C, A, 0, None, 0, A, 1e-6, 0, A, None, None, A, None) == INVALID
+    assert L.gdr_rmsnorm_workspace_bytes(3, C) == 0
+    assert L.gdr_rmsnorm_bwd(3, C, A, A, 0, A, A, None, A, 1 << 62, A, A, None) == INVALID
+    assert L.glr_fwd(_shape(x_stride=1 << 62), A, A, None, None, None, A, None, A, 1 << 62, None) == INVALID
+    assert L.glr_workspace_bytes(_shape(total_tokens=1 << 20, channels=1 << 20)) > 0
+
+
 def test_states_that_share_memory_refused(L):
     """Buffers of two sequences' states (2 x 8 float32) and of 256 x 8 bf16 tokens, at distinct addresses but
     for the pair in question."""
