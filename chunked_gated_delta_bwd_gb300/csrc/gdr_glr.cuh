@@ -50,6 +50,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ float2 clamp_exponent(float2 t) { return make_float2(max_nan(t.x, -126.f), max_nan(t.y, -126.f)); }
 __device__ __forceinline__ void exp2_parts(float2 t, float2& m, float2& scale) {  // (t clamped)
     const float2 shifted = __fadd2_rn(t, splat(12582912.f));  // 1.5 * 2^23: n in the low bits
@@ -82,7 +87,7 @@ template <int GATE>
 __device__ __forceinline__ float2 run_decay(float2 t) {
     const float2 a = decay(clamp_exponent(t));
     if (GATE == GLR_SOFTPLUS) return a;
-    return make_float2(t.x > 127.49f ? INFINITY : a.x, t.y > 127.49f ? INFINITY : a.y);
+    return make_float2(t.x > 127.4f ? INFINITY : a.x, t.y > 127.4f ? INFINITY : a.y);
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -130,7 +135,9 @@ struct GlrGate {
     }
     __device__ __forceinline__ float2 log2_gate(float2 raw) const {
         if constexpr (GATE == GLR_LOG) {
-            return clamp_exponent(__fmul2_rn(raw, splat(kLog2e)));
+            // (growth past 2^127 would carry into the sign; the softplus gate's t is never positive)
+            const float2 t = clamp_exponent(__fmul2_rn(raw, splat(kLog2e)));
+            return make_float2(min_nan(t.x, 127.f), min_nan(t.y, 127.f));
         } else {
             return clamp_exponent(__fmul2_rn(nA, softplus2(__ffma2_rn(raw, splat(kLog2e), bias))));
         }

@@ -279,8 +279,8 @@ gdr_status gdr_conv1d_step(int32_t rows, int32_t channels, int32_t width, int32_
  *  * A_log, dt_bias, dA_log, ddt_bias: float [C] (softplus gate only; else ignored).
  *  * h0, ht, dht, dh0: float [N, C]; h0, ht and dht may be NULL.  An empty sequence passes its
  *    state through (ht = h0, dh0 = dht).  T_total = 0 is a valid call.
- *  * Decays below 2^-126 count as 2^-126.  The log gate is meant to be negative: growth (a
- *    positive g) is computed as such up to a = 2^127, but a run of tokens whose product of decays
+ *  * Decays below 2^-126 count as 2^-126, above 2^127 as 2^127.  The log gate is meant to be
+ *    negative: growth (a positive g) is computed as such, but a run of tokens whose product of decays
  *    leaves fp32 gives infinities or NaN even where the state itself would not.
  *  * Inconsistent cu_seqlens raise GDR_DEV_BAD_SEQLENS in the workspace's status word; the
  *    results are then meaningless, but no access leaves the tensors.  GDR_DEV_TIMEOUT there means

@@ -275,6 +275,24 @@ def test_glr_gates_of_zero_and_infinity():
     assert rel_l2(f64(out["h"]), want) <= TOL_STATE and rel_l2(f64(out["ht"]), want_t) <= TOL_STATE
 
 
+@pytest.mark.parametrize("g", [60.0, 88.0, 89.0, 100.0, 177.0, 1e4, float("inf")])
+@pytest.mark.parametrize("types", range(3))
+def test_glr_growth_keeps_its_sign(g, types):
+    """A positive log gate multiplies the state by e^g, or by 2^127 where that is more; never by a wrapped exponent."""
+    act, gt = TYPES[types]
+    h0 = torch.tensor([[1e-30, -1e-30, 2e-30, 0.0]], device="cuda")
+    x = torch.zeros(1, 4, dtype=act, device="cuda")
+    gg = torch.full((1, 4), g, device="cuda").to(gt)
+    want = f64(h0) * min(np.exp(float(gg[0, 0])) if g < 700 else np.inf, 2.0 ** 127)
+    out = gdr.glr_fwd(x, gg, h0=h0)
+    assert rel_l2(f64(out["ht"]), want) <= 1e-5  # a log gate of 88 is off by up to 2^-24 of itself, the decay by that of 88
+    state = h0.clone()
+    gdr.glr_step(x, gg, state)
+    assert rel_l2(f64(state), want) <= 1e-5
+    back = gdr.glr_bwd(x, gg, out["h"], x, h0=h0, dht=h0)
+    assert rel_l2(f64(back["dh0"]), want) <= 1e-5
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
 def test_glr_one_sequence_does_not_reach_another(bad):
     # a NaN or an infinity in one packed sequence leaves every other sequence's results untouched
