@@ -62,8 +62,29 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(t):
+_SEVERAL = None  # whether there are several GPUs
+
+
+def _stream(t, *others):
+    """The current stream of t's device, which all tensors of a call are on and which is the current one."""
+    global _SEVERAL
+    if _SEVERAL is None:
+        _SEVERAL = torch.cuda.device_count() > 1
+    if _SEVERAL:
+        current = torch.cuda.current_device()
+        for u in (t,) + others:
+            if u is not None and u.get_device() != current:
+                raise ValueError("all tensors of a call must be on the current device %d (got %s)" % (current, u.device))
     return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+def _scratch(workspace, need, like):
+    """A workspace of ``need`` bytes: the caller's, or a new one."""
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
+    if workspace.dtype is not torch.uint8 or workspace.numel() < need or not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA uint8 tensor of at least %d bytes" % need)
+    return workspace
 
 
 def _bad(t, dtype, shape, name):
@@ -143,15 +164,6 @@ def _glr_shape(x, g, cu_seqlens, num_seqs, gate, complement):
     return P, GlrShape(P.N, P.T, P.C, _ptr(P.cu), gate, bool(complement), _TYPES[x.dtype], _TYPES[g.dtype], ldx, ldg)
 
 
-def _glr_workspace(sh, workspace, like):
-    need = _lib().glr_workspace_bytes(sh)
-    if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=like.device)
-    if workspace.dtype is not torch.uint8 or workspace.numel() < need:
-        raise ValueError("workspace must be a uint8 tensor of at least %d bytes" % need)
-    return workspace
-
-
 def glr_workspace_bytes(x, g, cu_seqlens=None, num_seqs=None, gate="log", complement=False):
     """Bytes of the workspace of glr_fwd / glr_bwd for these tensors."""
     return int(_lib().glr_workspace_bytes(_glr_shape(x, g, cu_seqlens, num_seqs, GATES[gate], complement)[1]))
@@ -166,11 +178,11 @@ def glr_fwd(x, g, h0=None, A_log=None, dt_bias=None, cu_seqlens=None, num_seqs=N
     gate, A_log, dt_bias = _gate(gate, A_log, dt_bias, x.shape[-1])
     P, sh = _glr_shape(x, g, cu_seqlens, num_seqs, gate, complement)
     _opt(h0, torch.float32, (P.N, P.C), "h0")
-    ws = _glr_workspace(sh, workspace, x)
+    ws = _scratch(workspace, _lib().glr_workspace_bytes(sh), x)
     h = _like(x)
     ht = torch.empty((P.N, P.C), dtype=torch.float32, device=x.device) if want_ht else None
     rc = _lib().glr_fwd(sh, x.data_ptr(), g.data_ptr(), _ptr(A_log), _ptr(dt_bias), _ptr(h0), h.data_ptr(), _ptr(ht),
-                        ws.data_ptr(), ws.numel(), _stream(x))
+                        ws.data_ptr(), ws.numel(), _stream(x, g, A_log, dt_bias, h0, P.cu, ws))
     if rc:
         _check(rc, "glr_fwd")
     return {"h": h, "ht": ht}
@@ -186,7 +198,7 @@ def glr_bwd(x, g, h, dh, h0=None, dht=None, A_log=None, dt_bias=None, cu_seqlens
     _need(dh, x.dtype, P.shape, "dh")
     _opt(h0, torch.float32, (P.N, P.C), "h0")
     _opt(dht, torch.float32, (P.N, P.C), "dht")
-    ws = _glr_workspace(sh, workspace, x)
+    ws = _scratch(workspace, _lib().glr_workspace_bytes(sh), x)
     out = {"dx": _like(x), "dg": _like(g),
            "dh0": torch.empty((P.N, P.C), dtype=torch.float32, device=x.device)}
     if gate:
@@ -195,7 +207,7 @@ def glr_bwd(x, g, h, dh, h0=None, dht=None, A_log=None, dt_bias=None, cu_seqlens
     rc = _lib().glr_bwd(sh, x.data_ptr(), g.data_ptr(), _ptr(A_log), _ptr(dt_bias), h.data_ptr(), _ptr(h0),
                         dh.data_ptr(), _ptr(dht), ws.data_ptr(), ws.numel(), out["dx"].data_ptr(),
                         out["dg"].data_ptr(), out["dh0"].data_ptr(), _ptr(out.get("dA_log")),
-                        _ptr(out.get("ddt_bias")), _stream(x))
+                        _ptr(out.get("ddt_bias")), _stream(x, g, A_log, dt_bias, h, h0, dh, dht, P.cu, ws))
     if rc:
         _check(rc, "glr_bwd")
     return out
@@ -226,7 +238,7 @@ def glr_step(x, g, state, slots=None, A_log=None, dt_bias=None, gate="log", comp
     y = _like(x) if out is None else _need(out, x.dtype, shape, "out")
     rc = _lib().glr_step(rows, C, pool, gate, bool(complement), _TYPES[x.dtype], _TYPES[g.dtype], x.data_ptr(), ldx,
                          g.data_ptr(), ldg, _ptr(A_log), _ptr(dt_bias), _ptr(slots), state.data_ptr(), y.data_ptr(),
-                         _stream(x))
+                         _stream(x, g, A_log, dt_bias, slots, state, y))
     if rc:
         _check(rc, "glr_step")
     return y
@@ -265,7 +277,7 @@ def rmsnorm_fwd(x, weight, residual=None, eps=1e-6, quant=None):
                                    device=x.device)
     rc = _lib().gdr_rmsnorm_fwd(rows, C, x.data_ptr(), ldx, _ptr(residual), res_type, weight.data_ptr(), eps,
                                 QUANTS[quant], out["y"].data_ptr(), _ptr(out.get("scale")), _ptr(out.get("residual")),
-                                out["rstd"].data_ptr(), _stream(x))
+                                out["rstd"].data_ptr(), _stream(x, weight, residual))
     if rc:
         _check(rc, "gdr_rmsnorm_fwd")
     return out
@@ -286,15 +298,12 @@ def rmsnorm_bwd(dy, s, weight, rstd, dres=None, workspace=None):
     _opt(dres, s.dtype, shape, "dres")
     rows = rstd.numel()
     need = _lib().gdr_rmsnorm_workspace_bytes(rows, C)
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=s.device)
-    elif workspace.dtype is not torch.uint8 or workspace.numel() < need:
-        raise ValueError("workspace must be a uint8 tensor of at least %d bytes" % need)
+    workspace = _scratch(workspace, need, s)
     out = {"dx": torch.empty_like(s),
            "dweight": torch.empty(C, dtype=torch.float32, device=s.device)}
     rc = _lib().gdr_rmsnorm_bwd(rows, C, dy.data_ptr(), s.data_ptr(), _TYPES[s.dtype], weight.data_ptr(),
                                 rstd.data_ptr(), _ptr(dres), workspace.data_ptr(), workspace.numel(),
-                                out["dx"].data_ptr(), out["dweight"].data_ptr(), _stream(s))
+                                out["dx"].data_ptr(), out["dweight"].data_ptr(), _stream(s, dy, weight, rstd, dres, workspace))
     if rc:
         _check(rc, "gdr_rmsnorm_bwd")
     return out
@@ -318,7 +327,7 @@ def conv1d_fwd(x, weight, bias=None, state=None, cu_seqlens=None, num_seqs=None,
     y = _like(x)
     new = torch.empty((P.N, K - 1, P.C), dtype=torch.bfloat16, device=x.device) if want_state else None
     rc = _lib().gdr_conv1d_fwd(P.N, P.T, P.C, K, _ptr(P.cu), x.data_ptr(), ldx, weight.data_ptr(), _ptr(bias),
-                               _ptr(state), bool(silu), y.data_ptr(), _ptr(new), _stream(x))
+                               _ptr(state), bool(silu), y.data_ptr(), _ptr(new), _stream(x, weight, bias, state, P.cu))
     if rc:
         _check(rc, "gdr_conv1d_fwd")
     return {"y": y, "state": new}
@@ -336,7 +345,7 @@ def conv1d_step(x, state, weight, bias=None, slots=None, silu=True, out=None):
     y = _like(x) if out is None else \
         _need(out, torch.bfloat16, shape, "out")
     rc = _lib().gdr_conv1d_step(rows, C, K, pool, x.data_ptr(), ldx, state.data_ptr(), weight.data_ptr(), _ptr(bias),
-                                _ptr(slots), bool(silu), y.data_ptr(), _stream(x))
+                                _ptr(slots), bool(silu), y.data_ptr(), _stream(x, state, weight, bias, slots, y))
     if rc:
         _check(rc, "gdr_conv1d_step")
     return y

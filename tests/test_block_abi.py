@@ -171,3 +171,27 @@ def test_row_strides():
     for bad in (wide[:, ::2][:, :2], wide[:, :3], wide[..., ::2], wide[0].t(), wide[0, :1].expand(4, 32)):
         with pytest.raises(ValueError):
             rule(bad)
+
+
+def test_workspaces_and_devices_refused(monkeypatch):
+    """A workspace that the kernels could not write as given; tensors of another GPU than the current one."""
+    from types import SimpleNamespace
+
+    def ws(**over):
+        d = dict(dtype=torch.uint8, numel=lambda: 512, is_cuda=True, is_contiguous=lambda: True)
+        return SimpleNamespace(**{**d, **over})
+
+    like = torch.zeros(1)
+    good = ws()
+    assert block._scratch(good, 512, like) is good and block._scratch(None, 100, like).numel() == 100
+    for bad in (ws(dtype=torch.int8), ws(numel=lambda: 511), ws(is_cuda=False), ws(is_contiguous=lambda: False)):
+        with pytest.raises(ValueError):
+            block._scratch(bad, 512, like)
+    on = lambda i: SimpleNamespace(get_device=lambda: i, device="cuda:%d" % i)  # noqa: E731
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 40 + d, raising=False)
+    monkeypatch.setattr(block, "_SEVERAL", True)
+    assert block._stream(on(0), None, on(0)) == 40
+    for tensors in ((on(1),), (on(0), on(1)), (on(0), None, on(1))):
+        with pytest.raises(ValueError):
+            block._stream(*tensors)
