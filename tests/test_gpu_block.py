@@ -263,6 +263,22 @@ def test_glr_complement_keeps_the_state_at_decay_one(types):
     assert torch.equal(state, h0)
 
 
+@pytest.mark.parametrize("gate", ["log", "softplus"])
+@pytest.mark.parametrize("comp", [False, True])
+def test_glr_every_channel_by_itself(gate, comp):
+    """Relative L2 per channel, where the tests above take all channels together."""
+    d = _glr_inputs([700, 0, 1, 1300], 130, 72, F32, F32, gate)
+    how = dict(gate=gate, complement=comp, cu_seqlens=d["cu"].cuda(), h0=d["h0"], **_params(d))
+    out = gdr.glr_fwd(d["x"], d["g"], **how)
+    want, _ = ref.glr_fwd(f64(d["x"]), f64(d["g"]), d["cu"].tolist(), f64(d["h0"]), complement=comp, **_ref_params(d))
+    assert _off(out["h"], want).max() <= TOL_STATE
+    grad = gdr.glr_bwd(d["x"], d["g"], out["h"], d["dh"], dht=d["dht"], **how)
+    back = ref.glr_bwd(f64(d["x"]), f64(d["g"]), f64(out["h"]), f64(d["dh"]), d["cu"].tolist(), f64(d["h0"]), f64(d["dht"]),
+                       complement=comp, **_ref_params(d))
+    for k in ("dx", "dg"):
+        assert _off(grad[k], back[k]).max() <= TOL_STATE, k
+
+
 def test_glr_gates_of_zero_and_infinity():
     # log gate 0 (nothing forgotten), -inf (everything forgotten) and large positive is not used;
     # the state stays finite and follows the definition exactly enough
@@ -375,6 +391,39 @@ def test_glr_graph_replay():
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(got["h"], want["h"]) and torch.equal(got["ht"], want["ht"])
+
+
+def test_backward_and_steps_in_a_graph():
+    """Captured calls replayed on new inputs: kernels launched ahead of the one before, steps in place."""
+    d = _glr_inputs([600, 41], 128, 73, gate="softplus")
+    how = dict(gate="softplus", complement=True, **_params(d))
+    cu, s = d["cu"].cuda(), d["x"]
+    w, rstd = torch.ones(128, device="cuda"), torch.ones(641, device="cuda")
+    conv_w, conv_b = torch.full((128, 4), 0.25, device="cuda"), torch.zeros(128, device="cuda")
+    taps, state = torch.zeros(8, 3, 128, dtype=BF16, device="cuda"), torch.zeros(8, 128, device="cuda")
+    h = gdr.glr_fwd(d["x"], d["g"], cu_seqlens=cu, **how)["h"]
+
+    def calls():
+        out = dict(gdr.glr_bwd(d["x"], d["g"], h, d["dh"], cu_seqlens=cu, **how))
+        out.update({"n" + k: v for k, v in gdr.rmsnorm_bwd(d["dh"], s, w, rstd).items()})
+        out["c"] = gdr.conv1d_step(d["x"][:8], taps, conv_w, conv_b)
+        out["y"] = gdr.glr_step(out["c"], d["g"][:8], state, **how)
+        return out
+
+    calls()  # (once outside the capture)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = calls()
+    for seed in (1, 2):
+        d["x"].copy_(torch.randn(641, 128, generator=torch.Generator().manual_seed(seed)))
+        d["dh"].copy_(d["dh"].flip(0))
+        taps.zero_(), state.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        after = {k: v.clone() for k, v in got.items()}, taps.clone(), state.clone()
+        taps.zero_(), state.zero_()
+        want = calls()
+        assert all(torch.equal(after[0][k], want[k]) for k in want) and torch.equal(after[1], taps) and torch.equal(after[2], state)
 
 
 def test_glr_inconsistent_cu_seqlens_reported():
@@ -635,6 +684,32 @@ def test_rmsnorm_backward(R, C, res):
     assert np.all(np.abs(f64(out["dweight"]) - dw) <= TOL_STATE * mw + 1e-30)
     again = gdr.rmsnorm_bwd(dy, s, w, r32, dres=dres)
     assert torch.equal(again["dx"], out["dx"]) and torch.equal(again["dweight"], out["dweight"])
+
+
+@pytest.mark.parametrize("C", [2048, 4098, 5120, 8192, 12290, 16384, 20000])
+@pytest.mark.parametrize("res", [None, BF16, F32])
+def test_rmsnorm_rows_in_turn(C, res):
+    """More rows than blocks, so that each walks several (one or more pieces a thread, rows past registers):
+    every row as when it is alone, and dweight of every channel by itself."""
+    R = 1300
+    x, w, r = _norm_inputs(R, C, res, C)
+    pick = [0, 1, 151, 152, 303, 304, 607, 608, 760, 1299]
+    for quant in (None, "token", "block"):
+        out = gdr.rmsnorm_fwd(x, w, residual=r, quant=quant)
+        for i in pick:
+            one = gdr.rmsnorm_fwd(x[i:i + 1].clone(), w, residual=None if r is None else r[i:i + 1].clone(), quant=quant)
+            for k in one:
+                assert torch.equal(out[k][i:i + 1].view(torch.uint8), one[k].view(torch.uint8)), (k, i)
+    s = x if r is None else out["residual"]
+    dy, dres = _norm_inputs(R, C, None, C + 3)[0], None if r is None else r.flip(0).contiguous()
+    back = gdr.rmsnorm_bwd(dy, s, w, out["rstd"], dres=dres)
+    for i in pick:
+        one = gdr.rmsnorm_bwd(dy[i:i + 1].clone(), s[i:i + 1].clone(), w, out["rstd"][i:i + 1].clone(),
+                              dres=None if dres is None else dres[i:i + 1].clone())
+        assert torch.equal(back["dx"][i:i + 1], one["dx"]), i
+    # float32 sums of 1300 terms: below 1300 / (number of partial sums) + 16 roundings, 2^-24 each, of the terms' magnitudes
+    n = dy.double() * s.double() * out["rstd"].double()[:, None]
+    assert ((back["dweight"].double() - n.sum(0)).abs() <= TOL_STATE * n.abs().sum(0)).all()
 
 
 def test_rmsnorm_backward_of_no_rows():
