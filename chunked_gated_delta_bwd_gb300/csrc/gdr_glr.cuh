@@ -22,8 +22,8 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 template <class T> struct PairOf;
 template <> struct PairOf<__nv_bfloat16> {
     using raw = uint32_t;
-    // (a shift and a mask: the conversion function takes three instructions, 225 us instead of 219 for
-    // 30011 x 4096 with the softplus gate)
+    // (a shift and a mask: the conversion function takes three instructions, 3% more time for 30011 x 4096
+    // with the softplus gate)
     static __device__ __forceinline__ float2 widen(raw r) {
         return make_float2(__uint_as_float(r << 16), __uint_as_float(r & 0xffff0000u));
     }
@@ -40,8 +40,8 @@ template <> struct PairOf<float> {
 // The gate is evaluated in base 2: t = g / ln 2, a = 2^t.
 //
 // 2^t = 2^n (1 + m) with n the integer nearest t and m = 2^f - 1 = f q(f), |f| <= 1/2, q the
-// polynomial of degree 5 with the least relative error (1.1e-8; fitted by Lawson's reweighted
-// least squares).  A slow channel (t near 0) keeps its state for hundreds of tokens, over which
+// polynomial of degree 5 with the least relative error (2.1e-8 with these coefficients; fitted by Lawson's
+// reweighted least squares).  A slow channel (t near 0) keeps its state for hundreds of tokens, over which
 // an error of a that has one sign grows with the number of tokens; n is 0 there, so a = 1 + m is
 // rounded once, and s = 1 - a = -m does not cancel (glr_update).  No hardware exponential and no branch: 15
 // instructions for two channels.  Decays below 2^-126 count as 2^-126; NaN stays NaN.
@@ -722,8 +722,8 @@ __device__ __forceinline__ void glr_copy_rows(void* to, const CUtensorMap* map, 
             asm volatile("cp.async.ca.shared.global [%0], [%1], %2;\n" ::"r"(at + q * PITCH), "l"(row), "n"(2 * sizeof(T)) : "memory");
         };
         // (few instructions a row: one warp copies for eight, which wait for it.  32768 x 2050, softplus:
-        // forward 176 us, backward 338; 200 and 384 with the addresses worked out row by row; 2048 channels
-        // by the tensor maps 119 and 221)
+        // forward 197 us, backward 351, an eighth more with the addresses worked out row by row; 2048
+        // channels by the tensor maps 132 and 232)
 #pragma unroll 1
         for (int i = 0; i < rows; i += 8, at += EVERY) {
             if (i >= first && i + 8 <= rows) {

@@ -14,16 +14,18 @@
 namespace gdr {
 
 // Bytes bound it with a given log gate (g, h, dh, and x with the complement, are read once, dx and
-// dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 69 us, 73%
-// of the measured copy rate), the arithmetic with the softplus gate (32768 x 2048: 219 us, 55%).
+// dg written once: 10 or 12 bytes a token and channel in bf16, 20 in float32: 8192 x 2048 71 us, 71%
+// of the measured copy rate, one block an SM by the tiles' shared memory).  With the softplus gate no pipe is
+// saturated (32768 x 2048 with the complement: 229 us, 53%; FMA 59%, issue slots 62%, DRAM 45% of its peak):
+// see the forward.
 // The first walk leaves the base-2 log gates in fp32 where g was; the second derives the decays, and
 // the softplus gate's slope, from them.  g and dh are copied ahead, h and x, which only the second
 // walk needs, when their one buffer is free.
 // Warps without a sequence's beginning or end among their tokens walk in the short loops also where
-// the chunk has one (512 sequences of 32768 tokens, 2048 channels, softplus: 271 us; 286 when all of
+// the chunk has one (512 sequences of 32768 tokens, 2048 channels, softplus: 285 us, 5% more when all of
 // the chunk's warps walked token by token).
-// tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (4: 226 us
-// for 32768 x 2048 with the softplus gate, 2: 218, 1: 229)
+// tokens of an unrolled step: the instruction cache holds more of the walks the shorter it is (against 2,
+// 4: 3% slower for 32768 x 2048 with the softplus gate, 1: 5%)
 constexpr int BWD_WARPS = 8, BWD_SUB = GLR_CHUNK / BWD_WARPS, AT_ONCE = 2;
 template <class TX, bool COMP, bool SUMS>
 struct GlrBwdTile {

@@ -8,16 +8,18 @@ namespace gdr {
 size_t glr_published_bytes(const GlrParams& p) { return glr_runs_bytes(glr_chunks(p), p.C); }
 
 // Bytes bound it with a given log gate (x and g are read once, h is written once: 6 bytes a token
-// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 106 us, 75% of the measured copy
-// rate), the arithmetic with the softplus gate (some 40 instructions a token and channel, all warps'
-// counted; 30011 x 4096: 211 us, 52%) and, in both, the states' way from block to block.  The gate is
-// evaluated once: the first walk leaves the decays in fp32 where g was, for the second one, after the
-// state in front of the chunk is known.  Both walk in rolled loops (unrolled over restarts too, the
+// and channel in bf16; 32768 x 2048 with a float32 gate, 8 bytes: 109 us, 74% of the measured copy
+// rate).  With the softplus gate no pipe is saturated (30011 x 4096 with the complement, some 50
+// instructions a token and channel, all warps' counted: 241 us, 46%; issue slots 66%, FMA 49%, ALU 46%, DRAM
+// 39% of its peak): a tile waits for its rows, for issue slots between twelve warps a block, and for the
+// states' way from block to block.  The gate is
+// evaluated once: the first walk leaves the decays (glr_update) in fp32 where g was, for the second one,
+// after the state in front of the chunk is known.  Both walk in rolled loops (unrolled over restarts too, the
 // code did not fit the instruction cache, which then bound the kernel); a warp in whose tokens a
 // sequence begins or ends folds its run again, token by token, from the decays it has just left
-// (32768 tokens in 512 sequences, 2048 channels, softplus: 151 us; 167 with the gates evaluated token
-// by token in every warp of such a chunk; 119 for one sequence).
-// (tokens of an unrolled step: 30011 x 4096 took 215 us with 8, 219 with 4 or 2)
+// (32768 tokens in 512 sequences, 2048 channels, softplus: 177 us, a tenth more with the gates evaluated
+// token by token in every warp of such a chunk; 132 for one sequence).
+// (tokens of an unrolled step: 30011 x 4096 took 234 us with 8, 237 with 4)
 constexpr int FWD_WARPS = 8, FWD_SUB = GLR_CHUNK / FWD_WARPS, AT_ONCE = 8;
 template <class TX>
 struct GlrFwdTile {
@@ -220,7 +222,7 @@ cudaError_t launch_glr_fwd(const GlrParams& p, cudaStream_t s) {
 // Bytes bound it, and at the sizes of a decoding batch the two memory latencies of a slot and its
 // state: a thread takes V channels, four (8 bytes of bf16, 16 of the state) where rows are whole
 // numbers of aligned pieces, else two, and asks for everything else while the slot is on its way.
-// 509 x 4096 with slots and the softplus gate, from cold caches: 7.0 us (8.3 with two channels and the slot first).
+// 509 x 4096 with slots and the softplus gate, from cold caches: 7.4 us (a sixth more with two channels and the slot first).
 template <class R, int P>
 struct __align__(sizeof(R) * P) Pairs {
     R v[P];
