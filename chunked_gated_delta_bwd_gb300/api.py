@@ -355,7 +355,7 @@ def test_stall_next_call(cta: int):
     lib().gdr_test_stall_next_call(int(cta))
 
 
-KERNEL_NAMES = ("chunk_table", "prep", "states", "main", "out", "conv", "glr", "norm")
+KERNEL_NAMES = ("chunk_table", "prep", "states", "main", "out", "conv", "glr", "norm", "dla", "e4m3")
 
 
 def profile_begin(max_launches: int):

@@ -13,7 +13,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libgdr.so")
 SOURCES = ["gdr_api.cu", "gdr_prep_kda.cu", "gdr_prep_gdn.cu", "gdr_states_tc.cu", "gdr_main_kda.cu", "gdr_main_gdn.cu", "gdr_out.cu", "gdr_conv.cu",
-           "gdr_block_api.cu", "gdr_glr_fwd.cu", "gdr_glr_bwd.cu", "gdr_norm.cu", "gdr_conv_fwd.cu"]
+           "gdr_block_api.cu", "gdr_glr_fwd.cu", "gdr_glr_bwd.cu", "gdr_norm.cu", "gdr_conv_fwd.cu",
+           "gdr_dla_api.cu", "gdr_dla.cu", "gdr_dla_step.cu", "gdr_e4m3_api.cu", "gdr_linear.cu", "gdr_quant.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

@@ -349,6 +349,77 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
                            const void* dres, void* workspace, size_t workspace_bytes, void* dx,
                            float* dweight, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head (the layer next to the delta rule: the same q, k, v,
+ * states and sequences, without the delta term), and the 8-bit products of the projections around
+ * it.  The conventions at the top hold.
+ *
+ *     S_t = e^{g_h} S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t
+ *
+ * per (sequence, value head h) from h0 (or zero), with a constant log decay g_h for each head.
+ *  * q, k: bf16 [T_total, Hk, D]; v, o: bf16 [T_total, H, D]; D = 64 or 128; H a multiple of Hk, value
+ *    head h reads q / k head h / (H / Hk).  q, k and v may be columns of a wider tensor: their token
+ *    strides are given in elements (0 = contiguous, else a multiple of 8).
+ *  * log_decay: float [H].  It is meant to be <= 0 (below -10^4 it counts as -10^4: no memory);
+ *    growth is computed as such until fp32 overflows.  It is a constant: it has no gradient here.
+ *  * h0, ht, dht, dh0: float [N, H, D, D] (row = key channel); h0, ht and dht may be NULL.  An empty
+ *    sequence passes its state through (ht = h0, dh0 = dht).  T_total = 0 is a valid call.
+ *  * The states are carried in fp32 (the tokens' terms in twice bf16's 8 bits); the products that
+ *    o, dq, dk and dv are read from have bf16 operands: q k^T with its decays, and the state.
+ *  * A value that is not finite reaches its whole chunk of 128 tokens and, through the state, what
+ *    follows it in its sequence and head; never another sequence.
+ *  * Inconsistent cu_seqlens raise GDR_DEV_BAD_SEQLENS in the workspace's status word and nothing is
+ *    written; GDR_DEV_TIMEOUT means that a bounded wait ran out: results are missing.
+ *  * Sizes: T_total at most 2^30, N H at most 2^24, T_total H at most 2^36.  No output shares memory
+ *    with an input, another output or the workspace.  Every result is the same, bit for bit, from one
+ *    call to the next.  The workspace need not be initialised; calls that may overlap need one each. */
+typedef struct {
+    int32_t num_seqs;          /* N >= 1 */
+    int64_t total_tokens;      /* T_total >= 0 */
+    int32_t num_heads;         /* H >= 1 */
+    int32_t num_k_heads;       /* Hk, 0 = H */
+    int32_t head_dim;          /* D, 64 or 128 */
+    const int64_t* cu_seqlens; /* device int64 [N + 1], or NULL for dense */
+    float scale;               /* finite */
+    int64_t q_stride, k_stride, v_stride; /* token strides in elements, 0 = contiguous */
+} dla_shape;
+
+/* Bytes of the workspace of dla_fwd (backward = 0) or dla_bwd (backward = 1); 0 for an invalid shape. */
+size_t dla_workspace_bytes(const dla_shape* shape, int32_t backward);
+gdr_status dla_fwd(const dla_shape* shape, const void* q, const void* k, const void* v, const float* log_decay,
+                   const float* h0, void* o, float* ht, void* workspace, size_t workspace_bytes, void* stream);
+/* The gradients of sum <dO_t, o_t> + sum <dht, ht>: dq, dk (bf16 [T_total, Hk, D], summed over the value
+ * heads that share a q / k head), dv (bf16 [T_total, H, D]) and dh0 (always written).  dO is contiguous. */
+gdr_status dla_bwd(const dla_shape* shape, const void* q, const void* k, const void* v, const float* log_decay,
+                   const float* h0, const void* dO, const float* dht, void* workspace, size_t workspace_bytes,
+                   void* dq, void* dk, void* dv, float* dh0, void* stream);
+/* One token of `rows` sequences: q, k bf16 [rows, Hk, D], v, o bf16 [rows, H, D]; state float
+ * [pool, H, D, D], updated in place; slots as for the other single-token steps. */
+gdr_status dla_step(int32_t rows, int32_t num_heads, int32_t num_k_heads, int32_t head_dim, int32_t pool, float scale,
+                    const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                    const float* log_decay, const int64_t* slots, float* state, void* o, void* stream);
+
+/* Quantisation to 8 bits (e4m3) with a scale for each 128 channels of a row, or for each tile of 128 rows
+ * and 128 channels: scale = max |x| / 448 over it (1 where all are zero; the smallest float32 where the
+ * quotient rounds to zero), y = e4m3(x / scale), as gdr_rmsnorm_fwd with GDR_QUANT_BLOCK.
+ *  * x: [rows, C] of x_type (GDR_TYPE_*), rows of stride x_stride (0 = C) as for the norm, C even.
+ *  * tiles = 0: scale float [rows, ceil(C / 128)].  tiles = 1: float [ceil(rows / 128), ceil(C / 128)].
+ *  * y_t, scale_t (tiles only, both or neither; else NULL): the transposes, y_t [C, rows], scale_t
+ *    [ceil(C / 128), ceil(rows / 128)], with the same codes: the operand of the product's backward.
+ *  * A group that holds an infinity gets an infinite scale, one that holds a NaN a NaN among its codes. */
+gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t x_stride, int32_t x_type,
+                          int32_t tiles, void* y, float* scale, void* y_t, float* scale_t, void* stream);
+/* The product of two such operands:
+ *     y[m, n] = bias[n] + sum_b x_scale[m, b] w_scale[n / 128, b] sum_{k in b} x[m, k] w[n, k]
+ * over the blocks b of 128 of the inner dimension K.
+ *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows below 2^31.
+ *  * x_scale: float [rows, ceil(K / 128)], or with x_blocks = 1 [rows, 1] for the whole row (x_blocks is
+ *    1 or ceil(K / 128)); w_scale: float [ceil(N / 128), ceil(K / 128)]; bias float [N] or NULL.
+ *  * y: bf16 [rows, N], rounded once from sums in fp32. */
+gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const void* x, const float* x_scale,
+                           int32_t x_blocks, const void* w, const float* w_scale, const float* bias, void* y,
+                           void* stream);
+
 /* Waits for `stream`, then returns in *device_status the OR of the GDR_DEV_*
  * bits raised by the last call that used `workspace` (0 = none). */
 gdr_status gdr_workspace_status(const void* workspace, void* stream, int* device_status);
@@ -387,7 +458,9 @@ const char* gdr_last_error(void);
 #define GDR_KERNEL_CONV 5        /* causal conv1d (gdr_conv1d_bwd, _fwd, _step) */
 #define GDR_KERNEL_GLR 6         /* gated linear recurrence (glr_fwd, glr_bwd, glr_step) */
 #define GDR_KERNEL_NORM 7        /* RMS norm (gdr_rmsnorm_fwd, gdr_rmsnorm_bwd) */
-#define GDR_KERNEL_COUNT 8
+#define GDR_KERNEL_DLA 8         /* linear attention with a decay for each head (dla_fwd, dla_bwd, dla_step) */
+#define GDR_KERNEL_E4M3 9        /* 8-bit product and quantisation (gdr_linear_e4m3, gdr_quant_e4m3) */
+#define GDR_KERNEL_COUNT 10
 gdr_status gdr_profile_begin(int max_launches);
 gdr_status gdr_profile_end(double* total_ms, int* launches);
 
