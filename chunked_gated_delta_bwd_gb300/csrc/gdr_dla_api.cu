@@ -52,7 +52,10 @@ static gdr_status check_dla(const dla_shape* sh, DlaParams* p) {
 // workspace: status word, states, then the gradients of each value head where heads share q and k
 static size_t heads_bytes(const DlaParams& p) { return p.H == p.Hk ? 0 : sizeof(float) * (size_t)p.T * p.H * p.D; }
 static size_t dla_workspace(const DlaParams& p, bool backward) {
-    return 256 + dla_states_bytes(p, backward) + (backward ? 2 * heads_bytes(p) : 0);
+    const size_t forward = 256 + dla_states_bytes(p, false);
+    if (!backward) return forward;
+    const size_t both = 256 + dla_states_bytes(p, true) + 2 * heads_bytes(p);
+    return both > forward ? both : forward;
 }
 
 struct Span {

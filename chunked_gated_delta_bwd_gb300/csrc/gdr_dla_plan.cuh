@@ -1,0 +1,178 @@
+// How the chunks of linear attention with a decay for each head are shared out.
+//
+// A chain is one (sequence, head): its chunks of 128 tokens in the order in which the state passes through
+// them (back to front for the gradients' walk).  All chunks of a call stand in one line, chain after
+// chain (sequence by sequence, head by head), and each block takes one range of it: ranges of equal
+// length, so that every multiprocessor has the same work whatever the sequences' lengths.  A chain that
+// crosses from one range into the next hands its state over (gdr_dla.cu); where chains are short
+// the ranges end with whole chains instead (`snap`).
+#pragma once
+#include "gdr_common.cuh"
+#include "gdr_dla.h"
+
+namespace gdr {
+namespace dla {
+
+constexpr int CHUNK = 128;
+
+// A chunk of the line.
+struct Place {
+    int seq, head, pos, count;  // the chunk's number in its chain, and the chain's chunks
+    int len;                    // the sequence's tokens
+    int64_t begin;              // its first token
+};
+
+struct Line {
+    int N, H;
+    int64_t T, seq_len;
+    const int64_t* cu;
+    int back;
+
+    __device__ __forceinline__ void sequence(Place& p) const {
+        p.begin = cu ? cu[p.seq] : p.seq * seq_len;
+        p.len = (int)(cu ? cu[p.seq + 1] - p.begin : seq_len);
+        p.count = (p.len + CHUNK - 1) / CHUNK;
+    }
+    // the next chunk (after the last one `seq` is N)
+    __device__ __forceinline__ void next(Place& p) const {
+        if (++p.pos < p.count) return;
+        p.pos = 0;
+        if (++p.head < H) return;
+        p.head = 0;
+        while (++p.seq < N) {
+            sequence(p);
+            if (p.count) return;
+        }
+    }
+    // tokens of the chain before its chunk `pos`, in the order of the walk
+    __device__ __forceinline__ int before(const Place& p, int pos) const {
+        if (!back) return min(pos * CHUNK, p.len);
+        return pos == 0 ? 0 : p.len - (p.count - pos) * CHUNK;
+    }
+    __device__ __forceinline__ int first_row(const Place& p) const { return (back ? p.count - 1 - p.pos : p.pos) * CHUNK; }
+    __device__ __forceinline__ int rows(const Place& p) const { return min(CHUNK, p.len - first_row(p)); }
+    __device__ __forceinline__ int token(const Place& p) const { return (int)p.begin + first_row(p); }
+};
+
+// What a block learns before it starts, through shared memory.
+struct Plan {
+    int total;    // chunks of the line; -1: the sequences' borders are inconsistent
+    int ranges;   // ranges that have chunks (no more than there are chunks)
+    int f0, f1;   // the range
+    Place at;     // its first chunk
+};
+
+__device__ __forceinline__ int range_begin(int total, int r, int ranges) { return (int)((int64_t)total * r / ranges); }
+
+// The place of chunk f of the line, from the sequence that holds it and the chunks of the sequences before it.
+__device__ __forceinline__ Place place_of(const Line& line, int f, int seq, int chunks_before) {
+    Place p;
+    p.seq = seq;
+    line.sequence(p);
+    const int in = f - chunks_before * line.H;
+    p.head = in / p.count;
+    p.pos = in - p.head * p.count;
+    return p;
+}
+
+__device__ __forceinline__ void set_range(Plan* out, int total, int range, int ranges) {
+    ranges = max(min(ranges, total), 1);
+    out->total = total;
+    out->ranges = ranges;
+    out->f0 = total < 0 || range >= ranges ? 0 : range_begin(total, range, ranges);
+    out->f1 = total < 0 || range >= ranges ? 0 : range_begin(total, range + 1, ranges);
+}
+
+// All THREADS threads of the block; `out` and `scratch` (THREADS / 32 ints) in shared memory.
+template <int THREADS>
+__device__ __forceinline__ void make_plan(const Line& line, int range, int ranges, int snap, Plan* out, int* scratch) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!line.cu) {
+        if (tid == 0) {
+            const int per = (int)((line.seq_len + CHUNK - 1) / CHUNK);
+            set_range(out, per * line.N * line.H, range, ranges);
+            const int seq = out->f0 / (per * line.H);
+            out->at = place_of(line, out->f0, seq, seq * per);
+        }
+        __syncthreads();
+    } else {
+        // every block adds up the sequences' chunks: N reads, all of them hits in the second-level cache
+        int sum = 0;
+        bool bad = line.cu[0] != 0 || line.cu[line.N] != line.T;
+        for (int i = tid; i < line.N; i += THREADS) {
+            const int64_t len = line.cu[i + 1] - line.cu[i];
+            bad |= len < 0 || len > line.T;
+            sum += (int)((len + CHUNK - 1) / CHUNK);
+        }
+        // (borders that never decrease from 0 to T are all inside)
+        bad = __syncthreads_or(bad);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        if (lane == 0) scratch[warp] = sum;
+        __syncthreads();
+        int total = 0;
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) total += scratch[i];
+        if (tid == 0) set_range(out, bad ? -1 : total * line.H, range, ranges);
+        __syncthreads();
+        const int f0 = out->f0;
+        // the sequence that holds chunk f0 (none where the range is empty)
+        int base = 0;
+        for (int i0 = 0; f0 < out->f1 && i0 < line.N; i0 += THREADS) {
+            const int i = i0 + tid;
+            const int mine = i < line.N ? (int)((line.cu[i + 1] - line.cu[i] + CHUNK - 1) / CHUNK) : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int u = __shfl_up_sync(~0u, upto, o);
+                if (lane >= o) upto += u;
+            }
+            __syncthreads();
+            if (lane == 31) scratch[warp] = upto;
+            __syncthreads();
+            int strip = 0;
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) {
+                if (w < warp) upto += scratch[w];
+                strip += scratch[w];
+            }
+            const int before = base + upto - mine;
+            if (mine && before <= f0 / line.H && f0 / line.H < before + mine) out->at = place_of(line, f0, i, before);
+            base += strip;
+            if (base > f0 / line.H) break;
+        }
+        __syncthreads();
+    }
+    if (snap && tid == 0 && out->f0 < out->f1) {
+        // whole chains: the first that begins in the range, to the end of the last that does
+        if (out->at.pos != 0) {
+            out->f0 += out->at.count - out->at.pos;
+            out->at.pos = out->at.count - 1;
+            if (out->f0 < out->f1) line.next(out->at);
+        }
+        if (out->f0 > out->f1) out->f0 = out->f1;
+    }
+    if (snap) __syncthreads();
+}
+
+// whether the walk of a range goes on at `p`, chunk f of the line
+__device__ __forceinline__ bool more(const Plan& plan, const Place& p, int f, int snap) {
+    return plan.f0 < plan.f1 && f < plan.total && (f < plan.f1 || (snap && p.pos != 0));
+}
+
+// The log decay of a head.  (Below -10^4 no token remembers another; an infinite one would make 0 times infinity.)
+__device__ __forceinline__ float log_decay(const float* g, int head) {
+    const float x = __ldg(g + head);
+    return x < -1e4f ? -1e4f : x;
+}
+// e^(g n)
+__device__ __forceinline__ float power(float g, int n) { return expf(g * (float)n); }
+// e^(g n) S + t as c.y S + (c.x S + t): a decay near 1 is held by its distance from 1, so that its rounding
+// does not add up over thousands of chunks.
+__device__ __forceinline__ float2 carry(float g, int n) {
+    const float a = g * (float)n;
+    return a > -0.5f && a < 0.5f ? make_float2(expm1f(a), 1.f) : make_float2(expf(a), 0.f);
+}
+
+}  // namespace dla
+}  // namespace gdr

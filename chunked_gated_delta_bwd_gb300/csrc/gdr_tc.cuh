@@ -94,6 +94,10 @@ __device__ __forceinline__ bool mbar_wait(uint32_t mbar, uint32_t parity, int li
     return done != 0;
 }
 
+__device__ __forceinline__ void mbar_arrive(uint32_t mbar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(mbar) : "memory");
+}
+
 // (the "memory" clobbers keep the compiler from moving shared-memory accesses across them)
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }

@@ -74,6 +74,16 @@ inline bool encode_tokens_map(CUtensorMap* m, const void* base, uint64_t T, uint
     return encode_bf16_map(m, base, 3, dims, strides, box);
 }
 
+// tokens of stride ld elements, each [heads][D] bf16, viewed as [D / 64 column blocks][T][heads][64]: one copy
+// moves box_tokens tokens of one head as SW128 column blocks
+inline bool encode_heads_map(CUtensorMap* m, const void* base, uint64_t T, uint64_t heads, uint64_t D, uint64_t ld,
+                             uint32_t box_tokens) {
+    const cuuint64_t dims[4] = {64, heads, T, D / 64};
+    const cuuint64_t strides[3] = {D * 2, ld * 2, 128};
+    const cuuint32_t box[4] = {64, 1, box_tokens, (cuuint32_t)(D / 64)};
+    return encode_bf16_map(m, base, 4, dims, strides, box);
+}
+
 // [rows][cols] bf16 or float32 rows of stride ld elements, boxes of box_rows x 64 columns, not
 // swizzled (a box lies row after row in shared memory); what is outside the tensor reads as zero
 inline bool encode_plain_map(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t cols, uint64_t ld,

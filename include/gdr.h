@@ -384,7 +384,8 @@ typedef struct {
     int64_t q_stride, k_stride, v_stride; /* token strides in elements, 0 = contiguous */
 } dla_shape;
 
-/* Bytes of the workspace of dla_fwd (backward = 0) or dla_bwd (backward = 1); 0 for an invalid shape. */
+/* Bytes of the workspace of dla_fwd (backward = 0) or dla_bwd (backward = 1, enough for dla_fwd too); 0 for an
+ * invalid shape. */
 size_t dla_workspace_bytes(const dla_shape* shape, int32_t backward);
 gdr_status dla_fwd(const dla_shape* shape, const void* q, const void* k, const void* v, const float* log_decay,
                    const float* h0, void* o, float* ht, void* workspace, size_t workspace_bytes, void* stream);
