@@ -1,67 +1,358 @@
-// The product of e4m3 operands with a scale for each block of 128 of the inner dimension.
-#include <cuda_fp8.h>
-
+// The product of e4m3 operands with a scale for each block of 128 of the inner dimension:
+//
+//   y[m, n] = bias[n] + sum_b xs[m, b] ws[n / 128, b] sum_{k in b} x[m, k] w[n, k]
+//
+// The scales are any fp32 numbers, so the tensor cores cannot apply them: each block's product (four
+// steps of 32 of the inner dimension) goes into tensor memory by itself, and groups of threads add it, times its scale,
+// to sums in fp32 registers while the next block's product runs into the other half of the tensor memory.
+//
+// Two forms, the same loop:
+//   rows of x as the product's rows  (many rows of x): a thread holds one row, its scale is one number; blocks
+//       walk the tiles, and the output leaves through shared memory by TMA.
+//   rows of w as the product's rows  (up to 64 rows of x, decoding): the weights' bytes bound it; the tile is 128 outputs by
+//       all rows of x, and a thread holds one output, its scales come from shared memory.
+// Where there are fewer tiles than multiprocessors the inner dimension is split over the blocks of a cluster (up
+// to 8), which add up their parts through one another's shared memory in a fixed order.
 #include "gdr_common.cuh"
 #include "gdr_e4m3.h"
+#include "gdr_internal.h"
+#include "gdr_tc.cuh"
+#include "gdr_tma.h"
 
 namespace gdr {
 namespace {
 
-__device__ __forceinline__ float wide8(uint8_t c) {
-    __nv_fp8_e4m3 v;
-    v.__x = c;
-    return float(v);
+constexpr int KB = 128;  // inner block
+
+// X_ROWS: rows of x as the product's rows; BN: its columns
+template <bool X_ROWS, int BN>
+struct Lin {
+    static constexpr int GROUPS = BN >= 128 ? 2 : 1, COLS = BN / GROUPS, THREADS = 128 + 128 * GROUPS;
+    static constexpr int A = 128 * KB, B = BN * KB, STAGE = A + B;
+    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 5 : 6;
+    static constexpr int oStore = STAGES * STAGE;  // (rows of x: a 128 x 64 bf16 tile for each group)
+    static constexpr int oScale = oStore + (X_ROWS ? GROUPS * 16384 : 0);
+    static constexpr int oBar = oScale + (X_ROWS ? 0 : 2 * 8 * BN * 4);
+    static constexpr int BARS = 2 * STAGES + 9;
+    static constexpr int SMEM = oBar + 8 * BARS + 8 + 1024;
+    static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+};
+
+struct Maps {
+    CUtensorMap a, b, y;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ float4 ld_peer(uint32_t addr, uint32_t rank) {
+    float4 v;
+    asm volatile(
+        "{\n.reg .b32 a;\nmapa.shared::cluster.u32 a, %4, %5;\nld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [a];\n}\n"
+        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+        : "r"(addr), "r"(rank)
+        : "memory");
+    return v;
 }
 
-// 64 x 64 outputs a block, 4 x 4 a thread, 16 of the inner dimension at a time
-__global__ void __launch_bounds__(256) k_linear(const LinearParams p) {
-    __shared__ float a[16][68], b[16][68];
-    const int64_t m0 = (int64_t)blockIdx.x * 64;
-    const int n0 = blockIdx.y * 64, tx = threadIdx.x % 16, ty = threadIdx.x / 16, nb = (p.K + 127) / 128;
-    float acc[4][4] = {};
-    for (int kb = 0; kb < nb; ++kb) {
-        float part[4][4] = {};
-        for (int k0 = kb * 128; k0 < p.K && k0 < kb * 128 + 128; k0 += 16) {
-            __syncthreads();
-            for (int i = threadIdx.x; i < 1024; i += 256) {
-                const int r = i / 16, k = i % 16;
-                a[k][r] = m0 + r < p.M ? wide8(p.x[(m0 + r) * p.K + k0 + k]) : 0.f;
-                b[k][r] = n0 + r < p.N ? wide8(p.w[(int64_t)(n0 + r) * p.K + k0 + k]) : 0.f;
-            }
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) part[i][j] = fmaf(a[k][ty * 4 + i], b[k][tx * 4 + j], part[i][j]);
+template <bool X_ROWS, int BN>
+__global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
+    k_linear(const __grid_constant__ Maps maps, const LinearParams p, int tiles_b, int tiles, int split) {
+    using L = Lin<X_ROWS, BN>;
+    constexpr int COLS = L::COLS;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint32_t tslot;
+    __shared__ int gone_s;
+    unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    const uint32_t sb = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int nkb = (p.K + KB - 1) / KB;
+    const int rank = split > 1 ? (int)cluster_rank() : 0;
+    const int kb0 = (int)((int64_t)nkb * rank / split), kb1 = (int)((int64_t)nkb * (rank + 1) / split);
+
+    const uint32_t bar0 = sb + L::oBar;
+    auto full = [&](int s) { return bar0 + 8 * s; };
+    auto empty = [&](int s) { return bar0 + 8 * (L::STAGES + s); };
+    const uint32_t t_full = bar0 + 16 * L::STAGES, t_empty = t_full + 16, sc_full = t_full + 32, sc_empty = t_full + 48, ended = t_full + 64;
+    if (tid == 0) {
+        for (int i = 0; i < 2 * L::STAGES; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) {
+            tc::mbar_init(t_full + 8 * i, 1);
+            tc::mbar_init(t_empty + 8 * i, 4 * L::GROUPS);
+            tc::mbar_init(sc_full + 8 * i, 32);
+            tc::mbar_init(sc_empty + 8 * i, 4 * L::GROUPS);
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t m = m0 + ty * 4 + i;
-            const float s = m < p.M ? p.xs[m * p.x_blocks + (p.x_blocks > 1 ? kb : 0)] : 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int n = n0 + tx * 4 + j;
-                if (n < p.N) acc[i][j] = fmaf(part[i][j], s * p.ws[(int64_t)(n / 128) * nb + kb], acc[i][j]);
-            }
-        }
+        tc::mbar_init(ended, 1);
+        gone_s = 0;
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int64_t m = m0 + ty * 4 + i;
-            const int n = n0 + tx * 4 + j;
-            if (m < p.M && n < p.N) p.y[m * p.N + n] = __float2bfloat16(acc[i][j] + (p.bias ? p.bias[n] : 0.f));
+    if (warp == 0) tc::alloc(smem_u32(&tslot), L::TMEM);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    const uint32_t tmem = tslot;
+    // Waits are bounded: one that runs out turns every later wait and issue of the block into nothing, and its outputs into NaN.
+    volatile int* gone = &gone_s;
+    auto ok = [&]() { return *gone == 0; };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (ok() && !tc::mbar_wait(bar, parity, 1 << 22)) *gone = 1;
+    };
+    const int first = blockIdx.x / split, step = gridDim.x / split;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- loader ----------------
+            tc::prefetch_map(&maps.a);
+            tc::prefetch_map(&maps.b);
+            int l = 0;
+            for (int t = first; t < tiles && ok(); t += step) {
+                const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
+                for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                    const int s = l % L::STAGES;
+                    if (l >= L::STAGES) wait(empty(s), (l / L::STAGES & 1) ^ 1);
+                    if (!ok()) break;
+                    tc::mbar_expect_tx(full(s), L::STAGE);
+                    tc::tma_load_2d(sb + s * L::STAGE, &maps.a, kb * KB, a0, full(s));
+                    tc::tma_load_2d(sb + s * L::STAGE + L::A, &maps.b, kb * KB, b0, full(s));
+                }
+            }
+            if (!ok())
+                for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
         }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            // ---------------- issuer ----------------
+            constexpr uint32_t id = tc::idesc_e4m3(128, BN);
+            int l = 0;
+            for (int t = first; t < tiles && ok(); t += step) {
+                for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                    const int s = l % L::STAGES, b = l & 1;
+                    wait(full(s), l / L::STAGES & 1);
+                    if (l >= 2) wait(t_empty + 8 * b, (l >> 1 & 1) ^ 1);
+                    if (!ok()) break;
+                    tc::fence_after();
+                    const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < KB / 32; ++k) tc::mma_e4m3(tmem + b * BN, da + 2 * k, db + 2 * k, id, k > 0);
+                    tc::commit(empty(s));
+                    tc::commit(t_full + 8 * b);
+                }
+            }
+            if (!ok()) {
+                tc::commit(ended);
+                tc::mbar_wait(ended, 0);
+            }
+        }
+    } else if (warp == 2 && !X_ROWS) {
+        // ---------------- scales of the columns, eight blocks at a time ----------------
+        int u = 0;
+        for (int t = first; t < tiles; t += step) {
+            const int nb = t / tiles_b;
+            const int64_t m0 = (int64_t)(t % tiles_b) * BN;
+            for (int kb = kb0; kb < kb1; kb += 8, ++u) {
+                if (u >= 2) wait(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
+                float* sc = reinterpret_cast<float*>(smem + L::oScale) + (u & 1) * 8 * BN;
+                for (int j = lane; j < BN; j += 32) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const bool on = m0 + j < p.M && kb + i < kb1;
+                        v[i] = on ? p.xs[(m0 + j) * p.x_blocks + (p.x_blocks > 1 ? kb + i : 0)] * p.ws[(int64_t)nb * nkb + kb + i] : 0.f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) sc[i * BN + j] = v[i];
+                }
+                tc::mbar_arrive(sc_full + 8 * (u & 1));
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- sums ----------------
+        const int q4 = warp & 3, group = (warp - 4) >> 2, i = 32 * q4 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + group * COLS;
+        int l = 0, u = 0;
+        for (int t = first; t < tiles; t += step) {
+            const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
+            float acc[COLS];
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
+            const int64_t row = (int64_t)a0 + i;
+            const float* xs = X_ROWS && row < p.M ? p.xs + row * p.x_blocks : nullptr;
+            const float* ws = p.ws + (int64_t)min((b0 + group * COLS) / 128, (p.N - 1) / 128) * nkb;
+            auto scale_at = [&](int kb) { return xs && kb < kb1 ? __ldg(xs + (p.x_blocks > 1 ? kb : 0)) * __ldg(ws + kb) : 0.f; };
+            float next = X_ROWS ? scale_at(kb0) : 0.f;
+            for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                const int b = l & 1;
+                const float s = next;
+                if (X_ROWS) next = scale_at(kb + 1);
+                const float* sc = reinterpret_cast<const float*>(smem + L::oScale) + (u & 1) * 8 * BN + ((kb - kb0) & 7) * BN;
+                if (!X_ROWS && ((kb - kb0) & 7) == 0) wait(sc_full + 8 * (u & 1), u >> 1 & 1);
+                wait(t_full + 8 * b, l >> 1 & 1);
+                tc::fence_after();
+                constexpr int PART = COLS < 32 ? COLS : 32;
+#pragma unroll
+                for (int c = 0; c < COLS; c += PART) {
+                    uint32_t v[PART / 16][16];
+#pragma unroll
+                    for (int h = 0; h < PART / 16; ++h) tc::ld16_nowait(lanes + b * BN + c + 16 * h, v[h]);
+                    if constexpr (PART == 32) tc::ld_wait(v[0], v[1]);
+                    else tc::ld_wait(v[0]);
+#pragma unroll
+                    for (int j = 0; j < PART; j += 4) {
+                        float4 f = make_float4(s, s, s, s);
+                        if (!X_ROWS) f = *reinterpret_cast<const float4*>(sc + c + j);
+                        const uint32_t* w = v[j / 16] + j % 16;
+                        ACC2(acc, c + j, __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), make_float2(f.x, f.y), F2(acc, c + j)));
+                        ACC2(acc, c + j + 2, __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), make_float2(f.z, f.w), F2(acc, c + j + 2)));
+                    }
+                }
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(t_empty + 8 * b);
+                if (!X_ROWS && (((kb - kb0) & 7) == 7 || kb + 1 == kb1)) {
+                    if (lane == 0) tc::mbar_arrive(sc_empty + 8 * (u & 1));
+                    ++u;
+                }
+            }
+            if (!ok()) {
+#pragma unroll
+                for (int j = 0; j < COLS; ++j) acc[j] = __int_as_float(0x7fffffff);
+            }
+            if (X_ROWS && split == 1) {
+                // out through a 128 x 64 tile for each group (what lies outside y is cut off by the copy)
+                unsigned char* stage = smem + L::oStore + group * 16384;
+#pragma unroll
+                for (int c = 0; c < COLS; c += 64) {
+                    if (i == 0) tc::bulk_wait_read();
+                    tc::named_sync(1 + group, 128);
+                    const int n0 = b0 + group * COLS + c;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        if (p.bias) {
+#pragma unroll
+                            for (int h = 0; h < 8; h += 4) {
+                                if (n0 + 8 * j + h >= p.N) continue;
+                                const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + n0 + 8 * j + h));
+                                float* a = acc + c + 8 * j + h;
+                                a[0] += f.x, a[1] += f.y, a[2] += f.z, a[3] += f.w;
+                            }
+                        }
+                        const float* a = acc + c + 8 * j;
+                        *reinterpret_cast<uint4*>(stage + tc::sw_chunk(i, j, 128)) =
+                            make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+                    }
+                    tc::fence_async_smem();
+                    tc::named_sync(1 + group, 128);
+                    if (i == 0 && n0 < p.N) {
+                        tc::tma_store_2d(&maps.y, n0, a0, smem_u32(stage));
+                        tc::bulk_commit();
+                    }
+                }
+            } else {
+                // the part of this block, for the cluster (the tiles' memory is free: this is the block's only tile)
+                float* part = reinterpret_cast<float*>(smem);
+                if (X_ROWS) {
+#pragma unroll
+                    for (int j = 0; j < COLS; j += 4)
+                        *reinterpret_cast<float4*>(part + ((group * COLS + j) / 4 * 128 + i) * 4) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < COLS; ++j) part[j * 128 + i] = acc[j];
+                }
+            }
+        }
+        if (X_ROWS && split == 1 && i == 0) tc::bulk_wait_all();
+    }
+    __syncwarp();
+    if (!X_ROWS || split > 1) {
+        if (split > 1) cluster_sync();
+        else __syncthreads();
+        const int a0 = first / tiles_b * 128, b0 = first % tiles_b * BN;
+        auto total = [&](int word) {
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int r = 0; r < split; ++r) {
+                const float4 v = split > 1 ? ld_peer(sb + 4 * word, r) : *reinterpret_cast<const float4*>(smem + 4 * word);
+                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
+            }
+            return s;
+        };
+        auto put = [&](int64_t m, int n, const float4& s) {
+            float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p.bias) f = __ldg(reinterpret_cast<const float4*>(p.bias + n));
+            *reinterpret_cast<uint2*>(p.y + m * p.N + n) = make_uint2(pack_bf16(s.x + f.x, s.y + f.y), pack_bf16(s.z + f.z, s.w + f.w));
+        };
+        // the ranks share out the tile's quadruples of outputs
+        constexpr int QUADS = 128 * BN / 4;
+        for (int e = rank * L::THREADS + tid; e < QUADS; e += split * L::THREADS) {
+            if (X_ROWS) {  // quadruple e: columns 4 (e / 128), row e % 128
+                const int n = b0 + e / 128 * 4;
+                const int64_t m = (int64_t)a0 + e % 128;
+                if (m < p.M && n < p.N) put(m, n, total(4 * e));
+            } else {       // column (row of x) e / 32, outputs 4 (e % 32)
+                const int64_t m = (int64_t)b0 + e / 32;
+                const int n = a0 + e % 32 * 4;
+                if (m < p.M && n < p.N) put(m, n, total(4 * e));
+            }
+        }
+        if (split > 1) cluster_sync();
+    }
+    tc::fence_before();
+    __syncthreads();
+    if (warp == 0) tc::dealloc(tmem, L::TMEM);
+}
+
+template <bool X_ROWS, int BN>
+cudaError_t go(const LinearParams& p, int split, cudaStream_t s) {
+    using L = Lin<X_ROWS, BN>;
+    Maps maps;
+    memset(&maps, 0, sizeof(maps));
+    const int a_rows = X_ROWS ? (int)p.M : p.N, b_rows = X_ROWS ? p.N : (int)p.M;
+    if (!encode_bytes_map(&maps.a, X_ROWS ? p.x : p.w, a_rows, p.K, 128) || !encode_bytes_map(&maps.b, X_ROWS ? p.w : p.x, b_rows, p.K, BN) ||
+        !encode_rows_map(&maps.y, p.y, p.M, p.N, 128))
+        return cudaErrorInvalidValue;
+    const int tiles_b = (b_rows + BN - 1) / BN;
+    const int64_t tiles = (int64_t)((a_rows + 127) / 128) * tiles_b;
+    if (tiles > (1 << 30) / 8) return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(k_linear<X_ROWS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    // (one tile a cluster; blocks that store by TMA walk the tiles)
+    cfg.gridDim = dim3((unsigned)(X_ROWS && split == 1 ? (tiles < num_sms() ? tiles : num_sms()) : tiles * split));
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = split > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, k_linear<X_ROWS, BN>, maps, p, tiles_b, (int)tiles, split);
+}
+
+// blocks of the inner dimension's split for `tiles` tiles: as many as fill the multiprocessors, at most 8, two blocks of 128 each at least
+int split_of(int64_t tiles, int K) {
+    const int nkb = (K + KB - 1) / KB;
+    int s = 1;
+    while (s < 8 && 2 * s * tiles <= num_sms() + num_sms() / 2 && 4 * s <= nkb) s *= 2;
+    return s;
 }
 
 }  // namespace
 
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s) {
-    k_linear<<<dim3((unsigned)((p.M + 63) / 64), (p.N + 63) / 64), 256, 0, s>>>(p);
-    return cudaGetLastError();
+    const int64_t n128 = (p.N + 127) / 128, m128 = (p.M + 127) / 128;
+    if (p.M <= 64) {
+        const int split = split_of(n128, p.K);
+        if (p.M <= 16) return go<false, 16>(p, split, s);
+        if (p.M <= 32) return go<false, 32>(p, split, s);
+        return go<false, 64>(p, split, s);
+    }
+    if (m128 * ((p.N + 255) / 256) >= num_sms()) return go<true, 256>(p, 1, s);
+    return go<true, 128>(p, split_of(m128 * n128, p.K), s);
 }
 
 }  // namespace gdr

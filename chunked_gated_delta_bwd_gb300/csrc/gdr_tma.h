@@ -84,6 +84,18 @@ inline bool encode_heads_map(CUtensorMap* m, const void* base, uint64_t T, uint6
     return encode_bf16_map(m, base, 4, dims, strides, box);
 }
 
+// [rows][cols] bytes, boxes of box_rows x 128 bytes (one SW128 column block)
+inline bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
+    memset(m, 0, sizeof(*m));
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {cols};
+    const cuuint32_t box[2] = {128, box_rows}, elem[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [rows][cols] bf16 or float32 rows of stride ld elements, boxes of box_rows x 64 columns, not
 // swizzled (a box lies row after row in shared memory); what is outside the tensor reads as zero
 inline bool encode_plain_map(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t cols, uint64_t ld,

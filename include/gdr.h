@@ -416,7 +416,8 @@ gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t
  *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows below 2^31.
  *  * x_scale: float [rows, ceil(K / 128)], or with x_blocks = 1 [rows, 1] for the whole row (x_blocks is
  *    1 or ceil(K / 128)); w_scale: float [ceil(N / 128), ceil(K / 128)]; bias float [N] or NULL.
- *  * y: bf16 [rows, N], rounded once from sums in fp32. */
+ *  * y: bf16 [rows, N], rounded once from sums in fp32; it shares no memory with an input.  Should a bounded
+ *    wait inside run out, the outputs concerned are NaN. */
 gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const void* x, const float* x_scale,
                            int32_t x_blocks, const void* w, const float* w_scale, const float* bias, void* y,
                            void* stream);
