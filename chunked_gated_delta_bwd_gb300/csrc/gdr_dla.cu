@@ -41,31 +41,40 @@ namespace {
 
 using namespace dla;
 
+// Tiles in shared memory: X, Y and Z of the chunks to come (a slot of X is free when its output has been
+// stored from it, of Y when P is there and Y' has been made from it, of Z when its products are done), both halves of Y',
+// the state's copy.
 template <int D>
 struct Cfg {
-    static constexpr int TILE = CHUNK * D * 2, RING = D == 128 ? 5 : 8;
-    static constexpr int oLo = RING * TILE, oS = oLo + TILE, oTab = oS + D * D * 2;
+    static constexpr int TILE = CHUNK * D * 2;
+    static constexpr int NX = D == 128 ? 2 : 3, NY = D == 128 ? 1 : 2, NZ = NY, SLOTS = NX + NY + NZ;
+    static constexpr int oHi = SLOTS * TILE, oLo = oHi + TILE, oS = oLo + TILE, oTab = oS + D * D * 2;
     // (the product Y'^T Z has 128 rows; with 64 channels the upper ones read what lies behind the tile)
-    static constexpr int oEnd = (oTab + 1024 > oLo + 2 * CHUNK * 128 ? oTab + 1024 : oLo + 2 * CHUNK * 128);
-    static constexpr int oBar = oEnd, BARS = 2 * RING + 10;
-    static constexpr int SMEM = oBar + 8 * BARS + 128 + 1024;
+    static constexpr int oEnd = (oTab + 512 > oLo + 2 * CHUNK * 128 ? oTab + 512 : oLo + 2 * CHUNK * 128);
+    static constexpr int oBar = oEnd, BARS = 2 * SLOTS + 10 + 2 * NX;
+    static constexpr int SMEM = oBar + 8 * BARS + 1024;
+    static constexpr int THREADS = 640;  // a warpgroup of single threads' roles, two each for groups A and B
+    static constexpr int REGS = 96, REGS_1 = 80, REGS_B = 104;  // at the launch (and group A), of the single threads, of group B
 };
+static_assert(Cfg<128>::REGS_1 + 2 * Cfg<128>::REGS_B <= 3 * Cfg<128>::REGS, "the groups' registers come out of the launch's");
 template <int D>
 struct TailCfg {
     static constexpr int TILE = CHUNK * D * 2, RING = D == 128 ? 5 : 8;
     static constexpr int oLo = RING * TILE, oEnd = oLo + 2 * TILE + (D == 128 ? 0 : CHUNK * 128);
     static constexpr int oBar = oEnd, BARS = 2 * RING + 5;
-    static constexpr int SMEM = oBar + 8 * BARS + 128 + 1024;
+    static constexpr int SMEM = oBar + 8 * BARS + 1024;
+    static constexpr int THREADS = 384;
 };
 
 struct Walk {
-    CUtensorMap X, Y, Z, out;
+    CUtensorMap X, Y, Z, out;       // (out: bf16, or fp32 where value heads share a head of it)
     int gx, gy, gz;                 // value heads that share a head of the tensor
     int back, turned;               // walked back in time; on transposed states
     float p_scale, o_scale, w_scale;  // of P, of X C, of the state's terms
     const float* init;              // [N][H][D][D] or nullptr
     const float* joined;            // incoming states of ranges that begin inside a chain
     float* last;                    // final states or nullptr
+    int twice;                      // Y' in two bf16 halves: the final states are wanted as fp32 results
     __nv_bfloat16* o;
     float* o32;                     // fp32 outputs for each value head instead
 };
@@ -76,6 +85,7 @@ struct Walks {
 
 struct Grid {
     int N, H, D, ranges, snap;
+    int pieces;  // blocks that share the sum of a range's last chain
     int64_t T, seq_len;
     const int64_t* cu;
     const float* g;
@@ -83,395 +93,500 @@ struct Grid {
 };
 __device__ __forceinline__ Line line_of(const Grid& p, int back) { return Line{p.N, p.H, p.T, p.seq_len, p.cu, back}; }
 
-// Waits are bounded: one that runs out records it, and turns every later wait and issue of the block into nothing.
+// Waits are bounded: one that runs out records it, and ends every role of the block at its next wait.
 struct Waiter {
     volatile int* gone;
     int* status;
     __device__ __forceinline__ bool ok() const { return *gone == 0; }
-    __device__ __forceinline__ void operator()(uint32_t bar, uint32_t parity) const {
-        if (ok() && !tc::mbar_wait(bar, parity, 1 << 22)) {
-            *gone = 1;
-            atomicOr(status, ST_MMA_TIMEOUT);
+    // by one thread
+    __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+        if (tc::mbar_try(bar, parity)) return true;
+        for (int i = 0; i < 1 << 22; ++i) {
+            if (!ok()) return false;
+            if (tc::mbar_try(bar, parity)) return true;
         }
+        give_up();
+        return false;
+    }
+    // by a whole warp, which goes on converged
+    __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+        if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+        for (int i = 0; i < 1 << 22; ++i) {
+            if (__any_sync(~0u, !ok())) return false;
+            if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+        }
+        give_up();
+        return false;
+    }
+    __device__ __forceinline__ void give_up() const {
+        *gone = 1;
+        atomicOr(status, ST_MMA_TIMEOUT);
     }
 };
 
-// Row `row` of a tile times w, as two bf16 rows: the first over the row, the rest into `lo`.  w = 0 takes
-// whatever the row holds as zero.
-template <int D>
-__device__ __forceinline__ void split_row(unsigned char* tile, unsigned char* lo, int row, float w) {
-#pragma unroll 4
-    for (int j = 0; j < D / 8; ++j) {
-        const uint32_t at = tc::sw_chunk(row, j, CHUNK);
-        uint4 hi4 = make_uint4(0, 0, 0, 0), lo4 = hi4;
-        if (w != 0.f) {
-            const uint4 u = *reinterpret_cast<const uint4*>(tile + at);
-            const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+// Chunks j0 to j0 + N of 16 bytes of row `row` of a tile times w, rounded to bf16 (`hi`) and, TWICE, what that leaves
+// (`lo`).  (Not unrolled: what eight warps of two groups run in turn has to stay in the instruction caches.)
+template <int N, bool TWICE>
+__device__ __forceinline__ void split_row(const unsigned char* tile, unsigned char* hi, unsigned char* lo, int row, int j0, float w) {
+#pragma unroll 1
+    for (int j2 = j0; j2 < j0 + N; j2 += 2) {
+        uint4 u[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) u[j] = *reinterpret_cast<const uint4*>(tile + tc::sw_chunk(row, j2 + j, CHUNK));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t in[4] = {u[j].x, u[j].y, u[j].z, u[j].w};
             uint32_t h[4], l[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = __fmul2_rn(make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), make_float2(w, w));
                 h[i] = pack_bf16(f.x, f.y);
-                l[i] = pack_bf16(f.x - __uint_as_float(h[i] << 16), f.y - __uint_as_float(h[i] & 0xffff0000u));
+                if (TWICE) {
+                    const float2 r = __ffma2_rn(make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)), make_float2(-1.f, -1.f), f);
+                    l[i] = pack_bf16(r.x, r.y);
+                }
             }
-            hi4 = make_uint4(h[0], h[1], h[2], h[3]);
-            lo4 = make_uint4(l[0], l[1], l[2], l[3]);
+            const uint32_t at = tc::sw_chunk(row, j2 + j, CHUNK);
+            *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+            if (TWICE) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
         }
-        *reinterpret_cast<uint4*>(tile + at) = hi4;
-        *reinterpret_cast<uint4*>(lo + at) = lo4;
     }
 }
-// row `row` of a tile made zero (a row of another sequence, whose values must not reach a product)
-template <int D>
-__device__ __forceinline__ void clear_row(unsigned char* tile, int row) {
+// the same chunks of a row made zero (a row of another sequence, whose values must not reach a product)
+template <int N>
+__device__ __forceinline__ void clear_row(unsigned char* tile, int row, int j0) {
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j) *reinterpret_cast<uint4*>(tile + tc::sw_chunk(row, j, CHUNK)) = make_uint4(0, 0, 0, 0);
+    for (int j = 0; j < N; ++j) *reinterpret_cast<uint4*>(tile + tc::sw_chunk(row, j0 + j, CHUNK)) = make_uint4(0, 0, 0, 0);
+}
+// What the loader tells the other roles of a chunk (the walk along the line costs registers that they need for sums).
+struct Chunk {
+    int t0;     // first token
+    int rows;   // tokens, and the bits below
+    int head;
+    int chain;  // seq * H + head
+    static constexpr int ENDS = 256, LAST = 512;  // the chain ends with it; the range does
+    __device__ __forceinline__ int tokens() const { return rows & 255; }
+    __device__ __forceinline__ bool ends() const { return rows & ENDS; }
+    __device__ __forceinline__ bool last() const { return rows & LAST; }
+};
+__device__ __forceinline__ Chunk chunk_at(const int4* chunks, int it) {
+    const int4 c = chunks[it & 7];
+    return Chunk{c.x, c.y, c.z, c.w};
 }
 
-// the state's terms of a chunk: Y'^T Z from both halves of Y'
+// one arrival for a warp, after all of its threads' work
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// the state's terms of a chunk: Y'^T Z, from both halves of Y' if there are two
 template <int D>
-__device__ __forceinline__ void issue_terms(uint32_t to, uint32_t hi, uint32_t lo, uint32_t z) {
+__device__ __forceinline__ void issue_terms(uint32_t on, uint32_t to, uint32_t hi, uint32_t lo, uint32_t z, bool twice) {
     constexpr uint32_t id = tc::idesc(128, D, 1, 1);
 #pragma unroll
-    for (int k = 0; k < CHUNK; k += 16) tc::mma(to, tc::mdesc(hi, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, k > 0);
+    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(hi, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, k > 0);
+    if (!twice) return;
 #pragma unroll
-    for (int k = 0; k < CHUNK; k += 16) tc::mma(to, tc::mdesc(lo, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, 1);
+    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(lo, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, 1);
 }
 
 template <int D, int WALKS>
-__global__ void __launch_bounds__(384, 1) k_dla(const __grid_constant__ Walks<WALKS> walks, const Grid p) {
+__global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constant__ Walks<WALKS> walks, const Grid p) {
     using K = Cfg<D>;
+    constexpr int HALF = D / 2;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Plan plan_s;
-    __shared__ int scratch[12];
+    __shared__ int scratch[K::THREADS / 32];
     __shared__ int gone_s;
     __shared__ uint32_t tslot;
+    __shared__ int4 chunks[8];
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int range = blockIdx.x / WALKS;
     const Walk& w = walks.w[WALKS == 1 ? 0 : blockIdx.x % WALKS];
-    const Line line = line_of(p, w.back);
+    const bool back = WALKS > 1 && w.back, wide = WALKS > 1 && w.o32;  // (the forward is one walk, forward in time, into bf16)
+    const Line line = line_of(p, back);
 
+    // slot of chunk `it`'s tile, and how often that slot has been used before
     const uint32_t bar0 = sb + K::oBar;
     auto full = [&](int slot) { return bar0 + 8 * slot; };
-    auto empty = [&](int slot) { return bar0 + 8 * (K::RING + slot); };
-    const uint32_t more_bars = bar0 + 16 * K::RING;
+    auto empty = [&](int slot) { return bar0 + 8 * (K::SLOTS + slot); };
+    auto slot_x = [&](int it) { return it % K::NX; };
+    auto slot_y = [&](int it) { return K::NX + it % K::NY; };
+    auto slot_z = [&](int it) { return K::NX + K::NY + it % K::NZ; };
+    auto turn = [&](int it, int n) { return (uint32_t)(it / n & 1); };
+    const uint32_t more_bars = bar0 + 16 * K::SLOTS;
     const uint32_t p_full = more_bars, p_ready = more_bars + 8, o_full = more_bars + 16, o_free = more_bars + 24,
                    s_ready = more_bars + 32, s_free = more_bars + 40, y_ready = more_bars + 48, d_full = more_bars + 56,
-                   staged = more_bars + 64, ended = more_bars + 72;
+                   half_out = more_bars + 64, ended = more_bars + 72;
+    // (group A may be chunks ahead of the stores: a barrier for each of X's slots, and each half of a wide output)
+    auto staged = [&](int it, int half) { return more_bars + 80 + 16 * slot_x(it) + 8 * half; };
     if (tid == 0) {
-        for (int i = 0; i < 2 * K::RING; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+        // (Y's slots are given back by P's product and by group B's eight warps)
+        for (int i = 0; i < 2 * K::SLOTS; ++i) tc::mbar_init(bar0 + 8 * i, i >= K::SLOTS + K::NX && i < K::SLOTS + K::NX + K::NY ? 9 : 1);
         tc::mbar_init(p_full, 1);
-        tc::mbar_init(p_ready, 128);
+        tc::mbar_init(p_ready, 8);
         tc::mbar_init(o_full, 1);
-        tc::mbar_init(o_free, 128);
-        tc::mbar_init(s_ready, 128);
+        tc::mbar_init(o_free, 8);
+        tc::mbar_init(s_ready, 8);
         tc::mbar_init(s_free, 1);
-        tc::mbar_init(y_ready, 128);
+        tc::mbar_init(y_ready, 8);
         tc::mbar_init(d_full, 1);
-        tc::mbar_init(staged, 128);
+        for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_init(staged(0, 0) + 8 * i, wide ? 4 : 8);
+        tc::mbar_init(half_out, 1);
         tc::mbar_init(ended, 1);
         gone_s = 0;
     }
     if (warp == 0) tc::alloc(smem_u32(&tslot), 512);
-    make_plan<384>(line, range, p.ranges, p.snap, &plan_s, scratch);
+    make_plan<K::THREADS>(line, range, p.ranges, p.snap, &plan_s, scratch);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tslot;
     const Waiter wait{&gone_s, p.status};
-    const Plan plan = plan_s;
-    if (plan.total < 0 && tid == 0) atomicOr(p.status, ST_BAD_SEQLENS);
-
-    // load l of the block: Y, Z, X of its chunk l / 3
-    auto slot_of = [&](int l) { return l % K::RING; };
-    auto parity_of = [&](int l) { return (uint32_t)((l / K::RING) & 1); };
+    if (plan_s.total < 0 && tid == 0) atomicOr(p.status, ST_BAD_SEQLENS);
+    const bool any = plan_s.f0 < plan_s.f1;
 
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
-        if (warp == 0 && lane == 0) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(K::REGS_1));
+        if (warp == 0 && lane == 0 && any) {
             // ---------------- loader ----------------
+            tc::prefetch_map(&w.X);
             tc::prefetch_map(&w.Y);
             tc::prefetch_map(&w.Z);
-            tc::prefetch_map(&w.X);
-            int l = 0;
+            int it = 0;
+            bool on[3] = {};  // copies issued into Y's, X's, Z's slots in the last turn that was begun
+            const Plan plan = plan_s;
             Place at = plan.at;
-            for (int f = plan.f0; more(plan, at, f, p.snap); ++f, line.next(at)) {
-                const int t0 = line.token(at);
+            bool go_on = true;
+            for (int f = plan.f0; go_on; ++it) {
+                const int t0 = line.token(at), h0 = at.head;
+                int4 c = make_int4(t0, line.rows(at), h0, at.seq * p.H + h0);
+                if (at.pos + 1 == at.count) c.y |= Chunk::ENDS;
+                line.next(at);
+                go_on = more(plan, at, ++f, p.snap);
+                if (!go_on) c.y |= Chunk::LAST;
+                chunks[it & 7] = c;
+                on[0] = on[1] = on[2] = false;
 #pragma unroll
-                for (int j = 0; j < 3; ++j, ++l) {
-                    const int s = slot_of(l);
-                    if (l >= K::RING) wait(empty(s), parity_of(l) ^ 1);
-                    if (!wait.ok()) break;
-                    const CUtensorMap* m = j == 0 ? &w.Y : j == 1 ? &w.Z : &w.X;
-                    const int h = at.head / (j == 0 ? w.gy : j == 1 ? w.gz : w.gx);
+                for (int j = 0; j < 3; ++j) {
+                    const int n = j == 0 ? K::NY : j == 1 ? K::NX : K::NZ, s = j == 0 ? slot_y(it) : j == 1 ? slot_x(it) : slot_z(it);
+                    if (it >= n && !wait(empty(s), turn(it, n) ^ 1)) break;
+                    const CUtensorMap* m = j == 0 ? &w.Y : j == 1 ? &w.X : &w.Z;
+                    const int h = h0 / (j == 0 ? w.gy : j == 1 ? w.gx : w.gz);
                     tc::mbar_expect_tx(full(s), K::TILE);
                     tc::tma_load_4d(sb + s * K::TILE, m, 0, h, t0, 0, full(s));
+                    on[j] = true;
                 }
                 if (!wait.ok()) break;
             }
-            // (where the block gave up: its copies have to land before it ends)
-            if (!wait.ok())
-                for (int i = l > K::RING ? l - K::RING : 0; i < l; ++i) tc::mbar_wait(full(slot_of(i)), parity_of(i));
-        } else if (warp == 1 && lane == 0) {
-            // ---------------- issuer ----------------
+            if (!wait.ok()) {  // (the block gave up: its copies have to land before it ends)
+                auto landed = [&](int last, int n, int which) {
+                    for (int i = last - n + 1 > 0 ? last - n + 1 : 0; i <= last; ++i)
+                        tc::mbar_wait(full(which == 0 ? slot_y(i) : which == 1 ? slot_x(i) : slot_z(i)), turn(i, n));
+                };
+                landed(on[0] ? it : it - 1, K::NY, 0);
+                landed(on[1] ? it : it - 1, K::NX, 1);
+                landed(on[2] ? it : it - 1, K::NZ, 2);
+            }
+        } else if (warp == 1 && any) {
+            // ---------------- issuer (the whole warp, converged; lane 0 issues) ----------------
+            const uint32_t on = lane == 0;
             const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 256, tD = tmem + 384;
             constexpr uint32_t idP = tc::idesc(128, 128, 0, 0), idO = tc::idesc(128, D, 0, 1);
-            Place at = plan.at;
-            int it = 0;
-            for (int f = plan.f0; more(plan, at, f, p.snap); ++f, line.next(at), ++it) {
-                const int ly = 3 * it, lz = ly + 1, lx = ly + 2;
-                const uint32_t Y = sb + slot_of(ly) * K::TILE, Z = sb + slot_of(lz) * K::TILE, X = sb + slot_of(lx) * K::TILE;
+            for (int it = 0;; ++it) {
+                const int sx = slot_x(it), sy = slot_y(it), sz = slot_z(it);
+                const uint32_t X = sb + sx * K::TILE, Y = sb + sy * K::TILE, Z = sb + sz * K::TILE;
                 const uint32_t ph = it & 1;
-                wait(full(slot_of(ly)), parity_of(ly));
-                wait(full(slot_of(lx)), parity_of(lx));
-                if (it) wait(o_full, ph ^ 1);  // (P Z of the chunk before has read P)
-                if (!wait.ok()) break;
+                if (!wait.warp(full(sy), turn(it, K::NY)) || !wait.warp(full(sx), turn(it, K::NX))) break;
+                if (it && !wait.warp(o_full, ph ^ 1)) break;  // (P Z of the chunk before has read P)
                 tc::fence_after();
 #pragma unroll
-                for (int k = 0; k < D; k += 16) tc::mma(tP, tc::kdesc(X, CHUNK, 0, k), tc::kdesc(Y, CHUNK, 0, k), idP, k > 0);
-                tc::commit(p_full);
-                wait(s_ready, ph);
-                if (it) wait(o_free, ph ^ 1);
-                if (!wait.ok()) break;
+                for (int k = 0; k < D; k += 16) tc::mma_if(on, tP, tc::kdesc(X, CHUNK, 0, k), tc::kdesc(Y, CHUNK, 0, k), idP, k > 0);
+                tc::commit_if(on, p_full);
+                tc::commit_if(on, empty(sy));
+                if (!wait.warp(full(sz), turn(it, K::NZ)) || !wait.warp(y_ready, ph)) break;
+                tc::fence_after();
+                issue_terms<D>(on, tD, sb + K::oHi, sb + K::oLo, Z, w.twice);
+                tc::commit_if(on, d_full);
+                if (!wait.warp(s_ready, ph) || (it && !wait.warp(o_free, ph ^ 1))) break;
                 tc::fence_after();
 #pragma unroll
-                for (int k = 0; k < D; k += 16) tc::mma(tO2, tc::kdesc(X, CHUNK, 0, k), tc::mdesc(sb + K::oS, D, 0, k), idO, k > 0);
-                tc::commit(s_free);
-                wait(full(slot_of(lz)), parity_of(lz));
-                const bool part = line.rows(at) < CHUNK;
-                if (part) wait(y_ready, ph);  // (group B clears rows of Z)
-                wait(p_ready, ph);
-                if (!wait.ok()) break;
+                for (int k = 0; k < D; k += 16) tc::mma_if(on, tO2, tc::kdesc(X, CHUNK, 0, k), tc::mdesc(sb + K::oS, D, 0, k), idO, k > 0);
+                tc::commit_if(on, s_free);
+                if (!wait.warp(p_ready, ph)) break;
                 tc::fence_after();
+                // (bf16 P: the 32 columns of slice s lie in the first 16 of the 32 that held them in fp32)
 #pragma unroll
-                for (int k = 0; k < CHUNK; k += 16) tc::mma_ts(tO1, tP + k / 2, tc::mdesc(Z, CHUNK, 0, k), idO, k > 0);
-                tc::commit(o_full);
-                if (!part) wait(y_ready, ph);
-                if (!wait.ok()) break;
-                tc::fence_after();
-                issue_terms<D>(tD, Y, sb + K::oLo, Z);
-                tc::commit(d_full);
-                tc::commit(empty(slot_of(ly)));
-                tc::commit(empty(slot_of(lz)));
+                for (int k = 0; k < CHUNK; k += 16) tc::mma_ts_if(on, tO1, tP + (k & ~31) + (k & 31) / 2, tc::mdesc(Z, CHUNK, 0, k), idO, k > 0);
+                tc::commit_if(on, o_full);
+                tc::commit_if(on, empty(sz));
+                if (__any_sync(~0u, chunk_at(chunks, it).last())) break;
             }
             if (!wait.ok()) {  // (the products in flight have to end before the tensor memory is given back)
-                tc::commit(ended);
+                tc::commit_if(on, ended);
                 tc::mbar_wait(ended, 0);
             }
-        } else if (warp == 2 && lane == 0) {
+        } else if (warp == 2 && lane == 0 && any) {
             // ---------------- stores ----------------
-            Place at = plan.at;
-            int it = 0;
-            for (int f = plan.f0; more(plan, at, f, p.snap); ++f, line.next(at), ++it) {
-                const int s = slot_of(3 * it + 2);
-                wait(staged, it & 1);
-                if (!wait.ok()) break;
-                if (!w.o32 && line.rows(at) == CHUNK) {
-                    tc::tma_store_4d(&w.out, 0, at.head, line.token(at), 0, sb + s * K::TILE);
+            for (int it = 0;; ++it) {
+                const uint32_t X = sb + slot_x(it) * K::TILE;
+                if (wide) {
+                    // fp32, half of the columns at a time: each fills X's tile
+                    if (!wait(staged(it, 0), turn(it, K::NX))) break;
+                    const Chunk now = chunk_at(chunks, it);
+                    const bool whole = now.tokens() == CHUNK;
+                    auto put = [&](int half) {
+                        if (!whole) return;
+                        tc::tma_store_4d(&w.out, 0, now.head, now.t0, half * (D / 64), X);
+                        tc::bulk_commit();
+                        tc::bulk_wait_read();
+                    };
+                    put(0);
+                    tc::mbar_arrive(half_out);
+                    if (!wait(staged(it, 1), turn(it, K::NX))) break;
+                    put(1);
+                    tc::mbar_arrive(empty(slot_x(it)));
+                    if (now.last()) break;
+                    continue;
+                }
+                if (!wait(staged(it, 0), turn(it, K::NX))) break;
+                const Chunk now = chunk_at(chunks, it);
+                if (now.tokens() == CHUNK) {
+                    tc::tma_store_4d(&w.out, 0, now.head, now.t0, 0, X);
                     tc::bulk_commit();
                     tc::bulk_wait_read();
                 }
-                tc::mbar_arrive(empty(s));
+                tc::mbar_arrive(empty(slot_x(it)));
+                if (now.last()) break;
             }
             tc::bulk_wait_all();
         }
-    } else if (warp < 8) {
+    } else if (warp < 12) {
         // ---------------- group A: P, outputs ----------------
-        const int q4 = warp & 3, i = 32 * q4 + lane;  // row of the chunk
+        // two warps for each 32 rows: of P's slices of 32 columns one takes 0 and 2, the other 1 and 3; of an output's
+        // columns each takes half
+        const int q4 = warp & 3, half = (warp - 4) >> 2, i = 32 * q4 + lane;  // row of the chunk
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
-        float* tab = reinterpret_cast<float*>(smem + K::oTab);  // tab[i - j + 127] = D_ij
-        Place at = plan.at;
-        int it = 0, head = -1;
-        float r_full = 0.f, g = 0.f;
-        for (int f = plan.f0; more(plan, at, f, p.snap); ++f, line.next(at), ++it) {
+        // decays: on the diagonal slice D_ij from a table (tab[lane - j + 31], j the column in the slice); elsewhere a
+        // factor of the column (cols[j]) times one of the row, neither above 1: forward gamma^{31-j} and
+        // gamma^{i - 32 s - 31}, back gamma^j and gamma^{32 s - i}
+        float* tab = reinterpret_cast<float*>(smem + K::oTab);
+        float* cols = tab + 64;
+        int head = -1;
+        float r_full = 0.f, g = 0.f, rf0 = 0.f, rf1 = 0.f;
+        for (int it = 0; any; ++it) {
             const uint32_t ph = it & 1;
-            if (at.head != head) {
-                head = at.head;
+            if (!wait.warp(full(slot_x(it)), turn(it, K::NX))) break;
+            const Chunk now = chunk_at(chunks, it);
+            if (now.head != head) {
+                head = now.head;
                 g = log_decay(p.g, head);
-                r_full = w.o_scale * power(g, w.back ? CHUNK - 1 - i : i + 1);
-                tc::named_sync(1, 128);
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int n = w.back ? 127 - (i + 128 * u) : i + 128 * u - 127;
-                    tab[i + 128 * u] = n >= 0 ? w.p_scale * power(g, n) : 0.f;
+                r_full = w.o_scale * power(g, back ? CHUNK - 1 - i : i + 1);
+                const int n0 = back ? 32 * half - i : i - 32 * half - 31, n1 = back ? n0 + 64 : n0 - 64;
+                rf0 = n0 >= 0 ? power(g, n0) : 0.f;
+                rf1 = n1 >= 0 ? power(g, n1) : 0.f;
+                tc::named_sync(1, 256);
+                if (warp == 4 || warp == 5) {  // 64 entries
+                    const int e = 32 * (warp & 1) + lane, n = back ? 31 - e : e - 31;
+                    tab[e] = n >= 0 ? w.p_scale * power(g, n) : 0.f;
+                } else if (warp == 6) {
+                    cols[lane] = w.p_scale * power(g, back ? lane : 31 - lane);
                 }
-                tc::named_sync(1, 128);
+                tc::named_sync(1, 256);
             }
-            const int rows = line.rows(at);
-            wait(p_full, ph);
+            const int rows = now.tokens();
+            if (!wait.warp(p_full, ph)) break;
             tc::fence_after();
-#pragma unroll
-            for (int s = 0; s < 4; ++s) {
+#pragma unroll 1
+            for (int s = half; s < 4; s += 2) {
+                const float rf = s < 2 ? rf0 : rf1;
                 uint32_t out[16];
-                if (w.back ? s < q4 : s > q4) {
+                if (back ? s < q4 : s > q4) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) out[j] = 0;
                 } else {
                     float v[32];
                     tc::ld32(lanes + 32 * s, v);
-                    const float* d = tab + i - 32 * s + 127;
-                    // (what the mask leaves out is set to zero, not multiplied by it: it may not be finite)
-                    const int from = w.back ? i - 32 * s : 0, to = (w.back ? rows - 1 : i) - 32 * s;
-                    if (s == q4 || (w.back && rows < CHUNK)) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = j >= from && j <= to ? v[j] * d[-j] : 0.f;
-                    } else {
+                    if (s == q4) {
+                        const float* d = tab + lane + 31;
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] *= d[-j];
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 c = *reinterpret_cast<const float4*>(cols + j);
+                            ACC2(v, j, __fmul2_rn(__fmul2_rn(F2(v, j), make_float2(c.x, c.y)), make_float2(rf, rf)));
+                            ACC2(v, j + 2, __fmul2_rn(__fmul2_rn(F2(v, j + 2), make_float2(c.z, c.w)), make_float2(rf, rf)));
+                        }
+                    }
+                    if (rows < CHUNK) {
+                        // (columns of the next sequence are set to zero, not multiplied by it: they may not be finite)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = 32 * s + j < rows ? v[j] : 0.f;
                     }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) out[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
                 }
-                tc::st16u_nowait(lanes + 16 * s, out);
+                tc::st16u_nowait(lanes + 32 * s, out);
             }
             tc::st_wait();
             tc::fence_before();
-            tc::mbar_arrive(p_ready);
+            warp_arrive(p_ready);
 
             float r = r_full;
-            if (w.back && rows < CHUNK) r = i < rows ? w.o_scale * power(g, rows - 1 - i) : 0.f;
-            const int slot = slot_of(3 * it + 2);
-            unsigned char* stage = smem + slot * K::TILE;
-            const int64_t row = (int64_t)line.token(at) + i;
-            wait(o_full, ph);
+            if (back && rows < CHUNK) r = i < rows ? w.o_scale * power(g, rows - 1 - i) : 0.f;
+            unsigned char* stage = smem + slot_x(it) * K::TILE;
+            const int64_t row = (int64_t)now.t0 + i;
+            if (!wait.warp(o_full, ph)) break;
+            if (wide && half == 1 && !wait.warp(half_out, ph)) break;  // (the first half has left X's tile)
             tc::fence_after();
+#pragma unroll 1
+            for (int c = 0; c < HALF; c += 16) {
+                const int n = half * HALF + c;
+                uint32_t a[16], b[16];
+                tc::ld16_nowait(lanes + 128 + n, a);
+                tc::ld16_nowait(lanes + 256 + n, b);
+                tc::ld_wait(a, b);
+                float o[16];
 #pragma unroll
-            for (int s = 0; s < D / 32; ++s) {
-                float a[32], b[32];
-                tc::ld32(lanes + 128 + 32 * s, a);
-                tc::ld32(lanes + 256 + 32 * s, b);
+                for (int j = 0; j < 16; j += 2)
+                    ACC2(o, j, __ffma2_rn(make_float2(r, r), make_float2(__uint_as_float(b[j]), __uint_as_float(b[j + 1])),
+                                          make_float2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]))));
+                if (wide) {
 #pragma unroll
-                for (int j = 0; j < 32; j += 2) {
-                    const float2 u = __ffma2_rn(make_float2(r, r), F2(b, j), F2(a, j));
-                    a[j] = u.x;
-                    a[j + 1] = u.y;
-                }
-                if (w.o32) {
-                    if (i < rows && wait.ok()) {
-                        float4* to = reinterpret_cast<float4*>(w.o32 + (row * p.H + head) * D + 32 * s);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) to[j] = make_float4(a[4 * j], a[4 * j + 1], a[4 * j + 2], a[4 * j + 3]);
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 v = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        if (rows == CHUNK) *reinterpret_cast<float4*>(stage + tc::sw_chunk(i, c / 4 + j, CHUNK)) = v;
+                        else if (i < rows) *reinterpret_cast<float4*>(w.o32 + (row * p.H + head) * D + n + 4 * j) = v;
                     }
                 } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 u = make_uint4(pack_bf16(a[8 * j], a[8 * j + 1]), pack_bf16(a[8 * j + 2], a[8 * j + 3]),
-                                                   pack_bf16(a[8 * j + 4], a[8 * j + 5]), pack_bf16(a[8 * j + 6], a[8 * j + 7]));
-                        if (rows == CHUNK) *reinterpret_cast<uint4*>(stage + tc::sw_chunk(i, 4 * s + j, CHUNK)) = u;
-                        else if (i < rows && wait.ok()) *reinterpret_cast<uint4*>(w.o + (row * p.H + head) * D + 32 * s + 8 * j) = u;
+                    for (int j = 0; j < 2; ++j) {
+                        const uint4 v = make_uint4(pack_bf16(o[8 * j], o[8 * j + 1]), pack_bf16(o[8 * j + 2], o[8 * j + 3]),
+                                                   pack_bf16(o[8 * j + 4], o[8 * j + 5]), pack_bf16(o[8 * j + 6], o[8 * j + 7]));
+                        if (rows == CHUNK) *reinterpret_cast<uint4*>(stage + tc::sw_chunk(i, n / 8 + j, CHUNK)) = v;
+                        else if (i < rows) *reinterpret_cast<uint4*>(w.o + (row * p.H + head) * D + n + 8 * j) = v;
                     }
                 }
             }
             tc::fence_before();
-            tc::mbar_arrive(o_free);
+            warp_arrive(o_free);
             tc::fence_async_smem();
-            tc::mbar_arrive(staged);
+            warp_arrive(staged(it, wide ? half : 0));
+            if (now.last()) break;
         }
     } else {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 248;\n");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(K::REGS_B));
         // ---------------- group B: Y', the state ----------------
-        const int q4 = warp & 3, i = 32 * q4 + lane;  // token of Y; row of the state
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + 384;
-        const bool mine = i < D;  // (warps without rows of the state)
-        float S[D];
-        Place at = plan.at;
-        int it = 0;
+        // two warps for each 32 tokens of Y and 32 rows of the state, each with half of the columns
+        const int q4 = warp & 3, half = (warp - 12) >> 2, i = 32 * q4 + lane, col = half * HALF;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + 384 + col;
+        const bool mine = 32 * q4 < D;  // (warps without rows of the state)
+        float S[HALF];
         float g = 0.f, w_full = 0.f;
         float2 c_full = make_float2(0.f, 0.f);
-        auto incoming = [&]() {
+        auto incoming = [&](int chain, int head, bool inside) {
             const float* from = nullptr;
-            if (at.pos != 0) from = w.joined + (int64_t)(range - 1) * D * D;
-            else if (w.init) from = w.init + ((int64_t)at.seq * p.H + at.head) * D * D;
+            if (inside) from = w.joined + (int64_t)(range - 1) * p.pieces * D * D;
+            else if (w.init) from = w.init + (int64_t)chain * D * D;
             if (from && mine) {
-                if (w.turned) {
+                if (WALKS > 1 && w.turned) {
 #pragma unroll
-                    for (int c = 0; c < D; ++c) S[c] = from[c * D + i];
+                    for (int c = 0; c < HALF; ++c) S[c] = from[(col + c) * D + i];
                 } else {
 #pragma unroll
-                    for (int c = 0; c < D; c += 4) {
-                        const float4 u = *reinterpret_cast<const float4*>(from + i * D + c);
+                    for (int c = 0; c < HALF; c += 4) {
+                        const float4 u = *reinterpret_cast<const float4*>(from + i * D + col + c);
                         S[c] = u.x, S[c + 1] = u.y, S[c + 2] = u.z, S[c + 3] = u.w;
                     }
                 }
             } else {
 #pragma unroll
-                for (int c = 0; c < D; ++c) S[c] = 0.f;
+                for (int c = 0; c < HALF; ++c) S[c] = 0.f;
             }
-            g = log_decay(p.g, at.head);
-            w_full = w.w_scale * power(g, w.back ? i + 1 : CHUNK - 1 - i);
+            g = log_decay(p.g, head);
+            w_full = w.w_scale * power(g, back ? i + 1 : CHUNK - 1 - i);
             c_full = carry(g, CHUNK);
         };
         auto copy_state = [&]() {
             if (mine) {
 #pragma unroll
-                for (int j = 0; j < D / 8; ++j)
-                    *reinterpret_cast<uint4*>(smem + K::oS + tc::sw_chunk(i, j, D)) =
+                for (int j = 0; j < HALF / 8; ++j)
+                    *reinterpret_cast<uint4*>(smem + K::oS + tc::sw_chunk(i, col / 8 + j, D)) =
                         make_uint4(pack_bf16(S[8 * j], S[8 * j + 1]), pack_bf16(S[8 * j + 2], S[8 * j + 3]),
                                    pack_bf16(S[8 * j + 4], S[8 * j + 5]), pack_bf16(S[8 * j + 6], S[8 * j + 7]));
             }
             tc::fence_async_smem();
-            tc::mbar_arrive(s_ready);
+            warp_arrive(s_ready);
         };
-        int f = plan.f0;
-        if (more(plan, at, f, p.snap)) {
-            incoming();
-            copy_state();
-        }
-        while (more(plan, at, f, p.snap)) {
+        if (any) incoming(plan_s.at.seq * p.H + plan_s.at.head, plan_s.at.head, plan_s.at.pos != 0);
+        for (int it = 0; any; ++it) {
             const uint32_t ph = it & 1;
-            const int ly = 3 * it, lz = ly + 1;
-            const int rows = line.rows(at);
+            if (!wait.warp(full(slot_y(it)), turn(it, K::NY))) break;
+            const Chunk now = chunk_at(chunks, it);
+            const int rows = now.tokens();
             float wt = w_full;
             float2 c = c_full;
+            const unsigned char* tile = smem + slot_y(it) * K::TILE;
             if (rows < CHUNK) {
-                wt = i < rows ? w.w_scale * power(g, w.back ? i + 1 : rows - 1 - i) : 0.f;
+                wt = w.w_scale * power(g, back ? i + 1 : rows - 1 - i);
                 c = carry(g, rows);
-                wait(full(slot_of(lz)), parity_of(lz));
-                if (i >= rows && wait.ok()) clear_row<D>(smem + slot_of(lz) * K::TILE, i);
+                if (!wait.warp(full(slot_z(it)), turn(it, K::NZ))) break;
             }
-            wait(full(slot_of(ly)), parity_of(ly));
-            wait(p_full, ph);  // (X Y^T has read Y)
-            if (wait.ok()) split_row<D>(smem + slot_of(ly) * K::TILE, smem + K::oLo, i, wt);
+            // (Y' of the chunk before has been read: this group has waited for its terms)
+            if (i >= rows) {
+                clear_row<HALF / 8>(smem + K::oHi, i, col / 8);
+                clear_row<HALF / 8>(smem + K::oLo, i, col / 8);
+                clear_row<HALF / 8>(smem + slot_z(it) * K::TILE, i, col / 8);
+            } else if (w.twice) {
+                split_row<HALF / 8, true>(tile, smem + K::oHi, smem + K::oLo, i, col / 8, wt);
+            } else {
+                split_row<HALF / 8, false>(tile, smem + K::oHi, nullptr, i, col / 8, wt);
+            }
             tc::fence_async_smem();
-            tc::mbar_arrive(y_ready);
-            wait(d_full, ph);
+            warp_arrive(y_ready);
+            if (lane == 0) tc::mbar_arrive(empty(slot_y(it)));
+            if (it && !wait.warp(s_free, ph ^ 1)) break;  // (X C of the chunk before has read the copy)
+            copy_state();
+            if (!wait.warp(d_full, ph)) break;
             tc::fence_after();
-            if (32 * q4 < D) {
+            if (mine) {
 #pragma unroll
-                for (int s = 0; s < D / 32; ++s) {
-                    float v[32];
-                    tc::ld32(lanes + 32 * s, v);
+                for (int s = 0; s < HALF; s += 16) {
+                    uint32_t v[16];
+                    tc::ld16_nowait(lanes + s, v);
+                    tc::ld_wait(v);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const float2 old = F2(S, 32 * s + j);
-                        const float2 t = __ffma2_rn(make_float2(c.x, c.x), old, F2(v, j));
-                        ACC2(S, 32 * s + j, __ffma2_rn(make_float2(c.y, c.y), old, t));
+                    for (int j = 0; j < 16; j += 2) {
+                        const float2 old = F2(S, s + j);
+                        const float2 t = __ffma2_rn(make_float2(c.x, c.x), old, make_float2(__uint_as_float(v[j]), __uint_as_float(v[j + 1])));
+                        ACC2(S, s + j, __ffma2_rn(make_float2(c.y, c.y), old, t));
                     }
                 }
             }
             tc::fence_before();
-            const bool ends = at.pos + 1 == at.count;
-            if (ends && w.last && mine && wait.ok()) {
-                float* to = w.last + (((int64_t)at.seq * p.H + at.head) * D + i) * D;
+            if (now.ends() && w.last && mine) {
+                float* to = w.last + ((int64_t)now.chain * D + i) * D + col;
 #pragma unroll
-                for (int j = 0; j < D; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                for (int j = 0; j < HALF; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
             }
-            ++f, ++it;
-            line.next(at);
-            if (!more(plan, at, f, p.snap)) break;
-            if (ends) incoming();
-            wait(s_free, ph);  // (X C has read the copy)
-            copy_state();
+            if (now.last()) break;
+            if (now.ends()) {
+                if (!wait.warp(full(slot_y(it + 1)), turn(it + 1, K::NY))) break;
+                const Chunk next = chunk_at(chunks, it + 1);
+                incoming(next.chain, next.head, false);
+            }
         }
     }
     // empty sequences pass their states through
-    if (w.last && plan.total >= 0 && p.cu) {
+    if (w.last && plan_s.total >= 0 && p.cu) {
         const int64_t size = (int64_t)p.H * D * D;
         for (int n = range; n < p.N; n += p.ranges) {
             if (p.cu[n] != p.cu[n + 1]) continue;
-            for (int64_t e = tid; e < size; e += 384) w.last[n * size + e] = w.init ? w.init[n * size + e] : 0.f;
+            for (int64_t e = tid; e < size; e += K::THREADS) w.last[n * size + e] = w.init ? w.init[n * size + e] : 0.f;
         }
     }
     tc::fence_before();
@@ -483,7 +598,7 @@ struct TailWalk {
     CUtensorMap Y, Z;
     int gy, gz, back;
     float w_scale;
-    float* sums;        // [ranges][D][D]
+    float* sums;        // [ranges][pieces][D][D]
     const float* init;  // [N][H][D][D] or nullptr
 };
 template <int WALKS>
@@ -516,21 +631,29 @@ __device__ __forceinline__ Tail tail_of(const Line& line, const Plan& plan) {
     return t;
 }
 
-// For each range the sum of its last chain's terms, as the next range's state takes them.
+// the chunks of the last chain's part, counted from its end, that piece `piece` sums
+__device__ __forceinline__ int piece_begin(int chunks, int piece, int pieces) { return chunks * piece / pieces; }
+
+// For each range the sum of its last chain's terms, as the next range's state takes them.  `pieces` blocks share
+// one: with more chains than ranges the parts' lengths differ, and short blocks even that out.
 template <int D, int WALKS>
-__global__ void __launch_bounds__(256, 1) k_dla_tail(const __grid_constant__ TailWalks<WALKS> walks, const Grid p) {
+__global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __grid_constant__ TailWalks<WALKS> walks, const Grid p) {
     using K = TailCfg<D>;
     extern __shared__ unsigned char smem_raw[];
     __shared__ Plan plan_s;
-    __shared__ int scratch[8];
+    __shared__ int scratch[K::THREADS / 32];
     __shared__ int gone_s;
     __shared__ uint32_t tslot;
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int range = blockIdx.x / WALKS;
-    const TailWalk& w = walks.w[WALKS == 1 ? 0 : blockIdx.x % WALKS];
+    const int piece = blockIdx.x % p.pieces, range = blockIdx.x / p.pieces / WALKS;
+    const TailWalk& w = walks.w[WALKS == 1 ? 0 : blockIdx.x / p.pieces % WALKS];
     const Line line = line_of(p, w.back);
+    make_plan<K::THREADS>(line, range, p.ranges, 0, &plan_s, scratch);
+    const Tail tail = tail_of(line, plan_s);
+    const int begin = piece_begin(tail.chunks, piece, p.pieces), stop = piece_begin(tail.chunks, piece + 1, p.pieces);
+    if (begin == stop) return;
     const uint32_t bar0 = sb + K::oBar;
     auto full = [&](int slot) { return bar0 + 8 * slot; };
     auto empty = [&](int slot) { return bar0 + 8 * (K::RING + slot); };
@@ -538,27 +661,25 @@ __global__ void __launch_bounds__(256, 1) k_dla_tail(const __grid_constant__ Tai
     if (tid == 0) {
         for (int i = 0; i < 2 * K::RING; ++i) tc::mbar_init(bar0 + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(y_ready + 8 * i, 128);
+            tc::mbar_init(y_ready + 8 * i, 8);
             tc::mbar_init(d_full + 8 * i, 1);
         }
         tc::mbar_init(ended, 1);
         gone_s = 0;
     }
     if (warp == 0) tc::alloc(smem_u32(&tslot), 256);
-    make_plan<256>(line, range, p.ranges, 0, &plan_s, scratch);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tslot;
     const Waiter wait{&gone_s, p.status};
-    const Tail tail = tail_of(line, plan_s);
-    const float g = tail.chunks ? log_decay(p.g, tail.first.head) : 0.f;
-    const int end = tail.chunks ? line.before(tail.first, tail.last.pos + 1) : 0;  // tokens of the chain before the next range
-    // chunk `it` of the walk: from the last one backwards, as long as any decay is left
+    const float g = log_decay(p.g, tail.first.head);
+    const int end = line.before(tail.first, tail.last.pos + 1);  // tokens of the chain before the next range
+    // chunk `it` of the walk: from the piece's last one backwards, as long as any decay is left
     auto chunk = [&](int it, Place& at) {
         at = tail.last;
-        at.pos -= it;
-        return it < tail.chunks && power(g, end - line.before(at, at.pos + 1)) != 0.f;
+        at.pos -= begin + it;
+        return begin + it < stop && power(g, end - line.before(at, at.pos + 1)) != 0.f;
     };
     auto slot_of = [&](int l) { return l % K::RING; };
     auto parity_of = [&](int l) { return (uint32_t)((l / K::RING) & 1); };
@@ -570,8 +691,7 @@ __global__ void __launch_bounds__(256, 1) k_dla_tail(const __grid_constant__ Tai
 #pragma unroll
             for (int j = 0; j < 2; ++j, ++l) {
                 const int s = slot_of(l);
-                if (l >= K::RING) wait(empty(s), parity_of(l) ^ 1);
-                if (!wait.ok()) break;
+                if (l >= K::RING && !wait(empty(s), parity_of(l) ^ 1)) break;
                 tc::mbar_expect_tx(full(s), K::TILE);
                 tc::tma_load_4d(sb + s * K::TILE, j ? &w.Z : &w.Y, 0, at.head / (j ? w.gz : w.gy), t0, 0, full(s));
             }
@@ -579,66 +699,77 @@ __global__ void __launch_bounds__(256, 1) k_dla_tail(const __grid_constant__ Tai
         }
         if (!wait.ok())
             for (int i = l > K::RING ? l - K::RING : 0; i < l; ++i) tc::mbar_wait(full(slot_of(i)), parity_of(i));
-    } else if (warp == 1 && lane == 0) {
-        for (int it = 0; chunk(it, at); ++it) {
+    } else if (warp == 1) {
+        const uint32_t on = lane == 0;
+        for (int it = 0; __any_sync(~0u, chunk(it, at)); ++it) {
             const int b = it & 1;
             const uint32_t ph = (it >> 1) & 1;
-            wait(full(slot_of(2 * it + 1)), parity_of(2 * it + 1));
-            wait(y_ready + 8 * b, ph);
-            if (!wait.ok()) break;
+            const uint32_t y = sb + slot_of(2 * it) * K::TILE, z = sb + slot_of(2 * it + 1) * K::TILE;
+            if (!wait.warp(full(slot_of(2 * it + 1)), parity_of(2 * it + 1)) || !wait.warp(y_ready + 8 * b, ph)) break;
             tc::fence_after();
-            issue_terms<D>(tmem + 128 * b, sb + slot_of(2 * it) * K::TILE, sb + K::oLo + b * K::TILE, sb + slot_of(2 * it + 1) * K::TILE);
-            tc::commit(d_full + 8 * b);
-            tc::commit(empty(slot_of(2 * it)));
-            tc::commit(empty(slot_of(2 * it + 1)));
+            issue_terms<D>(on, tmem + 128 * b, y, sb + K::oLo + b * K::TILE, z, true);
+            tc::commit_if(on, d_full + 8 * b);
+            tc::commit_if(on, empty(slot_of(2 * it)));
+            tc::commit_if(on, empty(slot_of(2 * it + 1)));
         }
         if (!wait.ok()) {
-            tc::commit(ended);
+            tc::commit_if(on, ended);
             tc::mbar_wait(ended, 0);
         }
     } else if (warp >= 4) {
-        const int q4 = warp & 3, i = 32 * q4 + lane;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16);
-        float S[D];
+        constexpr int HALF = D / 2;
+        const int q4 = warp & 3, half = (warp - 4) >> 2, i = 32 * q4 + lane, col = half * HALF;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + col;
+        const bool mine = 32 * q4 < D;
+        float S[HALF];
 #pragma unroll
-        for (int c = 0; c < D; ++c) S[c] = 0.f;
+        for (int c = 0; c < HALF; ++c) S[c] = 0.f;
         auto bring = [&](int it) {
             Place c;
             if (!chunk(it, c)) return false;
             const int rows = line.rows(c), l = 2 * it;
             // tokens of the walk from token i on to the next range's first
             const int away = end - line.before(c, c.pos) - (w.back ? rows - 1 - i : i);
-            const float wt = i < rows ? w.w_scale * power(g, w.back ? away : away - 1) : 0.f;
-            wait(full(slot_of(l)), parity_of(l));
-            if (wait.ok()) split_row<D>(smem + slot_of(l) * K::TILE, smem + K::oLo + (it & 1) * K::TILE, i, wt);
-            if (rows < CHUNK) {
-                wait(full(slot_of(l + 1)), parity_of(l + 1));
-                if (i >= rows && wait.ok()) clear_row<D>(smem + slot_of(l + 1) * K::TILE, i);
+            const float wt = w.w_scale * power(g, w.back ? away : away - 1);
+            unsigned char *tile = smem + slot_of(l) * K::TILE, *lo = smem + K::oLo + (it & 1) * K::TILE;
+            if (!wait.warp(full(slot_of(l)), parity_of(l))) return false;
+            if (rows < CHUNK && !wait.warp(full(slot_of(l + 1)), parity_of(l + 1))) return false;
+            if (i < rows) {
+                split_row<HALF / 8, true>(tile, tile, lo, i, col / 8, wt);
+            } else {
+                clear_row<HALF / 8>(tile, i, col / 8);
+                clear_row<HALF / 8>(lo, i, col / 8);
+                clear_row<HALF / 8>(smem + slot_of(l + 1) * K::TILE, i, col / 8);
             }
             tc::fence_async_smem();
-            tc::mbar_arrive(y_ready + 8 * (it & 1));
+            warp_arrive(y_ready + 8 * (it & 1));
             return true;
         };
         bool on = bring(0);
         for (int it = 0; on; ++it) {
             on = bring(it + 1);
-            wait(d_full + 8 * (it & 1), (it >> 1) & 1);
+            if (!wait.warp(d_full + 8 * (it & 1), (it >> 1) & 1)) break;
             tc::fence_after();
-            if (32 * q4 < D) {
+            if (mine) {
 #pragma unroll
-                for (int s = 0; s < D / 32; ++s) {
-                    float v[32];
-                    tc::ld32(lanes + 128 * (it & 1) + 32 * s, v);
+                for (int s = 0; s < HALF; s += 32) {
+                    uint32_t v0[16], v1[16];
+                    tc::ld16_nowait(lanes + 128 * (it & 1) + s, v0);
+                    tc::ld16_nowait(lanes + 128 * (it & 1) + s + 16, v1);
+                    tc::ld_wait(v0, v1);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) ACC2(S, 32 * s + j, __fadd2_rn(F2(S, 32 * s + j), F2(v, j)));
+                    for (int j = 0; j < 32; j += 2) {
+                        const uint32_t* v = (j < 16 ? v0 : v1) + j % 16;
+                        ACC2(S, s + j, __fadd2_rn(F2(S, s + j), make_float2(__uint_as_float(v[0]), __uint_as_float(v[1]))));
+                    }
                 }
             }
             tc::fence_before();
         }
-        if (tail.chunks && i < D && wait.ok()) {
-            float* to = w.sums + ((int64_t)range * D + i) * D;
+        if (mine && wait.ok()) {
+            float* to = w.sums + (((int64_t)range * p.pieces + piece) * D + i) * D + col;
 #pragma unroll
-            for (int j = 0; j < D; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            for (int j = 0; j < HALF; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
         }
     }
     tc::fence_before();
@@ -646,45 +777,64 @@ __global__ void __launch_bounds__(256, 1) k_dla_tail(const __grid_constant__ Tai
     if (warp == 0) tc::dealloc(tmem, 256);
 }
 
-// The states at the beginnings of ranges that begin inside a chain, in the place of the sums of the ranges
-// before them: along each such chain, from its initial state.  One block an eighth of a state.
+// The states at the beginnings of ranges that begin inside a chain, in the place of the first piece of the sum of
+// the range before: along each such chain, from its initial state.  Four blocks a state (most blocks have
+// nothing to do and have to end soon), the sums of two ranges asked for together.
+constexpr int JOIN_SLICES = 4, JOIN_THREADS = 256;
 template <int D, int WALKS>
-__global__ void __launch_bounds__(256) k_dla_join(const __grid_constant__ TailWalks<WALKS> walks, const Grid p) {
-    constexpr int SLICES = D * D / 2048;  // of 256 threads' two float4
+__global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant__ TailWalks<WALKS> walks, const Grid p) {
+    constexpr int AHEAD = 2, QUADS = D * D / JOIN_SLICES / (4 * JOIN_THREADS);  // float4 of a thread
     __shared__ Plan plan_s;
-    __shared__ int scratch[8];
-    const int slice = blockIdx.x % SLICES, which = blockIdx.x / SLICES % WALKS, range = blockIdx.x / SLICES / WALKS + 1;
+    __shared__ int scratch[JOIN_THREADS / 32];
+    const int slice = blockIdx.x % JOIN_SLICES, which = blockIdx.x / JOIN_SLICES % WALKS, range = blockIdx.x / JOIN_SLICES / WALKS + 1;
     const TailWalk& w = walks.w[which];
     const Line line = line_of(p, w.back);
-    make_plan<256>(line, range, p.ranges, 0, &plan_s, scratch);
+    make_plan<JOIN_THREADS>(line, range, p.ranges, 0, &plan_s, scratch);
     const Plan plan = plan_s;
     if (plan.total <= 0 || plan.f0 >= plan.f1 || plan.at.pos == 0) return;
     const Place at = plan.at;
-    const int begin = plan.f0 - at.pos;  // the chain's first chunk
-    if (begin < range_begin(plan.total, range - 1, plan.ranges)) return;  // (the chain's first crossing does them all)
+    const int first = plan.f0 - at.pos;  // the chain's first chunk
+    if (first < range_begin(plan.total, range - 1, plan.ranges)) return;  // (the chain's first crossing does them all)
     const float g = log_decay(p.g, at.head);
-    const int e = slice * 2048 + threadIdx.x * 4;
-    float4 s[2] = {};
+    const int e = slice * (D * D / JOIN_SLICES) + threadIdx.x * 4;
+    float4 s[QUADS] = {};
     if (w.init) {
         const float* from = w.init + ((int64_t)at.seq * p.H + at.head) * D * D + e;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) s[u] = *reinterpret_cast<const float4*>(from + 1024 * u);
+        for (int q = 0; q < QUADS; ++q) s[q] = *reinterpret_cast<const float4*>(from + q * 4 * JOIN_THREADS);
     }
     int done = 0;
-    for (int r = range; r < plan.ranges; ++r) {
-        const int f = range_begin(plan.total, r, plan.ranges);
-        if (f >= begin + at.count) break;
-        const int upto = line.before(at, f - begin);
-        const float2 c = carry(g, upto - done);
-        done = upto;
-        float* sum = w.sums + (int64_t)(r - 1) * D * D + e;
+    for (int r0 = range; r0 < plan.ranges && range_begin(plan.total, r0, plan.ranges) < first + at.count; r0 += AHEAD) {
+        float4 t[AHEAD][QUADS] = {};
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            float4* to = reinterpret_cast<float4*>(sum + 1024 * u);
-            const float4 t = *to;
-            s[u] = make_float4(fmaf(c.y, s[u].x, fmaf(c.x, s[u].x, t.x)), fmaf(c.y, s[u].y, fmaf(c.x, s[u].y, t.y)),
-                               fmaf(c.y, s[u].z, fmaf(c.x, s[u].z, t.z)), fmaf(c.y, s[u].w, fmaf(c.x, s[u].w, t.w)));
-            *to = s[u];
+        for (int u = 0; u < AHEAD; ++u) {
+            const int r = r0 + u, f = range_begin(plan.total, r, plan.ranges);
+            if (r >= plan.ranges || f >= first + at.count) continue;
+            const int chunks = f - max(first, range_begin(plan.total, r - 1, plan.ranges));
+            const float* from = w.sums + (int64_t)(r - 1) * p.pieces * D * D + e;
+            for (int k = 0; k < p.pieces; ++k) {
+                if (piece_begin(chunks, k, p.pieces) == piece_begin(chunks, k + 1, p.pieces)) continue;
+#pragma unroll
+                for (int q = 0; q < QUADS; ++q) {
+                    const float4 v = *reinterpret_cast<const float4*>(from + (int64_t)k * D * D + q * 4 * JOIN_THREADS);
+                    t[u][q] = make_float4(t[u][q].x + v.x, t[u][q].y + v.y, t[u][q].z + v.z, t[u][q].w + v.w);
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < AHEAD; ++u) {
+            const int r = r0 + u, f = range_begin(plan.total, r, plan.ranges);
+            if (r >= plan.ranges || f >= first + at.count) break;
+            const int upto = line.before(at, f - first);
+            const float2 c = carry(g, upto - done);
+            done = upto;
+            float* to = w.sums + (int64_t)(r - 1) * p.pieces * D * D + e;
+#pragma unroll
+            for (int q = 0; q < QUADS; ++q) {
+                s[q] = make_float4(fmaf(c.y, s[q].x, fmaf(c.x, s[q].x, t[u][q].x)), fmaf(c.y, s[q].y, fmaf(c.x, s[q].y, t[u][q].y)),
+                                   fmaf(c.y, s[q].z, fmaf(c.x, s[q].z, t[u][q].z)), fmaf(c.y, s[q].w, fmaf(c.x, s[q].w, t[u][q].w)));
+                *reinterpret_cast<float4*>(to + q * 4 * JOIN_THREADS) = s[q];
+            }
         }
     }
 }
@@ -703,9 +853,10 @@ __global__ void __launch_bounds__(256) k_dla_groups(const float* a, __nv_bfloat1
     reinterpret_cast<uint32_t*>(out)[i] = pack_bf16(s.x, s.y);
 }
 
-// How a call's chunks are shared out: the number of ranges (of each walk), and whether they end with whole chains.
+// How a call's chunks are shared out: the number of ranges (of each walk), whether they end with whole chains, and
+// the blocks that share the sum of a range's last chain.
 struct Shares {
-    int ranges, snap;
+    int ranges, snap, pieces;
 };
 Shares shares_of(const DlaParams& p, int walks) {
     const int64_t chains = (int64_t)p.N * p.H;
@@ -713,31 +864,31 @@ Shares shares_of(const DlaParams& p, int walks) {
     const int64_t most = p.cu_seqlens ? (p.T / CHUNK + p.N) * p.H : longest * chains;
     const int sms = num_sms();
     int64_t fit = sms / walks > 0 ? sms / walks : 1;
-    if (longest <= 4) return {(int)(chains < fit ? chains : fit), 1};
+    if (longest <= 4) return {(int)(chains < fit ? chains : fit), 1, 1};
     const int64_t ranges = (most + 3) / 4;  // of at least four chunks
-    return {(int)(ranges < fit ? ranges : fit), 0};
+    return {(int)(ranges < fit ? ranges : fit), 0, chains > fit ? 4 : 1};
 }
 
 template <int D, int WALKS, int TAILS>
 cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, const TailWalks<TAILS>& tails, cudaStream_t s) {
-    const Grid grid{p.N, p.H, D, sh.ranges, sh.snap, p.T, p.seq_len, p.cu_seqlens, p.g, p.status};
+    const Grid grid{p.N, p.H, D, sh.ranges, sh.snap, sh.pieces, p.T, p.seq_len, p.cu_seqlens, p.g, p.status};
     cudaError_t e = cudaMemsetAsync(p.status, 0, 256, s);
     if (e != cudaSuccess) return e;
     e = cudaFuncSetAttribute(k_dla<D, WALKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
     if (e != cudaSuccess) return e;
-    // (the groups' shares of the registers, 88 + 168 + 248 a thread of 128, have to be there at the launch)
+    // (the groups' shares of the registers have to be there at the launch)
     static const int regs = [] {
         cudaFuncAttributes at;
         return cudaFuncGetAttributes(&at, k_dla<D, WALKS>) == cudaSuccess ? at.numRegs : 0;
     }();
-    if (regs != 168) return cudaErrorInvalidConfiguration;
+    if (regs != Cfg<D>::REGS) return cudaErrorInvalidConfiguration;
     if (!sh.snap && sh.ranges > 1) {
         e = cudaFuncSetAttribute(k_dla_tail<D, TAILS>, cudaFuncAttributeMaxDynamicSharedMemorySize, TailCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
-        k_dla_tail<D, TAILS><<<(sh.ranges - 1) * TAILS, 256, TailCfg<D>::SMEM, s>>>(tails, grid);
-        k_dla_join<D, TAILS><<<(sh.ranges - 1) * TAILS * (D * D / 2048), 256, 0, s>>>(tails, grid);
+        k_dla_tail<D, TAILS><<<(sh.ranges - 1) * TAILS * sh.pieces, TailCfg<D>::THREADS, TailCfg<D>::SMEM, s>>>(tails, grid);
+        k_dla_join<D, TAILS><<<(sh.ranges - 1) * TAILS * JOIN_SLICES, JOIN_THREADS, 0, s>>>(tails, grid);
     }
-    k_dla<D, WALKS><<<sh.ranges * WALKS, 384, Cfg<D>::SMEM, s>>>(walks, grid);
+    k_dla<D, WALKS><<<sh.ranges * WALKS, Cfg<D>::THREADS, Cfg<D>::SMEM, s>>>(walks, grid);
     return cudaGetLastError();
 }
 
@@ -749,11 +900,12 @@ struct Tensor {
 bool encode(CUtensorMap* m, const Tensor& t, const DlaParams& p) {
     return encode_heads_map(m, t.at, p.T, t.heads, p.D, t.ld, CHUNK);
 }
-bool make_walk(Walk* w, const DlaParams& p, const Tensor& x, const Tensor& y, const Tensor& z, void* out, int out_heads) {
+bool make_walk(Walk* w, const DlaParams& p, const Tensor& x, const Tensor& y, const Tensor& z, void* out, int out_heads, float* out32) {
     w->gx = p.H / x.heads, w->gy = p.H / y.heads, w->gz = p.H / z.heads;
     w->o = static_cast<__nv_bfloat16*>(out);
-    return encode(&w->X, x, p) && encode(&w->Y, y, p) && encode(&w->Z, z, p) &&
-           encode(&w->out, Tensor{out, out_heads, (int64_t)out_heads * p.D}, p);
+    w->o32 = out32;
+    if (!encode(&w->X, x, p) || !encode(&w->Y, y, p) || !encode(&w->Z, z, p)) return false;
+    return out32 ? encode_heads_f32_map(&w->out, out32, p.T, p.H, p.D, CHUNK) : encode(&w->out, Tensor{out, out_heads, (int64_t)out_heads * p.D}, p);
 }
 
 template <int D>
@@ -765,9 +917,9 @@ cudaError_t forward(const DlaParams& p, cudaStream_t s) {
     TailWalks<1> t;
     memset(&t, 0, sizeof(t));
     Walk& o = w.w[0];
-    if (!make_walk(&o, p, q, k, v, p.o, p.H)) return cudaErrorInvalidValue;
+    if (!make_walk(&o, p, q, k, v, p.o, p.H, nullptr)) return cudaErrorInvalidValue;
     o.p_scale = o.o_scale = p.scale, o.w_scale = 1.f;
-    o.init = p.h0, o.joined = p.states, o.last = p.ht;
+    o.init = p.h0, o.joined = p.states, o.last = p.ht, o.twice = 1;
     t.w[0] = TailWalk{o.Y, o.Z, o.gy, o.gz, 0, 1.f, p.states, p.h0};
     return go<D, 1, 1>(p, sh, w, t, s);
 }
@@ -781,15 +933,16 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
     TailWalks<2> t;
     memset(&t, 0, sizeof(t));
     Walk &dq = w.w[0], &dk = w.w[1], &dv = w.w[2];
-    if (!make_walk(&dq, p, dO, v, k, p.dq, p.Hk) || !make_walk(&dk, p, v, dO, q, p.dk, p.Hk) || !make_walk(&dv, p, k, q, dO, p.dv, p.H))
+    if (!make_walk(&dq, p, dO, v, k, p.dq, p.Hk, p.dq_heads) || !make_walk(&dk, p, v, dO, q, p.dk, p.Hk, p.dk_heads) ||
+        !make_walk(&dv, p, k, q, dO, p.dv, p.H, nullptr))
         return cudaErrorInvalidValue;
-    float* back = p.states + (size_t)sh.ranges * D * D;
+    float* back = p.states + (size_t)sh.ranges * sh.pieces * D * D;
     dq.turned = 1, dq.p_scale = dq.o_scale = p.scale, dq.w_scale = 1.f;
-    dq.init = p.h0, dq.joined = p.states, dq.o32 = p.dq_heads;
+    dq.init = p.h0, dq.joined = p.states;
     dk.turned = 1, dk.back = 1, dk.p_scale = dk.w_scale = p.scale, dk.o_scale = 1.f;
-    dk.init = p.dht, dk.joined = back, dk.o32 = p.dk_heads;
+    dk.init = p.dht, dk.joined = back;
     dv.back = 1, dv.p_scale = dv.w_scale = p.scale, dv.o_scale = 1.f;
-    dv.init = p.dht, dv.joined = back, dv.last = p.dh0;
+    dv.init = p.dht, dv.joined = back, dv.last = p.dh0, dv.twice = 1;
     t.w[0] = TailWalk{dq.Z, dq.Y, dq.gz, dq.gy, 0, 1.f, p.states, p.h0};
     t.w[1] = TailWalk{dv.Y, dv.Z, dv.gy, dv.gz, 1, p.scale, back, p.dht};
     cudaError_t e = go<D, 3, 2>(p, sh, w, t, s);
@@ -805,7 +958,7 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
 
 size_t dla_states_bytes(const DlaParams& p, bool backward) {
     const Shares sh = shares_of(p, backward ? 3 : 1);
-    return sh.snap || sh.ranges < 2 ? 0 : (backward ? 2 : 1) * sizeof(float) * (size_t)sh.ranges * p.D * p.D;
+    return sh.snap || sh.ranges < 2 ? 0 : (backward ? 2 : 1) * sizeof(float) * (size_t)sh.ranges * sh.pieces * p.D * p.D;
 }
 int dla_kernels(const DlaParams& p, bool backward) {
     const Shares sh = shares_of(p, backward ? 3 : 1);

@@ -98,8 +98,23 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     // Waits are bounded: one that runs out turns every later wait and issue of the block into nothing, and its outputs into NaN.
     volatile int* gone = &gone_s;
     auto ok = [&]() { return *gone == 0; };
-    auto wait = [&](uint32_t bar, uint32_t parity) {
-        if (ok() && !tc::mbar_wait(bar, parity, 1 << 22)) *gone = 1;
+    auto wait = [&](uint32_t bar, uint32_t parity) {  // by one thread
+        if (tc::mbar_try(bar, parity)) return true;
+        for (int i = 0; i < 1 << 22; ++i) {
+            if (!ok()) return false;
+            if (tc::mbar_try(bar, parity)) return true;
+        }
+        *gone = 1;
+        return false;
+    };
+    auto wait_warp = [&](uint32_t bar, uint32_t parity) {  // by a whole warp, which goes on converged
+        if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+        for (int i = 0; i < 1 << 22; ++i) {
+            if (__any_sync(~0u, !ok())) return false;
+            if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+        }
+        *gone = 1;
+        return false;
     };
     const int first = blockIdx.x / split, step = gridDim.x / split;
 
@@ -113,8 +128,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
                 for (int kb = kb0; kb < kb1; ++kb, ++l) {
                     const int s = l % L::STAGES;
-                    if (l >= L::STAGES) wait(empty(s), (l / L::STAGES & 1) ^ 1);
-                    if (!ok()) break;
+                    if (l >= L::STAGES && !wait(empty(s), (l / L::STAGES & 1) ^ 1)) break;
                     tc::mbar_expect_tx(full(s), L::STAGE);
                     tc::tma_load_2d(sb + s * L::STAGE, &maps.a, kb * KB, a0, full(s));
                     tc::tma_load_2d(sb + s * L::STAGE + L::A, &maps.b, kb * KB, b0, full(s));
@@ -124,28 +138,27 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            // ---------------- issuer ----------------
-            constexpr uint32_t id = tc::idesc_e4m3(128, BN);
-            int l = 0;
-            for (int t = first; t < tiles && ok(); t += step) {
-                for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                    const int s = l % L::STAGES, b = l & 1;
-                    wait(full(s), l / L::STAGES & 1);
-                    if (l >= 2) wait(t_empty + 8 * b, (l >> 1 & 1) ^ 1);
-                    if (!ok()) break;
-                    tc::fence_after();
-                    const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
+        // ---------------- issuer (the whole warp, converged; lane 0 issues) ----------------
+        constexpr uint32_t id = tc::idesc_e4m3(128, BN);
+        const uint32_t on = lane == 0;
+        int l = 0;
+        bool fine = true;
+        for (int t = first; t < tiles && fine; t += step) {
+            for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                const int s = l % L::STAGES, b = l & 1;
+                fine = wait_warp(full(s), l / L::STAGES & 1) && (l < 2 || wait_warp(t_empty + 8 * b, (l >> 1 & 1) ^ 1));
+                if (!fine) break;
+                tc::fence_after();
+                const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
 #pragma unroll
-                    for (int k = 0; k < KB / 32; ++k) tc::mma_e4m3(tmem + b * BN, da + 2 * k, db + 2 * k, id, k > 0);
-                    tc::commit(empty(s));
-                    tc::commit(t_full + 8 * b);
-                }
+                for (int k = 0; k < KB / 32; ++k) tc::mma_e4m3_if(on, tmem + b * BN, da + 2 * k, db + 2 * k, id, k > 0);
+                tc::commit_if(on, empty(s));
+                tc::commit_if(on, t_full + 8 * b);
             }
-            if (!ok()) {
-                tc::commit(ended);
-                tc::mbar_wait(ended, 0);
-            }
+        }
+        if (!fine) {
+            tc::commit_if(on, ended);
+            tc::mbar_wait(ended, 0);
         }
     } else if (warp == 2 && !X_ROWS) {
         // ---------------- scales of the columns, eight blocks at a time ----------------
@@ -154,7 +167,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             const int nb = t / tiles_b;
             const int64_t m0 = (int64_t)(t % tiles_b) * BN;
             for (int kb = kb0; kb < kb1; kb += 8, ++u) {
-                if (u >= 2) wait(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
+                if (u >= 2) wait_warp(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
                 float* sc = reinterpret_cast<float*>(smem + L::oScale) + (u & 1) * 8 * BN;
                 for (int j = lane; j < BN; j += 32) {
                     float v[8];
@@ -189,8 +202,8 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 const float s = next;
                 if (X_ROWS) next = scale_at(kb + 1);
                 const float* sc = reinterpret_cast<const float*>(smem + L::oScale) + (u & 1) * 8 * BN + ((kb - kb0) & 7) * BN;
-                if (!X_ROWS && ((kb - kb0) & 7) == 0) wait(sc_full + 8 * (u & 1), u >> 1 & 1);
-                wait(t_full + 8 * b, l >> 1 & 1);
+                if (!X_ROWS && ((kb - kb0) & 7) == 0) wait_warp(sc_full + 8 * (u & 1), u >> 1 & 1);
+                wait_warp(t_full + 8 * b, l >> 1 & 1);
                 tc::fence_after();
                 constexpr int PART = COLS < 32 ? COLS : 32;
 #pragma unroll

@@ -71,24 +71,57 @@ __device__ __forceinline__ void mma_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_
         "r"(tmem_a), "l"(b), "r"(id), "r"(accumulate));
 }
 
-// kind::f8f6f4, e4m3 A and B, fp32 D: instruction descriptor (K = 32 elements a step, both operands K-major) and issue
+// kind::f8f6f4, e4m3 A and B, fp32 D: instruction descriptor (K = 32 elements a step, both operands K-major)
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N) {
     return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
-__device__ __forceinline__ void mma_e4m3(uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
-    asm volatile(
-        "{\n.reg .pred p;\nsetp.ne.u32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
-        "l"(a), "l"(b), "r"(id), "r"(accumulate));
 }
 
 __device__ __forceinline__ void commit(uint32_t mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar));
 }
 
+// The same instructions as a converged warp issues them, through the one lane whose `on` is not zero.  Where one lane
+// alone runs the code around them, every operand is moved to a uniform register at each instruction: a product of
+// 16 of the inner dimension then takes 100 cycles to issue, and 64 (128 x 128) to compute.
+__device__ __forceinline__ void mma_if(uint32_t on, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(on));
+}
+__device__ __forceinline__ void mma_ts_if(uint32_t on, uint32_t tmem_d, uint32_t tmem_a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(b), "r"(id), "r"(accumulate), "r"(on));
+}
+__device__ __forceinline__ void mma_e4m3_if(uint32_t on, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
+    asm volatile(
+        "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(tmem_d),
+        "l"(a), "l"(b), "r"(id), "r"(accumulate), "r"(on));
+}
+__device__ __forceinline__ void commit_if(uint32_t on, uint32_t mbar) {
+    asm volatile(
+        "{\n.reg .pred q;\nsetp.ne.u32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(mbar),
+        "r"(on));
+}
+
 __device__ __forceinline__ void mbar_init(uint32_t mbar, int count) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count));
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::);
+}
+
+// whether the phase `parity` of an mbarrier has completed (waits for a short while, which the hardware chooses)
+__device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n.reg .pred p;\nmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(mbar), "r"(parity)
+        : "memory");
+    return done != 0;
 }
 
 // Bounded wait for the phase `parity` of an mbarrier.  Returns false (and the

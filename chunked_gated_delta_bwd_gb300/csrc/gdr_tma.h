@@ -84,6 +84,19 @@ inline bool encode_heads_map(CUtensorMap* m, const void* base, uint64_t T, uint6
     return encode_bf16_map(m, base, 4, dims, strides, box);
 }
 
+// contiguous [T][heads][D] float32 viewed as [D / 32 column blocks][T][heads][32]: one copy moves box_tokens tokens of one
+// head, D / 2 columns, as SW128 column blocks
+inline bool encode_heads_f32_map(CUtensorMap* m, const void* base, uint64_t T, uint64_t heads, uint64_t D, uint32_t box_tokens) {
+    memset(m, 0, sizeof(*m));
+    PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[4] = {32, heads, T, D / 32}, strides[3] = {D * 4, heads * D * 4, 128};
+    const cuuint32_t box[4] = {32, 1, box_tokens, (cuuint32_t)(D / 64)}, elem[4] = {1, 1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, const_cast<void*>(base), dims, strides, box, elem,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [rows][cols] bytes, boxes of box_rows x 128 bytes (one SW128 column block)
 inline bool encode_bytes_map(CUtensorMap* m, const void* base, uint64_t rows, uint64_t cols, uint32_t box_rows) {
     memset(m, 0, sizeof(*m));
