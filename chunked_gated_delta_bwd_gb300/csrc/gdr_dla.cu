@@ -51,7 +51,7 @@ struct Cfg {
     static constexpr int oHi = SLOTS * TILE, oLo = oHi + TILE, oS = oLo + TILE, oTab = oS + D * D * 2;
     // (the product Y'^T Z has 128 rows; with 64 channels the upper ones read what lies behind the tile)
     static constexpr int oEnd = (oTab + 512 > oLo + 2 * CHUNK * 128 ? oTab + 512 : oLo + 2 * CHUNK * 128);
-    static constexpr int oBar = oEnd, BARS = 2 * SLOTS + 10 + 2 * NX;
+    static constexpr int oBar = oEnd, BARS = 2 * SLOTS + 11 + 2 * NX;
     static constexpr int SMEM = oBar + 8 * BARS + 1024;
     static constexpr int THREADS = 640;  // a warpgroup of single threads' roles, two each for groups A and B
     static constexpr int REGS = 96, REGS_1 = 80, REGS_B = 104;  // at the launch (and group A), of the single threads, of group B
@@ -101,6 +101,7 @@ struct Waiter {
     // by one thread
     __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
         if (tc::mbar_try(bar, parity)) return true;
+#pragma unroll 1
         for (int i = 0; i < 1 << 22; ++i) {
             if (!ok()) return false;
             if (tc::mbar_try(bar, parity)) return true;
@@ -111,6 +112,7 @@ struct Waiter {
     // by a whole warp, which goes on converged
     __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
         if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+#pragma unroll 1
         for (int i = 0; i < 1 << 22; ++i) {
             if (__any_sync(~0u, !ok())) return false;
             if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
@@ -184,10 +186,10 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 template <int D>
 __device__ __forceinline__ void issue_terms(uint32_t on, uint32_t to, uint32_t hi, uint32_t lo, uint32_t z, bool twice) {
     constexpr uint32_t id = tc::idesc(128, D, 1, 1);
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(hi, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, k > 0);
     if (!twice) return;
-#pragma unroll
+#pragma unroll 1
     for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(lo, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, 1);
 }
 
@@ -220,15 +222,18 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     const uint32_t more_bars = bar0 + 16 * K::SLOTS;
     const uint32_t p_full = more_bars, p_ready = more_bars + 8, o_full = more_bars + 16, o_free = more_bars + 24,
                    s_ready = more_bars + 32, s_free = more_bars + 40, y_ready = more_bars + 48, d_full = more_bars + 56,
-                   half_out = more_bars + 64, ended = more_bars + 72;
+                   half_out = more_bars + 64, ended = more_bars + 72, ended_3 = more_bars + 80 + 16 * K::NX;
     // (group A may be chunks ahead of the stores: a barrier for each of X's slots, and each half of a wide output)
     auto staged = [&](int it, int half) { return more_bars + 80 + 16 * slot_x(it) + 8 * half; };
     if (tid == 0) {
-        // (Y's slots are given back by P's product and by group B's eight warps)
-        for (int i = 0; i < 2 * K::SLOTS; ++i) tc::mbar_init(bar0 + 8 * i, i >= K::SLOTS + K::NX && i < K::SLOTS + K::NX + K::NY ? 9 : 1);
+        // (Y's slots are given back by P's product and by group B's eight warps, Z's by the products of both issuers)
+        for (int i = 0; i < K::SLOTS; ++i) {
+            tc::mbar_init(full(i), 1);
+            tc::mbar_init(empty(i), i < K::NX ? 1 : i < K::NX + K::NY ? 9 : 2);
+        }
         tc::mbar_init(p_full, 1);
         tc::mbar_init(p_ready, 8);
-        tc::mbar_init(o_full, 1);
+        tc::mbar_init(o_full, 2);  // P Z and X C
         tc::mbar_init(o_free, 8);
         tc::mbar_init(s_ready, 8);
         tc::mbar_init(s_free, 1);
@@ -237,6 +242,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_init(staged(0, 0) + 8 * i, wide ? 4 : 8);
         tc::mbar_init(half_out, 1);
         tc::mbar_init(ended, 1);
+        tc::mbar_init(ended_3, 1);
         gone_s = 0;
     }
     if (warp == 0) tc::alloc(smem_u32(&tslot), 512);
@@ -261,6 +267,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             const Plan plan = plan_s;
             Place at = plan.at;
             bool go_on = true;
+#pragma unroll 1
             for (int f = plan.f0; go_on; ++it) {
                 const int t0 = line.token(at), h0 = at.head;
                 int4 c = make_int4(t0, line.rows(at), h0, at.seq * p.H + h0);
@@ -270,7 +277,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 if (!go_on) c.y |= Chunk::LAST;
                 chunks[it & 7] = c;
                 on[0] = on[1] = on[2] = false;
-#pragma unroll
+#pragma unroll 1
                 for (int j = 0; j < 3; ++j) {
                     const int n = j == 0 ? K::NY : j == 1 ? K::NX : K::NZ, s = j == 0 ? slot_y(it) : j == 1 ? slot_x(it) : slot_z(it);
                     if (it >= n && !wait(empty(s), turn(it, n) ^ 1)) break;
@@ -284,6 +291,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             }
             if (!wait.ok()) {  // (the block gave up: its copies have to land before it ends)
                 auto landed = [&](int last, int n, int which) {
+#pragma unroll 1
                     for (int i = last - n + 1 > 0 ? last - n + 1 : 0; i <= last; ++i)
                         tc::mbar_wait(full(which == 0 ? slot_y(i) : which == 1 ? slot_x(i) : slot_z(i)), turn(i, n));
                 };
@@ -291,46 +299,55 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 landed(on[1] ? it : it - 1, K::NX, 1);
                 landed(on[2] ? it : it - 1, K::NZ, 2);
             }
-        } else if (warp == 1 && any) {
-            // ---------------- issuer (the whole warp, converged; lane 0 issues) ----------------
+        } else if ((warp == 1 || warp == 3) && any) {
+            // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
+            // A warp that waits, commits or fences issues no product (60 to 120 cycles each, against 64 for a product
+            // of 16 of the inner dimension, and products do not queue up): two share them, P's chain and the state's.
             const uint32_t on = lane == 0;
             const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 256, tD = tmem + 384;
             constexpr uint32_t idP = tc::idesc(128, 128, 0, 0), idO = tc::idesc(128, D, 0, 1);
+#pragma unroll 1
             for (int it = 0;; ++it) {
                 const int sx = slot_x(it), sy = slot_y(it), sz = slot_z(it);
                 const uint32_t X = sb + sx * K::TILE, Y = sb + sy * K::TILE, Z = sb + sz * K::TILE;
                 const uint32_t ph = it & 1;
-                if (!wait.warp(full(sy), turn(it, K::NY)) || !wait.warp(full(sx), turn(it, K::NX))) break;
-                if (it && !wait.warp(o_full, ph ^ 1)) break;  // (P Z of the chunk before has read P)
-                tc::fence_after();
-#pragma unroll
-                for (int k = 0; k < D; k += 16) tc::mma_if(on, tP, tc::kdesc(X, CHUNK, 0, k), tc::kdesc(Y, CHUNK, 0, k), idP, k > 0);
-                tc::commit_if(on, p_full);
-                tc::commit_if(on, empty(sy));
-                if (!wait.warp(full(sz), turn(it, K::NZ)) || !wait.warp(y_ready, ph)) break;
-                tc::fence_after();
-                issue_terms<D>(on, tD, sb + K::oHi, sb + K::oLo, Z, w.twice);
-                tc::commit_if(on, d_full);
-                if (!wait.warp(s_ready, ph) || (it && !wait.warp(o_free, ph ^ 1))) break;
-                tc::fence_after();
-#pragma unroll
-                for (int k = 0; k < D; k += 16) tc::mma_if(on, tO2, tc::kdesc(X, CHUNK, 0, k), tc::mdesc(sb + K::oS, D, 0, k), idO, k > 0);
-                tc::commit_if(on, s_free);
-                if (!wait.warp(p_ready, ph)) break;
-                tc::fence_after();
-                // (bf16 P: the 32 columns of slice s lie in the first 16 of the 32 that held them in fp32)
-#pragma unroll
-                for (int k = 0; k < CHUNK; k += 16) tc::mma_ts_if(on, tO1, tP + (k & ~31) + (k & 31) / 2, tc::mdesc(Z, CHUNK, 0, k), idO, k > 0);
+                if (warp == 1) {
+                    if (!wait.warp(full(sy), turn(it, K::NY)) || !wait.warp(full(sx), turn(it, K::NX))) break;
+                    if (it && !wait.warp(o_full, ph ^ 1)) break;  // (P Z of the chunk before has read P)
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 16) tc::mma_if(on, tP, tc::kdesc(X, CHUNK, 0, k), tc::kdesc(Y, CHUNK, 0, k), idP, k > 0);
+                    tc::commit_if(on, p_full);
+                    tc::commit_if(on, empty(sy));
+                    if (!wait.warp(full(sz), turn(it, K::NZ))) break;
+                    if ((it && !wait.warp(o_free, ph ^ 1)) || !wait.warp(p_ready, ph)) break;
+                    tc::fence_after();
+                    // (bf16 P: the 32 columns of slice s lie in the first 16 of the 32 that held them in fp32)
+#pragma unroll 1
+                    for (int k = 0; k < CHUNK; k += 16) tc::mma_ts_if(on, tO1, tP + (k & ~31) + (k & 31) / 2, tc::mdesc(Z, CHUNK, 0, k), idO, k > 0);
+                } else {
+                    if (!wait.warp(full(sz), turn(it, K::NZ)) || !wait.warp(y_ready, ph)) break;
+                    tc::fence_after();
+                    issue_terms<D>(on, tD, sb + K::oHi, sb + K::oLo, Z, w.twice);
+                    tc::commit_if(on, d_full);
+                    tc::commit_if(on, empty(sz));
+                    if (!wait.warp(full(sx), turn(it, K::NX)) || !wait.warp(s_ready, ph) || (it && !wait.warp(o_free, ph ^ 1))) break;
+                    tc::fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 16) tc::mma_if(on, tO2, tc::kdesc(X, CHUNK, 0, k), tc::mdesc(sb + K::oS, D, 0, k), idO, k > 0);
+                    tc::commit_if(on, s_free);
+                }
                 tc::commit_if(on, o_full);
-                tc::commit_if(on, empty(sz));
+                if (warp == 1) tc::commit_if(on, empty(sz));
                 if (__any_sync(~0u, chunk_at(chunks, it).last())) break;
             }
             if (!wait.ok()) {  // (the products in flight have to end before the tensor memory is given back)
-                tc::commit_if(on, ended);
-                tc::mbar_wait(ended, 0);
+                tc::commit_if(on, warp == 1 ? ended : ended_3);
+                tc::mbar_wait(warp == 1 ? ended : ended_3, 0);
             }
         } else if (warp == 2 && lane == 0 && any) {
             // ---------------- stores ----------------
+#pragma unroll 1
             for (int it = 0;; ++it) {
                 const uint32_t X = sb + slot_x(it) * K::TILE;
                 if (wide) {
@@ -377,6 +394,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         float* cols = tab + 64;
         int head = -1;
         float r_full = 0.f, g = 0.f, rf0 = 0.f, rf1 = 0.f;
+#pragma unroll 1
         for (int it = 0; any; ++it) {
             const uint32_t ph = it & 1;
             if (!wait.warp(full(slot_x(it)), turn(it, K::NX))) break;
@@ -431,6 +449,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                     for (int j = 0; j < 16; ++j) out[j] = pack_bf16(v[2 * j], v[2 * j + 1]);
                 }
                 tc::st16u_nowait(lanes + 32 * s, out);
+            }
+            if (rows < CHUNK) {  // (the rows of Z that belong to the next sequence: each group clears them for its product)
+                if (!wait.warp(full(slot_z(it)), turn(it, K::NZ))) break;
+                if (i >= rows) clear_row<HALF / 8>(smem + slot_z(it) * K::TILE, i, half * (HALF / 8));
+                tc::fence_async_smem();
             }
             tc::st_wait();
             tc::fence_before();
@@ -523,6 +546,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             warp_arrive(s_ready);
         };
         if (any) incoming(plan_s.at.seq * p.H + plan_s.at.head, plan_s.at.head, plan_s.at.pos != 0);
+#pragma unroll 1
         for (int it = 0; any; ++it) {
             const uint32_t ph = it & 1;
             if (!wait.warp(full(slot_y(it)), turn(it, K::NY))) break;
@@ -584,8 +608,10 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     // empty sequences pass their states through
     if (w.last && plan_s.total >= 0 && p.cu) {
         const int64_t size = (int64_t)p.H * D * D;
+#pragma unroll 1
         for (int n = range; n < p.N; n += p.ranges) {
             if (p.cu[n] != p.cu[n + 1]) continue;
+#pragma unroll 1
             for (int64_t e = tid; e < size; e += K::THREADS) w.last[n * size + e] = w.init ? w.init[n * size + e] : 0.f;
         }
     }
@@ -619,6 +645,7 @@ __device__ __forceinline__ Tail tail_of(const Line& line, const Plan& plan) {
     // chain by chain to the one that holds the range's last chunk
     Place at = plan.at;
     int f = plan.f0;
+#pragma unroll 1
     while (f + (at.count - at.pos) < plan.f1) {
         f += at.count - at.pos;
         at.pos = at.count - 1;
@@ -686,6 +713,7 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
     Place at;
     if (warp == 0 && lane == 0) {
         int l = 0;
+#pragma unroll 1
         for (int it = 0; chunk(it, at); ++it) {
             const int t0 = line.token(at);
 #pragma unroll
@@ -698,9 +726,11 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
             if (!wait.ok()) break;
         }
         if (!wait.ok())
+#pragma unroll 1
             for (int i = l > K::RING ? l - K::RING : 0; i < l; ++i) tc::mbar_wait(full(slot_of(i)), parity_of(i));
     } else if (warp == 1) {
         const uint32_t on = lane == 0;
+#pragma unroll 1
         for (int it = 0; __any_sync(~0u, chunk(it, at)); ++it) {
             const int b = it & 1;
             const uint32_t ph = (it >> 1) & 1;
@@ -746,6 +776,7 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
             return true;
         };
         bool on = bring(0);
+#pragma unroll 1
         for (int it = 0; on; ++it) {
             on = bring(it + 1);
             if (!wait.warp(d_full + 8 * (it & 1), (it >> 1) & 1)) break;
@@ -804,6 +835,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
         for (int q = 0; q < QUADS; ++q) s[q] = *reinterpret_cast<const float4*>(from + q * 4 * JOIN_THREADS);
     }
     int done = 0;
+#pragma unroll 1
     for (int r0 = range; r0 < plan.ranges && range_begin(plan.total, r0, plan.ranges) < first + at.count; r0 += AHEAD) {
         float4 t[AHEAD][QUADS] = {};
 #pragma unroll
@@ -812,6 +844,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
             if (r >= plan.ranges || f >= first + at.count) continue;
             const int chunks = f - max(first, range_begin(plan.total, r - 1, plan.ranges));
             const float* from = w.sums + (int64_t)(r - 1) * p.pieces * D * D + e;
+#pragma unroll 1
             for (int k = 0; k < p.pieces; ++k) {
                 if (piece_begin(chunks, k, p.pieces) == piece_begin(chunks, k + 1, p.pieces)) continue;
 #pragma unroll

@@ -39,6 +39,7 @@ struct Line {
         p.pos = 0;
         if (++p.head < H) return;
         p.head = 0;
+#pragma unroll 1
         while (++p.seq < N) {
             sequence(p);
             if (p.count) return;
@@ -99,6 +100,7 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
         // every block adds up the sequences' chunks: N reads, all of them hits in the second-level cache
         int sum = 0;
         bool bad = line.cu[0] != 0 || line.cu[line.N] != line.T;
+#pragma unroll 1
         for (int i = tid; i < line.N; i += THREADS) {
             const int64_t len = line.cu[i + 1] - line.cu[i];
             bad |= len < 0 || len > line.T;
@@ -118,6 +120,7 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
         const int f0 = out->f0;
         // the sequence that holds chunk f0 (none where the range is empty)
         int base = 0;
+#pragma unroll 1
         for (int i0 = 0; f0 < out->f1 && i0 < line.N; i0 += THREADS) {
             const int i = i0 + tid;
             const int mine = i < line.N ? (int)((line.cu[i + 1] - line.cu[i] + CHUNK - 1) / CHUNK) : 0;

@@ -33,7 +33,7 @@ struct Lin {
     static constexpr int oStore = STAGES * STAGE;  // (rows of x: a 128 x 64 bf16 tile for each group)
     static constexpr int oScale = oStore + (X_ROWS ? GROUPS * 16384 : 0);
     static constexpr int oBar = oScale + (X_ROWS ? 0 : 2 * 8 * BN * 4);
-    static constexpr int BARS = 2 * STAGES + 9;
+    static constexpr int BARS = 2 * STAGES + 10;
     static constexpr int SMEM = oBar + 8 * BARS + 8 + 1024;
     static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
 };
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             tc::mbar_init(sc_full + 8 * i, 32);
             tc::mbar_init(sc_empty + 8 * i, 4 * L::GROUPS);
         }
-        tc::mbar_init(ended, 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(ended + 8 * i, 1);
         gone_s = 0;
     }
     if (warp == 0) tc::alloc(smem_u32(&tslot), L::TMEM);
@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     auto ok = [&]() { return *gone == 0; };
     auto wait = [&](uint32_t bar, uint32_t parity) {  // by one thread
         if (tc::mbar_try(bar, parity)) return true;
+#pragma unroll 1
         for (int i = 0; i < 1 << 22; ++i) {
             if (!ok()) return false;
             if (tc::mbar_try(bar, parity)) return true;
@@ -109,6 +110,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     };
     auto wait_warp = [&](uint32_t bar, uint32_t parity) {  // by a whole warp, which goes on converged
         if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
+#pragma unroll 1
         for (int i = 0; i < 1 << 22; ++i) {
             if (__any_sync(~0u, !ok())) return false;
             if (__all_sync(~0u, tc::mbar_try(bar, parity))) return true;
@@ -124,9 +126,12 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             tc::prefetch_map(&maps.a);
             tc::prefetch_map(&maps.b);
             int l = 0;
+#pragma unroll 1
             for (int t = first; t < tiles && ok(); t += step) {
                 const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
-                for (int kb = kb0; kb < kb1; ++kb, ++l) {
+#pragma unroll 1
+    #pragma unroll 1
+            for (int kb = kb0; kb < kb1; ++kb, ++l) {
                     const int s = l % L::STAGES;
                     if (l >= L::STAGES && !wait(empty(s), (l / L::STAGES & 1) ^ 1)) break;
                     tc::mbar_expect_tx(full(s), L::STAGE);
@@ -135,18 +140,26 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 }
             }
             if (!ok())
+#pragma unroll 1
                 for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
         }
-    } else if (warp == 1) {
-        // ---------------- issuer (the whole warp, converged; lane 0 issues) ----------------
+    } else if (warp == 1 || warp == 3) {
+        // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
+        // A warp that waits, commits or fences issues no product (60 to 120 cycles each, 400 a block of 128, against 512
+        // for its products, and products do not queue up): two take the blocks in turn, each with its half of the
+        // tensor memory.
         constexpr uint32_t id = tc::idesc_e4m3(128, BN);
         const uint32_t on = lane == 0;
+        const int b = warp == 3;
         int l = 0;
         bool fine = true;
+#pragma unroll 1
         for (int t = first; t < tiles && fine; t += step) {
+#pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                const int s = l % L::STAGES, b = l & 1;
-                fine = wait_warp(full(s), l / L::STAGES & 1) && (l < 2 || wait_warp(t_empty + 8 * b, (l >> 1 & 1) ^ 1));
+                if ((l & 1) != b) continue;
+                const int s = l % L::STAGES;
+                fine = (l < 2 || wait_warp(t_empty + 8 * b, (l >> 1 & 1) ^ 1)) && wait_warp(full(s), l / L::STAGES & 1);
                 if (!fine) break;
                 tc::fence_after();
                 const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
@@ -157,15 +170,17 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             }
         }
         if (!fine) {
-            tc::commit_if(on, ended);
-            tc::mbar_wait(ended, 0);
+            tc::commit_if(on, ended + 8 * b);
+            tc::mbar_wait(ended + 8 * b, 0);
         }
     } else if (warp == 2 && !X_ROWS) {
         // ---------------- scales of the columns, eight blocks at a time ----------------
         int u = 0;
+#pragma unroll 1
         for (int t = first; t < tiles; t += step) {
             const int nb = t / tiles_b;
             const int64_t m0 = (int64_t)(t % tiles_b) * BN;
+#pragma unroll 1
             for (int kb = kb0; kb < kb1; kb += 8, ++u) {
                 if (u >= 2) wait_warp(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
                 float* sc = reinterpret_cast<float*>(smem + L::oScale) + (u & 1) * 8 * BN;
@@ -187,6 +202,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         const int q4 = warp & 3, group = (warp - 4) >> 2, i = 32 * q4 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + group * COLS;
         int l = 0, u = 0;
+#pragma unroll 1
         for (int t = first; t < tiles; t += step) {
             const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
             float acc[COLS];
@@ -197,6 +213,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             const float* ws = p.ws + (int64_t)min((b0 + group * COLS) / 128, (p.N - 1) / 128) * nkb;
             auto scale_at = [&](int kb) { return xs && kb < kb1 ? __ldg(xs + (p.x_blocks > 1 ? kb : 0)) * __ldg(ws + kb) : 0.f; };
             float next = X_ROWS ? scale_at(kb0) : 0.f;
+#pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
                 const int b = l & 1;
                 const float s = next;
@@ -286,6 +303,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         const int a0 = first / tiles_b * 128, b0 = first % tiles_b * BN;
         auto total = [&](int word) {
             float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
             for (int r = 0; r < split; ++r) {
                 const float4 v = split > 1 ? ld_peer(sb + 4 * word, r) : *reinterpret_cast<const float4*>(smem + 4 * word);
                 s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
@@ -299,6 +317,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         };
         // the ranks share out the tile's quadruples of outputs
         constexpr int QUADS = 128 * BN / 4;
+#pragma unroll 1
         for (int e = rank * L::THREADS + tid; e < QUADS; e += split * L::THREADS) {
             if (X_ROWS) {  // quadruple e: columns 4 (e / 128), row e % 128
                 const int n = b0 + e / 128 * 4;
