@@ -182,15 +182,15 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
-// the state's terms of a chunk: Y'^T Z, from both halves of Y' if there are two
+// the state's terms of a chunk, transposed: Z^T Y', from both halves of Y' if there are two
 template <int D>
 __device__ __forceinline__ void issue_terms(uint32_t on, uint32_t to, uint32_t hi, uint32_t lo, uint32_t z, bool twice) {
     constexpr uint32_t id = tc::idesc(128, D, 1, 1);
 #pragma unroll 1
-    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(hi, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, k > 0);
+    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(z, CHUNK, 0, k), tc::mdesc(hi, CHUNK, 0, k), id, k > 0);
     if (!twice) return;
 #pragma unroll 1
-    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(lo, CHUNK, 0, k), tc::mdesc(z, CHUNK, 0, k), id, 1);
+    for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(z, CHUNK, 0, k), tc::mdesc(lo, CHUNK, 0, k), id, 1);
 }
 
 template <int D, int WALKS>
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     const uint32_t tmem = tslot;
     const Waiter wait{&gone_s, p.status};
     if (plan_s.total < 0 && tid == 0) atomicOr(p.status, ST_BAD_SEQLENS);
-    const bool any = plan_s.f0 < plan_s.f1;
+    const bool any = more(plan_s, plan_s.at, plan_s.f, p.snap);
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(K::REGS_1));
@@ -267,13 +267,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             const Plan plan = plan_s;
             Place at = plan.at;
             bool go_on = true;
+            int f = plan.f;
 #pragma unroll 1
-            for (int f = plan.f0; go_on; ++it) {
+            for (; go_on; ++it) {
                 const int t0 = line.token(at), h0 = at.head;
                 int4 c = make_int4(t0, line.rows(at), h0, at.seq * p.H + h0);
+                if (at.pos == 0 && w.init && it)  // (the chain's state will be asked for soon)
+                    tc::prefetch_l2(w.init + (int64_t)c.w * D * D, D * D * sizeof(float));
                 if (at.pos + 1 == at.count) c.y |= Chunk::ENDS;
-                line.next(at);
-                go_on = more(plan, at, ++f, p.snap);
+                line.next(at, f);
+                go_on = more(plan, at, f, p.snap);
                 if (!go_on) c.y |= Chunk::LAST;
                 chunks[it & 7] = c;
                 on[0] = on[1] = on[2] = false;
@@ -305,7 +308,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             // of 16 of the inner dimension, and products do not queue up): two share them, P's chain and the state's.
             const uint32_t on = lane == 0;
             const uint32_t tP = tmem, tO1 = tmem + 128, tO2 = tmem + 256, tD = tmem + 384;
-            constexpr uint32_t idP = tc::idesc(128, 128, 0, 0), idO = tc::idesc(128, D, 0, 1);
+            constexpr uint32_t idP = tc::idesc(128, 128, 0, 0), idO = tc::idesc(128, D, 0, 1), idS = tc::idesc(128, D, 0, 0);
 #pragma unroll 1
             for (int it = 0;; ++it) {
                 const int sx = slot_x(it), sy = slot_y(it), sz = slot_z(it);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                     if (!wait.warp(full(sx), turn(it, K::NX)) || !wait.warp(s_ready, ph) || (it && !wait.warp(o_free, ph ^ 1))) break;
                     tc::fence_after();
 #pragma unroll 1
-                    for (int k = 0; k < D; k += 16) tc::mma_if(on, tO2, tc::kdesc(X, CHUNK, 0, k), tc::mdesc(sb + K::oS, D, 0, k), idO, k > 0);
+                    for (int k = 0; k < D; k += 16) tc::mma_if(on, tO2, tc::kdesc(X, CHUNK, 0, k), tc::kdesc(sb + K::oS, D, 0, k), idS, k > 0);
                     tc::commit_if(on, s_free);
                 }
                 tc::commit_if(on, o_full);
@@ -504,11 +507,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(K::REGS_B));
         // ---------------- group B: Y', the state ----------------
-        // two warps for each 32 tokens of Y and 32 rows of the state, each with half of the columns
+        // two warps for each 32 tokens of Y and 32 columns of the state (Z's channels, so that what one instruction
+        // moves of a state in memory is contiguous), each with half of Y's channels
         const int q4 = warp & 3, half = (warp - 12) >> 2, i = 32 * q4 + lane, col = half * HALF;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + 384 + col;
-        const bool mine = 32 * q4 < D;  // (warps without rows of the state)
-        float S[HALF];
+        const bool mine = 32 * q4 < D;  // (warps without columns of the state)
+        float S[HALF];  // rows `col` and on of column i
         float g = 0.f, w_full = 0.f;
         float2 c_full = make_float2(0.f, 0.f);
         auto incoming = [&](int chain, int head, bool inside) {
@@ -518,13 +522,13 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             if (from && mine) {
                 if (WALKS > 1 && w.turned) {
 #pragma unroll
-                    for (int c = 0; c < HALF; ++c) S[c] = from[(col + c) * D + i];
-                } else {
-#pragma unroll
                     for (int c = 0; c < HALF; c += 4) {
                         const float4 u = *reinterpret_cast<const float4*>(from + i * D + col + c);
                         S[c] = u.x, S[c + 1] = u.y, S[c + 2] = u.z, S[c + 3] = u.w;
                     }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < HALF; ++c) S[c] = from[(col + c) * D + i];
                 }
             } else {
 #pragma unroll
@@ -545,6 +549,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             tc::fence_async_smem();
             warp_arrive(s_ready);
         };
+        cudaGridDependencySynchronize();  // (the states that k_dla_join carries)
         if (any) incoming(plan_s.at.seq * p.H + plan_s.at.head, plan_s.at.head, plan_s.at.pos != 0);
 #pragma unroll 1
         for (int it = 0; any; ++it) {
@@ -593,9 +598,9 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             }
             tc::fence_before();
             if (now.ends() && w.last && mine) {
-                float* to = w.last + ((int64_t)now.chain * D + i) * D + col;
+                float* to = w.last + ((int64_t)now.chain * D + col) * D + i;
 #pragma unroll
-                for (int j = 0; j < HALF; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+                for (int j = 0; j < HALF; ++j) to[j * D] = S[j];
             }
             if (now.last()) break;
             if (now.ends()) {
@@ -644,17 +649,17 @@ __device__ __forceinline__ Tail tail_of(const Line& line, const Plan& plan) {
     if (plan.total <= 0 || plan.f0 >= plan.f1) return t;
     // chain by chain to the one that holds the range's last chunk
     Place at = plan.at;
-    int f = plan.f0;
+    int f = plan.f;
 #pragma unroll 1
-    while (f + (at.count - at.pos) < plan.f1) {
-        f += at.count - at.pos;
+    while (f + (at.count - at.pos) + 1 < plan.f1) {
+        f += at.count - 1 - at.pos;
         at.pos = at.count - 1;
-        line.next(at);
+        line.next(at, f);
     }
     t.first = at;
     t.last = at;
     t.last.pos = at.pos + (plan.f1 - 1 - f);
-    if (t.last.pos + 1 < at.count) t.chunks = plan.f1 - f;
+    if (f < plan.f1 && t.last.pos + 1 < at.count) t.chunks = plan.f1 - f;
     return t;
 }
 
@@ -798,9 +803,9 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
             tc::fence_before();
         }
         if (mine && wait.ok()) {
-            float* to = w.sums + (((int64_t)range * p.pieces + piece) * D + i) * D + col;
+            float* to = w.sums + (((int64_t)range * p.pieces + piece) * D + col) * D + i;
 #pragma unroll
-            for (int j = 0; j < HALF; j += 4) *reinterpret_cast<float4*>(to + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+            for (int j = 0; j < HALF; ++j) to[j * D] = S[j];
         }
     }
     tc::fence_before();
@@ -809,25 +814,28 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
 }
 
 // The states at the beginnings of ranges that begin inside a chain, in the place of the first piece of the sum of
-// the range before: along each such chain, from its initial state.  Four blocks a state (most blocks have
-// nothing to do and have to end soon), the sums of two ranges asked for together.
-constexpr int JOIN_SLICES = 4, JOIN_THREADS = 256;
+// the range before: along each such chain, from its initial state.  A few blocks a state (most blocks have
+// nothing to do and have to end soon), the sums of four ranges asked for together.
+constexpr int JOIN_THREADS = 256;
+template <int D>
+__host__ __device__ constexpr int join_slices() { return D == 128 ? 8 : 2; }
 template <int D, int WALKS>
 __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant__ TailWalks<WALKS> walks, const Grid p) {
-    constexpr int AHEAD = 2, QUADS = D * D / JOIN_SLICES / (4 * JOIN_THREADS);  // float4 of a thread
+    constexpr int SLICES = join_slices<D>(), AHEAD = 4, QUADS = D * D / SLICES / (4 * JOIN_THREADS);  // float4 of a thread
     __shared__ Plan plan_s;
     __shared__ int scratch[JOIN_THREADS / 32];
-    const int slice = blockIdx.x % JOIN_SLICES, which = blockIdx.x / JOIN_SLICES % WALKS, range = blockIdx.x / JOIN_SLICES / WALKS + 1;
+    const int slice = blockIdx.x % SLICES, which = blockIdx.x / SLICES % WALKS, range = blockIdx.x / SLICES / WALKS + 1;
     const TailWalk& w = walks.w[which];
     const Line line = line_of(p, w.back);
     make_plan<JOIN_THREADS>(line, range, p.ranges, 0, &plan_s, scratch);
     const Plan plan = plan_s;
+    cudaGridDependencySynchronize();  // (the sums of k_dla_tail)
     if (plan.total <= 0 || plan.f0 >= plan.f1 || plan.at.pos == 0) return;
     const Place at = plan.at;
-    const int first = plan.f0 - at.pos;  // the chain's first chunk
-    if (first < range_begin(plan.total, range - 1, plan.ranges)) return;  // (the chain's first crossing does them all)
+    const int first = plan.f0 - at.pos, stop = first + at.count;  // the places of the chain's chunks
+    if (range_begin(plan.total, range - 1, plan.ranges) > first) return;  // (the chain's first crossing does them all)
     const float g = log_decay(p.g, at.head);
-    const int e = slice * (D * D / JOIN_SLICES) + threadIdx.x * 4;
+    const int e = slice * (D * D / SLICES) + threadIdx.x * 4;
     float4 s[QUADS] = {};
     if (w.init) {
         const float* from = w.init + ((int64_t)at.seq * p.H + at.head) * D * D + e;
@@ -836,12 +844,12 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
     }
     int done = 0;
 #pragma unroll 1
-    for (int r0 = range; r0 < plan.ranges && range_begin(plan.total, r0, plan.ranges) < first + at.count; r0 += AHEAD) {
+    for (int r0 = range; r0 < plan.ranges && range_begin(plan.total, r0, plan.ranges) < stop; r0 += AHEAD) {
         float4 t[AHEAD][QUADS] = {};
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             const int r = r0 + u, f = range_begin(plan.total, r, plan.ranges);
-            if (r >= plan.ranges || f >= first + at.count) continue;
+            if (r >= plan.ranges || f >= stop) continue;
             const int chunks = f - max(first, range_begin(plan.total, r - 1, plan.ranges));
             const float* from = w.sums + (int64_t)(r - 1) * p.pieces * D * D + e;
 #pragma unroll 1
@@ -857,7 +865,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
 #pragma unroll
         for (int u = 0; u < AHEAD; ++u) {
             const int r = r0 + u, f = range_begin(plan.total, r, plan.ranges);
-            if (r >= plan.ranges || f >= first + at.count) break;
+            if (r >= plan.ranges || f >= stop) break;
             const int upto = line.before(at, f - first);
             const float2 c = carry(g, upto - done);
             done = upto;
@@ -902,6 +910,23 @@ Shares shares_of(const DlaParams& p, int walks) {
     return {(int)(ranges < fit ? ranges : fit), 0, chains > fit ? 4 : 1};
 }
 
+// Launches a kernel whose blocks may be in place before the kernel ahead of it has ended: it waits for that one itself
+// (cudaGridDependencySynchronize) before it reads what that has written.
+template <class... P, class... A>
+cudaError_t launch_after(unsigned grid, unsigned threads, size_t smem, cudaStream_t s, void (*kernel)(P...), const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 template <int D, int WALKS, int TAILS>
 cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, const TailWalks<TAILS>& tails, cudaStream_t s) {
     const Grid grid{p.N, p.H, D, sh.ranges, sh.snap, sh.pieces, p.T, p.seq_len, p.cu_seqlens, p.g, p.status};
@@ -919,7 +944,10 @@ cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, 
         e = cudaFuncSetAttribute(k_dla_tail<D, TAILS>, cudaFuncAttributeMaxDynamicSharedMemorySize, TailCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
         k_dla_tail<D, TAILS><<<(sh.ranges - 1) * TAILS * sh.pieces, TailCfg<D>::THREADS, TailCfg<D>::SMEM, s>>>(tails, grid);
-        k_dla_join<D, TAILS><<<(sh.ranges - 1) * TAILS * JOIN_SLICES, JOIN_THREADS, 0, s>>>(tails, grid);
+        e = cudaGetLastError();
+        if (e == cudaSuccess) e = launch_after((sh.ranges - 1) * TAILS * join_slices<D>(), JOIN_THREADS, 0, s, k_dla_join<D, TAILS>, tails, grid);
+        if (e == cudaSuccess) e = launch_after(sh.ranges * WALKS, Cfg<D>::THREADS, Cfg<D>::SMEM, s, k_dla<D, WALKS>, walks, grid);
+        return e;
     }
     k_dla<D, WALKS><<<sh.ranges * WALKS, Cfg<D>::THREADS, Cfg<D>::SMEM, s>>>(walks, grid);
     return cudaGetLastError();

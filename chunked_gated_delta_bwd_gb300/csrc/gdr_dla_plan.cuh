@@ -3,7 +3,9 @@
 // A chain is one (sequence, head): its chunks of 128 tokens in the order in which the state passes through
 // them (back to front for the gradients' walk).  All chunks of a call stand in one line, chain after
 // chain (sequence by sequence, head by head), and each block takes one range of it: ranges of equal
-// length, so that every multiprocessor has the same work whatever the sequences' lengths.  A chain that
+// length, so that every multiprocessor has the same work whatever the sequences' lengths.  A chain
+// takes one place more than it has chunks, ahead of them: its states in and out are as many bytes as a
+// chunk's.  (16 sequences of 1 to 60 chunks: the ranges with many short ones were 1.9 times as long.)  A chain that
 // crosses from one range into the next hands its state over (gdr_dla.cu); where chains are short
 // the ranges end with whole chains instead (`snap`).
 #pragma once
@@ -33,9 +35,11 @@ struct Line {
         p.len = (int)(cu ? cu[p.seq + 1] - p.begin : seq_len);
         p.count = (p.len + CHUNK - 1) / CHUNK;
     }
-    // the next chunk (after the last one `seq` is N)
-    __device__ __forceinline__ void next(Place& p) const {
+    // the next chunk, at place f of the line (after the last one `seq` is N)
+    __device__ __forceinline__ void next(Place& p, int& f) const {
+        ++f;
         if (++p.pos < p.count) return;
+        ++f;
         p.pos = 0;
         if (++p.head < H) return;
         p.head = 0;
@@ -57,30 +61,35 @@ struct Line {
 
 // What a block learns before it starts, through shared memory.
 struct Plan {
-    int total;    // chunks of the line; -1: the sequences' borders are inconsistent
-    int ranges;   // ranges that have chunks (no more than there are chunks)
+    int total;    // places of the line; -1: the sequences' borders are inconsistent
+    int ranges;   // ranges that are not empty (no more than there are places)
     int f0, f1;   // the range
+    int f;        // the place of its first chunk
     Place at;     // its first chunk
 };
 
 __device__ __forceinline__ int range_begin(int total, int r, int ranges) { return (int)((int64_t)total * r / ranges); }
 
-// The place of chunk f of the line, from the sequence that holds it and the chunks of the sequences before it.
-__device__ __forceinline__ Place place_of(const Line& line, int f, int seq, int chunks_before) {
+// places of a chain of that many tokens
+__device__ __forceinline__ int places(int64_t tokens) { return tokens > 0 ? (int)((tokens + CHUNK - 1) / CHUNK) + 1 : 0; }
+// The first chunk from place f0 of the line on, from the sequence that holds the place and the places of a head before it.
+__device__ __forceinline__ void set_first(Plan* out, const Line& line, int seq, int before) {
     Place p;
     p.seq = seq;
     line.sequence(p);
-    const int in = f - chunks_before * line.H;
-    p.head = in / p.count;
-    p.pos = in - p.head * p.count;
-    return p;
+    const int in = out->f0 - before * line.H;
+    p.head = in / (p.count + 1);
+    p.pos = in - p.head * (p.count + 1) - 1;
+    out->f = out->f0;
+    if (p.pos < 0) p.pos = 0, ++out->f;
+    out->at = p;
 }
 
 __device__ __forceinline__ void set_range(Plan* out, int total, int range, int ranges) {
     ranges = max(min(ranges, total), 1);
     out->total = total;
     out->ranges = ranges;
-    out->f0 = total < 0 || range >= ranges ? 0 : range_begin(total, range, ranges);
+    out->f = out->f0 = total < 0 || range >= ranges ? 0 : range_begin(total, range, ranges);
     out->f1 = total < 0 || range >= ranges ? 0 : range_begin(total, range + 1, ranges);
 }
 
@@ -90,21 +99,21 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (!line.cu) {
         if (tid == 0) {
-            const int per = (int)((line.seq_len + CHUNK - 1) / CHUNK);
+            const int per = places(line.seq_len);
             set_range(out, per * line.N * line.H, range, ranges);
             const int seq = out->f0 / (per * line.H);
-            out->at = place_of(line, out->f0, seq, seq * per);
+            set_first(out, line, seq, seq * per);
         }
         __syncthreads();
     } else {
-        // every block adds up the sequences' chunks: N reads, all of them hits in the second-level cache
+        // every block adds up the sequences' places: N reads, all of them hits in the second-level cache
         int sum = 0;
         bool bad = line.cu[0] != 0 || line.cu[line.N] != line.T;
 #pragma unroll 1
         for (int i = tid; i < line.N; i += THREADS) {
             const int64_t len = line.cu[i + 1] - line.cu[i];
             bad |= len < 0 || len > line.T;
-            sum += (int)((len + CHUNK - 1) / CHUNK);
+            sum += places(len);
         }
         // (borders that never decrease from 0 to T are all inside)
         bad = __syncthreads_or(bad);
@@ -118,12 +127,12 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
         if (tid == 0) set_range(out, bad ? -1 : total * line.H, range, ranges);
         __syncthreads();
         const int f0 = out->f0;
-        // the sequence that holds chunk f0 (none where the range is empty)
+        // the sequence that holds place f0 (none where the range is empty)
         int base = 0;
 #pragma unroll 1
         for (int i0 = 0; f0 < out->f1 && i0 < line.N; i0 += THREADS) {
             const int i = i0 + tid;
-            const int mine = i < line.N ? (int)((line.cu[i + 1] - line.cu[i] + CHUNK - 1) / CHUNK) : 0;
+            const int mine = i < line.N ? places(line.cu[i + 1] - line.cu[i]) : 0;
             int upto = mine;
 #pragma unroll
             for (int o = 1; o < 32; o *= 2) {
@@ -140,7 +149,7 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
                 strip += scratch[w];
             }
             const int before = base + upto - mine;
-            if (mine && before <= f0 / line.H && f0 / line.H < before + mine) out->at = place_of(line, f0, i, before);
+            if (mine && before <= f0 / line.H && f0 / line.H < before + mine) set_first(out, line, i, before);
             base += strip;
             if (base > f0 / line.H) break;
         }
@@ -148,19 +157,19 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
     }
     if (snap && tid == 0 && out->f0 < out->f1) {
         // whole chains: the first that begins in the range, to the end of the last that does
-        if (out->at.pos != 0) {
-            out->f0 += out->at.count - out->at.pos;
+        if (out->f - out->at.pos - 1 < out->f0) {
+            out->f += out->at.count - 1 - out->at.pos;
             out->at.pos = out->at.count - 1;
-            if (out->f0 < out->f1) line.next(out->at);
+            if (out->f + 1 < out->f1) line.next(out->at, out->f);
+            else out->f1 = out->f0;  // (none does)
         }
-        if (out->f0 > out->f1) out->f0 = out->f1;
     }
     if (snap) __syncthreads();
 }
 
-// whether the walk of a range goes on at `p`, chunk f of the line
+// whether the walk of a range goes on at `p`, place f of the line
 __device__ __forceinline__ bool more(const Plan& plan, const Place& p, int f, int snap) {
-    return plan.f0 < plan.f1 && f < plan.total && (f < plan.f1 || (snap && p.pos != 0));
+    return plan.f0 < plan.f1 && f < plan.total && (snap ? p.pos != 0 || f - 1 < plan.f1 : f < plan.f1);
 }
 
 // The log decay of a head.  (Below -10^4 no token remembers another; an infinite one would make 0 times infinity.)

@@ -307,6 +307,10 @@ __device__ __forceinline__ void tma_prefetch_2d(const void* map, int x, int y) {
                  "r"(x), "r"(y)
                  : "memory");
 }
+// contiguous memory into L2 only (16-byte aligned, a multiple of 16 bytes)
+__device__ __forceinline__ void prefetch_l2(const void* src, uint32_t bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;\n" ::"l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void prefetch_map(const void* map) {
     asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
