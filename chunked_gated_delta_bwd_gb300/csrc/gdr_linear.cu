@@ -36,6 +36,7 @@ struct Lin {
     static constexpr int BARS = 2 * STAGES + 10;
     static constexpr int SMEM = oBar + 8 * BARS + 8 + 1024;
     static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr bool MOVE_REGS = BN == 256;  // 64 x 128 + 216 x 256 registers out of the launch's 168 x 384
 };
 
 struct Maps {
@@ -120,6 +121,9 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     };
     const int first = blockIdx.x / split, step = gridDim.x / split;
 
+    // (the registers of group sums: 128, and the 64 that come in; all warps of a group of four take part)
+    if (warp < 4) {
+    if (L::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
     if (warp == 0) {
         if (lane == 0) {
             // ---------------- loader ----------------
@@ -197,7 +201,9 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 tc::mbar_arrive(sc_full + 8 * (u & 1));
             }
         }
-    } else if (warp >= 4) {
+    }
+    } else {
+        if (L::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
         // ---------------- sums ----------------
         const int q4 = warp & 3, group = (warp - 4) >> 2, i = 32 * q4 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + group * COLS;
@@ -222,14 +228,21 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 if (!X_ROWS && ((kb - kb0) & 7) == 0) wait_warp(sc_full + 8 * (u & 1), u >> 1 & 1);
                 wait_warp(t_full + 8 * b, l >> 1 & 1);
                 tc::fence_after();
-                constexpr int PART = COLS < 32 ? COLS : 32;
+                // (64 columns asked for at once, and the buffer given back before the last ones are added: what bounds the
+                // loop is how soon the next product may have it)
+                constexpr int PART = COLS < 64 ? COLS : 64;
 #pragma unroll
                 for (int c = 0; c < COLS; c += PART) {
                     uint32_t v[PART / 16][16];
 #pragma unroll
                     for (int h = 0; h < PART / 16; ++h) tc::ld16_nowait(lanes + b * BN + c + 16 * h, v[h]);
-                    if constexpr (PART == 32) tc::ld_wait(v[0], v[1]);
-                    else tc::ld_wait(v[0]);
+#pragma unroll
+                    for (int h = 0; h < PART / 16; ++h) tc::ld_wait(v[h]);
+                    if (c + PART == COLS) {
+                        tc::fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(t_empty + 8 * b);
+                    }
 #pragma unroll
                     for (int j = 0; j < PART; j += 4) {
                         float4 f = make_float4(s, s, s, s);
@@ -239,9 +252,6 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                         ACC2(acc, c + j + 2, __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), make_float2(f.z, f.w), F2(acc, c + j + 2)));
                     }
                 }
-                tc::fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(t_empty + 8 * b);
                 if (!X_ROWS && (((kb - kb0) & 7) == 7 || kb + 1 == kb1)) {
                     if (lane == 0) tc::mbar_arrive(sc_empty + 8 * (u & 1));
                     ++u;
@@ -350,6 +360,13 @@ cudaError_t go(const LinearParams& p, int split, cudaStream_t s) {
     if (tiles > (1 << 30) / 8) return cudaErrorInvalidValue;
     cudaError_t e = cudaFuncSetAttribute(k_linear<X_ROWS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
     if (e != cudaSuccess) return e;
+    if (L::MOVE_REGS) {  // (the groups' shares of the registers have to be there at the launch)
+        static const int regs = [] {
+            cudaFuncAttributes at;
+            return cudaFuncGetAttributes(&at, k_linear<X_ROWS, BN>) == cudaSuccess ? at.numRegs : 0;
+        }();
+        if (regs != 168) return cudaErrorInvalidConfiguration;
+    }
     cudaLaunchConfig_t cfg = {};
     // (one tile a cluster; blocks that store by TMA walk the tiles)
     cfg.gridDim = dim3((unsigned)(X_ROWS && split == 1 ? (tiles < num_sms() ? tiles : num_sms()) : tiles * split));

@@ -3,8 +3,8 @@
 //   scale = max |x| / 448 (1 where all are zero),  y = e4m3(x / scale)
 //
 // Bytes bound it: every value is read once and held in registers between the maximum and its code.
-// Rows: 16 threads hold 128 channels, eight each; a group of threads takes several such blocks with
-// their loads in flight together.  Tiles: a block of 256 threads holds a tile, 64 values each; the transposed
+// Rows: eight threads hold 128 channels, 16 each, of two rows, with their loads in flight together
+// (instructions bound it next: 16 threads with eight each took 45 us for 8191 x 6144 in bf16).  Tiles: a block of 256 threads holds a tile, 64 values each; the transposed
 // copy is turned round in shared memory.
 #include "gdr_e4m3.h"
 #include "gdr_internal.h"
@@ -13,13 +13,22 @@
 namespace gdr {
 namespace {
 
-constexpr int ITEMS = 4;  // blocks of 128 channels a group of 16 threads holds at once
+constexpr int ROWS_AT_ONCE = 2;  // rows a group of eight threads holds at once
 
 __device__ __forceinline__ float most_of(const Eight& e) {
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(e.v[i]));
     return m;
+}
+__device__ __forceinline__ float most_of(const RawOf<float>& r) { return most_of(r.widen()); }
+__device__ __forceinline__ float most_of(const RawOf<__nv_bfloat16>& r) {  // (in pairs)
+    const uint32_t w[4] = {r.u.x & 0x7fff7fffu, r.u.y & 0x7fff7fffu, r.u.z & 0x7fff7fffu, r.u.w & 0x7fff7fffu};
+    __nv_bfloat162 m = *reinterpret_cast<const __nv_bfloat162*>(w);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2(m, *reinterpret_cast<const __nv_bfloat162*>(w + i));
+    const float2 f = __bfloat1622float2(m);
+    return fmaxf(fmaxf(f.x, f.y), 0.f);
 }
 // eight codes of a row whose `n` channels from here on exist
 __device__ __forceinline__ void put_codes(uint8_t* y, const uint32_t (&h)[4], int n, bool wide) {
@@ -32,35 +41,40 @@ __device__ __forceinline__ void put_codes(uint8_t* y, const uint32_t (&h)[4], in
     }
 }
 
+// Eight threads hold a block of 128 channels, two pieces of eight each (64 channels apart).  A warp takes 4 of them: 1 << cw
+// blocks side by side, of 4 >> cw rows.
 template <class T>
-__global__ void __launch_bounds__(256) k_quant_rows(const QuantParams p, int nb, int64_t items, int wide) {
-    const int lane = threadIdx.x % 16;
-    const int64_t first = (int64_t)blockIdx.x * (16 * ITEMS) + threadIdx.x / 16;
-    RawOf<T> raw[ITEMS];
-    int64_t at[ITEMS];
-    int n[ITEMS];
+__global__ void __launch_bounds__(256) k_quant_rows(const QuantParams p, int nb, int across, int cw, int wide) {
+    const int lane = threadIdx.x % 8, group = threadIdx.x / 8;
+    const int down = blockIdx.x / across, block = (blockIdx.x - down * across) << cw | (group & ((1 << cw) - 1)), c = block * 128 + 8 * lane;
+    const int64_t row0 = (int64_t)down * ((32 >> cw) * ROWS_AT_ONCE) + (group >> cw);
+    RawOf<T> raw[ROWS_AT_ONCE][2];
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const int64_t item = first + 16 * i;
-        const int64_t row = items < (1ll << 31) ? (int64_t)((uint32_t)item / (uint32_t)nb) : item / nb;
-        const int c = (int)(item - row * nb) * 128 + 8 * lane;
-        n[i] = item < items ? p.C - c : 0;
-        at[i] = row * p.C + c;
-        raw[i] = RawOf<T>{};
-        if (n[i] > 0) raw[i] = ld8(static_cast<const T*>(p.x) + row * p.ldx + c, n[i], wide);
-    }
+    for (int i = 0; i < ROWS_AT_ONCE; ++i)
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-        const Eight e = raw[i].widen();
-        float m = most_of(e);
+        for (int h = 0; h < 2; ++h) {
+            const int64_t row = row0 + i * (32 >> cw);
+            const int n = p.C - c - 64 * h;
+            raw[i][h] = RawOf<T>{};
+            if (row < p.R && n > 0) raw[i][h] = ld8(static_cast<const T*>(p.x) + row * p.ldx + c + 64 * h, n, wide);
+        }
 #pragma unroll
-        for (int o = 8; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    for (int i = 0; i < ROWS_AT_ONCE; ++i) {
+        const int64_t row = row0 + i * (32 >> cw);
+        float m = fmaxf(most_of(raw[i][0]), most_of(raw[i][1]));
+#pragma unroll
+        for (int o = 4; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (row >= p.R || block >= nb) continue;
         const float scale = scale_of(m);
-        if (n[i] <= 0) continue;
-        uint32_t h[4];
-        codes_of(e, scale, h);
-        put_codes(p.y + at[i], h, n[i], wide);
-        if (lane == 0) p.scale[first + 16 * i] = scale;
+        if (lane == 0) p.scale[row * nb + block] = scale;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int n = p.C - c - 64 * h;
+            if (n <= 0) continue;
+            uint32_t code[4];
+            codes_of(raw[i][h].widen(), scale, code);
+            put_codes(p.y + row * p.C + c + 64 * h, code, n, wide);
+        }
     }
 }
 
@@ -137,8 +151,8 @@ cudaError_t go(const QuantParams& p, cudaStream_t s) {
     const int nb = (p.C + 127) / 128;
     const int wide = (reinterpret_cast<uintptr_t>(p.x) & 15) == 0 && p.ldx % 8 == 0 && p.C % 8 == 0;
     if (!p.tiles) {
-        const int64_t items = p.R * nb;
-        k_quant_rows<T><<<(unsigned)((items + 16 * ITEMS - 1) / (16 * ITEMS)), 256, 0, s>>>(p, nb, items, wide);
+        const int cw = nb > 2 ? 2 : nb - 1, across = (nb + (1 << cw) - 1) >> cw, rows = (32 >> cw) * ROWS_AT_ONCE;
+        k_quant_rows<T><<<(unsigned)((p.R + rows - 1) / rows * across), 256, 0, s>>>(p, nb, across, cw, wide);
     } else {
         const int64_t nr = (p.R + 127) / 128;
         k_quant_tiles<T><<<(unsigned)(nr * nb), 256, 0, s>>>(p, nb, (int)nr, wide, p.R % 16 == 0);
