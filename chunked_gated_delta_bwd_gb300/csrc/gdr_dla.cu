@@ -932,7 +932,8 @@ cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, 
     const Grid grid{p.N, p.H, D, sh.ranges, sh.snap, sh.pieces, p.T, p.seq_len, p.cu_seqlens, p.g, p.status};
     cudaError_t e = cudaMemsetAsync(p.status, 0, 256, s);
     if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(k_dla<D, WALKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<D>::SMEM);
+    static bool allowed[64], allowed_tail[64];
+    e = allow_smem((const void*)k_dla<D, WALKS>, Cfg<D>::SMEM, allowed);
     if (e != cudaSuccess) return e;
     // (the groups' shares of the registers have to be there at the launch)
     static const int regs = [] {
@@ -941,7 +942,7 @@ cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, 
     }();
     if (regs != Cfg<D>::REGS) return cudaErrorInvalidConfiguration;
     if (!sh.snap && sh.ranges > 1) {
-        e = cudaFuncSetAttribute(k_dla_tail<D, TAILS>, cudaFuncAttributeMaxDynamicSharedMemorySize, TailCfg<D>::SMEM);
+        e = allow_smem((const void*)k_dla_tail<D, TAILS>, TailCfg<D>::SMEM, allowed_tail);
         if (e != cudaSuccess) return e;
         k_dla_tail<D, TAILS><<<(sh.ranges - 1) * TAILS * sh.pieces, TailCfg<D>::THREADS, TailCfg<D>::SMEM, s>>>(tails, grid);
         e = cudaGetLastError();

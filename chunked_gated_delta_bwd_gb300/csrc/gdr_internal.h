@@ -91,6 +91,17 @@ inline int num_sms() {
     return cache[dev];
 }
 
+// The dynamic shared memory of a kernel above 48 KB, allowed once for each device (the call takes a
+// good part of a microsecond; `done` is the kernel's own).
+inline cudaError_t allow_smem(const void* kernel, int bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev])) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = true;
+    return e;
+}
+
 // causal depthwise conv1d backward (gdr_conv1d_bwd)
 struct ConvParams {
     int N;                        // sequences

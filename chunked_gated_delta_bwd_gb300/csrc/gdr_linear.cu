@@ -352,13 +352,14 @@ cudaError_t go(const LinearParams& p, int split, cudaStream_t s) {
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     const int a_rows = X_ROWS ? (int)p.M : p.N, b_rows = X_ROWS ? p.N : (int)p.M;
-    if (!encode_bytes_map(&maps.a, X_ROWS ? p.x : p.w, a_rows, p.K, 128) || !encode_bytes_map(&maps.b, X_ROWS ? p.w : p.x, b_rows, p.K, BN) ||
-        !encode_rows_map(&maps.y, p.y, p.M, p.N, 128))
+    if (!encode_bytes_map(&maps.a, X_ROWS ? p.x : p.w, a_rows, p.K, 128) || !encode_bytes_map(&maps.b, X_ROWS ? p.w : p.x, b_rows, p.K, BN))
         return cudaErrorInvalidValue;
+    if (X_ROWS && split == 1 && !encode_rows_map(&maps.y, p.y, p.M, p.N, 128)) return cudaErrorInvalidValue;
     const int tiles_b = (b_rows + BN - 1) / BN;
     const int64_t tiles = (int64_t)((a_rows + 127) / 128) * tiles_b;
     if (tiles > (1 << 30) / 8) return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(k_linear<X_ROWS, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+    static bool allowed[64];
+    cudaError_t e = allow_smem((const void*)k_linear<X_ROWS, BN>, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
     if (L::MOVE_REGS) {  // (the groups' shares of the registers have to be there at the launch)
         static const int regs = [] {

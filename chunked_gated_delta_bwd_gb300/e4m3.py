@@ -8,7 +8,7 @@ import ctypes
 import torch
 
 from .api import _check, lib
-from .block import _TYPES, _need, _opt, _ptr, _rows, _stream
+from .block import _TYPES, _need, _ptr, _rows, _stream
 
 E4M3 = torch.float8_e4m3fn
 _LIB = None
@@ -60,15 +60,16 @@ def linear_e4m3(x, x_scale, weight, weight_scale, bias=None, out=None):
     Returns y bf16 [..., N]."""
     if x is None or x.dim() < 1 or weight is None or weight.dim() != 2:
         raise ValueError("x must be [..., K] and weight [N, K]")
-    K, N = x.shape[-1], weight.shape[0]
-    rows, nb = x.shape[:-1].numel(), (K + 127) // 128
-    _need(x, E4M3, x.shape, "x")
+    xshape, (N, K) = x.shape, weight.shape
+    rows, nb = xshape[0] if len(xshape) == 2 else xshape[:-1].numel(), (K + 127) // 128
+    _need(x, E4M3, xshape[:-1] + (K,) if xshape[-1] != K else xshape, "x")
     _need(weight, E4M3, (N, K), "weight")
-    blocks = x_scale.shape[1] if x_scale is not None and x_scale.dim() == 2 and x_scale.shape[1] == 1 else nb
+    blocks = 1 if x_scale is not None and x_scale.dim() == 2 and x_scale.shape[1] == 1 else nb
     _need(x_scale, torch.float32, (rows, blocks), "x_scale")
     _need(weight_scale, torch.float32, ((N + 127) // 128, nb), "weight_scale")
-    _opt(bias, torch.float32, (N,), "bias")
-    shape = x.shape[:-1] + (N,)
+    if bias is not None:
+        _need(bias, torch.float32, (N,), "bias")
+    shape = (rows, N) if len(xshape) == 2 else xshape[:-1] + (N,)
     y = torch.empty(shape, dtype=torch.bfloat16, device=x.device) if out is None else _need(out, torch.bfloat16, shape, "out")
     rc = _lib().gdr_linear_e4m3(rows, K, N, x.data_ptr(), x_scale.data_ptr(), blocks, weight.data_ptr(),
                                 weight_scale.data_ptr(), _ptr(bias), y.data_ptr(),

@@ -63,6 +63,24 @@ def test_quant_rows_and_tiles(R, C, dtype):
     assert torch.equal(b["y_t"].view(torch.uint8), b["y"].view(torch.uint8).t()) and torch.equal(b["scale_t"], b["scale"].t())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quant_codes_are_those_of_the_division(dtype):
+    """Code for code, also on ties (which ratios of bf16 numbers often are): the fp32 quotient, rounded to e4m3; scales
+    of every size, down to where quotients of subnormal numbers are taken."""
+    gen = torch.Generator().manual_seed(9)
+    x = torch.randn(4096, 256, generator=gen) * torch.exp2(torch.linspace(-140, 110, 4096))[:, None]
+    x[::7] = torch.round(x[::7] / x[::7].abs().amax(1, keepdim=True) * 64)
+    x = x.to(dtype).cuda()
+    for tiles in (False, True):
+        q = gdr.quant_e4m3(x, tiles=tiles)
+        s = q["scale"].repeat_interleave(128, dim=1)
+        s = s.repeat_interleave(128, dim=0) if tiles else s
+        # (float64 division of float32 numbers, rounded to float32, is the float32 division; scales that are subnormal
+        # numbers are rounded so far that quotients pass 448, where the codes end)
+        want = (x.double() / s.double()).float().clamp(-448, 448).to(E4M3)
+        assert torch.equal(q["y"].view(torch.uint8), want.view(torch.uint8))
+
+
 def test_quant_slices_shapes_and_zeros():
     wide = _matrix(40, 500, 1, BF16)
     for a, b in ((0, 256), (6, 300), (2, 4)):
