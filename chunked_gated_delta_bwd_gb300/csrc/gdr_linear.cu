@@ -4,7 +4,7 @@
 //
 // The scales are any fp32 numbers, so the tensor cores cannot apply them: each block's product (four
 // steps of 32 of the inner dimension) goes into tensor memory by itself, and groups of threads add it, times its scale,
-// to sums in fp32 registers while the next block's product runs into the other half of the tensor memory.
+// to sums in fp32 registers while the next blocks' products run into other columns of the tensor memory.
 //
 // Two forms, the same loop:
 //   rows of x as the product's rows  (many rows of x): a thread holds one row, its scale is one number; blocks
@@ -33,9 +33,12 @@ struct Lin {
     static constexpr int oStore = STAGES * STAGE;  // (rows of x: a 128 x 64 bf16 tile for each group)
     static constexpr int oScale = oStore + (X_ROWS ? GROUPS * 16384 : 0);
     static constexpr int oBar = oScale + (X_ROWS ? 0 : 2 * 8 * BN * 4);
-    static constexpr int BARS = 2 * STAGES + 10;
+    // accumulators in tensor memory (with two, what a block's product takes from its issue to its sums is not hidden
+    // where products are short: 1024 x 4096 x 2048 took 15.8 us)
+    static constexpr int BUFS = BN == 256 ? 2 : 4;
+    static constexpr int BARS = 2 * STAGES + 2 * BUFS + 6;
     static constexpr int SMEM = oBar + 8 * BARS + 8 + 1024;
-    static constexpr int TMEM = 2 * BN < 32 ? 32 : 2 * BN;
+    static constexpr int TMEM = BUFS * BN;
     static constexpr bool MOVE_REGS = BN == 256;  // 64 x 128 + 216 x 256 registers out of the launch's 168 x 384
 };
 
@@ -79,12 +82,15 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     const uint32_t bar0 = sb + L::oBar;
     auto full = [&](int s) { return bar0 + 8 * s; };
     auto empty = [&](int s) { return bar0 + 8 * (L::STAGES + s); };
-    const uint32_t t_full = bar0 + 16 * L::STAGES, t_empty = t_full + 16, sc_full = t_full + 32, sc_empty = t_full + 48, ended = t_full + 64;
+    const uint32_t t_full = bar0 + 16 * L::STAGES, t_empty = t_full + 8 * L::BUFS, sc_full = t_empty + 8 * L::BUFS, sc_empty = sc_full + 16,
+                   ended = sc_empty + 16;
     if (tid == 0) {
         for (int i = 0; i < 2 * L::STAGES; ++i) tc::mbar_init(bar0 + 8 * i, 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < L::BUFS; ++i) {
             tc::mbar_init(t_full + 8 * i, 1);
             tc::mbar_init(t_empty + 8 * i, 4 * L::GROUPS);
+        }
+        for (int i = 0; i < 2; ++i) {
             tc::mbar_init(sc_full + 8 * i, 32);
             tc::mbar_init(sc_empty + 8 * i, 4 * L::GROUPS);
         }
@@ -150,20 +156,19 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     } else if (warp == 1 || warp == 3) {
         // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
         // A warp that waits, commits or fences issues no product (60 to 120 cycles each, 400 a block of 128, against 512
-        // for its products, and products do not queue up): two take the blocks in turn, each with its half of the
-        // tensor memory.
+        // for its products of 128 x 256, and products do not queue up): two take the blocks in turn.
         constexpr uint32_t id = tc::idesc_e4m3(128, BN);
         const uint32_t on = lane == 0;
-        const int b = warp == 3;
+        const int mine = warp == 3;
         int l = 0;
         bool fine = true;
 #pragma unroll 1
         for (int t = first; t < tiles && fine; t += step) {
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                if ((l & 1) != b) continue;
-                const int s = l % L::STAGES;
-                fine = (l < 2 || wait_warp(t_empty + 8 * b, (l >> 1 & 1) ^ 1)) && wait_warp(full(s), l / L::STAGES & 1);
+                if ((l & 1) != mine) continue;
+                const int s = l % L::STAGES, b = l % L::BUFS;
+                fine = (l < L::BUFS || wait_warp(t_empty + 8 * b, (l / L::BUFS & 1) ^ 1)) && wait_warp(full(s), l / L::STAGES & 1);
                 if (!fine) break;
                 tc::fence_after();
                 const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
@@ -174,8 +179,8 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             }
         }
         if (!fine) {
-            tc::commit_if(on, ended + 8 * b);
-            tc::mbar_wait(ended + 8 * b, 0);
+            tc::commit_if(on, ended + 8 * mine);
+            tc::mbar_wait(ended + 8 * mine, 0);
         }
     } else if (warp == 2 && !X_ROWS) {
         // ---------------- scales of the columns, eight blocks at a time ----------------
@@ -221,12 +226,12 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             float next = X_ROWS ? scale_at(kb0) : 0.f;
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                const int b = l & 1;
+                const int b = l % L::BUFS;
                 const float s = next;
                 if (X_ROWS) next = scale_at(kb + 1);
                 const float* sc = reinterpret_cast<const float*>(smem + L::oScale) + (u & 1) * 8 * BN + ((kb - kb0) & 7) * BN;
                 if (!X_ROWS && ((kb - kb0) & 7) == 0) wait_warp(sc_full + 8 * (u & 1), u >> 1 & 1);
-                wait_warp(t_full + 8 * b, l >> 1 & 1);
+                wait_warp(t_full + 8 * b, l / L::BUFS & 1);
                 tc::fence_after();
                 // (64 columns asked for at once, and the buffer given back before the last ones are added: what bounds the
                 // loop is how soon the next product may have it)
@@ -311,13 +316,15 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         if (split > 1) cluster_sync();
         else __syncthreads();
         const int a0 = first / tiles_b * 128, b0 = first % tiles_b * BN;
-        auto total = [&](int word) {
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 1
-            for (int r = 0; r < split; ++r) {
-                const float4 v = split > 1 ? ld_peer(sb + 4 * word, r) : *reinterpret_cast<const float4*>(smem + 4 * word);
-                s = make_float4(s.x + v.x, s.y + v.y, s.z + v.z, s.w + v.w);
-            }
+        auto total = [&](int word) {  // (all parts asked for before any is added)
+            float4 v[8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r)
+                if (r < split) v[r] = split > 1 ? ld_peer(sb + 4 * word, r) : *reinterpret_cast<const float4*>(smem + 4 * word);
+            float4 s = v[0];
+#pragma unroll
+            for (int r = 1; r < 8; ++r)
+                if (r < split) s = make_float4(s.x + v[r].x, s.y + v[r].y, s.z + v[r].z, s.w + v[r].w);
             return s;
         };
         auto put = [&](int64_t m, int n, const float4& s) {
@@ -346,21 +353,58 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     if (warp == 0) tc::dealloc(tmem, L::TMEM);
 }
 
+// Clusters of `split` blocks of a kernel that the device holds at once (asked once a device).
 template <bool X_ROWS, int BN>
-cudaError_t go(const LinearParams& p, int split, cudaStream_t s) {
+int clusters_at_once(int split) {
+    using L = Lin<X_ROWS, BN>;
+    static int known[64][4];
+    int dev = 0, which = split == 1 ? 0 : split == 2 ? 1 : split == 4 ? 2 : 3;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+    if (known[dev][which]) return known[dev][which];
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split);
+    cfg.blockDim = dim3(L::THREADS);
+    cfg.dynamicSmemBytes = L::SMEM;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = split;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, k_linear<X_ROWS, BN>, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        n = 0;
+    }
+    return known[dev][which] = n > 0 ? n : 1;
+}
+
+// Blocks that share a tile's inner dimension: as many as leave all tiles in place at once (a second round would cost what
+// the split gains: 128 x 2048 x 6144 in 48 clusters of four 17 us, of two 10), at most 8, two blocks of 128 each at least.
+template <bool X_ROWS, int BN>
+int split_of(int64_t tiles, int K) {
+    const int nkb = (K + KB - 1) / KB;
+    int s = 1;
+    while (s < 8 && 4 * s <= nkb && tiles <= clusters_at_once<X_ROWS, BN>(2 * s)) s *= 2;
+    return s;
+}
+
+template <bool X_ROWS, int BN>
+cudaError_t go(const LinearParams& p, cudaStream_t s) {
     using L = Lin<X_ROWS, BN>;
     Maps maps;
     memset(&maps, 0, sizeof(maps));
     const int a_rows = X_ROWS ? (int)p.M : p.N, b_rows = X_ROWS ? p.N : (int)p.M;
     if (!encode_bytes_map(&maps.a, X_ROWS ? p.x : p.w, a_rows, p.K, 128) || !encode_bytes_map(&maps.b, X_ROWS ? p.w : p.x, b_rows, p.K, BN))
         return cudaErrorInvalidValue;
-    if (X_ROWS && split == 1 && !encode_rows_map(&maps.y, p.y, p.M, p.N, 128)) return cudaErrorInvalidValue;
     const int tiles_b = (b_rows + BN - 1) / BN;
     const int64_t tiles = (int64_t)((a_rows + 127) / 128) * tiles_b;
     if (tiles > (1 << 30) / 8) return cudaErrorInvalidValue;
     static bool allowed[64];
     cudaError_t e = allow_smem((const void*)k_linear<X_ROWS, BN>, L::SMEM, allowed);
     if (e != cudaSuccess) return e;
+    const int split = BN == 256 ? 1 : split_of<X_ROWS, BN>(tiles, p.K);
+    if (X_ROWS && split == 1 && !encode_rows_map(&maps.y, p.y, p.M, p.N, 128)) return cudaErrorInvalidValue;
     if (L::MOVE_REGS) {  // (the groups' shares of the registers have to be there at the launch)
         static const int regs = [] {
             cudaFuncAttributes at;
@@ -383,26 +427,14 @@ cudaError_t go(const LinearParams& p, int split, cudaStream_t s) {
     return cudaLaunchKernelEx(&cfg, k_linear<X_ROWS, BN>, maps, p, tiles_b, (int)tiles, split);
 }
 
-// blocks of the inner dimension's split for `tiles` tiles: as many as fill the multiprocessors, at most 8, two blocks of 128 each at least
-int split_of(int64_t tiles, int K) {
-    const int nkb = (K + KB - 1) / KB;
-    int s = 1;
-    while (s < 8 && 2 * s * tiles <= num_sms() + num_sms() / 2 && 4 * s <= nkb) s *= 2;
-    return s;
-}
-
 }  // namespace
 
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s) {
-    const int64_t n128 = (p.N + 127) / 128, m128 = (p.M + 127) / 128;
-    if (p.M <= 64) {
-        const int split = split_of(n128, p.K);
-        if (p.M <= 16) return go<false, 16>(p, split, s);
-        if (p.M <= 32) return go<false, 32>(p, split, s);
-        return go<false, 64>(p, split, s);
-    }
-    if (m128 * ((p.N + 255) / 256) >= num_sms()) return go<true, 256>(p, 1, s);
-    return go<true, 128>(p, split_of(m128 * n128, p.K), s);
+    if (p.M <= 16) return go<false, 16>(p, s);
+    if (p.M <= 32) return go<false, 32>(p, s);
+    if (p.M <= 64) return go<false, 64>(p, s);
+    if ((p.M + 127) / 128 * ((p.N + 255) / 256) >= num_sms()) return go<true, 256>(p, s);
+    return go<true, 128>(p, s);
 }
 
 }  // namespace gdr
