@@ -29,9 +29,9 @@ template <bool X_ROWS, int BN>
 struct Lin {
     static constexpr int GROUPS = BN >= 128 ? 2 : 1, COLS = BN / GROUPS, THREADS = 128 + 128 * GROUPS;
     static constexpr int A = 128 * KB, B = BN * KB, STAGE = A + B;
-    static constexpr int STAGES = BN == 256 ? 4 : BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 5 : 6;
-    static constexpr int oStore = STAGES * STAGE;  // (rows of x: a 128 x 64 bf16 tile for each group)
-    static constexpr int oScale = oStore + (X_ROWS ? GROUPS * 16384 : 0);
+    static constexpr int STAGES = BN == 256 ? 3 : BN == 128 ? 6 : BN == 64 ? 8 : BN == 32 ? 5 : 6;
+    static constexpr int oStore = STAGES * STAGE;  // (rows of x: 128 x 64 bf16 tiles, COLS / 64 for each group)
+    static constexpr int oScale = oStore + (X_ROWS ? BN / 64 * 16384 : 0);
     static constexpr int oBar = oScale + (X_ROWS ? 0 : 2 * 8 * BN * 4);
     // accumulators in tensor memory (with two, what a block's product takes from its issue to its sums is not hidden
     // where products are short: 1024 x 4096 x 2048 took 15.8 us)
@@ -213,6 +213,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         const int q4 = warp & 3, group = (warp - 4) >> 2, i = 32 * q4 + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + group * COLS;
         int l = 0, u = 0;
+        bool there = false;  // the next block's product has been seen to be done
 #pragma unroll 1
         for (int t = first; t < tiles; t += step) {
             const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
@@ -222,16 +223,22 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             const int64_t row = (int64_t)a0 + i;
             const float* xs = X_ROWS && row < p.M ? p.xs + row * p.x_blocks : nullptr;
             const float* ws = p.ws + (int64_t)min((b0 + group * COLS) / 128, (p.N - 1) / 128) * nkb;
-            auto scale_at = [&](int kb) { return xs && kb < kb1 ? __ldg(xs + (p.x_blocks > 1 ? kb : 0)) * __ldg(ws + kb) : 0.f; };
-            float next = X_ROWS ? scale_at(kb0) : 0.f;
+            // the two factors of a block's scale, asked for two blocks ahead and multiplied when they are wanted (a product of
+            // look-ups that are still on their way stops the thread: 400 of 700 cycles a block)
+            auto scales_at = [&](int kb) {
+                return xs && kb < kb1 ? make_float2(__ldg(xs + (p.x_blocks > 1 ? kb : 0)), __ldg(ws + kb)) : make_float2(0.f, 0.f);
+            };
+            float2 next = make_float2(0.f, 0.f), then = next;
+            if (X_ROWS) next = scales_at(kb0), then = scales_at(kb0 + 1);
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
                 const int b = l % L::BUFS;
-                const float s = next;
-                if (X_ROWS) next = scale_at(kb + 1);
+                const float s = next.x * next.y;
+                next = then;
+                if (X_ROWS) then = scales_at(kb + 2);
                 const float* sc = reinterpret_cast<const float*>(smem + L::oScale) + (u & 1) * 8 * BN + ((kb - kb0) & 7) * BN;
                 if (!X_ROWS && ((kb - kb0) & 7) == 0) wait_warp(sc_full + 8 * (u & 1), u >> 1 & 1);
-                wait_warp(t_full + 8 * b, l / L::BUFS & 1);
+                if (!there) wait_warp(t_full + 8 * b, l / L::BUFS & 1);
                 tc::fence_after();
                 // (64 columns asked for at once, and the buffer given back before the last ones are added: what bounds the
                 // loop is how soon the next product may have it)
@@ -247,6 +254,9 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                         tc::fence_before();
                         __syncwarp();
                         if (lane == 0) tc::mbar_arrive(t_empty + 8 * b);
+                        // (looked at now, decided on when the last columns have been added: 5% of narrow tiles' time; with 256
+                        // columns it costs 8%)
+                        if (BN < 256) there = tc::mbar_test(t_full + 8 * ((l + 1) % L::BUFS), (l + 1) / L::BUFS & 1);
                     }
 #pragma unroll
                     for (int j = 0; j < PART; j += 4) {
@@ -257,6 +267,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                         ACC2(acc, c + j + 2, __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), make_float2(f.z, f.w), F2(acc, c + j + 2)));
                     }
                 }
+                if (BN < 256) there = __all_sync(~0u, there);
                 if (!X_ROWS && (((kb - kb0) & 7) == 7 || kb + 1 == kb1)) {
                     if (lane == 0) tc::mbar_arrive(sc_empty + 8 * (u & 1));
                     ++u;
@@ -267,34 +278,33 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 for (int j = 0; j < COLS; ++j) acc[j] = __int_as_float(0x7fffffff);
             }
             if (X_ROWS && split == 1) {
-                // out through a 128 x 64 tile for each group (what lies outside y is cut off by the copy)
-                unsigned char* stage = smem + L::oStore + group * 16384;
+                // out through 128 x 64 tiles in shared memory, which the copies have left by the next time (what lies
+                // outside y is cut off by the copy)
+                unsigned char* stage = smem + L::oStore + group * (COLS / 64) * 16384;
+                const int n0 = b0 + group * COLS;
+                if (i == 0) tc::bulk_wait_read();
+                tc::named_sync(1 + group, 128);
 #pragma unroll
-                for (int c = 0; c < COLS; c += 64) {
-                    if (i == 0) tc::bulk_wait_read();
-                    tc::named_sync(1 + group, 128);
-                    const int n0 = b0 + group * COLS + c;
+                for (int j = 0; j < COLS / 8; ++j) {
+                    float* a = acc + 8 * j;
+                    if (p.bias) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        if (p.bias) {
-#pragma unroll
-                            for (int h = 0; h < 8; h += 4) {
-                                if (n0 + 8 * j + h >= p.N) continue;
-                                const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + n0 + 8 * j + h));
-                                float* a = acc + c + 8 * j + h;
-                                a[0] += f.x, a[1] += f.y, a[2] += f.z, a[3] += f.w;
-                            }
+                        for (int h = 0; h < 8; h += 4) {
+                            if (n0 + 8 * j + h >= p.N) continue;
+                            const float4 f = __ldg(reinterpret_cast<const float4*>(p.bias + n0 + 8 * j + h));
+                            a[h] += f.x, a[h + 1] += f.y, a[h + 2] += f.z, a[h + 3] += f.w;
                         }
-                        const float* a = acc + c + 8 * j;
-                        *reinterpret_cast<uint4*>(stage + tc::sw_chunk(i, j, 128)) =
-                            make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
                     }
-                    tc::fence_async_smem();
-                    tc::named_sync(1 + group, 128);
-                    if (i == 0 && n0 < p.N) {
-                        tc::tma_store_2d(&maps.y, n0, a0, smem_u32(stage));
-                        tc::bulk_commit();
-                    }
+                    *reinterpret_cast<uint4*>(stage + tc::sw_chunk(i, j, 128)) =
+                        make_uint4(pack_bf16(a[0], a[1]), pack_bf16(a[2], a[3]), pack_bf16(a[4], a[5]), pack_bf16(a[6], a[7]));
+                }
+                tc::fence_async_smem();
+                tc::named_sync(1 + group, 128);
+                if (i == 0) {
+#pragma unroll
+                    for (int c = 0; c < COLS; c += 64)
+                        if (n0 + c < p.N) tc::tma_store_2d(&maps.y, n0 + c, a0, smem_u32(stage) + c / 64 * 16384);
+                    tc::bulk_commit();
                 }
             } else {
                 // the part of this block, for the cluster (the tiles' memory is free: this is the block's only tile)
