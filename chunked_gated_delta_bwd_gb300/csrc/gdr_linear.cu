@@ -214,22 +214,28 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         const uint32_t lanes = tmem + ((uint32_t)(32 * q4) << 16) + group * COLS;
         int l = 0, u = 0;
         bool there = false;  // the next block's product has been seen to be done
+        // The two factors of a block's scale, asked for two blocks ahead (a tile's first ones before the last tile's outputs
+        // are written) and multiplied when they are wanted: a product of look-ups that are still on their way stops
+        // the thread (400 of 700 cycles a block).
+        const float *xs = nullptr, *ws = nullptr;
+        float2 next = make_float2(0.f, 0.f), then = next;
+        auto scales_at = [&](int kb) {
+            return xs && kb < kb1 ? make_float2(__ldg(xs + (p.x_blocks > 1 ? kb : 0)), __ldg(ws + kb)) : make_float2(0.f, 0.f);
+        };
+        auto begin = [&](int t) {
+            if (!X_ROWS || t >= tiles) return;
+            const int64_t row = (int64_t)(t / tiles_b) * 128 + i;
+            xs = row < p.M ? p.xs + row * p.x_blocks : nullptr;
+            ws = p.ws + (int64_t)min((t % tiles_b * BN + group * COLS) / 128, (p.N - 1) / 128) * nkb;
+            next = scales_at(kb0), then = scales_at(kb0 + 1);
+        };
+        begin(first);
 #pragma unroll 1
         for (int t = first; t < tiles; t += step) {
             const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
             float acc[COLS];
 #pragma unroll
             for (int j = 0; j < COLS; ++j) acc[j] = 0.f;
-            const int64_t row = (int64_t)a0 + i;
-            const float* xs = X_ROWS && row < p.M ? p.xs + row * p.x_blocks : nullptr;
-            const float* ws = p.ws + (int64_t)min((b0 + group * COLS) / 128, (p.N - 1) / 128) * nkb;
-            // the two factors of a block's scale, asked for two blocks ahead and multiplied when they are wanted (a product of
-            // look-ups that are still on their way stops the thread: 400 of 700 cycles a block)
-            auto scales_at = [&](int kb) {
-                return xs && kb < kb1 ? make_float2(__ldg(xs + (p.x_blocks > 1 ? kb : 0)), __ldg(ws + kb)) : make_float2(0.f, 0.f);
-            };
-            float2 next = make_float2(0.f, 0.f), then = next;
-            if (X_ROWS) next = scales_at(kb0), then = scales_at(kb0 + 1);
 #pragma unroll 1
             for (int kb = kb0; kb < kb1; ++kb, ++l) {
                 const int b = l % L::BUFS;
@@ -273,6 +279,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                     ++u;
                 }
             }
+            begin(t + step);
             if (!ok()) {
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) acc[j] = __int_as_float(0x7fffffff);
