@@ -51,7 +51,9 @@ struct Cfg {
     static constexpr int oHi = SLOTS * TILE, oLo = oHi + TILE, oS = oLo + TILE, oTab = oS + D * D * 2;
     // (the product Y'^T Z has 128 rows; with 64 channels the upper ones read what lies behind the tile)
     static constexpr int oEnd = (oTab + 512 > oLo + 2 * CHUNK * 128 ? oTab + 512 : oLo + 2 * CHUNK * 128);
-    static constexpr int oBar = oEnd, BARS = 2 * SLOTS + 11 + 2 * NX;
+    // (an fp32 output is twice X's tile: with 64 channels there is room for it, with 128 one half goes out after the other)
+    static constexpr int oWide = (oEnd + 1023) / 1024 * 1024;
+    static constexpr int oBar = D == 64 ? oWide + 2 * TILE : oEnd, BARS = 2 * SLOTS + 11 + 2 * NX;
     static constexpr int SMEM = oBar + 8 * BARS + 1024;
     static constexpr int THREADS = 640;  // a warpgroup of single threads' roles, two each for groups A and B
     static constexpr int REGS = 96, REGS_1 = 80, REGS_B = 104;  // at the launch (and group A), of the single threads, of group B
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         tc::mbar_init(s_free, 1);
         tc::mbar_init(y_ready, 8);
         tc::mbar_init(d_full, 1);
-        for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_init(staged(0, 0) + 8 * i, wide ? 4 : 8);
+        for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_init(staged(0, 0) + 8 * i, wide && D == 128 ? 4 : 8);
         tc::mbar_init(half_out, 1);
         tc::mbar_init(ended, 1);
         tc::mbar_init(ended_3, 1);
@@ -354,21 +356,31 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             for (int it = 0;; ++it) {
                 const uint32_t X = sb + slot_x(it) * K::TILE;
                 if (wide) {
-                    // fp32, half of the columns at a time: each fills X's tile
                     if (!wait(staged(it, 0), turn(it, K::NX))) break;
                     const Chunk now = chunk_at(chunks, it);
                     const bool whole = now.tokens() == CHUNK;
-                    auto put = [&](int half) {
-                        if (!whole) return;
-                        tc::tma_store_4d(&w.out, 0, now.head, now.t0, half * (D / 64), X);
+                    auto put = [&](int half, uint32_t from) {
+                        if (whole) tc::tma_store_4d(&w.out, 0, now.head, now.t0, half * (D / 64), from);
+                    };
+                    auto out = [&]() {
                         tc::bulk_commit();
                         tc::bulk_wait_read();
+                        tc::mbar_arrive(half_out);
                     };
-                    put(0);
-                    tc::mbar_arrive(half_out);
-                    if (!wait(staged(it, 1), turn(it, K::NX))) break;
-                    put(1);
-                    tc::mbar_arrive(empty(slot_x(it)));
+                    if (D == 64) {
+                        tc::mbar_arrive(empty(slot_x(it)));
+                        put(0, sb + K::oWide);
+                        put(1, sb + K::oWide + K::TILE);
+                        out();
+                    } else {
+                        put(0, X);
+                        out();
+                        if (!wait(staged(it, 1), turn(it, K::NX))) break;
+                        put(1, X);
+                        tc::bulk_commit();
+                        tc::bulk_wait_read();
+                        tc::mbar_arrive(empty(slot_x(it)));
+                    }
                     if (now.last()) break;
                     continue;
                 }
@@ -464,10 +476,11 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
 
             float r = r_full;
             if (back && rows < CHUNK) r = i < rows ? w.o_scale * power(g, rows - 1 - i) : 0.f;
-            unsigned char* stage = smem + slot_x(it) * K::TILE;
+            unsigned char* stage = smem + (wide && D == 64 ? K::oWide + half * K::TILE : slot_x(it) * K::TILE);
             const int64_t row = (int64_t)now.t0 + i;
             if (!wait.warp(o_full, ph)) break;
-            if (wide && half == 1 && !wait.warp(half_out, ph)) break;  // (the first half has left X's tile)
+            // (a wide output's first half has left X's tile; the last chunk's output has left its own)
+            if (wide && (D == 64 ? it && !wait.warp(half_out, ph ^ 1) : half == 1 && !wait.warp(half_out, ph))) break;
             tc::fence_after();
 #pragma unroll 1
             for (int c = 0; c < HALF; c += 16) {
@@ -501,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             tc::fence_before();
             warp_arrive(o_free);
             tc::fence_async_smem();
-            warp_arrive(staged(it, wide ? half : 0));
+            warp_arrive(staged(it, wide && D == 128 ? half : 0));
             if (now.last()) break;
         }
     } else {
@@ -880,18 +893,20 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
     }
 }
 
-// the gradients of shared heads: sums over the value heads of a group
-__global__ void __launch_bounds__(256) k_dla_groups(const float* a, __nv_bfloat16* out, int64_t pairs, int group, int D) {
+// The gradients of shared heads: sums over the value heads of a group, in fp32; dq and dk (blockIdx.y), four channels a thread.
+__global__ void __launch_bounds__(256) k_dla_groups(const float* dq_heads, const float* dk_heads, __nv_bfloat16* dq, __nv_bfloat16* dk, int64_t quads,
+                                                    int group, int D) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= pairs) return;
-    const int64_t row = i * 2 / D;  // (token, k head)
-    const float* from = a + row * group * D + (i * 2 - row * D);
-    float2 s = make_float2(0.f, 0.f);
-    for (int j = 0; j < group; ++j) {
-        const float2 u = *reinterpret_cast<const float2*>(from + (int64_t)j * D);
-        s = make_float2(s.x + u.x, s.y + u.y);
+    if (i >= quads) return;
+    const int per = D / 4;
+    const int64_t row = i / per;  // (token, k head)
+    const float* from = (blockIdx.y ? dk_heads : dq_heads) + (row * group * per + (i - row * per)) * 4;
+    float4 s = *reinterpret_cast<const float4*>(from);
+    for (int j = 1; j < group; ++j) {
+        const float4 u = *reinterpret_cast<const float4*>(from + (int64_t)j * D);
+        s = make_float4(s.x + u.x, s.y + u.y, s.z + u.z, s.w + u.w);
     }
-    reinterpret_cast<uint32_t*>(out)[i] = pack_bf16(s.x, s.y);
+    reinterpret_cast<uint2*>(blockIdx.y ? dk : dq)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
 // How a call's chunks are shared out: the number of ranges (of each walk), whether they end with whole chains, and
@@ -907,7 +922,21 @@ Shares shares_of(const DlaParams& p, int walks) {
     int64_t fit = sms / walks > 0 ? sms / walks : 1;
     if (longest <= 4) return {(int)(chains < fit ? chains : fit), 1, 1};
     const int64_t ranges = (most + 3) / 4;  // of at least four chunks
-    return {(int)(ranges < fit ? ranges : fit), 0, chains > fit ? 4 : 1};
+    Shares sh{(int)(ranges < fit ? ranges : fit), 0, 1};
+    // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and four short blocks each
+    // even that out; else as many as leave the fewest rounds of blocks (three for the backward's two sums of 49
+    // ranges each: two rounds of a third, 105 -> 75 us at T = 32768, 16 heads).
+    if (chains > fit) {
+        sh.pieces = 4;
+    } else {
+        const int blocks = (sh.ranges - 1) * (walks == 1 ? 1 : 2);
+        double best = 1e9;
+        for (int n = 1; n <= 4; ++n) {
+            const double rounds = (double)((blocks * n + sms - 1) / sms) / n + 0.02 * n;
+            if (rounds < best) best = rounds, sh.pieces = n;
+        }
+    }
+    return sh;
 }
 
 // Launches a kernel whose blocks may be in place before the kernel ahead of it has ended: it waits for that one itself
@@ -1009,10 +1038,8 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
     t.w[1] = TailWalk{dv.Y, dv.Z, dv.gy, dv.gz, 1, p.scale, back, p.dht};
     cudaError_t e = go<D, 3, 2>(p, sh, w, t, s);
     if (e != cudaSuccess || !p.dq_heads) return e;
-    const int64_t pairs = p.T * p.Hk * D / 2;
-    const unsigned grid = (unsigned)((pairs + 255) / 256);
-    k_dla_groups<<<grid, 256, 0, s>>>(p.dq_heads, p.dq, pairs, p.H / p.Hk, D);
-    k_dla_groups<<<grid, 256, 0, s>>>(p.dk_heads, p.dk, pairs, p.H / p.Hk, D);
+    const int64_t quads = p.T * p.Hk * D / 4;
+    k_dla_groups<<<dim3((unsigned)((quads + 255) / 256), 2), 256, 0, s>>>(p.dq_heads, p.dk_heads, p.dq, p.dk, quads, p.H / p.Hk, D);
     return cudaGetLastError();
 }
 
@@ -1024,7 +1051,7 @@ size_t dla_states_bytes(const DlaParams& p, bool backward) {
 }
 int dla_kernels(const DlaParams& p, bool backward) {
     const Shares sh = shares_of(p, backward ? 3 : 1);
-    return (sh.snap || sh.ranges < 2 ? 1 : 3) + (backward && p.H != p.Hk ? 2 : 0);
+    return (sh.snap || sh.ranges < 2 ? 1 : 3) + (backward && p.H != p.Hk ? 1 : 0);
 }
 
 cudaError_t launch_dla_fwd(const DlaParams& p, cudaStream_t s) { return p.D == 64 ? forward<64>(p, s) : forward<128>(p, s); }
