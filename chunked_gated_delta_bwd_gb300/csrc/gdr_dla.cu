@@ -227,27 +227,28 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                    half_out = more_bars + 64, ended = more_bars + 72, ended_3 = more_bars + 80 + 16 * K::NX;
     // (group A may be chunks ahead of the stores: a barrier for each of X's slots, and each half of a wide output)
     auto staged = [&](int it, int half) { return more_bars + 80 + 16 * slot_x(it) + 8 * half; };
-    if (tid == 0) {
+    if (tid == 64) {  // (beside the warp that makes the plan)
         // (Y's slots are given back by P's product and by group B's eight warps, Z's by the products of both issuers)
         for (int i = 0; i < K::SLOTS; ++i) {
-            tc::mbar_init(full(i), 1);
-            tc::mbar_init(empty(i), i < K::NX ? 1 : i < K::NX + K::NY ? 9 : 2);
+            tc::mbar_set(full(i), 1);
+            tc::mbar_set(empty(i), i < K::NX ? 1 : i < K::NX + K::NY ? 9 : 2);
         }
-        tc::mbar_init(p_full, 1);
-        tc::mbar_init(p_ready, 8);
-        tc::mbar_init(o_full, 2);  // P Z and X C
-        tc::mbar_init(o_free, 8);
-        tc::mbar_init(s_ready, 8);
-        tc::mbar_init(s_free, 1);
-        tc::mbar_init(y_ready, 8);
-        tc::mbar_init(d_full, 1);
-        for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_init(staged(0, 0) + 8 * i, wide && D == 128 ? 4 : 8);
-        tc::mbar_init(half_out, 1);
-        tc::mbar_init(ended, 1);
-        tc::mbar_init(ended_3, 1);
+        tc::mbar_set(p_full, 1);
+        tc::mbar_set(p_ready, 8);
+        tc::mbar_set(o_full, 2);  // P Z and X C
+        tc::mbar_set(o_free, 8);
+        tc::mbar_set(s_ready, 8);
+        tc::mbar_set(s_free, 1);
+        tc::mbar_set(y_ready, 8);
+        tc::mbar_set(d_full, 1);
+        for (int i = 0; i < 2 * K::NX; ++i) tc::mbar_set(staged(0, 0) + 8 * i, wide && D == 128 ? 4 : 8);
+        tc::mbar_set(half_out, 1);
+        tc::mbar_set(ended, 1);
+        tc::mbar_set(ended_3, 1);
+        tc::mbar_set_fence();
         gone_s = 0;
     }
-    if (warp == 0) tc::alloc(smem_u32(&tslot), 512);
+    if (warp == 1) tc::alloc(smem_u32(&tslot), 512);
     make_plan<K::THREADS>(line, range, p.ranges, p.snap, &plan_s, scratch);
     tc::fence_before();
     __syncthreads();
@@ -394,7 +395,6 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 tc::mbar_arrive(empty(slot_x(it)));
                 if (now.last()) break;
             }
-            tc::bulk_wait_all();
         }
     } else if (warp < 12) {
         // ---------------- group A: P, outputs ----------------
@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) tc::dealloc(tmem, 512);
+    if (warp == 1) tc::dealloc(tmem, 512);
 }
 
 struct TailWalk {
@@ -704,15 +704,16 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
     auto empty = [&](int slot) { return bar0 + 8 * (K::RING + slot); };
     const uint32_t y_ready = bar0 + 16 * K::RING, d_full = y_ready + 16 /* two each */, ended = d_full + 16;
     if (tid == 0) {
-        for (int i = 0; i < 2 * K::RING; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+        for (int i = 0; i < 2 * K::RING; ++i) tc::mbar_set(bar0 + 8 * i, 1);
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(y_ready + 8 * i, 8);
-            tc::mbar_init(d_full + 8 * i, 1);
+            tc::mbar_set(y_ready + 8 * i, 8);
+            tc::mbar_set(d_full + 8 * i, 1);
         }
-        tc::mbar_init(ended, 1);
+        tc::mbar_set(ended, 1);
+        tc::mbar_set_fence();
         gone_s = 0;
     }
-    if (warp == 0) tc::alloc(smem_u32(&tslot), 256);
+    if (warp == 1) tc::alloc(smem_u32(&tslot), 256);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -823,7 +824,7 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) tc::dealloc(tmem, 256);
+    if (warp == 1) tc::dealloc(tmem, 256);
 }
 
 // The states at the beginnings of ranges that begin inside a chain, in the place of the first piece of the sum of

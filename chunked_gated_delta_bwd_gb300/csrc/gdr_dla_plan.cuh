@@ -68,7 +68,11 @@ struct Plan {
     Place at;     // its first chunk
 };
 
-__device__ __forceinline__ int range_begin(int total, int r, int ranges) { return (int)((int64_t)total * r / ranges); }
+// total r / ranges, in 32 bits (there are a few hundred ranges at most)
+__device__ __forceinline__ int range_begin(int total, int r, int ranges) {
+    const uint32_t whole = (uint32_t)total / (uint32_t)ranges, rest = (uint32_t)total - whole * ranges;
+    return (int)(whole * r + rest * r / (uint32_t)ranges);
+}
 
 // places of a chain of that many tokens
 __device__ __forceinline__ int places(int64_t tokens) { return tokens > 0 ? (int)((tokens + CHUNK - 1) / CHUNK) + 1 : 0; }
@@ -103,6 +107,27 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
             set_range(out, per * line.N * line.H, range, ranges);
             const int seq = out->f0 / (per * line.H);
             set_first(out, line, seq, seq * per);
+        }
+        __syncthreads();
+    } else if (line.N <= 32) {
+        // one warp, a sequence a lane
+        if (warp == 0) {
+            int64_t begin = 0, end = 0;
+            if (lane < line.N) begin = line.cu[lane], end = line.cu[lane + 1];
+            const int64_t len = end - begin;
+            const bool bad = __any_sync(~0u, lane < line.N && (len < 0 || len > line.T || (lane == 0 && begin != 0) || (lane == line.N - 1 && end != line.T)));
+            const int mine = lane < line.N && !bad ? places(len) : 0;
+            int upto = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int u = __shfl_up_sync(~0u, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const int total = bad ? -1 : __shfl_sync(~0u, upto, 31) * line.H;
+            if (lane == 0) set_range(out, total, range, ranges);
+            __syncwarp();
+            const int at = out->f0 / line.H, before = upto - mine;
+            if (out->f0 < out->f1 && mine && before <= at && at < upto) set_first(out, line, lane, before);
         }
         __syncthreads();
     } else {

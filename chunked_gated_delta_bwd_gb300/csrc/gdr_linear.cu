@@ -85,19 +85,20 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     const uint32_t t_full = bar0 + 16 * L::STAGES, t_empty = t_full + 8 * L::BUFS, sc_full = t_empty + 8 * L::BUFS, sc_empty = sc_full + 16,
                    ended = sc_empty + 16;
     if (tid == 0) {
-        for (int i = 0; i < 2 * L::STAGES; ++i) tc::mbar_init(bar0 + 8 * i, 1);
+        for (int i = 0; i < 2 * L::STAGES; ++i) tc::mbar_set(bar0 + 8 * i, 1);
         for (int i = 0; i < L::BUFS; ++i) {
-            tc::mbar_init(t_full + 8 * i, 1);
-            tc::mbar_init(t_empty + 8 * i, 4 * L::GROUPS);
+            tc::mbar_set(t_full + 8 * i, 1);
+            tc::mbar_set(t_empty + 8 * i, 4 * L::GROUPS);
         }
         for (int i = 0; i < 2; ++i) {
-            tc::mbar_init(sc_full + 8 * i, 32);
-            tc::mbar_init(sc_empty + 8 * i, 4 * L::GROUPS);
+            tc::mbar_set(sc_full + 8 * i, 32);
+            tc::mbar_set(sc_empty + 8 * i, 4 * L::GROUPS);
         }
-        for (int i = 0; i < 2; ++i) tc::mbar_init(ended + 8 * i, 1);
+        for (int i = 0; i < 2; ++i) tc::mbar_set(ended + 8 * i, 1);
+        tc::mbar_set_fence();
         gone_s = 0;
     }
-    if (warp == 0) tc::alloc(smem_u32(&tslot), L::TMEM);
+    if (warp == 1) tc::alloc(smem_u32(&tslot), L::TMEM);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 }
             }
         }
-        if (X_ROWS && split == 1 && i == 0) tc::bulk_wait_all();
+        if (X_ROWS && split == 1 && i == 0) tc::bulk_wait_read();
     }
     __syncwarp();
     if (!X_ROWS || split > 1) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     }
     tc::fence_before();
     __syncthreads();
-    if (warp == 0) tc::dealloc(tmem, L::TMEM);
+    if (warp == 1) tc::dealloc(tmem, L::TMEM);
 }
 
 // Clusters of `split` blocks of a kernel that the device holds at once (asked once a device).

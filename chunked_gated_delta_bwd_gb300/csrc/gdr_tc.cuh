@@ -113,6 +113,12 @@ __device__ __forceinline__ void mbar_init(uint32_t mbar, int count) {
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::);
 }
 
+// The same without the fence, which one thread needs once after all of them (a fence for each of 30 took 700 cycles).
+__device__ __forceinline__ void mbar_set(uint32_t mbar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;\n" ::"r"(mbar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_set_fence() { asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory"); }
+
 // whether the phase `parity` of an mbarrier has completed (waits for a short while, which the hardware chooses)
 __device__ __forceinline__ bool mbar_try(uint32_t mbar, uint32_t parity) {
     uint32_t done;
