@@ -53,7 +53,7 @@ struct Cfg {
     static constexpr int oEnd = (oTab + 512 > oLo + 2 * CHUNK * 128 ? oTab + 512 : oLo + 2 * CHUNK * 128);
     // (an fp32 output is twice X's tile: with 64 channels there is room for it, with 128 one half goes out after the other)
     static constexpr int oWide = (oEnd + 1023) / 1024 * 1024;
-    static constexpr int oBar = D == 64 ? oWide + 2 * TILE : oEnd, BARS = 2 * SLOTS + 11 + 2 * NX;
+    static constexpr int oBar = D == 64 ? oWide + 2 * TILE : oEnd, BARS = 2 * SLOTS + 13 + 2 * NX;
     static constexpr int SMEM = oBar + 8 * BARS + 1024;
     static constexpr int THREADS = 640;  // a warpgroup of single threads' roles, two each for groups A and B
     static constexpr int REGS = 96, REGS_1 = 80, REGS_B = 104;  // at the launch (and group A), of the single threads, of group B
@@ -224,7 +224,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     const uint32_t more_bars = bar0 + 16 * K::SLOTS;
     const uint32_t p_full = more_bars, p_ready = more_bars + 8, o_full = more_bars + 16, o_free = more_bars + 24,
                    s_ready = more_bars + 32, s_free = more_bars + 40, y_ready = more_bars + 48, d_full = more_bars + 56,
-                   half_out = more_bars + 64, ended = more_bars + 72, ended_3 = more_bars + 80 + 16 * K::NX;
+                   half_out = more_bars + 64, ended = more_bars + 72, ended_3 = more_bars + 80 + 16 * K::NX,
+                   tab_free = ended_3 + 8, tab_ready = ended_3 + 16;
     // (group A may be chunks ahead of the stores: a barrier for each of X's slots, and each half of a wide output)
     auto staged = [&](int it, int half) { return more_bars + 80 + 16 * slot_x(it) + 8 * half; };
     if (tid == 64) {  // (beside the warp that makes the plan)
@@ -245,6 +246,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         tc::mbar_set(half_out, 1);
         tc::mbar_set(ended, 1);
         tc::mbar_set(ended_3, 1);
+        tc::mbar_set(tab_free, 8);
+        tc::mbar_set(tab_ready, 8);
         tc::mbar_set_fence();
         gone_s = 0;
     }
@@ -408,6 +411,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         float* tab = reinterpret_cast<float*>(smem + K::oTab);
         float* cols = tab + 64;
         int head = -1;
+        uint32_t tables = 0;  // heads whose tables have been made
         float r_full = 0.f, g = 0.f, rf0 = 0.f, rf1 = 0.f;
 #pragma unroll 1
         for (int it = 0; any; ++it) {
@@ -421,14 +425,17 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 const int n0 = back ? 32 * half - i : i - 32 * half - 31, n1 = back ? n0 + 64 : n0 - 64;
                 rf0 = n0 >= 0 ? power(g, n0) : 0.f;
                 rf1 = n1 >= 0 ? power(g, n1) : 0.f;
-                tc::named_sync(1, 256);
+                // (barriers with bounded waits, as all: a warp that gives up arrives at none)
+                warp_arrive(tab_free);
+                if (!wait.warp(tab_free, tables & 1)) break;
                 if (warp == 4 || warp == 5) {  // 64 entries
                     const int e = 32 * (warp & 1) + lane, n = back ? 31 - e : e - 31;
                     tab[e] = n >= 0 ? w.p_scale * power(g, n) : 0.f;
                 } else if (warp == 6) {
                     cols[lane] = w.p_scale * power(g, back ? lane : 31 - lane);
                 }
-                tc::named_sync(1, 256);
+                warp_arrive(tab_ready);
+                if (!wait.warp(tab_ready, tables++ & 1)) break;
             }
             const int rows = now.tokens();
             if (!wait.warp(p_full, ph)) break;

@@ -66,8 +66,8 @@ class _Call:
     def __init__(self, q, k, v, log_decay, cu_seqlens, num_seqs, scale):
         if q is None or v is None or q.dim() not in (3, 4) or v.dim() != q.dim():
             raise ValueError("q and v must be [T_total, heads, D] or [B, T, heads, D]")
-        self.vshape, self.qshape = v.shape, v.shape[:-2] + q.shape[-2:]
         self.H, self.D, self.Hk = v.shape[-2], v.shape[-1], q.shape[-2]
+        self.vshape, self.qshape = v.shape, v.shape[:-2] + (self.Hk, self.D)
         if v.dim() == 4:
             if cu_seqlens is not None:
                 raise ValueError("cu_seqlens goes with packed [T_total, heads, D] tensors")

@@ -132,7 +132,7 @@ def test_binding_refuses():
     c = torch.zeros(4, 128).to(torch.float8_e4m3fn)
     for call in (lambda: gdr.dla_fwd(x, x, x, g), lambda: gdr.dla_bwd(x, x, x, g, x), lambda: gdr.dla_step(x, x, x, g, s),
                  lambda: gdr.dla_fwd(x[0], x[0], x[0], g), lambda: gdr.dla_step(x[0], x[0], x[0], g, s),
-                 lambda: gdr.dla_fwd(None, x, x, g), lambda: gdr.quant_e4m3(x.to(torch.float16)), lambda: gdr.quant_e4m3(x),
+                 lambda: gdr.dla_fwd(None, x, x, g), lambda: gdr.dla_fwd(x.repeat(1, 1, 2), x.repeat(1, 1, 2), x, g), lambda: gdr.quant_e4m3(x.to(torch.float16)), lambda: gdr.quant_e4m3(x),
                  lambda: gdr.quant_e4m3(x, tiles=True), lambda: gdr.quant_e4m3(x[0], transposed=True), lambda: gdr.quant_e4m3(None),
                  lambda: gdr.linear_e4m3(c, torch.ones(4, 1), c, torch.ones(1, 1)), lambda: gdr.linear_e4m3(c, None, None, None)):
         with pytest.raises(ValueError):

@@ -144,6 +144,64 @@ def test_many_sequences():
     _check(_inputs([3, 0, 1, 130] * 200, 1, 1, 64, 76))
 
 
+@pytest.mark.parametrize("n", [31, 32, 33, 64])
+def test_sequences_around_a_warp(n):
+    _check(_inputs([(37 * i) % 150 for i in range(n)], 2, 2, 64, 77))
+
+
+def test_very_many_sequences():
+    """Tens of thousands of sequences of zero to two tokens, against the closed form."""
+    lens = [1, 0, 2] * 15000
+    d = _inputs(lens, 2, 2, 64, 78, states=False, decays=[-0.5, -0.1])
+    cu = d["cu"].cuda()
+    out = gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], cu_seqlens=cu)
+    q, k, v = (d[n].double() for n in ("q", "k", "v"))
+    first = torch.zeros(v.shape[0], dtype=torch.bool, device="cuda")
+    first[cu[:-1][cu[1:] > cu[:-1]]] = True
+    own = (q * k).sum(2, keepdim=True) * v
+    before = torch.exp(d["g"].double())[:, None] * (q[1:] * k[:-1]).sum(2, keepdim=True) * v[:-1]
+    own[1:] += torch.where(first[1:, None, None], 0.0, before)
+    assert rel_l2(f64(out["o"]), f64(own * 64 ** -0.5)) <= U
+    last = torch.cat([first[1:], torch.ones(1, dtype=torch.bool, device="cuda")])
+    state = k[:, :, :, None] * v[:, :, None, :]
+    state[1:] += torch.where(first[1:, None, None, None], 0.0, torch.exp(d["g"].double())[:, None, None] * state[:-1])
+    assert not out["ht"][1::3].any()
+    full = torch.ones(len(lens), dtype=torch.bool, device="cuda")
+    full[1::3] = False
+    assert rel_l2(f64(out["ht"][full]), f64(state[last])) <= 2.0 ** -16
+
+
+def test_sequences_of_one_length_given_by_their_number():
+    d = _inputs([200, 200, 200], 2, 1, 128, 79)
+    a = gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], h0=d["h0"], cu_seqlens=d["cu"].cuda())
+    b = gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], h0=d["h0"], num_seqs=3)
+    assert _same(a, b)
+    a = gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], h0=d["h0"], dht=d["dht"], cu_seqlens=d["cu"].cuda())
+    b = gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], h0=d["h0"], dht=d["dht"], num_seqs=3)
+    assert _same(a, b)
+
+
+def test_offsets_past_32_bits():
+    """v, o and the gradients beyond 2^32 elements: the last tokens, whose memory is short, are those of a call of their own."""
+    H, D, T, tail = 40, 128, 850_000, 1500
+    assert T * H * D > 1 << 32
+    gen = torch.Generator("cuda").manual_seed(93)
+    n = lambda t, h: torch.randn(t, h, D, generator=gen, device="cuda", dtype=BF16)  # noqa: E731
+    q, k = n(T, 1), n(T, 1)
+    v, dO = n(20_000, H).repeat(T // 20_000 + 1, 1, 1)[:T], n(10_000, H).repeat(T // 10_000, 1, 1)
+    g = torch.full((H,), -0.3, device="cuda")
+    out = gdr.dla_fwd(q, k, v, g)["o"]
+    assert torch.isfinite(out[::997]).all()
+    part = gdr.dla_fwd(q[-tail:], k[-tail:], v[-tail:].contiguous(), g)["o"]
+    assert rel_l2(f64(out[-500:]), f64(part[-500:])) <= U
+    del out, part
+    cu = torch.tensor([0, 1000, T - 3000, T], device="cuda")
+    grad = gdr.dla_bwd(q, k, v, g, dO, cu_seqlens=cu)
+    part = gdr.dla_bwd(q[-3000:], k[-3000:], v[-3000:].contiguous(), g, dO[-3000:].contiguous())
+    for name in ("dq", "dk", "dv"):
+        assert rel_l2(f64(grad[name][-3000:]), f64(part[name])) <= U, name
+
+
 def test_extreme_decays():
     """No memory at all (also by an infinite log decay), growth, a state that has to survive many tokens."""
     d = _inputs([200, 77], 6, 6, 64, 80, decays=[float("-inf"), -1e30, -104.0, 0.02, -1e-9, -20.0])
@@ -228,6 +286,11 @@ def test_bad_sequence_borders(cu):
     assert api.workspace_status(ws) == api.GDR_DEV_BAD_SEQLENS
     gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu_seqlens=cu, workspace=ws)
     assert api.workspace_status(ws) == api.GDR_DEV_BAD_SEQLENS
+    many = torch.cat([cu[:-1], cu[-2:-1].clamp(0, 300).repeat(40), cu[-1:]])  # (more sequences than a warp has lanes)
+    if (many[1:] < many[:-1]).any() or many[0] != 0 or many[-1] != 300:
+        wide = torch.empty(gdr.dla_workspace_bytes(d["q"], d["k"], d["v"], d["g"], cu_seqlens=many, backward=True), dtype=torch.uint8, device="cuda")
+        gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], cu_seqlens=many, workspace=wide)
+        assert api.workspace_status(wide) == api.GDR_DEV_BAD_SEQLENS
     good = torch.tensor([0, 10, 20, 300], device="cuda")
     gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], cu_seqlens=good, workspace=ws)
     assert api.workspace_status(ws) == 0
