@@ -76,7 +76,6 @@ struct Walk {
     const float* init;              // [N][H][D][D] or nullptr
     const float* joined;            // incoming states of ranges that begin inside a chain
     float* last;                    // final states or nullptr
-    int twice;                      // Y' in two bf16 halves: the final states are wanted as fp32 results
     __nv_bfloat16* o;
     float* o32;                     // fp32 outputs for each value head instead
 };
@@ -128,9 +127,9 @@ struct Waiter {
     }
 };
 
-// Chunks j0 to j0 + N of 16 bytes of row `row` of a tile times w, rounded to bf16 (`hi`) and, TWICE, what that leaves
-// (`lo`).  (Not unrolled: what eight warps of two groups run in turn has to stay in the instruction caches.)
-template <int N, bool TWICE>
+// Chunks j0 to j0 + N of 16 bytes of row `row` of a tile times w, rounded to bf16 (`hi`) and what that leaves (`lo`).
+// (Not unrolled: what eight warps of two groups run in turn has to stay in the instruction caches.)
+template <int N>
 __device__ __forceinline__ void split_row(const unsigned char* tile, unsigned char* hi, unsigned char* lo, int row, int j0, float w) {
 #pragma unroll 1
     for (int j2 = j0; j2 < j0 + N; j2 += 2) {
@@ -145,14 +144,12 @@ __device__ __forceinline__ void split_row(const unsigned char* tile, unsigned ch
             for (int i = 0; i < 4; ++i) {
                 const float2 f = __fmul2_rn(make_float2(__uint_as_float(in[i] << 16), __uint_as_float(in[i] & 0xffff0000u)), make_float2(w, w));
                 h[i] = pack_bf16(f.x, f.y);
-                if (TWICE) {
-                    const float2 r = __ffma2_rn(make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)), make_float2(-1.f, -1.f), f);
-                    l[i] = pack_bf16(r.x, r.y);
-                }
+                const float2 r = __ffma2_rn(make_float2(__uint_as_float(h[i] << 16), __uint_as_float(h[i] & 0xffff0000u)), make_float2(-1.f, -1.f), f);
+                l[i] = pack_bf16(r.x, r.y);
             }
             const uint32_t at = tc::sw_chunk(row, j2 + j, CHUNK);
             *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
-            if (TWICE) *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
+            *reinterpret_cast<uint4*>(lo + at) = make_uint4(l[0], l[1], l[2], l[3]);
         }
     }
 }
@@ -184,13 +181,12 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
 }
 
-// the state's terms of a chunk, transposed: Z^T Y', from both halves of Y' if there are two
+// the state's terms of a chunk, transposed: Z^T Y', from both halves of Y'
 template <int D>
-__device__ __forceinline__ void issue_terms(uint32_t on, uint32_t to, uint32_t hi, uint32_t lo, uint32_t z, bool twice) {
+__device__ __forceinline__ void issue_terms(uint32_t on, uint32_t to, uint32_t hi, uint32_t lo, uint32_t z) {
     constexpr uint32_t id = tc::idesc(128, D, 1, 1);
 #pragma unroll 1
     for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(z, CHUNK, 0, k), tc::mdesc(hi, CHUNK, 0, k), id, k > 0);
-    if (!twice) return;
 #pragma unroll 1
     for (int k = 0; k < CHUNK; k += 16) tc::mma_if(on, to, tc::mdesc(z, CHUNK, 0, k), tc::mdesc(lo, CHUNK, 0, k), id, 1);
 }
@@ -337,7 +333,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 } else {
                     if (!wait.warp(full(sz), turn(it, K::NZ)) || !wait.warp(y_ready, ph)) break;
                     tc::fence_after();
-                    issue_terms<D>(on, tD, sb + K::oHi, sb + K::oLo, Z, w.twice);
+                    issue_terms<D>(on, tD, sb + K::oHi, sb + K::oLo, Z);
                     tc::commit_if(on, d_full);
                     tc::commit_if(on, empty(sz));
                     if (!wait.warp(full(sx), turn(it, K::NX)) || !wait.warp(s_ready, ph) || (it && !wait.warp(o_free, ph ^ 1))) break;
@@ -590,10 +586,8 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 clear_row<HALF / 8>(smem + K::oHi, i, col / 8);
                 clear_row<HALF / 8>(smem + K::oLo, i, col / 8);
                 clear_row<HALF / 8>(smem + slot_z(it) * K::TILE, i, col / 8);
-            } else if (w.twice) {
-                split_row<HALF / 8, true>(tile, smem + K::oHi, smem + K::oLo, i, col / 8, wt);
             } else {
-                split_row<HALF / 8, false>(tile, smem + K::oHi, nullptr, i, col / 8, wt);
+                split_row<HALF / 8>(tile, smem + K::oHi, smem + K::oLo, i, col / 8, wt);
             }
             tc::fence_async_smem();
             warp_arrive(y_ready);
@@ -763,7 +757,7 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
             const uint32_t y = sb + slot_of(2 * it) * K::TILE, z = sb + slot_of(2 * it + 1) * K::TILE;
             if (!wait.warp(full(slot_of(2 * it + 1)), parity_of(2 * it + 1)) || !wait.warp(y_ready + 8 * b, ph)) break;
             tc::fence_after();
-            issue_terms<D>(on, tmem + 128 * b, y, sb + K::oLo + b * K::TILE, z, true);
+            issue_terms<D>(on, tmem + 128 * b, y, sb + K::oLo + b * K::TILE, z);
             tc::commit_if(on, d_full + 8 * b);
             tc::commit_if(on, empty(slot_of(2 * it)));
             tc::commit_if(on, empty(slot_of(2 * it + 1)));
@@ -791,7 +785,7 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
             if (!wait.warp(full(slot_of(l)), parity_of(l))) return false;
             if (rows < CHUNK && !wait.warp(full(slot_of(l + 1)), parity_of(l + 1))) return false;
             if (i < rows) {
-                split_row<HALF / 8, true>(tile, tile, lo, i, col / 8, wt);
+                split_row<HALF / 8>(tile, tile, lo, i, col / 8, wt);
             } else {
                 clear_row<HALF / 8>(tile, i, col / 8);
                 clear_row<HALF / 8>(lo, i, col / 8);
@@ -1018,7 +1012,7 @@ cudaError_t forward(const DlaParams& p, cudaStream_t s) {
     Walk& o = w.w[0];
     if (!make_walk(&o, p, q, k, v, p.o, p.H, nullptr)) return cudaErrorInvalidValue;
     o.p_scale = o.o_scale = p.scale, o.w_scale = 1.f;
-    o.init = p.h0, o.joined = p.states, o.last = p.ht, o.twice = 1;
+    o.init = p.h0, o.joined = p.states, o.last = p.ht;
     t.w[0] = TailWalk{o.Y, o.Z, o.gy, o.gz, 0, 1.f, p.states, p.h0};
     return go<D, 1, 1>(p, sh, w, t, s);
 }
@@ -1041,7 +1035,7 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
     dk.turned = 1, dk.back = 1, dk.p_scale = dk.w_scale = p.scale, dk.o_scale = 1.f;
     dk.init = p.dht, dk.joined = back;
     dv.back = 1, dv.p_scale = dv.w_scale = p.scale, dv.o_scale = 1.f;
-    dv.init = p.dht, dv.joined = back, dv.last = p.dh0, dv.twice = 1;
+    dv.init = p.dht, dv.joined = back, dv.last = p.dh0;
     t.w[0] = TailWalk{dq.Z, dq.Y, dq.gz, dq.gy, 0, 1.f, p.states, p.h0};
     t.w[1] = TailWalk{dv.Y, dv.Z, dv.gy, dv.gz, 1, p.scale, back, p.dht};
     cudaError_t e = go<D, 3, 2>(p, sh, w, t, s);
