@@ -85,14 +85,17 @@ struct Walks {
 };
 
 struct Grid {
-    int N, H, D, ranges, snap;
+    int N, H, D, ranges, mode;
     int pieces;  // blocks that share the sum of a range's last chain
     int64_t T, seq_len;
     const int64_t* cu;
     const float* g;
     int* status;
+    int* taken;  // for each walk the chains that its blocks have taken from the queue beyond their first
 };
-__device__ __forceinline__ Line line_of(const Grid& p, int back) { return Line{p.N, p.H, p.T, p.seq_len, p.cu, back}; }
+__device__ __forceinline__ Line line_of(const Grid& p, int back, const Plan* plan) {
+    return Line{p.N, p.H, p.T, p.seq_len, p.cu, back, plan};
+}
 
 // Waits are bounded: one that runs out records it, and ends every role of the block at its next wait.
 struct Waiter {
@@ -165,10 +168,12 @@ struct Chunk {
     int rows;   // tokens, and the bits below
     int head;
     int chain;  // seq * H + head
-    static constexpr int ENDS = 256, LAST = 512;  // the chain ends with it; the range does
+    // the chain ends with it; it is the block's last; the next one is another chain's first (a range may end inside a chain)
+    static constexpr int ENDS = 256, LAST = 512, TURNS = 1024;
     __device__ __forceinline__ int tokens() const { return rows & 255; }
     __device__ __forceinline__ bool ends() const { return rows & ENDS; }
     __device__ __forceinline__ bool last() const { return rows & LAST; }
+    __device__ __forceinline__ bool turns() const { return rows & TURNS; }
 };
 __device__ __forceinline__ Chunk chunk_at(const int4* chunks, int it) {
     const int4 c = chunks[it & 7];
@@ -207,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
     const int range = blockIdx.x / WALKS;
     const Walk& w = walks.w[WALKS == 1 ? 0 : blockIdx.x % WALKS];
     const bool back = WALKS > 1 && w.back, wide = WALKS > 1 && w.o32;  // (the forward is one walk, forward in time, into bf16)
-    const Line line = line_of(p, back);
+    const Line line = line_of(p, back, &plan_s);
 
     // slot of chunk `it`'s tile, and how often that slot has been used before
     const uint32_t bar0 = sb + K::oBar;
@@ -248,14 +253,19 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
         gone_s = 0;
     }
     if (warp == 1) tc::alloc(smem_u32(&tslot), 512);
-    make_plan<K::THREADS>(line, range, p.ranges, p.snap, &plan_s, scratch);
+    make_plan<K::THREADS>(line, range, p.ranges, p.mode, &plan_s, scratch);
+    // (blocks without a range begin with the first chains of the queue, a chain each)
+    const int first_chain = range - plan_s.ranges;
+    const bool queued = plan_s.f0 == plan_s.f1 && first_chain >= 0 && first_chain < plan_s.chains;
+    if (tid == 0 && queued) plan_s.at = line.chain(first_chain);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     const uint32_t tmem = tslot;
     const Waiter wait{&gone_s, p.status};
     if (plan_s.total < 0 && tid == 0) atomicOr(p.status, ST_BAD_SEQLENS);
-    const bool any = more(plan_s, plan_s.at, plan_s.f, p.snap);
+    const bool any = queued || more(plan_s, plan_s.at, plan_s.f, p.mode);
+
 
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(K::REGS_1));
@@ -266,10 +276,12 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             tc::prefetch_map(&w.Z);
             int it = 0;
             bool on[3] = {};  // copies issued into Y's, X's, Z's slots in the last turn that was begun
-            const Plan plan = plan_s;
+            const Plan& plan = plan_s;
             Place at = plan.at;
             bool go_on = true;
-            int f = plan.f;
+            bool in_line = plan.f0 < plan.f1;
+            int f = plan.f, taken = -1;
+            auto take = [&]() { return p.ranges - plan.ranges + atomicAdd(p.taken + (WALKS == 1 ? 0 : blockIdx.x % WALKS), 1); };
 #pragma unroll 1
             for (; go_on; ++it) {
                 const int t0 = line.token(at), h0 = at.head;
@@ -277,9 +289,22 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 if (at.pos == 0 && w.init && it)  // (the chain's state will be asked for soon)
                     tc::prefetch_l2(w.init + (int64_t)c.w * D * D, D * D * sizeof(float));
                 if (at.pos + 1 == at.count) c.y |= Chunk::ENDS;
-                line.next(at, f);
-                go_on = more(plan, at, f, p.snap);
-                if (!go_on) c.y |= Chunk::LAST;
+                if (in_line) {
+                    line.next(at, f);
+                    go_on = more(plan, at, f, p.mode);
+                } else {
+                    go_on = ++at.pos < at.count;
+                }
+                if (plan.chains) {  // (the next chain is asked for a chunk ahead)
+                    if (taken < 0 && (!go_on || (in_line ? f + 2 >= plan.f1 : at.pos + 1 == at.count))) taken = take();
+                    if (!go_on && taken < plan.chains) {
+                        at = line.chain(taken);
+                        taken = -1;
+                        in_line = false;
+                        go_on = true;
+                    }
+                }
+                c.y |= !go_on ? Chunk::LAST : at.pos == 0 ? Chunk::TURNS : 0;
                 chunks[it & 7] = c;
                 on[0] = on[1] = on[2] = false;
 #pragma unroll 1
@@ -617,7 +642,7 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
                 for (int j = 0; j < HALF; ++j) to[j * D] = S[j];
             }
             if (now.last()) break;
-            if (now.ends()) {
+            if (now.turns()) {
                 if (!wait.warp(full(slot_y(it + 1)), turn(it + 1, K::NY))) break;
                 const Chunk next = chunk_at(chunks, it + 1);
                 incoming(next.chain, next.head, false);
@@ -695,8 +720,8 @@ __global__ void __launch_bounds__(TailCfg<D>::THREADS, 1) k_dla_tail(const __gri
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int piece = blockIdx.x % p.pieces, range = blockIdx.x / p.pieces / WALKS;
     const TailWalk& w = walks.w[WALKS == 1 ? 0 : blockIdx.x / p.pieces % WALKS];
-    const Line line = line_of(p, w.back);
-    make_plan<K::THREADS>(line, range, p.ranges, 0, &plan_s, scratch);
+    const Line line = line_of(p, w.back, &plan_s);
+    make_plan<K::THREADS>(line, range, p.ranges, RANGES, &plan_s, scratch);
     const Tail tail = tail_of(line, plan_s);
     const int begin = piece_begin(tail.chunks, piece, p.pieces), stop = piece_begin(tail.chunks, piece + 1, p.pieces);
     if (begin == stop) return;
@@ -841,9 +866,9 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
     __shared__ int scratch[JOIN_THREADS / 32];
     const int slice = blockIdx.x % SLICES, which = blockIdx.x / SLICES % WALKS, range = blockIdx.x / SLICES / WALKS + 1;
     const TailWalk& w = walks.w[which];
-    const Line line = line_of(p, w.back);
-    make_plan<JOIN_THREADS>(line, range, p.ranges, 0, &plan_s, scratch);
-    const Plan plan = plan_s;
+    const Line line = line_of(p, w.back, &plan_s);
+    make_plan<JOIN_THREADS>(line, range, p.ranges, RANGES, &plan_s, scratch);
+    const Plan& plan = plan_s;
     cudaGridDependencySynchronize();  // (the sums of k_dla_tail)
     if (plan.total <= 0 || plan.f0 >= plan.f1 || plan.at.pos == 0) return;
     const Place at = plan.at;
@@ -911,10 +936,12 @@ __global__ void __launch_bounds__(256) k_dla_groups(const float* dq_heads, const
     reinterpret_cast<uint2*>(blockIdx.y ? dk : dq)[i] = make_uint2(pack_bf16(s.x, s.y), pack_bf16(s.z, s.w));
 }
 
-// How a call's chunks are shared out: the number of ranges (of each walk), whether they end with whole chains, and
-// the blocks that share the sum of a range's last chain.
+// How a call's chunks are shared out: the number of ranges (of each walk), what they are, and the blocks that share the
+// sum of a range's last chain.
 struct Shares {
-    int ranges, snap, pieces;
+    int ranges;
+    Mode mode;
+    int pieces;
 };
 Shares shares_of(const DlaParams& p, int walks) {
     const int64_t chains = (int64_t)p.N * p.H;
@@ -922,9 +949,17 @@ Shares shares_of(const DlaParams& p, int walks) {
     const int64_t most = p.cu_seqlens ? (p.T / CHUNK + p.N) * p.H : longest * chains;
     const int sms = num_sms();
     int64_t fit = sms / walks > 0 ? sms / walks : 1;
-    if (longest <= 4) return {(int)(chains < fit ? chains : fit), 1, 1};
+    if (longest <= 4) return {(int)(chains < fit ? chains : fit), SNAP, 1};
     const int64_t ranges = (most + 3) / 4;  // of at least four chunks
-    Shares sh{(int)(ranges < fit ? ranges : fit), 0, 1};
+    Shares sh{(int)(ranges < fit ? ranges : fit), RANGES, 1};
+    if (!p.cu_seqlens) {
+        const int64_t places = longest + 1;
+        if (short_enough((chains + sh.ranges - 1) / sh.ranges * places, chains * places / sh.ranges)) {
+            sh.mode = WHOLE;
+            if (chains < sh.ranges) sh.ranges = (int)chains;
+            return sh;
+        }
+    }
     // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and four short blocks each
     // even that out; else as many as leave the fewest rounds of blocks (three for the backward's two sums of 49
     // ranges each: two rounds of a third, 105 -> 75 us at T = 32768, 16 heads).
@@ -960,7 +995,7 @@ cudaError_t launch_after(unsigned grid, unsigned threads, size_t smem, cudaStrea
 
 template <int D, int WALKS, int TAILS>
 cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, const TailWalks<TAILS>& tails, cudaStream_t s) {
-    const Grid grid{p.N, p.H, D, sh.ranges, sh.snap, sh.pieces, p.T, p.seq_len, p.cu_seqlens, p.g, p.status};
+    const Grid grid{p.N, p.H, D, sh.ranges, sh.mode, sh.pieces, p.T, p.seq_len, p.cu_seqlens, p.g, p.status, p.status + 1};
     cudaError_t e = cudaMemsetAsync(p.status, 0, 256, s);
     if (e != cudaSuccess) return e;
     static bool allowed[64], allowed_tail[64];
@@ -972,7 +1007,7 @@ cudaError_t go(const DlaParams& p, const Shares& sh, const Walks<WALKS>& walks, 
         return cudaFuncGetAttributes(&at, k_dla<D, WALKS>) == cudaSuccess ? at.numRegs : 0;
     }();
     if (regs != Cfg<D>::REGS) return cudaErrorInvalidConfiguration;
-    if (!sh.snap && sh.ranges > 1) {
+    if (sh.mode == RANGES && sh.ranges > 1) {
         e = allow_smem((const void*)k_dla_tail<D, TAILS>, TailCfg<D>::SMEM, allowed_tail);
         if (e != cudaSuccess) return e;
         k_dla_tail<D, TAILS><<<(sh.ranges - 1) * TAILS * sh.pieces, TailCfg<D>::THREADS, TailCfg<D>::SMEM, s>>>(tails, grid);
@@ -1049,11 +1084,11 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
 
 size_t dla_states_bytes(const DlaParams& p, bool backward) {
     const Shares sh = shares_of(p, backward ? 3 : 1);
-    return sh.snap || sh.ranges < 2 ? 0 : (backward ? 2 : 1) * sizeof(float) * (size_t)sh.ranges * sh.pieces * p.D * p.D;
+    return sh.mode != RANGES || sh.ranges < 2 ? 0 : (backward ? 2 : 1) * sizeof(float) * (size_t)sh.ranges * sh.pieces * p.D * p.D;
 }
 int dla_kernels(const DlaParams& p, bool backward) {
     const Shares sh = shares_of(p, backward ? 3 : 1);
-    return (sh.snap || sh.ranges < 2 ? 1 : 3) + (backward && p.H != p.Hk ? 1 : 0);
+    return (sh.mode != RANGES || sh.ranges < 2 ? 1 : 3) + (backward && p.H != p.Hk ? 1 : 0);
 }
 
 cudaError_t launch_dla_fwd(const DlaParams& p, cudaStream_t s) { return p.D == 64 ? forward<64>(p, s) : forward<128>(p, s); }

@@ -136,6 +136,28 @@ def test_long_sequences(lens, D):
     _check(_inputs(lens, 5, 5, D, 70, decays=[0.0, -1e-4, -0.05, -1.0, -0.003]))
 
 
+@pytest.mark.parametrize("heads,D,dense", [((16, 4), 64, (19, 300)), ((6, 6), 128, (25, 260)), ((40, 40), 64, (1, 1300)),
+                                           ((76, 2), 128, (1, 520)), ((150, 1), 64, (1, 640))])
+def test_whole_chains_of_one_length(heads, D, dense):
+    """As many chains as the blocks share evenly, or nearly: each block walks whole ones."""
+    _check(_inputs([dense[1]] * dense[0], *heads, D, 70 + D, decays=DECAYS * 19), dense=dense)
+
+
+# sequences too long to be walked whole beside many short ones, and empty ones
+MIXED = [3000, 0, 129, 1, 700, 128, 127, 0, 640, 1300, 513, 2]
+
+
+@pytest.mark.parametrize("lens,heads,D", [(MIXED, (12, 3), 64), (MIXED[::-1], (10, 10), 128),
+                                          ([900, 0, 905, 1023, 1024, 1025, 130, 7], (30, 10), 64),
+                                          ([5000] + [300] * 31, (6, 3), 64), ([300] * 31 + [3000], (6, 6), 128)])
+def test_whole_chains_beside_ranges(lens, heads, D):
+    _check(_inputs(lens, *heads, D, len(lens) + D, decays=DECAYS * 4))
+
+
+def test_whole_chains_without_states_and_column_slices():
+    _check(_inputs(MIXED, 10, 5, 128, 75, states=False, split=True, decays=DECAYS * 3))
+
+
 def test_many_heads():
     _check(_inputs([300, 5, 129], 40, 8, 64, 75, decays=[-0.02 * i for i in range(40)]))
 
@@ -300,7 +322,7 @@ def _same(a, b):
     return all(torch.equal(a[n], b[n]) for n in a if a[n] is not None)
 
 
-@pytest.mark.parametrize("lens,H", [([300, 7], 2), ([9000, 40], 3)])
+@pytest.mark.parametrize("lens,H", [([300, 7], 2), ([9000, 40], 3), (MIXED, 16)])
 def test_same_results_every_time_and_in_a_graph(lens, H):
     d = _inputs(lens, H, 1, 64, 86)
     cu = d["cu"].cuda()
