@@ -649,14 +649,16 @@ __global__ void __launch_bounds__(Cfg<D>::THREADS, 1) k_dla(const __grid_constan
             }
         }
     }
-    // empty sequences pass their states through
+    // empty sequences pass their states through, chain by chain shared by all blocks
     if (w.last && plan_s.total >= 0 && p.cu) {
-        const int64_t size = (int64_t)p.H * D * D;
+        const int chains = p.N * p.H;
 #pragma unroll 1
-        for (int n = range; n < p.N; n += p.ranges) {
-            if (p.cu[n] != p.cu[n + 1]) continue;
-#pragma unroll 1
-            for (int64_t e = tid; e < size; e += K::THREADS) w.last[n * size + e] = w.init ? w.init[n * size + e] : 0.f;
+        for (int c = range; c < chains; c += p.ranges) {
+            if (p.cu[c / p.H] != p.cu[c / p.H + 1]) continue;
+            const float4* from = reinterpret_cast<const float4*>(w.init + (int64_t)c * D * D);
+            float4* to = reinterpret_cast<float4*>(w.last + (int64_t)c * D * D);
+#pragma unroll 4
+            for (int e = tid; e < D * D / 4; e += K::THREADS) to[e] = w.init ? from[e] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
     }
     tc::fence_before();
@@ -960,11 +962,11 @@ Shares shares_of(const DlaParams& p, int walks) {
             return sh;
         }
     }
-    // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and four short blocks each
-    // even that out; else as many as leave the fewest rounds of blocks (three for the backward's two sums of 49
+    // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and two blocks each even that
+    // out (30011 tokens in 8 sequences, 32 heads: 263 us with one, 240 with two, 246 with four); else as many as leave the fewest rounds of blocks (three for the backward's two sums of 49
     // ranges each: two rounds of a third, 105 -> 75 us at T = 32768, 16 heads).
     if (chains > fit) {
-        sh.pieces = 4;
+        sh.pieces = 2;
     } else {
         const int blocks = (sh.ranges - 1) * (walks == 1 ? 1 : 2);
         double best = 1e9;
