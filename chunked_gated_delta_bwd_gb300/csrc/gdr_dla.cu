@@ -14,22 +14,33 @@
 // so that the backward is three such walks in one launch, which meet in the second-level cache: dv's and
 // dk's walk the same chunks at the same time.
 //
-// Bytes bound it: a chunk and head of 128 moves 128 KB (2.9 us of a multiprocessor's share of the
-// measured copy rate) for five products of 128^3 (1.3 us of tensor cores).  So one block a multiprocessor
-// walks a range of chunks (gdr_dla_plan.cuh) with the loads of the next chunk in flight, the state in fp32
-// registers, and four roles that overlap:
-//   loader   Y, Z, X tiles of the chunks to come, by TMA, through a ring of tiles
-//   issuer   the products: P = X Y^T, X C, P Z (P from tensor memory), Y'^T Z
-//   group A  P times the decays, rounded to bf16 (tensor memory); out, staged in X's tile for a TMA store
-//   group B  Y' = w Y as two bf16 tiles (the first in Y's place): their products with Z make the state's
-//            terms good to 2^-16, so that the states that leave (ht, dh0) are fp32 results; the state's
-//            sum, and its bf16 copy for X C
-// P and the state's copy are rounded to bf16: each adds 2^-9 at most to a term of an output that is
-// rounded to bf16 itself.
+// Bytes bound it: a chunk and head of 128 channels moves 128 KB (2.9 us of a multiprocessor's share of the measured copy
+// rate) for five products of 128^3 and one more for the states' accuracy (1.6 us of tensor cores).  So one block a
+// multiprocessor walks chunks (gdr_dla_plan.cuh: a range, or whole chains from a queue), the state in fp32 registers, in
+// roles that overlap:
+//   loader    Y, X, Z tiles of the chunks to come, by TMA, through a ring of tiles; what the others have to know of a chunk
+//   issuer 1  P = X Y^T, and P Z (P from tensor memory)
+//   issuer 3  the state's terms Y'^T Z, and X C
+//   stores    the outputs, by TMA
+//   group A   (eight warps) P times the decays, rounded to bf16 (tensor memory); out, staged in X's tile
+//   group B   (eight warps) Y' = w Y as two bf16 tiles, whose products with Z make the state's terms good to 2^-16; the
+//             state's sum in fp32, and its bf16 copy for X C
+// P and the state's copy are rounded to bf16: each adds 2^-9 at most to a term of an output that is rounded to bf16 itself
+// (o and the gradients are off by 2.3e-3 in the 2-norm; their own rounding alone is 1.7e-3).  The tokens' terms of the
+// states keep 2^-17 (ht, dh0: 2.5e-6).  With one half of Y' in the walks whose states do not leave, dq and dk were off by
+// 2.7e-3, for 2 us in 355.
+//
+// Measured (32768 tokens, 16 heads of 128): forward 155 us, its walk 98 (5.5 TB/s); backward 355, its three walks 265.  A
+// chunk takes 6000 cycles where 5400 are its bytes' time (forward) and 2560 its products': what is left is the turn of P,
+// decays, P Z and output, which wait for one another in group A, beside split, product and sum in group B.  With 64
+// channels it is this turn alone: 4500 cycles a chunk of half the bytes.  Tried: Y' of 64 channels as one operand of 128
+// columns (98 -> 103 us at 2 x 4095 backward, 16 heads); two tiles of Y; tiles asked into the second-level cache two chunks
+// ahead; more columns a tensor memory load; two loaders: all as fast or slower.
 //
 // A chain that crosses from one range into the next: k_dla_tail first sums, for each range, the terms of
 // its last chain's tokens (it reads only Y and Z, from the range's end backwards, and stops where the decay
-// has underflowed), k_dla_join carries them along the chain, and the walk starts from there.
+// has underflowed; 41 us for the forward's 268 MB, 77 for the backward's 537: the copy rate), k_dla_join carries them along
+// the chain (8 to 12 us), and the walk starts from there.
 #include "gdr_dla.h"
 #include "gdr_dla_plan.cuh"
 #include "gdr_internal.h"
@@ -951,20 +962,21 @@ Shares shares_of(const DlaParams& p, int walks) {
     const int64_t most = p.cu_seqlens ? (p.T / CHUNK + p.N) * p.H : longest * chains;
     const int sms = num_sms();
     int64_t fit = sms / walks > 0 ? sms / walks : 1;
-    if (longest <= 4) return {(int)(chains < fit ? chains : fit), SNAP, 1};
-    const int64_t ranges = (most + 3) / 4;  // of at least four chunks
+    // Chains of four chunks are walked whole (10 sequences of 512, 16 heads: ranges 50 us, whole chains 35).
+    const int all_chains = (int)(chains < fit ? chains : fit);
+    if (longest <= 4) return {all_chains, p.cu_seqlens ? SNAP : WHOLE, 1};
+    // Ranges of at least four chunks: against two, 900 tokens of 8 heads 33 us (29), 16384 of one head 87 (93), the backward
+    // of 4096 of 4 heads 43 (52).
+    const int64_t ranges = (most + 3) / 4;
     Shares sh{(int)(ranges < fit ? ranges : fit), RANGES, 1};
     if (!p.cu_seqlens) {
         const int64_t places = longest + 1;
-        if (short_enough((chains + sh.ranges - 1) / sh.ranges * places, chains * places / sh.ranges)) {
-            sh.mode = WHOLE;
-            if (chains < sh.ranges) sh.ranges = (int)chains;
-            return sh;
-        }
+        if (short_enough((chains + sh.ranges - 1) / sh.ranges * places, chains * places / sh.ranges)) return {all_chains, WHOLE, 1};
     }
-    // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and two blocks each even that
-    // out (30011 tokens in 8 sequences, 32 heads: 263 us with one, 240 with two, 246 with four); else as many as leave the fewest rounds of blocks (three for the backward's two sums of 49
-    // ranges each: two rounds of a third, 105 -> 75 us at T = 32768, 16 heads).
+    // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and two blocks each even
+    // that out (30011 tokens in 8 sequences, 32 heads: 263 us with one, 240 with two, 246 with four); else as many as leave
+    // the fewest rounds of blocks (three for the backward's two sums of 49 ranges each: two rounds of a third, 105 -> 75 us
+    // at T = 32768, 16 heads).
     if (chains > fit) {
         sh.pieces = 2;
     } else {

@@ -21,8 +21,8 @@ namespace dla {
 
 constexpr int CHUNK = 128;
 
-// What the blocks are asked for: ranges, and a queue where sequences are few; ranges of whole chains (SNAP: chains of
-// a few chunks); all chains from the queue (WHOLE: sequences of one length).
+// What the blocks are asked for: ranges, and a queue where packed sequences are few (32: a sequence a lane); ranges of
+// whole chains (SNAP: packed sequences of a few chunks); all chains from the queue (WHOLE: sequences of one length).
 enum Mode { RANGES, SNAP, WHOLE };
 
 // A chunk of the line or the queue.

@@ -6,6 +6,10 @@
 // steps of 32 of the inner dimension) goes into tensor memory by itself, and groups of threads add it, times its scale,
 // to sums in fp32 registers while the next blocks' products run into other columns of the tensor memory.
 //
+// What bounds it with many rows: 128 x 256 sums of a block of 128 take 512 cycles of products and about 700 of what follows
+// them (the accumulators' way from tensor memory into the sums, and the hand-over of the buffer), with the tensor cores at
+// 59% of their cycles.  32768 x 2048 x 6144 takes 305 us, 2.7 PFLOP/s (340 in a long loop, under the power cap).
+//
 // Two forms, the same loop:
 //   rows of x as the product's rows  (many rows of x): a thread holds one row, its scale is one number; blocks
 //       walk the tiles, and the output leaves through shared memory by TMA.
@@ -130,84 +134,83 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
 
     // (the registers of group sums: 128, and the 64 that come in; all warps of a group of four take part)
     if (warp < 4) {
-    if (L::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (warp == 0) {
-        if (lane == 0) {
-            // ---------------- loader ----------------
-            tc::prefetch_map(&maps.a);
-            tc::prefetch_map(&maps.b);
-            int l = 0;
+        if (L::MOVE_REGS) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
+        if (warp == 0) {
+            if (lane == 0) {
+                // ---------------- loader ----------------
+                tc::prefetch_map(&maps.a);
+                tc::prefetch_map(&maps.b);
+                int l = 0;
 #pragma unroll 1
-            for (int t = first; t < tiles && ok(); t += step) {
-                const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
+                for (int t = first; t < tiles && ok(); t += step) {
+                    const int a0 = t / tiles_b * 128, b0 = t % tiles_b * BN;
 #pragma unroll 1
-    #pragma unroll 1
-            for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                    const int s = l % L::STAGES;
-                    if (l >= L::STAGES && !wait(empty(s), (l / L::STAGES & 1) ^ 1)) break;
-                    tc::mbar_expect_tx(full(s), L::STAGE);
-                    tc::tma_load_2d(sb + s * L::STAGE, &maps.a, kb * KB, a0, full(s));
-                    tc::tma_load_2d(sb + s * L::STAGE + L::A, &maps.b, kb * KB, b0, full(s));
-                }
-            }
-            if (!ok())
-#pragma unroll 1
-                for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
-        }
-    } else if (warp == 1 || warp == 3) {
-        // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
-        // A warp that waits, commits or fences issues no product (60 to 120 cycles each, 400 a block of 128, against 512
-        // for its products of 128 x 256, and products do not queue up): two take the blocks in turn.
-        constexpr uint32_t id = tc::idesc_e4m3(128, BN);
-        const uint32_t on = lane == 0;
-        const int mine = warp == 3;
-        int l = 0;
-        bool fine = true;
-#pragma unroll 1
-        for (int t = first; t < tiles && fine; t += step) {
-#pragma unroll 1
-            for (int kb = kb0; kb < kb1; ++kb, ++l) {
-                if ((l & 1) != mine) continue;
-                const int s = l % L::STAGES, b = l % L::BUFS;
-                fine = (l < L::BUFS || wait_warp(t_empty + 8 * b, (l / L::BUFS & 1) ^ 1)) && wait_warp(full(s), l / L::STAGES & 1);
-                if (!fine) break;
-                tc::fence_after();
-                const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
-#pragma unroll
-                for (int k = 0; k < KB / 32; ++k) tc::mma_e4m3_if(on, tmem + b * BN, da + 2 * k, db + 2 * k, id, k > 0);
-                tc::commit_if(on, empty(s));
-                tc::commit_if(on, t_full + 8 * b);
-            }
-        }
-        if (!fine) {
-            tc::commit_if(on, ended + 8 * mine);
-            tc::mbar_wait(ended + 8 * mine, 0);
-        }
-    } else if (warp == 2 && !X_ROWS) {
-        // ---------------- scales of the columns, eight blocks at a time ----------------
-        int u = 0;
-#pragma unroll 1
-        for (int t = first; t < tiles; t += step) {
-            const int nb = t / tiles_b;
-            const int64_t m0 = (int64_t)(t % tiles_b) * BN;
-#pragma unroll 1
-            for (int kb = kb0; kb < kb1; kb += 8, ++u) {
-                if (u >= 2) wait_warp(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
-                float* sc = reinterpret_cast<float*>(smem + L::oScale) + (u & 1) * 8 * BN;
-                for (int j = lane; j < BN; j += 32) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const bool on = m0 + j < p.M && kb + i < kb1;
-                        v[i] = on ? p.xs[(m0 + j) * p.x_blocks + (p.x_blocks > 1 ? kb + i : 0)] * p.ws[(int64_t)nb * nkb + kb + i] : 0.f;
+                    for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                        const int s = l % L::STAGES;
+                        if (l >= L::STAGES && !wait(empty(s), (l / L::STAGES & 1) ^ 1)) break;
+                        tc::mbar_expect_tx(full(s), L::STAGE);
+                        tc::tma_load_2d(sb + s * L::STAGE, &maps.a, kb * KB, a0, full(s));
+                        tc::tma_load_2d(sb + s * L::STAGE + L::A, &maps.b, kb * KB, b0, full(s));
                     }
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) sc[i * BN + j] = v[i];
                 }
-                tc::mbar_arrive(sc_full + 8 * (u & 1));
+                if (!ok())
+#pragma unroll 1
+                    for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
+            }
+        } else if (warp == 1 || warp == 3) {
+            // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
+            // A warp that waits, commits or fences issues no product (60 to 120 cycles each, 400 a block of 128, against 512
+            // for its products of 128 x 256, and products do not queue up): two take the blocks in turn.
+            constexpr uint32_t id = tc::idesc_e4m3(128, BN);
+            const uint32_t on = lane == 0;
+            const int mine = warp == 3;
+            int l = 0;
+            bool fine = true;
+#pragma unroll 1
+            for (int t = first; t < tiles && fine; t += step) {
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1; ++kb, ++l) {
+                    if ((l & 1) != mine) continue;
+                    const int s = l % L::STAGES, b = l % L::BUFS;
+                    fine = (l < L::BUFS || wait_warp(t_empty + 8 * b, (l / L::BUFS & 1) ^ 1)) && wait_warp(full(s), l / L::STAGES & 1);
+                    if (!fine) break;
+                    tc::fence_after();
+                    const uint64_t da = tc::desc(sb + s * L::STAGE, 16, 1024), db = tc::desc(sb + s * L::STAGE + L::A, 16, 1024);
+#pragma unroll
+                    for (int k = 0; k < KB / 32; ++k) tc::mma_e4m3_if(on, tmem + b * BN, da + 2 * k, db + 2 * k, id, k > 0);
+                    tc::commit_if(on, empty(s));
+                    tc::commit_if(on, t_full + 8 * b);
+                }
+            }
+            if (!fine) {
+                tc::commit_if(on, ended + 8 * mine);
+                tc::mbar_wait(ended + 8 * mine, 0);
+            }
+        } else if (warp == 2 && !X_ROWS) {
+            // ---------------- scales of the columns, eight blocks at a time ----------------
+            int u = 0;
+#pragma unroll 1
+            for (int t = first; t < tiles; t += step) {
+                const int nb = t / tiles_b;
+                const int64_t m0 = (int64_t)(t % tiles_b) * BN;
+#pragma unroll 1
+                for (int kb = kb0; kb < kb1; kb += 8, ++u) {
+                    if (u >= 2) wait_warp(sc_empty + 8 * (u & 1), (u >> 1 & 1) ^ 1);
+                    float* sc = reinterpret_cast<float*>(smem + L::oScale) + (u & 1) * 8 * BN;
+                    for (int j = lane; j < BN; j += 32) {
+                        float v[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const bool on = m0 + j < p.M && kb + i < kb1;
+                            v[i] = on ? p.xs[(m0 + j) * p.x_blocks + (p.x_blocks > 1 ? kb + i : 0)] * p.ws[(int64_t)nb * nkb + kb + i] : 0.f;
+                        }
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sc[i * BN + j] = v[i];
+                    }
+                    tc::mbar_arrive(sc_full + 8 * (u & 1));
+                }
             }
         }
-    }
     } else {
         if (L::MOVE_REGS) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n");
         // ---------------- sums ----------------
@@ -448,10 +451,14 @@ cudaError_t go(const LinearParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_linear(const LinearParams& p, cudaStream_t s) {
+    // Weights as rows against rows of x as rows, K = 2048, N = 6144, in a graph: 5 rows 5.9 and 9.2 us, 32 6.5 and 9.2,
+    // 64 7.8 and 8.6.  Of the narrow ones the narrowest (16 rows in 16 columns 5.8 us, in 64 6.7).
     if (p.M <= 16) return go<false, 16>(p, s);
     if (p.M <= 32) return go<false, 32>(p, s);
     if (p.M <= 64) return go<false, 64>(p, s);
-    if ((p.M + 127) / 128 * ((p.N + 255) / 256) >= num_sms()) return go<true, 256>(p, s);
+    // Tiles of 128 x 128 where all of them are in place at once, else of 128 x 256, K = N = 2048: 1024 rows 8.9 and 11.0 us, 1280
+    // 13.7 and 11.1, 8192 37.8 and 32.3.
+    if ((p.M + 127) / 128 * ((p.N + 127) / 128) > num_sms()) return go<true, 256>(p, s);
     return go<true, 128>(p, s);
 }
 
