@@ -39,8 +39,8 @@
 //
 // A chain that crosses from one range into the next: k_dla_tail first sums, for each range, the terms of
 // its last chain's tokens (it reads only Y and Z, from the range's end backwards, and stops where the decay
-// has underflowed; 41 us for the forward's 268 MB, 77 for the backward's 537: the copy rate), k_dla_join carries them along
-// the chain (8 to 12 us), and the walk starts from there.
+// has underflowed; 41 us forward, 77 for the backward's two sums), k_dla_join carries them along the chain (8 to 12 us),
+// and the walk starts from there.
 #include "gdr_dla.h"
 #include "gdr_dla_plan.cuh"
 #include "gdr_internal.h"
@@ -974,17 +974,19 @@ Shares shares_of(const DlaParams& p, int walks) {
         if (short_enough((chains + sh.ranges - 1) / sh.ranges * places, chains * places / sh.ranges)) return {all_chains, WHOLE, 1};
     }
     // The sums of the ranges' last chains: with more chains than ranges they are of all lengths, and two blocks each even
-    // that out (30011 tokens in 8 sequences, 32 heads: 263 us with one, 240 with two, 246 with four); else as many as leave
-    // the fewest rounds of blocks (three for the backward's two sums of 49 ranges each: two rounds of a third, 105 -> 75 us
-    // at T = 32768, 16 heads).
+    // that out (30011 tokens in 8 sequences, 32 heads: 263 us with one, 240 with two, 246 with four); else as many as end
+    // soonest, at 1.5 us a chunk and 2.5 us for each more sum that the join adds (T = 32768, 16 heads: three for the
+    // backward's two sums of 49 ranges each, two rounds of a third, 75 us where one took 105; one forward, where two would
+    // take 13 us more.  4096 tokens of 4 heads, chains of 32 chunks: two, 44 us, against one 48 and four 49).
     if (chains > fit) {
         sh.pieces = 2;
     } else {
         const int blocks = (sh.ranges - 1) * (walks == 1 ? 1 : 2);
-        double best = 1e9;
+        const double chunks = (double)most / sh.ranges;
+        double best = 1e30;
         for (int n = 1; n <= 4; ++n) {
-            const double rounds = (double)((blocks * n + sms - 1) / sms) / n + 0.02 * n;
-            if (rounds < best) best = rounds, sh.pieces = n;
+            const double us = 1.5 * chunks * ((blocks * n + sms - 1) / sms) / n + 2.5 * n;
+            if (us < best) best = us, sh.pieces = n;
         }
     }
     return sh;
