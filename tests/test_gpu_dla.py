@@ -158,6 +158,29 @@ def test_whole_chains_without_states_and_column_slices():
     _check(_inputs(MIXED, 10, 5, 128, 75, states=False, split=True, decays=DECAYS * 3))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_whole_chains_keep_what_is_not_finite(D):
+    """The blocks that walk a chain of NaN go on with other chains, whose results are those of a clean call."""
+    H = 12
+    d = _inputs(MIXED, H, H, D, 76 + D, decays=DECAYS * 2)
+    cu = d["cu"].cuda()
+    call = lambda: {**gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], h0=d["h0"], cu_seqlens=cu),  # noqa: E731
+                    **gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], h0=d["h0"], dht=d["dht"], cu_seqlens=cu)}
+    clean = call()
+    hit = torch.zeros(len(MIXED), H, dtype=torch.bool)
+    for seq, head, bad in ((0, 2, float("nan")), (4, 5, float("inf")), (9, 0, float("nan"))):
+        hit[seq, head] = True
+        a, b = d["cu"][seq].item(), d["cu"][seq + 1].item()
+        for n in ("q", "k", "v", "dO"):
+            d[n][a:b, head] = bad
+        d["h0"][seq, head], d["dht"][seq, head] = bad, -bad
+    rows = torch.repeat_interleave(~hit, torch.tensor(MIXED), dim=0).cuda()
+    out = call()
+    for n, t in out.items():
+        keep = ~hit.cuda() if n in ("ht", "dh0") else rows
+        assert torch.equal(t[keep], clean[n][keep]), n
+
+
 def test_many_heads():
     _check(_inputs([300, 5, 129], 40, 8, 64, 75, decays=[-0.02 * i for i in range(40)]))
 
