@@ -21,8 +21,8 @@ namespace dla {
 
 constexpr int CHUNK = 128;
 
-// What the blocks are asked for: ranges, and a queue where packed sequences are few (32: a sequence a lane); ranges of
-// whole chains (SNAP: packed sequences of a few chunks); all chains from the queue (WHOLE: sequences of one length).
+// What the blocks are asked for: ranges, and a queue where packed sequences allow it (the longest first where they are
+// few, 32: a sequence a lane); ranges of whole chains (SNAP: packed sequences of a few chunks); all chains from the queue (WHOLE: sequences of one length).
 enum Mode { RANGES, SNAP, WHOLE };
 
 // A chunk of the line or the queue.
@@ -190,24 +190,40 @@ __device__ __forceinline__ void make_plan(const Line& line, int range, int range
         __syncthreads();
     } else {
         // every block adds up the sequences' places: N reads, all of them hits in the second-level cache
-        int sum = 0;
+        int sum = 0, longest = 0;
+        bool holes = false;
         bool bad = line.cu[0] != 0 || line.cu[line.N] != line.T;
 #pragma unroll 1
         for (int i = tid; i < line.N; i += THREADS) {
             const int64_t len = line.cu[i + 1] - line.cu[i];
             bad |= len < 0 || len > line.T;
             sum += places(len);
+            longest = max(longest, places(len));
+            holes |= len == 0;
         }
         // (borders that never decrease from 0 to T are all inside)
         bad = __syncthreads_or(bad);
+        holes = __syncthreads_or(holes);
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o), longest = max(longest, __shfl_xor_sync(~0u, longest, o));
         if (lane == 0) scratch[warp] = sum;
         __syncthreads();
         int total = 0;
 #pragma unroll
         for (int i = 0; i < THREADS / 32; ++i) total += scratch[i];
-        if (tid == 0) set_range(out, bad ? -1 : total * line.H, range, ranges, line.N, 0);
+        __syncthreads();
+        if (lane == 0) scratch[warp] = longest;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < THREADS / 32; ++i) longest = max(longest, scratch[i]);
+        // (not in the order of lengths: the last block ends at most one chain after the blocks have shared out all evenly;
+        // a queue with empty sequences would have to skip them one by one)
+        const int64_t mean = (int64_t)total * line.H / ranges;
+        const bool queue = mode == RANGES && !bad && !holes && short_enough(mean + longest, mean);
+        if (tid == 0) {
+            if (queue) set_range(out, 0, range, ranges, 0, line.N * line.H);
+            else set_range(out, bad ? -1 : total * line.H, range, ranges, line.N, 0);
+        }
         __syncthreads();
         const int f0 = out->f0;
         // the sequence that holds place f0 (none where the range is empty)

@@ -149,7 +149,9 @@ MIXED = [3000, 0, 129, 1, 700, 128, 127, 0, 640, 1300, 513, 2]
 
 @pytest.mark.parametrize("lens,heads,D", [(MIXED, (12, 3), 64), (MIXED[::-1], (10, 10), 128),
                                           ([900, 0, 905, 1023, 1024, 1025, 130, 7], (30, 10), 64),
-                                          ([5000] + [300] * 31, (6, 3), 64), ([300] * 31 + [3000], (6, 6), 128)])
+                                          ([5000] + [300] * 31, (6, 3), 64), ([300] * 31 + [3000], (6, 6), 128),
+                                          ([130, 7, 513, 128, 300] * 8, (9, 3), 64), ([257, 1, 300] * 12 + [700], (12, 12), 64),
+                                          ([257, 1, 300] * 12 + [700, 0], (12, 12), 64)])
 def test_whole_chains_beside_ranges(lens, heads, D):
     _check(_inputs(lens, *heads, D, len(lens) + D, decays=DECAYS * 4))
 
