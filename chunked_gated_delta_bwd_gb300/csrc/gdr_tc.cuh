@@ -80,9 +80,9 @@ __device__ __forceinline__ void commit(uint32_t mbar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(mbar));
 }
 
-// The same instructions as a converged warp issues them, through the one lane whose `on` is not zero.  Where one lane
-// alone runs the code around them, every operand is moved to a uniform register at each instruction: a product of
-// 16 of the inner dimension then takes 100 cycles to issue, and 64 (128 x 128) to compute.
+// The same instructions as a converged warp issues them, through the one lane whose `on` is not zero.  From a branch
+// that one lane alone runs, a product of 16 of the inner dimension took 100 cycles to issue (by clock reads), where
+// 128 x 128 of it take 64 to compute.
 __device__ __forceinline__ void mma_if(uint32_t on, uint32_t tmem_d, uint64_t a, uint64_t b, uint32_t id, uint32_t accumulate) {
     asm volatile(
         "{\n.reg .pred p, q;\nsetp.ne.u32 p, %4, 0;\nsetp.ne.u32 q, %5, 0;\n"
