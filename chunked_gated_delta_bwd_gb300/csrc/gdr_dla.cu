@@ -934,10 +934,11 @@ __global__ void __launch_bounds__(JOIN_THREADS) k_dla_join(const __grid_constant
 }
 
 // The gradients of shared heads: sums over the value heads of a group, in fp32; dq and dk (blockIdx.y), four channels a thread.
+// (Nothing where the sequences' borders are inconsistent: the walks have written no gradients to add up.)
 __global__ void __launch_bounds__(256) k_dla_groups(const float* dq_heads, const float* dk_heads, __nv_bfloat16* dq, __nv_bfloat16* dk, int64_t quads,
-                                                    int group, int D) {
+                                                    int group, int D, const int* status) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= quads) return;
+    if (i >= quads || (*status & ST_BAD_SEQLENS)) return;
     const int per = D / 4;
     const int64_t row = i / per;  // (token, k head)
     const float* from = (blockIdx.y ? dk_heads : dq_heads) + (row * group * per + (i - row * per)) * 4;
@@ -1092,7 +1093,7 @@ cudaError_t backward(const DlaParams& p, cudaStream_t s) {
     cudaError_t e = go<D, 3, 2>(p, sh, w, t, s);
     if (e != cudaSuccess || !p.dq_heads) return e;
     const int64_t quads = p.T * p.Hk * D / 4;
-    k_dla_groups<<<dim3((unsigned)((quads + 255) / 256), 2), 256, 0, s>>>(p.dq_heads, p.dk_heads, p.dq, p.dk, quads, p.H / p.Hk, D);
+    k_dla_groups<<<dim3((unsigned)((quads + 255) / 256), 2), 256, 0, s>>>(p.dq_heads, p.dk_heads, p.dq, p.dk, quads, p.H / p.Hk, D, p.status);
     return cudaGetLastError();
 }
 

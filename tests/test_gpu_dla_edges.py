@@ -1,0 +1,34 @@
+"""Linear attention with a decay for each head at the edges of what its header allows.  Inputs as in test_gpu_dla.py."""
+import pytest
+import torch
+
+import chunked_gated_delta_bwd_gb300 as gdr
+from chunked_gated_delta_bwd_gb300 import api, dla
+from tests.test_gpu_dla import _built, _inputs  # noqa: F401  (the fixture builds the library)
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("Hk", [4, 2, 1])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cu", [[0, 10, 5, 300], [1, 10, 20, 300], [0, 10, 20, 299], [0] + [9] * 40 + [301], [0] + [9, 8] * 20 + [300]])
+def test_bad_sequence_borders_write_nothing(cu, D, Hk):
+    """No output is touched, the gradients of shared heads among them; the workspace holds what an earlier call might have left."""
+    H, N, T = 4, len(cu) - 1, 300
+    d = _inputs([T], H, Hk, D, 94, states=False)
+    cu = torch.tensor(cu, device="cuda")
+    args = [d["q"], d["k"], d["v"], d["g"]]
+    ws = torch.full((gdr.dla_workspace_bytes(*args, cu_seqlens=cu, backward=True),), 0x41, dtype=torch.uint8, device="cuda")
+    states = torch.ones(N, H, D, D, device="cuda")
+    out = {n: torch.full_like(t, 7.0) for n, t in dict(o=d["v"], ht=states, dq=d["q"], dk=d["k"], dv=d["v"], dh0=states).items()}
+    P, L = dla._Call(*args, cu, None, None), dla._lib()
+    at = lambda *names: [out[n].data_ptr() for n in names]  # noqa: E731
+    plain, stream = [t.data_ptr() for t in args], torch.cuda.current_stream().cuda_stream
+    assert L.dla_fwd(P.shape, *plain, states.data_ptr(), *at("o", "ht"), ws.data_ptr(), ws.numel(), stream) == 0
+    assert api.workspace_status(ws) == api.GDR_DEV_BAD_SEQLENS
+    ws.fill_(0x41)
+    assert L.dla_bwd(P.shape, *plain, states.data_ptr(), d["dO"].data_ptr(), states.data_ptr(), ws.data_ptr(), ws.numel(),
+                     *at("dq", "dk", "dv", "dh0"), stream) == 0
+    assert api.workspace_status(ws) == api.GDR_DEV_BAD_SEQLENS
+    for n, t in out.items():
+        assert (t == 7.0).all(), n
