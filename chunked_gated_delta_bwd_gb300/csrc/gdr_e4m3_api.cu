@@ -38,7 +38,8 @@ gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const voi
                            void* stream) {
     LinearParams p;
     memset(&p, 0, sizeof(p));
-    if (rows < 0 || rows > INT_MAX) return fail(GDR_ERR_INVALID, "rows must be 0 to 2^31 - 1%s");
+    // (tiles of 128 rows are counted in 32 bits, from rows + 127)
+    if (rows < 0 || rows > INT_MAX - 127) return fail(GDR_ERR_INVALID, "rows must be 0 to 2^31 - 128%s");
     if (inner < 1 || inner % 16 != 0 || inner > (1 << 24)) return fail(GDR_ERR_INVALID, "the inner dimension must be a multiple of 16, at most 2^24%s");
     if (outer < 1 || outer % 8 != 0 || outer > (1 << 24)) return fail(GDR_ERR_INVALID, "the outer dimension must be a multiple of 8, at most 2^24%s");
     const int blocks = (inner + 127) / 128;

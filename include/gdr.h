@@ -413,7 +413,7 @@ gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t
 /* The product of two such operands:
  *     y[m, n] = bias[n] + sum_b x_scale[m, b] w_scale[n / 128, b] sum_{k in b} x[m, k] w[n, k]
  * over the blocks b of 128 of the inner dimension K.
- *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows below 2^31.
+ *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows at most 2^31 - 128.
  *  * x_scale: float [rows, ceil(K / 128)], or with x_blocks = 1 [rows, 1] for the whole row (x_blocks is
  *    1 or ceil(K / 128)); w_scale: float [ceil(N / 128), ceil(K / 128)]; bias float [N] or NULL.
  *  * y: bf16 [rows, N], rounded once from sums in fp32; it shares no memory with an input.  Should a bounded
