@@ -279,6 +279,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                 }
                 if (BN < 256) there = __all_sync(~0u, there);
                 if (!X_ROWS && (((kb - kb0) & 7) == 7 || kb + 1 == kb1)) {
+                    __syncwarp();  // (all lanes have read the scales before they are given back)
                     if (lane == 0) tc::mbar_arrive(sc_empty + 8 * (u & 1));
                     ++u;
                 }
