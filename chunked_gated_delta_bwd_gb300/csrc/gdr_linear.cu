@@ -76,6 +76,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint32_t tslot;
     __shared__ int gone_s;
+    __shared__ volatile int asked_s;  // tiles that the loader has asked for, once it asks for no more
     unsigned char* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
     const uint32_t sb = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -101,6 +102,7 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         for (int i = 0; i < 2; ++i) tc::mbar_set(ended + 8 * i, 1);
         tc::mbar_set_fence();
         gone_s = 0;
+        asked_s = -1;
     }
     if (warp == 1) tc::alloc(smem_u32(&tslot), L::TMEM);
     tc::fence_before();
@@ -130,6 +132,10 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
         *gone = 1;
         return false;
     };
+    auto landed = [&](int asked) {  // (of a block that gave up: all copies that it asked for)
+#pragma unroll 1
+        for (int i = asked > L::STAGES ? asked - L::STAGES : 0; i < asked; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
+    };
     const int first = blockIdx.x / split, step = gridDim.x / split;
 
     // (the registers of group sums: 128, and the 64 that come in; all warps of a group of four take part)
@@ -153,9 +159,8 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
                         tc::tma_load_2d(sb + s * L::STAGE + L::A, &maps.b, kb * KB, b0, full(s));
                     }
                 }
-                if (!ok())
-#pragma unroll 1
-                    for (int i = l > L::STAGES ? l - L::STAGES : 0; i < l; ++i) tc::mbar_wait(full(i % L::STAGES), i / L::STAGES & 1);
+                asked_s = l;
+                if (!ok()) landed(l);
             }
         } else if (warp == 1 || warp == 3) {
             // ---------------- issuers (whole warps, converged; lane 0 issues) ----------------
@@ -288,6 +293,11 @@ __global__ void __launch_bounds__(Lin<X_ROWS, BN>::THREADS, BN <= 32 ? 2 : 1)
             if (!ok()) {
 #pragma unroll
                 for (int j = 0; j < COLS; ++j) acc[j] = __int_as_float(0x7fffffff);
+                if (BN < 256 && (!X_ROWS || split > 1)) {  // (what follows takes the memory that copies may still be on their way to)
+#pragma unroll 1
+                    for (int n = 0; asked_s < 0 && n < 1 << 22; ++n) {}
+                    landed(asked_s);
+                }
             }
             if (X_ROWS && split == 1) {
                 // out through 128 x 64 tiles in shared memory, which the copies have left by the next time (what lies
