@@ -58,24 +58,6 @@ static size_t dla_workspace(const DlaParams& p, bool backward) {
     return both > forward ? both : forward;
 }
 
-struct Span {
-    const void* at;
-    size_t bytes;
-    const char* name;
-};
-// refuses an output that shares memory with another tensor of the call
-static gdr_status apart(const Span* out, int outs, const Span* in, int ins) {
-    for (int i = 0; i < outs; ++i) {
-        const uintptr_t u = reinterpret_cast<uintptr_t>(out[i].at);
-        if (!u) continue;
-        for (int j = 0; j < ins + i; ++j) {
-            const Span& b = j < ins ? in[j] : out[j - ins];
-            const uintptr_t v = reinterpret_cast<uintptr_t>(b.at);
-            if (v && u < v + b.bytes && v < u + out[i].bytes) return fail(GDR_ERR_INVALID, "%s must not share memory with another tensor of the call", out[i].name);
-        }
-    }
-    return GDR_OK;
-}
 static size_t extent(int64_t tokens, int64_t ld, int64_t width) { return tokens ? 2 * (size_t)((tokens - 1) * ld + width) : 0; }
 
 // no tokens: the states pass through

@@ -26,6 +26,11 @@ gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t
     if (!x) return fail(GDR_ERR_INVALID, "required pointer %s is NULL", "x");
     if (!aligned_to(x, x_type == GDR_TYPE_F32 ? 8 : 4)) return fail(GDR_ERR_INVALID, "pointer %s is not aligned to two elements", "x");
     NEED(y); NEED(scale); OPT(y_t); OPT(scale_t);
+    const size_t codes = (size_t)rows * channels, blocks = (channels + 127) / 128;
+    const size_t scales = sizeof(float) * (tiles ? ((size_t)rows + 127) / 128 : (size_t)rows) * blocks;
+    const Span in[] = {{x, ((size_t)(rows - 1) * x_stride + channels) * (x_type == GDR_TYPE_F32 ? 4 : 2), "x"}};
+    const Span out[] = {{y, codes, "y"}, {scale, scales, "scale"}, {y_t, codes, "y_t"}, {scale_t, scales, "scale_t"}};
+    if (gdr_status st = apart(out, 4, in, 1)) return st;
     p.R = rows; p.ldx = x_stride; p.C = channels; p.x_f32 = x_type == GDR_TYPE_F32; p.tiles = tiles != 0;
     p.x = x; p.y = (uint8_t*)y; p.scale = scale; p.yt = (uint8_t*)y_t; p.scale_t = scale_t;
     cudaStream_t s = (cudaStream_t)stream;
@@ -46,6 +51,11 @@ gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const voi
     if (x_blocks != 1 && x_blocks != blocks) return fail(GDR_ERR_INVALID, "x_blocks must be 1 or ceil(inner / 128)%s");
     if (rows == 0) return ok();
     NEED(x); NEED(x_scale); NEED(w); NEED(w_scale); OPT(bias); NEED(y);
+    const size_t nb = x_blocks, nk = blocks, nr = (outer + 127) / 128;
+    const Span in[] = {{x, (size_t)rows * inner, "x"}, {x_scale, sizeof(float) * rows * nb, "x_scale"}, {w, (size_t)outer * inner, "w"},
+                       {w_scale, sizeof(float) * nr * nk, "w_scale"}, {bias, sizeof(float) * (size_t)outer, "bias"}};
+    const Span out[] = {{y, 2 * (size_t)rows * outer, "y"}};
+    if (gdr_status st = apart(out, 1, in, 5)) return st;
     p.M = rows; p.K = inner; p.N = outer; p.x_blocks = x_blocks;
     p.x = (const uint8_t*)x; p.w = (const uint8_t*)w; p.xs = x_scale; p.ws = w_scale; p.bias = bias; p.y = (__nv_bfloat16*)y;
     cudaStream_t s = (cudaStream_t)stream;

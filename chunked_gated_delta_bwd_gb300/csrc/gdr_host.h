@@ -26,6 +26,27 @@ inline bool aligned16(const void* p) { return aligned_to(p, 16); }
         if ((ptr) && !aligned16(ptr)) return fail(GDR_ERR_INVALID, "pointer %s is not 16-byte aligned", #ptr); \
     } while (0)
 
+// memory of a tensor of the call
+struct Span {
+    const void* at;
+    size_t bytes;
+    const char* name;
+};
+// Refuses an output that shares memory with another tensor of the call
+inline gdr_status apart(const Span* out, int outs, const Span* in, int ins) {
+    for (int i = 0; i < outs; ++i) {
+        const uintptr_t u = reinterpret_cast<uintptr_t>(out[i].at);
+        if (!u) continue;
+        for (int j = 0; j < ins + i; ++j) {
+            const Span& b = j < ins ? in[j] : out[j - ins];
+            const uintptr_t v = reinterpret_cast<uintptr_t>(b.at);
+            if (v && u < v + b.bytes && v < u + out[i].bytes)
+                return fail(GDR_ERR_INVALID, "%s must not share memory with another tensor of the call", out[i].name);
+        }
+    }
+    return GDR_OK;
+}
+
 // Event timing of the launches (off unless gdr_profile_begin was called).
 struct Prof {
     bool on = false;

@@ -407,7 +407,8 @@ gdr_status dla_step(int32_t rows, int32_t num_heads, int32_t num_k_heads, int32_
  *  * tiles = 0: scale float [rows, ceil(C / 128)].  tiles = 1: float [ceil(rows / 128), ceil(C / 128)].
  *  * y_t, scale_t (tiles only, both or neither; else NULL): the transposes, y_t [C, rows], scale_t
  *    [ceil(C / 128), ceil(rows / 128)], with the same codes: the operand of the product's backward.
- *  * A group that holds an infinity gets an infinite scale, one that holds a NaN a NaN among its codes. */
+ *  * A group that holds an infinity gets an infinite scale, one that holds a NaN a NaN among its codes.
+ *  * No output shares memory with x or another output (refused). */
 gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t x_stride, int32_t x_type,
                           int32_t tiles, void* y, float* scale, void* y_t, float* scale_t, void* stream);
 /* The product of two such operands:
@@ -416,8 +417,8 @@ gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t
  *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows at most 2^31 - 128.
  *  * x_scale: float [rows, ceil(K / 128)], or with x_blocks = 1 [rows, 1] for the whole row (x_blocks is
  *    1 or ceil(K / 128)); w_scale: float [ceil(N / 128), ceil(K / 128)]; bias float [N] or NULL.
- *  * y: bf16 [rows, N], rounded once from sums in fp32; it shares no memory with an input.  Should a bounded
- *    wait inside run out, the outputs concerned are NaN. */
+ *  * y: bf16 [rows, N], rounded once from sums in fp32; it shares no memory with an input (refused).  Should a
+ *    bounded wait inside run out, the outputs concerned are NaN. */
 gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const void* x, const float* x_scale,
                            int32_t x_blocks, const void* w, const float* w_scale, const float* bias, void* y,
                            void* stream);
