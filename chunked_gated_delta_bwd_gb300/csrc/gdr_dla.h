@@ -37,5 +37,6 @@ struct DlaStepParams {
     __nv_bfloat16* o;
 };
 cudaError_t launch_dla_step(const DlaStepParams& p, cudaStream_t s);
+int dla_step_kernels(const DlaStepParams& p);  // kernels that a launch enqueues
 
 }  // namespace gdr

@@ -165,7 +165,7 @@ gdr_status dla_step(int32_t rows, int32_t num_heads, int32_t num_k_heads, int32_
     p.q = (const __nv_bfloat16*)q; p.k = (const __nv_bfloat16*)k; p.v = (const __nv_bfloat16*)v;
     p.g = log_decay; p.slots = slots; p.state = state; p.o = (__nv_bfloat16*)o;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = timed(GDR_KERNEL_DLA, s, [&] { return launch_dla_step(p, s); });
+    cudaError_t e = timed(GDR_KERNEL_DLA, s, [&] { return launch_dla_step(p, s); }, dla_step_kernels(p));
     return e == cudaSuccess ? ok() : cuda_fail(e, "linear attention step launch");
 }
 

@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(256) k_dla_step(const DlaStepParams p) {
     }
 }
 
+constexpr int MOST = 65535;  // rows of a launch: a grid's y
+
 template <int D, int W>
 cudaError_t go(const DlaStepParams& p, cudaStream_t s) {
-    constexpr int MOST = 65535;  // of a grid's y
     DlaStepParams part = p;
     for (int n = 0; n < p.rows; n += MOST) {
         part.rows = p.rows - n < MOST ? p.rows - n : MOST;
@@ -87,6 +88,8 @@ cudaError_t go(const DlaStepParams& p, cudaStream_t s) {
 }
 
 }  // namespace
+
+int dla_step_kernels(const DlaStepParams& p) { return (p.rows + MOST - 1) / MOST; }
 
 cudaError_t launch_dla_step(const DlaStepParams& p, cudaStream_t s) {
     if (p.D == 64) return go<64, 64>(p, s);

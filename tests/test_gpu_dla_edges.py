@@ -32,3 +32,28 @@ def test_bad_sequence_borders_write_nothing(cu, D, Hk):
     assert api.workspace_status(ws) == api.GDR_DEV_BAD_SEQLENS
     for n, t in out.items():
         assert (t == 7.0).all(), n
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+def test_steps_of_more_rows_than_a_grid(pooled):
+    """The rows go out in two kernels, which are counted, and are those of two smaller calls."""
+    rows, first, D = 65535 + 6, 65000, 64
+    pool = rows + 3
+    gen = torch.Generator("cuda").manual_seed(95)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v = (n(rows, 1, D).to(torch.bfloat16) for _ in range(3))
+    g, state = torch.tensor([-0.1], device="cuda"), n(pool, 1, D, D)
+    slots = None
+    if pooled:
+        slots = torch.randperm(pool, generator=gen, device="cuda")[:rows]
+        slots[[5, rows - 2]] = torch.tensor([-1, pool], device="cuda")
+    want = state.clone()
+    parts = []
+    for a, b in ((0, first), (first, rows)):
+        mine = dict(slots=slots[a:b].clone()) if pooled else {}
+        parts.append(gdr.dla_step(q[a:b].clone(), k[a:b].clone(), v[a:b].clone(), g, want if pooled else want[a:], **mine))
+    api.profile_begin(2)
+    o = gdr.dla_step(q, k, v, g, state, slots=slots)
+    assert api.profile_end()["dla"][1] == 2
+    assert torch.equal(o, torch.cat(parts)) and torch.equal(state, want)
+    assert o[-1].any() and (not pooled or not o[rows - 2].any())
