@@ -367,7 +367,10 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
  *  * The states are carried in fp32 (the tokens' terms in twice bf16's 8 bits); the products that
  *    o, dq, dk and dv are read from have bf16 operands: q k^T with its decays, and the state.
  *  * A value that is not finite reaches its whole chunk of 128 tokens and, through the state, what
- *    follows it in its sequence and head; never another sequence.
+ *    follows it in its sequence and head (precedes it, for the gradients that are carried backwards), as far
+ *    as its decay e^{g n} over n tokens is not zero in fp32.  Beyond that it may stop: where one sequence is
+ *    shared by several multiprocessors, tokens whose decay is zero are not read again.  It never reaches
+ *    another sequence or head (but through q and k that heads share).
  *  * Inconsistent cu_seqlens raise GDR_DEV_BAD_SEQLENS in the workspace's status word and nothing is
  *    written; GDR_DEV_TIMEOUT means that a bounded wait ran out: results are missing.
  *  * Sizes: T_total at most 2^30, N H at most 2^24, T_total H at most 2^36.  No output shares memory

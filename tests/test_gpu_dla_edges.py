@@ -57,3 +57,35 @@ def test_steps_of_more_rows_than_a_grid(pooled):
     assert api.profile_end()["dla"][1] == 2
     assert torch.equal(o, torch.cat(parts)) and torch.equal(state, want)
     assert o[-1].any() and (not pooled or not o[rows - 2].any())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("at", [5, 1000, 5003])
+def test_what_is_not_finite_is_carried_along_a_shared_sequence(D, at):
+    """One sequence, long enough that several blocks share it: a token's NaN reaches all that its decay reaches in
+    fp32; where the decay is zero it is either carried on or gone, and nothing else comes of it."""
+    T, decays = 9000, [0.0, -1e-3, -0.02, -0.05, -2.0]
+    H = len(decays)
+    d = _inputs([T], H, H, D, 96, decays=decays)
+    call = lambda: {**gdr.dla_fwd(d["q"], d["k"], d["v"], d["g"], h0=d["h0"]),  # noqa: E731
+                    **gdr.dla_bwd(d["q"], d["k"], d["v"], d["g"], d["dO"], h0=d["h0"], dht=d["dht"])}
+    clean = call()
+    keep = {n: d[n].clone() for n in ("v", "dO")}
+    first = at // 128 * 128  # of the token's chunk
+    rows = torch.arange(T, device="cuda")[:, None]
+    for name, ahead, hit, state in (("v", rows - at, ("o", "dq"), "ht"), ("dO", at - rows, ("dk", "dv"), "dh0")):
+        d[name][at] = float("nan")
+        out = call()
+        d[name].copy_(keep[name])
+        # e^-100 = 3.7e-44, a subnormal number that is not zero; e^-104 rounds to zero
+        reached = (ahead >= 0) & (ahead * -d["g"] < 100)
+        before = rows < first if name == "v" else rows >= first + 128
+        for n in hit:
+            bad = torch.isnan(out[n])
+            assert bad[reached.expand(T, H)].all(), (name, n)
+            same = (out[n] == clean[n]).all(2)
+            assert same[before.expand(T, H)].all(), (name, n)
+            assert (bad.all(2) | same | ((rows >= first) & (rows < first + 128))).all(), (name, n)
+        end = torch.isnan(out[state])[0].flatten(1)
+        far = (T - at if name == "v" else at) * -d["g"]
+        assert end[far < 100].all() and (end.all(1) | (out[state][0] == clean[state][0]).flatten(1).all(1)).all(), name
