@@ -4,6 +4,7 @@ Each translation unit is compiled by its own nvcc process (in parallel), then
 linked into one shared library that exports the C ABI of include/gdr.h.
 """
 import os
+import re
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -19,6 +20,20 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
          "-Xptxas", "-v"]
+# Kernels whose warps move registers among themselves (setmaxnreg): the shares have to come out of what the compiler
+# gave a thread at the launch, or the warps that ask for more wait for ever.
+REGISTERS = {"gdr_dla.cu": (r"k_dlaILi\d+ELi\d+E", 96), "gdr_linear.cu": (r"k_linearILb1ELi256E", 168)}
+
+
+def check_registers(src, log):
+    """Raises where the compiler's report (-Xptxas -v) gives a kernel of REGISTERS another number of registers."""
+    if src not in REGISTERS:
+        return
+    kernel, want = REGISTERS[src]
+    for name, got in re.findall(r"entry function '(\S+)' for .*?Used (\d+) registers", log, re.S):
+        if re.search(kernel, name) and int(got) != want:
+            raise RuntimeError("%s: the compiler gave %s %s registers a thread, and its warps' shares are made for %d"
+                               % (src, name, got, want))
 
 
 def _deps():
@@ -46,6 +61,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, r.stdout, r.stderr))
+        check_registers(src, r.stdout + r.stderr)
         return obj, r.stderr
 
     with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
