@@ -3,7 +3,8 @@
     s = x + residual;  y = RMSnorm(s);  u, g = y W_in;  c = SiLU(conv1d(u));  h = recurrence(c, g);  out = h W_out
 
 The norm, the conv and the recurrence are the library's calls (with their backward and their
-single-token forms); the two projections are torch products.  Run as a program it trains the
+single-token forms); the two projections are torch products, or for an 8-bit prefill the first is the
+library's product of the norm's e4m3 codes with those of the weight.  Run as a program it trains the
 block for a few steps to remember tokens, and checks that decoding token by token continues a
 prefill:
 
@@ -44,12 +45,11 @@ class RecurrentBlock:
         return dict(A_log=self.p["A_log"], dt_bias=self.p["dt_bias"], gate="softplus", complement=True)
 
     def _project(self, normed, weight):
-        """y W for y as rmsnorm_fwd gives it: bf16, or e4m3 with a scale for each 128 channels."""
-        y = normed["y"]
-        if "scale" in normed:
-            scale = normed["scale"].repeat_interleave(128, dim=1)[:, :y.shape[1]]
-            y = (y.float() * scale).to(torch.bfloat16)
-        return y @ weight.to(torch.bfloat16)
+        """y W for y as rmsnorm_fwd gives it: bf16, or e4m3 with a scale for each 128 channels (a multiple of 16)."""
+        if "scale" in normed:  # (a server whose weights stay would keep w)
+            w = gdr.quant_e4m3(weight, tiles=True, transposed=True)  # (weight is [in, out], the product's [out, in])
+            return gdr.linear_e4m3(normed["y"], normed["scale"], w["y_t"], w["scale_t"])
+        return normed["y"] @ weight.to(torch.bfloat16)
 
     def forward(self, x, residual, cu_seqlens, states=None, eight_bit=False):
         """x, residual bf16 [T, C]; ``states``: a pool's (conv, recurrence) states before the sequences.
