@@ -89,3 +89,31 @@ def test_what_is_not_finite_is_carried_along_a_shared_sequence(D, at):
         end = torch.isnan(out[state])[0].flatten(1)
         far = (T - at if name == "v" else at) * -d["g"]
         assert end[far < 100].all() and (end.all(1) | (out[state][0] == clean[state][0]).flatten(1).all(1)).all(), name
+
+
+def test_states_past_32_bits():
+    """More than 2^32 numbers of states, in sequences and in a pool: the last ones are those of a call of their own."""
+    N, H, D = 70_000, 4, 128
+    assert N * H * D * D > 1 << 32
+    gen = torch.Generator("cuda").manual_seed(97)
+    n = lambda *s: torch.randn(*s, generator=gen, device="cuda")  # noqa: E731
+    q, k, v, dO = (n(2 * N, H, D).to(torch.bfloat16) for _ in range(4))
+    g, some = torch.tensor([-0.1, -0.01, -1.0, 0.0], device="cuda"), n(7, H, D, D)
+    h0 = some.repeat(N // 7, 1, 1, 1)
+    out = gdr.dla_fwd(q, k, v, g, h0=h0, num_seqs=N)
+    grad = gdr.dla_bwd(q, k, v, g, dO, h0=h0, dht=h0, num_seqs=N)
+    for s in (0, 33_000, N - 7):  # (a multiple of 7 beyond 2^31 numbers is near the second)
+        s = s // 7 * 7
+        tail = lambda t: t[2 * s:2 * s + 14].clone()  # noqa: E731
+        a = gdr.dla_fwd(tail(q), tail(k), tail(v), g, h0=some, num_seqs=7)
+        b = gdr.dla_bwd(tail(q), tail(k), tail(v), g, tail(dO), h0=some, dht=some, num_seqs=7)
+        assert torch.equal(out["o"][2 * s:2 * s + 14], a["o"]) and torch.equal(out["ht"][s:s + 7], a["ht"])
+        for name in ("dq", "dk", "dv"):
+            assert torch.equal(grad[name][2 * s:2 * s + 14], b[name]), name
+        assert torch.equal(grad["dh0"][s:s + 7], b["dh0"])
+    del out, grad
+    slots = torch.tensor([N - 1, 0, 40_000], device="cuda")
+    part = h0[slots].clone()
+    o = gdr.dla_step(q[:3], k[:3], v[:3], g, h0, slots=slots)
+    assert torch.equal(o, gdr.dla_step(q[:3], k[:3], v[:3], g, part)) and torch.equal(h0[slots], part)
+    assert torch.equal(h0[N - 2], some[5]) and torch.equal(h0[40_001], some[40_001 % 7])
