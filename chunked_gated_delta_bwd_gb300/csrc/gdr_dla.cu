@@ -23,11 +23,14 @@
 //   issuer 3  the state's terms Y'^T Z, and X C
 //   stores    the outputs, by TMA
 //   group A   (eight warps) P times the decays, rounded to bf16 (tensor memory); out, staged in X's tile
-//   group B   (eight warps) Y' = w Y as two bf16 tiles, whose products with Z make the state's terms good to 2^-16; the
+//   group B   (eight warps) Y' = w Y as two bf16 tiles, whose products with Z make the state's terms good to 2^-17; the
 //             state's sum in fp32, and its bf16 copy for X C
-// P and the state's copy are rounded to bf16: each adds 2^-9 at most to a term of an output that is rounded to bf16 itself
+// P and the state's copy are rounded to bf16: each adds up to 2^-8 of a term of an output that is rounded to bf16 itself
 // (o and the gradients are off by 2.3e-3 in the 2-norm; their own rounding alone is 1.7e-3).  The tokens' terms of the
-// states keep 2^-17 (ht, dh0: 2.5e-6).  With one half of Y' in the walks whose states do not leave, dq and dk were off by
+// states keep 2^-17: the first part leaves 2^-8 of a value's power of two at most, whose half step is 2^-17 (ht, dh0: 2.5e-6; a
+// plain fp32 form 3e-7.  A third part does not fit: the seven tiles of 128 channels fill shared memory.  Y itself as an exact part
+// for long memories, and a third one in Y's place for the chunks near a chain's end, took 6.4e-7, and 12 to 20% more time, most of
+// it in calls that hardly ran them).  With one half of Y' in the walks whose states do not leave, dq and dk were off by
 // 2.7e-3, for 2 us in 355.
 //
 // Measured (32768 tokens, 16 heads of 128): forward 155 us, its walk 98 (5.5 TB/s); backward 355, its three walks 265.  A

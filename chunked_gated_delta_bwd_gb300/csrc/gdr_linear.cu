@@ -6,9 +6,10 @@
 // steps of 32 of the inner dimension) goes into tensor memory by itself, and groups of threads add it, times its scale,
 // to sums in fp32 registers while the next blocks' products run into other columns of the tensor memory.
 //
-// What bounds it with many rows: 128 x 256 sums of a block of 128 take 512 cycles of products and about 700 of what follows
-// them (the accumulators' way from tensor memory into the sums, and the hand-over of the buffer), with the tensor cores at
-// 59% of their cycles.  32768 x 2048 x 6144 takes 305 us, 2.7 PFLOP/s (340 in a long loop, under the power cap).
+// What bounds it with many rows is no part alone.  32768 x 2048 x 6144 takes 305 us, 2.7 PFLOP/s (340 in a long loop, under the
+// power cap), with the tensor cores at 59% of their cycles (512 for 128 x 256 sums of a block of 128).  Copies of the kernel that
+// leave out the sums take 288, the tiles' loads (4.8 GB from the second-level cache, 16 TB/s) 283, both 256: what is left then
+// is products and the hand-over of two accumulators between the warps that issue and those that add.
 //
 // Two forms, the same loop:
 //   rows of x as the product's rows  (many rows of x): a thread holds one row, its scale is one number; blocks

@@ -363,8 +363,9 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
  *  * log_decay: float [H].  It is meant to be <= 0 (below -10^4 it counts as -10^4: no memory);
  *    growth is computed as such until fp32 overflows.  It is a constant: it has no gradient here.
  *  * h0, ht, dht, dh0: float [N, H, D, D] (row = key channel); h0, ht and dht may be NULL.  An empty
- *    sequence passes its state through (ht = h0, dh0 = dht).  T_total = 0 is a valid call.
- *  * The states are carried in fp32 (the tokens' terms in twice bf16's 8 bits); the products that
+ *    sequence passes its state through (ht = h0, dh0 = dht).  T_total = 0 is a valid call (cu_seqlens is not
+ *    read then).
+ *  * The states are carried in fp32 (the tokens' terms in two bf16 parts, good to 2^-17); the products that
  *    o, dq, dk and dv are read from have bf16 operands: q k^T with its decays, and the state.
  *  * A value that is not finite reaches its whole chunk of 128 tokens and, through the state, what
  *    follows it in its sequence and head (precedes it, for the gradients that are carried backwards), as far
@@ -375,7 +376,8 @@ gdr_status gdr_rmsnorm_bwd(int64_t rows, int32_t channels, const void* dy, const
  *    written; GDR_DEV_TIMEOUT means that a bounded wait ran out: results are missing.
  *  * Sizes: T_total at most 2^30, N H at most 2^24, T_total H at most 2^36.  No output shares memory
  *    with an input, another output or the workspace.  Every result is the same, bit for bit, from one
- *    call to the next.  The workspace need not be initialised; calls that may overlap need one each. */
+ *    call to the next.  The workspace need not be initialised; calls that may overlap need one each.  It is
+ *    small but for dla_bwd with shared heads, which keeps dq and dk of each value head there: 8 T_total H D bytes. */
 typedef struct {
     int32_t num_seqs;          /* N >= 1 */
     int64_t total_tokens;      /* T_total >= 0 */
@@ -420,6 +422,10 @@ gdr_status gdr_quant_e4m3(int64_t rows, int32_t channels, const void* x, int64_t
  *  * x: e4m3 [rows, K]; w: e4m3 [N, K]; K a multiple of 16, N of 8, both at most 2^24; rows at most 2^31 - 128.
  *  * x_scale: float [rows, ceil(K / 128)], or with x_blocks = 1 [rows, 1] for the whole row (x_blocks is
  *    1 or ceil(K / 128)); w_scale: float [ceil(N / 128), ceil(K / 128)]; bias float [N] or NULL.
+ *  * A block's two scales are multiplied in fp32 before they are applied: where that product is below 2^-126 or above
+ *    2^128, so is what it makes of the block (fewer bits or zero; infinite, or NaN for a sum of zero).
+ *  * The gradient of x is the product with the weight's transposes (y_t, scale_t).  The weight's own, dy^T x, has
+ *    no 8-bit form here: both its operands would need scales along the rows, which the quantisation does not give.
  *  * y: bf16 [rows, N], rounded once from sums in fp32; it shares no memory with an input (refused).  Should a
  *    bounded wait inside run out, the outputs concerned are NaN. */
 gdr_status gdr_linear_e4m3(int64_t rows, int32_t inner, int32_t outer, const void* x, const float* x_scale,
