@@ -6,7 +6,8 @@ r's rounding is off by half a step of r's own binade, 2^(E-17) at most: 2^(2E-34
 2^(E-17) 0.44 in the root, 2^-17 0.31 = 2.4e-6 of f (whose root mean square is 1.4 2^E).  fp32 adds up to 2^-23 for each addition of
 the products of 16 tokens and a part to a sum (the tensor cores cut off; 16 for each chunk, of which the later ones count fully):
 1.2e-7 sqrt 16 = 4.8e-7 in the root mean square.  Together 2.5e-6; 2^-18 = 3.8e-6 leaves half of it again for states whose f lie low
-in their binades (0.44 2^-17 = 3.4e-6 where all do).  With growth the first tokens count most, and a chunk's growth (expf and its
+in their binades (0.44 2^-17 = 3.4e-6 where all do).  The terms of a few tokens share a few weights, whose products with y need not
+spread evenly: below 32 tokens the bound of every term counts, 2^-17, and 2^-20 for fp32.  With growth the first tokens count most, and a chunk's growth (expf and its
 argument: 2^-23 together) multiplies them once for each chunk that follows.
 """
 import numpy as np
@@ -53,5 +54,5 @@ def test_states_one_by_one(lens, D, states):
             size = want.flatten(1).norm(dim=1)
             # (where nothing but what has decayed to nothing is left, e^-104 and below counts as zero)
             growth = torch.where(g > 0, (e - b) / 128 * 2.0 ** -23, 0.0)
-            bad = off > (2.0 ** -18 + growth) * size + 2.0 ** -140
+            bad = off > ((2.0 ** -18 if e - b >= 32 else 2.0 ** -17 + 2.0 ** -20) + growth) * size + 2.0 ** -140
             assert not bad.any(), (name, s, [(DECAYS[i], float(off[i] / size[i])) for i in bad.nonzero().flatten().tolist()])
