@@ -42,7 +42,8 @@
 //
 // A chain that crosses from one range into the next: k_dla_tail first sums, for each range, the terms of
 // its last chain's tokens (it reads only Y and Z, from the range's end backwards, and stops where the decay
-// has underflowed, so that a NaN from there on does not reach the next range; 41 us forward, 77 for the backward's two sums), k_dla_join carries them along the chain (8 to 12 us),
+// has underflowed, so that a NaN from there on does not reach the next range; 41 us forward, 77 for the
+// backward's two sums), k_dla_join carries them along the chain (8 to 12 us),
 // and the walk starts from there.
 #include "gdr_dla.h"
 #include "gdr_dla_plan.cuh"
